@@ -62,12 +62,52 @@ class DcpPagedCacheC(ctypes.Structure):
                 ("hist_len", ctypes.c_void_p), ("hist_t", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+class DcpKvPoolC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int64),
+                ("s_block", ctypes.c_int64), ("s_head", ctypes.c_int64), ("s_row", ctypes.c_int64)]
+
+
+class DcpSeqBatchC(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("total_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("kv_len_per_head", ctypes.c_int32), ("max_kv", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("kv_len_add", ctypes.c_int64), ("q_start", ctypes.c_void_p), ("tables", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+DCP_ROPE_MAX_PAIRS = 64
+
+
+class DcpRopeConfigC(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("pair_layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class DcpRopePlanC(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("pair_layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * DCP_ROPE_MAX_PAIRS)]
+
+
+class DcpAttnConfigC(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class DcpPagePoolC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("L", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("n_blocks", ctypes.c_int64), ("page_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)]
+
+
 class DcpPrCounter(ctypes.Structure):
     _fields_ = [("visible", ctypes.c_int64), ("full", ctypes.c_int64)]
 
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _pc, _pg = ctypes.POINTER(DcpCacheC), ctypes.POINTER(DcpConfigC)
+_pk, _pb, _pa = ctypes.POINTER(DcpKvPoolC), ctypes.POINTER(DcpSeqBatchC), ctypes.POINTER(DcpAttnConfigC)
+_pp = ctypes.POINTER(DcpPagePoolC)
 _SIGS = {
     "dcp_workspace_size": ([_pc, _pg], _sz),
     "dcp_score_workspace_size": ([_i32], _sz),
@@ -98,6 +138,17 @@ _SIGS = {
     "dcp_snapshot": ([_pc, _pg, ctypes.c_uint32, _i32, _vp, _sz, _vp, _sz, _vp], _i32),
     "dcp_restore": ([_pc, _pg, _vp, _sz, ctypes.POINTER(_i32), ctypes.POINTER(ctypes.c_uint32), _vp, _sz, _vp],
                     _i32),
+    "dcp_rope_plan_init": ([ctypes.POINTER(DcpRopeConfigC), ctypes.POINTER(DcpRopePlanC)], _i32),
+    "dcp_rope_append": ([_pk, _pb, ctypes.POINTER(DcpRopePlanC), _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp],
+                        _i32),
+    "dcp_attention_workspace_size": ([_pk, _pb, _pa, _i32], _sz),
+    "dcp_paged_attention": ([_pk, _pb, _pa, _vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "dcp_pages_workspace_size": ([_pp, _i32, _i32], _sz),
+    "dcp_pages_copy": ([_pp, _vp, _vp, _i32, _vp], _i32),
+    "dcp_pages_fork": ([_pp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "dcp_pages_free": ([_pp, _vp, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
+    "dcp_pages_compact": ([_pp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "dcp_abi_serving_struct_size": ([_i32], ctypes.c_uint32),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -108,6 +159,9 @@ _sizes = lib.dcp_abi_struct_sizes()
 if (_sizes >> 16) != ctypes.sizeof(DcpCacheC) or (_sizes & 0xFFFF) != ctypes.sizeof(DcpConfigC) or \
         lib.dcp_abi_paged_cache_size() != ctypes.sizeof(DcpPagedCacheC):
     raise ImportError("libdcp struct layout does not match the binding")
+for _i, _t in enumerate((DcpKvPoolC, DcpSeqBatchC, DcpRopeConfigC, DcpRopePlanC, DcpAttnConfigC, DcpPagePoolC)):
+    if lib.dcp_abi_serving_struct_size(_i) != ctypes.sizeof(_t):
+        raise ImportError(f"libdcp struct layout does not match the binding: {_t.__name__}")
 
 
 class DcpError(RuntimeError):
@@ -433,3 +487,224 @@ def dcp_phase_table(cfg: Config, q0: int, frame_lo: int, frame_hi: int, out: tor
     gc = cfg.c()
     _check(lib.dcp_phase_table(ctypes.byref(gc), q0, frame_lo, frame_hi, _ptr(out), _stream(stream)),
            "dcp_phase_table")
+
+
+# ------------------------------------------------------------------------------------------ serving operators
+DCP_ROPE_INTERLEAVED, DCP_ROPE_HALF = 0, 1
+DCP_ROPE_PLAIN, DCP_ROPE_LINEAR, DCP_ROPE_BASE, DCP_ROPE_PARTS = range(4)
+
+
+class KVPool:
+    """One layer's pages (dcp_kv_pool).  k, v: [n_blocks][H][block_size][D] (DCP_PAGED_HND) or
+    [n_blocks][block_size][H][D] (DCP_PAGED_NHD), bf16 or fp32; views with other strides are fine as long as both
+    have the same and D is dense."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, layout: int):
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or \
+                k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float32):
+            raise DcpError("KVPool", DCP_EINVAL)
+        h, r = (1, 2) if layout == DCP_PAGED_HND else (2, 1)
+        self.k, self.v, self.D, self.H, self.dtype = k, v, k.shape[3], k.shape[h], k.dtype
+        self._c = DcpKvPoolC(_ptr(k), _ptr(v), k.shape[h], k.shape[3],
+                             DCP_BF16 if k.dtype == torch.bfloat16 else DCP_F32, k.shape[r], k.shape[0], k.stride(0),
+                             k.stride(h), k.stride(r))
+        self.ref = ctypes.byref(self._c)
+
+    def c(self) -> DcpKvPoolC:
+        return self._c
+
+
+def layer_pool(cache, layer: int, block_size: int = 0) -> KVPool:
+    """Layer `layer` of a PagedKVCache, or of a KVCache cut into pages of block_size rows (a divisor of cap): page b
+    of the latter holds rows [b * block_size, (b + 1) * block_size) of every plane."""
+    if isinstance(cache, PagedKVCache):
+        return KVPool(cache.k_pool[layer], cache.v_pool[layer], cache.layout)
+    if block_size < 1 or cache.cap % block_size:
+        raise DcpError("layer_pool", DCP_EINVAL)
+    k, v = (x[layer].view(cache.H, cache.cap // block_size, block_size, cache.D).transpose(0, 1)
+            for x in (cache.k, cache.v))
+    return KVPool(k, v, DCP_PAGED_HND)
+
+
+class SeqBatch:
+    """The ragged batch (dcp_seq_batch).  Device int32 tensors: q_start [n + 1], tables [n][stride], kv_len [n] (or
+    [n][H]), status [1].  max_q and max_kv are bounds the host knows."""
+
+    def __init__(self, q_start: torch.Tensor, tables: torch.Tensor, kv_len: torch.Tensor, status: torch.Tensor,
+                 total_q: int, max_q: int, max_kv: int, kv_len_add: int = 0):
+        n = tables.shape[0]
+        if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (q_start, tables, kv_len, status)) or \
+                tables.dim() != 2 or q_start.numel() != n + 1 or kv_len.dim() not in (1, 2) or kv_len.shape[0] != n:
+            raise DcpError("SeqBatch", DCP_EINVAL)
+        self.tensors = (q_start, tables, kv_len, status)
+        self.n_seqs, self.total_q, self.kv_heads = n, total_q, kv_len.shape[1] if kv_len.dim() == 2 else 0
+        self._c = DcpSeqBatchC(n, total_q, max_q, int(kv_len.dim() == 2), max_kv, tables.shape[1], kv_len_add,
+                               _ptr(q_start), _ptr(tables), _ptr(kv_len), _ptr(status))
+        self.ref = ctypes.byref(self._c)
+
+    def c(self) -> DcpSeqBatchC:
+        return self._c
+
+
+@dataclass
+class RopeConfig:
+    """Rotary positions (dcp_rope_config)."""
+    rot_dim: int
+    pair_layout: int = DCP_ROPE_INTERLEAVED
+    base: float = 10000.0
+    scaling: int = DCP_ROPE_PLAIN
+    factor: float = 1.0
+    orig_len: float = 4096.0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    amplitude: float = 1.0
+
+    def c(self) -> DcpRopeConfigC:
+        return DcpRopeConfigC(self.rot_dim, self.pair_layout, self.scaling, 0, self.base, self.factor, self.orig_len,
+                              self.beta_fast, self.beta_slow, self.amplitude)
+
+
+def dcp_rope_plan(cfg: RopeConfig) -> DcpRopePlanC:
+    """The rotary plan of a config: made once, kept by the caller, passed to every dcp_rope_append."""
+    plan, c = DcpRopePlanC(), cfg.c()
+    _check(lib.dcp_rope_plan_init(ctypes.byref(c), ctypes.byref(plan)), "dcp_rope_plan_init")
+    return plan
+
+
+def _rows_of(t: torch.Tensor, pool: KVPool, batch: SeqBatch, heads: int, what: str) -> int:
+    """Token stride of a [total_q][heads][D] tensor of the pool's type whose heads are dense."""
+    if t.dtype != pool.dtype or t.shape != (batch.total_q, heads, pool.D):
+        raise DcpError(what, DCP_EINVAL)
+    s = t.stride()
+    if s[2] != 1 or (s[1] != pool.D and heads > 1):
+        raise DcpError(what, DCP_EINVAL)
+    return s[0] if batch.total_q > 1 else heads * pool.D
+
+
+def dcp_rope_append(pool: KVPool, batch: SeqBatch, plan: DcpRopePlanC, q, k: torch.Tensor, v: torch.Tensor,
+                    positions, q_out, stream=None) -> None:
+    """Turn q and k of the new tokens, put k and v into the pool's pages; q_out gets the turned q.  q, k, v are
+    [total_q][heads][D] (views of one fused projection are fine), positions int32 [total_q] or None."""
+    kv_stride = _rows_of(k, pool, batch, pool.H, "dcp_rope_append")
+    if _rows_of(v, pool, batch, pool.H, "dcp_rope_append") != kv_stride or \
+            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
+                                        positions.numel() != batch.total_q)):
+        raise DcpError("dcp_rope_append", DCP_EINVAL)
+    hq, q_stride = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        q_stride = _rows_of(q, pool, batch, hq, "dcp_rope_append")
+        if q_out is None or _rows_of(q_out, pool, batch, hq, "dcp_rope_append") != hq * pool.D:
+            raise DcpError("dcp_rope_append", DCP_EINVAL)
+    _check(lib.dcp_rope_append(pool.ref, batch.ref, plan, _ptr(q), q_stride, hq, _ptr(k), _ptr(v), kv_stride,
+                               _ptr(positions), _ptr(q_out), _stream(stream)), "dcp_rope_append")
+
+
+@dataclass
+class AttnConfig:
+    """Attention over the paged cache (dcp_attn_config); scale None: D ** -0.5."""
+    scale: float | None = None
+    causal: bool = True
+    window: int = -1
+
+    def c(self, D: int) -> DcpAttnConfigC:
+        return DcpAttnConfigC(D ** -0.5 if self.scale is None else self.scale, int(self.causal), self.window, 0)
+
+
+def dcp_attention_workspace_size(pool: KVPool, batch: SeqBatch, cfg: AttnConfig, Hq: int) -> int:
+    n = lib.dcp_attention_workspace_size(pool.ref, batch.ref, cfg.c(pool.D), Hq)
+    if n == 0:
+        raise DcpError("dcp_attention_workspace_size", DCP_EINVAL)
+    return n
+
+
+def dcp_paged_attention(pool: KVPool, batch: SeqBatch, cfg: AttnConfig, q: torch.Tensor, out: torch.Tensor, lse,
+                        ws: torch.Tensor, stream=None) -> None:
+    """out [total_q][Hq][D] = attention of the new tokens q over the cache; lse (or None): fp32 [total_q][Hq]."""
+    hq = q.shape[1]
+    q_stride = _rows_of(q, pool, batch, hq, "dcp_paged_attention")
+    if _rows_of(out, pool, batch, hq, "dcp_paged_attention") != hq * pool.D or batch.kv_heads not in (0, pool.H) or \
+            (lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                                  lse.numel() != batch.total_q * hq)):
+        raise DcpError("dcp_paged_attention", DCP_EINVAL)
+    _check(lib.dcp_paged_attention(pool.ref, batch.ref, cfg.c(pool.D), _ptr(q), q_stride, hq, _ptr(out), _ptr(lse),
+                                   _ptr(ws), ws.numel(), _stream(stream)), "dcp_paged_attention")
+
+
+class PagePool:
+    """Every layer's pages (dcp_page_pool).  k, v: [L][n_blocks][...] contiguous, a page of block_size positions in
+    the trailing dims (either layout of PagedKVCache)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_size: int, status: torch.Tensor):
+        if k.shape != v.shape or k.dtype != v.dtype or k.dim() < 3 or not k.is_contiguous() or not v.is_contiguous():
+            raise DcpError("PagePool", DCP_EINVAL)
+        self.tensors, self.n_blocks = (k, v, status), k.shape[1]
+        self._c = DcpPagePoolC(_ptr(k), _ptr(v), k.shape[0], block_size, k.shape[1],
+                               k[0, 0].numel() * k.element_size(), _ptr(status))
+        self.ref = ctypes.byref(self._c)
+
+    @classmethod
+    def of(cls, cache: PagedKVCache) -> "PagePool":
+        return cls(cache.k_pool, cache.v_pool, cache.block_size, cache.status)
+
+    def c(self) -> DcpPagePoolC:
+        return self._c
+
+
+def _ints(what: str, *tensors) -> None:
+    for t in tensors:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise DcpError(what, DCP_EINVAL)
+
+
+def dcp_pages_workspace_size(pool: PagePool, n_rows: int, stride: int) -> int:
+    n = lib.dcp_pages_workspace_size(pool.ref, n_rows, stride)
+    if n == 0:
+        raise DcpError("dcp_pages_workspace_size", DCP_EINVAL)
+    return n
+
+
+def dcp_pages_copy(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Block dst[i] = block src[i] in every layer."""
+    _ints("dcp_pages_copy", src, dst)
+    if src.numel() != dst.numel():
+        raise DcpError("dcp_pages_copy", DCP_EINVAL)
+    _check(lib.dcp_pages_copy(pool.ref, _ptr(src), _ptr(dst), src.numel(), _stream(stream)), "dcp_pages_copy")
+
+
+def dcp_pages_fork(pool: PagePool, tables: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor, shared, reserve,
+                   ref: torch.Tensor, child_tables: torch.Tensor, ref_out: torch.Tensor, ws: torch.Tensor,
+                   stream=None) -> None:
+    """Branch rows parent[c] of `tables` into child_tables; shared and reserve (int32 [n_children]) may be None."""
+    _ints("dcp_pages_fork", tables, lens, parent, shared, reserve, ref, child_tables, ref_out)
+    (rows, stride), n = tables.shape, parent.numel()
+    if child_tables.shape != (n, stride) or lens.numel() != rows or ref.numel() != pool.n_blocks or \
+            ref_out.numel() != pool.n_blocks or any(t is not None and t.numel() != n for t in (shared, reserve)):
+        raise DcpError("dcp_pages_fork", DCP_EINVAL)
+    _check(lib.dcp_pages_fork(pool.ref, _ptr(tables), _ptr(lens), rows, stride, _ptr(parent), _ptr(shared),
+                              _ptr(reserve), n, _ptr(ref), _ptr(child_tables), _ptr(ref_out), _ptr(ws), ws.numel(),
+                              _stream(stream)), "dcp_pages_fork")
+
+
+def _tables_and_counts(what: str, pool: PagePool, tables, ref, tables_out, ref_out) -> None:
+    _ints(what, tables, ref, tables_out, ref_out)
+    if tables_out.shape != tables.shape or ref.numel() != pool.n_blocks or ref_out.numel() != pool.n_blocks:
+        raise DcpError(what, DCP_EINVAL)
+
+
+def dcp_pages_free(pool: PagePool, tables: torch.Tensor, ref: torch.Tensor, tables_out: torch.Tensor,
+                   ref_out: torch.Tensor, stream=None) -> None:
+    """Drop every row of `tables`."""
+    _tables_and_counts("dcp_pages_free", pool, tables, ref, tables_out, ref_out)
+    _check(lib.dcp_pages_free(pool.ref, _ptr(tables), tables.shape[0], tables.shape[1], _ptr(ref), _ptr(tables_out),
+                              _ptr(ref_out), _stream(stream)), "dcp_pages_free")
+
+
+def dcp_pages_compact(pool: PagePool, tables: torch.Tensor, ref: torch.Tensor, tables_out: torch.Tensor,
+                      ref_out: torch.Tensor, n_live, ws: torch.Tensor, stream=None) -> None:
+    """Pack the live blocks to the front of the pool; tables and counts follow, n_live (int32 [1] or None)."""
+    _tables_and_counts("dcp_pages_compact", pool, tables, ref, tables_out, ref_out)
+    _ints("dcp_pages_compact", n_live)
+    _check(lib.dcp_pages_compact(pool.ref, _ptr(tables), tables.shape[0], tables.shape[1], _ptr(ref),
+                                 _ptr(tables_out), _ptr(ref_out), _ptr(n_live), _ptr(ws), ws.numel(),
+                                 _stream(stream)), "dcp_pages_compact")

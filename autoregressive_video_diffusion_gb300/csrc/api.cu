@@ -794,7 +794,7 @@ const char* dcp_status_string(dcp_status s) {
     case DCP_EINVAL: return "invalid argument";
     case DCP_ECAPACITY: return "history capacity exceeded";
     case DCP_ECUDA: return "CUDA runtime error";
-    case DCP_ETIMEOUT: return "timed out (not produced by this version)";
+    case DCP_ETIMEOUT: return "a bounded wait inside a kernel ran out";
     case DCP_EDEVICE: return "inconsistent cache state on the device";
     default: return "unknown status";
   }

@@ -1,0 +1,242 @@
+// Pages of every layer's pool: copying, forking, packing and freeing.
+//
+// The bookkeeping (which block goes where) is one CTA's work over the reference counts and tables; it leaves a list
+// of (source, destination) blocks in the workspace, which the copy kernel behind it on the stream moves.
+#include "serve.cuh"
+
+namespace dcp {
+
+namespace {
+
+constexpr int kPlan = 1024;  // threads of a bookkeeping CTA
+
+// Workspace: [0] number of moves, then (from kHead on) the list of (source, destination) pairs.
+constexpr int kHead = 64;
+
+// Exclusive sum of x over the CTA, *total the whole sum.
+__device__ int block_scan(int x, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int w = lane < warps ? s_warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(~0u, w, warps - 1);
+  const int before = __shfl_sync(~0u, w, warp ? warp - 1 : 0);
+  return v - x + (warp ? before : 0);
+}
+
+// Moves the listed pages: an item is one page of one layer and tensor, blockIdx.x strides over all of them.
+__global__ void __launch_bounds__(kThreads) move_kernel(PageParams p, const int32_t* src, const int32_t* dst,
+                                                        int step, const int32_t* count, int32_t n) {
+  const int64_t items = (int64_t)(count ? *count : n) * p.L * 2;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t pair = it / (2 * p.L);
+    const int layer = (int)(it / 2 % p.L);
+    const int64_t a = src[pair * step], b = dst[pair * step];
+    if (a < 0 || b < 0 || a >= p.n_blocks || b >= p.n_blocks) {
+      if (threadIdx.x == 0) set_status(p.status, DCP_EDEVICE);
+      continue;
+    }
+    char* base = (it & 1 ? p.v : p.k) + layer * p.n_blocks * p.page_bytes;
+    const uint4* from = (const uint4*)(base + a * p.page_bytes);
+    uint4* to = (uint4*)(base + b * p.page_bytes);
+    for (int64_t i = threadIdx.x; i < p.page_bytes / 16; i += blockDim.x) to[i] = from[i];
+  }
+}
+
+__global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t* tables, const int32_t* len,
+                                                     int32_t n_rows, int32_t stride, const int32_t* parent,
+                                                     const int32_t* shared, const int32_t* reserve,
+                                                     int32_t n_children, const int32_t* ref_in, int32_t* child,
+                                                     int32_t* ref_out, int32_t* ws) {
+  __shared__ int s_warp[32];
+  __shared__ int s_bad, s_moves;
+  int2* moves = (int2*)(ws + kHead);
+  int32_t* first = ws + kHead + 2 * (int64_t)n_children * stride;  // fresh blocks before child c
+  int32_t* fresh = first + n_children;                             // the lowest free blocks
+  if (threadIdx.x == 0) s_bad = s_moves = 0;
+  __syncthreads();
+  // every child's shared, copied and reserved pages
+  int need = 0;
+  for (int c0 = 0; c0 < n_children; c0 += kPlan) {
+    const int c = c0 + threadIdx.x;
+    int want = 0;
+    if (c < n_children) {
+      const int r = parent[c];
+      if (r < 0 || r >= n_rows) {
+        s_bad = 1;
+      } else {
+        const int64_t n = len[r], np = (n + p.bs - 1) / p.bs;
+        const int64_t more = reserve ? ((int64_t)reserve[c] + p.bs - 1) / p.bs : 0;
+        const int64_t total = max(np, more), ns = shared ? shared[c] : n / p.bs;
+        if (n < 0 || total > stride || ns < 0 || ns > np) {
+          s_bad = 1;
+        } else {
+          want = (int)(total - ns);
+          for (int j = 0; j < np; ++j) {
+            const int b = tables[(int64_t)r * stride + j];
+            if (b < 0 || b >= p.n_blocks || ref_in[b] <= 0) s_bad = 1;
+          }
+        }
+      }
+    }
+    int sum;
+    const int at = block_scan(want, s_warp, &sum) + need;
+    if (c < n_children) first[c] = at;
+    need += sum;
+  }
+  // the lowest free blocks, as many as are needed
+  int found = 0;
+  for (int64_t b0 = 0; b0 < p.n_blocks && found < need; b0 += kPlan) {
+    const int64_t b = b0 + threadIdx.x;
+    const int is_free = b < p.n_blocks && ref_in[b] == 0;
+    int sum;
+    const int at = block_scan(is_free, s_warp, &sum) + found;
+    if (is_free && at < need) fresh[at] = (int)b;
+    found += sum;
+  }
+  __syncthreads();
+  if (ref_in != ref_out)
+    for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) ref_out[b] = ref_in[b];
+  const bool bad = s_bad, full = found < need;
+  __syncthreads();
+  if (bad || full) {
+    for (int64_t i = threadIdx.x; i < (int64_t)n_children * stride; i += kPlan) child[i] = -1;
+    if (threadIdx.x == 0) {
+      ws[0] = 0;
+      set_status(p.status, bad ? DCP_EDEVICE : DCP_ECAPACITY);
+    }
+    return;
+  }
+  for (int64_t i = threadIdx.x; i < (int64_t)n_children * stride; i += kPlan) {
+    const int c = (int)(i / stride), j = (int)(i % stride), r = parent[c];
+    const int64_t n = len[r], np = (n + p.bs - 1) / p.bs;
+    const int64_t ns = shared ? shared[c] : n / p.bs;
+    const int64_t total = max(np, reserve ? ((int64_t)reserve[c] + p.bs - 1) / p.bs : (int64_t)0);
+    int to = -1;
+    if (j < ns) {
+      to = tables[(int64_t)r * stride + j];
+      atomicAdd(ref_out + to, 1);
+    } else if (j < total) {
+      to = fresh[first[c] + j - ns];
+      ref_out[to] = 1;
+      if (j < np) moves[atomicAdd(&s_moves, 1)] = make_int2(tables[(int64_t)r * stride + j], to);
+    }
+    child[i] = to;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) ws[0] = s_moves;
+}
+
+__global__ void __launch_bounds__(kPlan) free_kernel(PageParams p, const int32_t* tables, int64_t n,
+                                                     const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out) {
+  if (ref_in != ref_out)
+    for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) ref_out[b] = ref_in[b];
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < n; i += kPlan) {
+    const int b = tables[i];
+    tables_out[i] = -1;
+    if (b < 0) continue;
+    if (b >= p.n_blocks) {
+      set_status(p.status, DCP_EDEVICE);
+    } else if (atomicSub(ref_out + b, 1) <= 0) {
+      atomicAdd(ref_out + b, 1);
+      set_status(p.status, DCP_EDEVICE);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int32_t* tables, int64_t n,
+                                                        const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out,
+                                                        int32_t* n_live, int32_t* ws) {
+  __shared__ int s_warp[32];
+  int2* moves = (int2*)(ws + kHead);
+  int32_t* to = ws + kHead + 2 * p.n_blocks;  // where every block goes
+  int mine = 0, live;
+  for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) mine += ref_in[b] > 0;
+  block_scan(mine, s_warp, &live);
+  int holes = 0, movers = 0;
+  for (int64_t b0 = 0; b0 < p.n_blocks; b0 += kPlan) {
+    const int64_t b = b0 + threadIdx.x;
+    const int r = b < p.n_blocks ? ref_in[b] : 0;
+    const int hole = b < live && r <= 0, mover = b >= live && r > 0;
+    int sum;
+    const int h = block_scan(hole, s_warp, &sum) + holes;
+    holes += sum;
+    const int m = block_scan(mover, s_warp, &sum) + movers;
+    movers += sum;
+    if (hole) moves[h].y = (int)b;
+    if (mover) moves[m].x = (int)b;
+    if (b < p.n_blocks) {
+      to[b] = (int)b;
+      ref_out[b] = r;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < movers; i += kPlan) {
+    const int2 m = moves[i];
+    to[m.x] = m.y;
+    ref_out[m.y] = ref_out[m.x];
+    ref_out[m.x] = 0;
+  }
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < n; i += kPlan) {
+    const int b = tables[i];
+    if (b >= p.n_blocks) set_status(p.status, DCP_EDEVICE);
+    tables_out[i] = b < 0 ? -1 : b >= p.n_blocks ? b : to[b];
+  }
+  if (threadIdx.x == 0) {
+    ws[0] = movers;
+    if (n_live) *n_live = live;
+  }
+}
+
+cudaError_t move_listed(const PageParams& p, int32_t* ws, cudaStream_t s) {
+  move_kernel<<<sm_count() * 8, kThreads, 0, s>>>(p, ws + kHead, ws + kHead + 1, 2, ws, 0);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_pages_copy(const PageParams& p, const int32_t* src, const int32_t* dst, int32_t n, cudaStream_t s) {
+  const int64_t items = (int64_t)n * p.L * 2;
+  move_kernel<<<(int)(items < sm_count() * 8 ? items : sm_count() * 8), kThreads, 0, s>>>(p, src, dst, 1, nullptr, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const int32_t* len, int32_t n_rows,
+                              int32_t stride, const int32_t* parent, const int32_t* shared, const int32_t* reserve,
+                              int32_t n_children, const int32_t* ref_in, int32_t* child_tables, int32_t* ref_out,
+                              int32_t* ws, cudaStream_t s) {
+  fork_kernel<<<1, kPlan, 0, s>>>(p, tables, len, n_rows, stride, parent, shared, reserve, n_children, ref_in,
+                                  child_tables, ref_out, ws);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : move_listed(p, ws, s);
+}
+
+cudaError_t launch_pages_free(const PageParams& p, const int32_t* tables, int32_t n_rows, int32_t stride,
+                              const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out, cudaStream_t s) {
+  free_kernel<<<1, kPlan, 0, s>>>(p, tables, (int64_t)n_rows * stride, ref_in, tables_out, ref_out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageParams& p, const int32_t* tables, int32_t n_rows, int32_t stride,
+                                 const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out, int32_t* n_live,
+                                 int32_t* ws, cudaStream_t s) {
+  compact_kernel<<<1, kPlan, 0, s>>>(p, tables, (int64_t)n_rows * stride, ref_in, tables_out, ref_out, n_live, ws);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : move_listed(p, ws, s);
+}
+
+}  // namespace dcp

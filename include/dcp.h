@@ -54,7 +54,7 @@ typedef int32_t dcp_status;
 #define DCP_EINVAL 1    /* invalid argument, detected on the host before any launch */
 #define DCP_ECAPACITY 2 /* device: history would exceed hist_cap; the step was skipped */
 #define DCP_ECUDA 3     /* a CUDA runtime call failed */
-#define DCP_ETIMEOUT 4  /* reserved: the kernels of this version contain no waits, so nothing times out */
+#define DCP_ETIMEOUT 4  /* device: a bounded wait inside dcp_paged_attention ran out; nothing else waits */
 #define DCP_EDEVICE 5   /* device: dynamic heads disagree on hist_len (corrupt cache state); the step was skipped */
 
 #define DCP_BF16 0
@@ -317,6 +317,186 @@ dcp_status dcp_snapshot(const dcp_cache* cache, const dcp_config* cfg, uint32_t 
 dcp_status dcp_restore(const dcp_cache* cache, const dcp_config* cfg, const void* image_host, size_t image_bytes,
                        int32_t* q0_out, uint32_t* live_slots_out, void* workspace_dev, size_t ws_bytes,
                        void* stream);
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * Serving operators around the paged cache: the new tokens' keys enter the cache at their rotary phase, attention
+ * reads the cache through its block tables, and the pages themselves are copied, forked, packed and freed.
+ * They share two descriptors.  dcp_kv_pool is one layer's pages (of a dcp_paged_cache, of a dcp_cache cut into pages,
+ * or of the caller's own pool); dcp_seq_batch is the ragged batch of sequences whose new tokens are worked on.
+ * Everything the descriptors point to is device memory owned by the caller; the descriptors themselves, the configs
+ * and the rotary plan are host structs, read before the call returns.
+ *
+ * Position j of sequence s, head h: row j % block_size of block tables[s][j / block_size], at element
+ *   block * s_block + h * s_head + row * s_row of k and v (D contiguous elements there).
+ * New token i of sequence s (row q_start[s] + i of q, k, v, out) sits at cache position
+ *   kv_len(s) - q_len(s) + i,  q_len(s) = q_start[s+1] - q_start[s],  kv_len(s) = kv_len[s] + kv_len_add:
+ * kv_len counts the new tokens.  With kv_len_per_head = 1, kv_len is [n_seqs][H] (a head-specialised cache, whose
+ * planes hold histories of different lengths: hist_len of one layer with kv_len_add = the rows before the history).
+ * A history that ends inside a page comes last in the table; the order of earlier regions is free where no causal
+ * mask is asked for (the keys carry their phase).
+ * Device errors shared by the calls: DCP_EDEVICE for a q_start that decreases, leaves [0, total_q] or gives a
+ * sequence more than max_q new tokens, a kv_len outside [0, table_stride * block_size], or a table entry outside
+ * [0, n_blocks) where a visible or new position lives.  Nothing out of bounds is read or written then; what the call
+ * computes for that sequence is unspecified.
+ * --------------------------------------------------------------------------------------------------------------- */
+typedef struct dcp_kv_pool {
+  void* k;                     /* device, 16-byte aligned */
+  void* v;
+  int32_t H, D;                /* KV heads; head_dim: D * element size a multiple of 16, D <= 128 */
+  int32_t dtype;               /* DCP_BF16 or DCP_F32 */
+  int32_t block_size;          /* positions per page, >= 1 */
+  int64_t n_blocks;            /* < 2^31 */
+  int64_t s_block, s_head, s_row; /* strides in elements (k and v alike), multiples of 16 bytes, > 0 */
+} dcp_kv_pool;
+
+typedef struct dcp_seq_batch {
+  int32_t n_seqs;              /* 1 .. 65535 */
+  int32_t total_q;             /* rows of q */
+  int32_t max_q;               /* no sequence has more new tokens */
+  int32_t kv_len_per_head;     /* 0 or 1 */
+  int64_t max_kv;              /* a bound of the longest kv_len(s), for dividing the work: larger ones still work */
+  int64_t table_stride;        /* entries of a table row */
+  int64_t kv_len_add;          /* added to every kv_len entry (0 .. 2^31 - 1) */
+  const int32_t* q_start;      /* device [n_seqs + 1] */
+  const int32_t* tables;       /* device [n_seqs][table_stride] */
+  const int32_t* kv_len;       /* device [n_seqs], or [n_seqs][H] */
+  int32_t* status;             /* device, one int32 */
+} dcp_seq_batch;
+
+/* Rotary positions.  Pair p of the first rot_dim dims turns by x * theta_p at phase position x,
+ * theta_p = base^(-2p / rot_dim), scaled for long contexts:
+ *   DCP_ROPE_LINEAR  theta_p / factor;
+ *   DCP_ROPE_BASE    base replaced by base * factor^(rot_dim / (rot_dim - 2)) (rot_dim > 2);
+ *   DCP_ROPE_PARTS   theta_p * (g + (1 - g) / factor), g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1),
+ *                    r = orig_len * theta_p / (2 pi): pairs that turn often over the original length keep their
+ *                    frequency, pairs that hardly turn are interpolated.
+ * (a, b) turns to amplitude * (a cos - b sin, a sin + b cos); dims from rot_dim on are copied. */
+#define DCP_ROPE_INTERLEAVED 0 /* pair p at dims (2p, 2p+1): the temporal ladder of this library, rot_dim = 2 n_t */
+#define DCP_ROPE_HALF 1        /* pair p at dims (p, p + rot_dim/2) */
+#define DCP_ROPE_PLAIN 0
+#define DCP_ROPE_LINEAR 1
+#define DCP_ROPE_BASE 2
+#define DCP_ROPE_PARTS 3
+#define DCP_ROPE_MAX_PAIRS 64
+
+typedef struct dcp_rope_config {
+  int32_t rot_dim;             /* even, 0 .. 128 */
+  int32_t pair_layout;         /* DCP_ROPE_INTERLEAVED or DCP_ROPE_HALF */
+  int32_t scaling;             /* DCP_ROPE_PLAIN .. DCP_ROPE_PARTS */
+  int32_t reserved;            /* 0 */
+  double base;                 /* > 0 */
+  double factor;               /* > 0 (ignored by DCP_ROPE_PLAIN) */
+  double orig_len;             /* DCP_ROPE_PARTS: > 0 */
+  double beta_fast, beta_slow; /* DCP_ROPE_PARTS: beta_fast > beta_slow */
+  double amplitude;            /* finite */
+} dcp_rope_config;
+
+/* Made once by dcp_rope_plan_init and kept by the caller: theta_p / (2 pi) as a 64-bit binary fraction of a turn, so
+ * that a position's phase is an integer product whose whole turns drop out exactly, however far the position is. */
+typedef struct dcp_rope_plan {
+  int32_t rot_dim, pair_layout;
+  float amplitude;
+  int32_t ready;
+  uint64_t turns[DCP_ROPE_MAX_PAIRS];
+} dcp_rope_plan;
+
+/* Host only.  DCP_EINVAL: null pointers or config fields outside their ranges. */
+dcp_status dcp_rope_plan_init(const dcp_rope_config* cfg, dcp_rope_plan* plan);
+
+/* Turn the new tokens' q and k and put k and v into the cache, one launch.
+ *   q_dev [total_q][Hq][D], k_dev, v_dev [total_q][H][D] of the pool's type; consecutive tokens q_stride / kv_stride
+ *         elements apart (views of one fused projection), heads D apart; 16-byte aligned, strides multiples of 16 bytes.
+ *   positions_dev (nullable): int32 [total_q] phase position of each token (a latent frame, a position in the text,
+ *         possibly negative); null: its cache position.
+ *   q_out_dev [total_q][Hq][D] contiguous (may be q_dev itself where q_stride == Hq * D).  Null with q_dev null (only
+ *         keys are appended).
+ * kv_len_per_head must be 0.  Rows of q that belong to no sequence are not written.  A new token whose cache position
+ * is negative (kv_len < q_len) is turned into q_out and not stored.
+ * Sequences must not share the pages their new tokens enter.  Angles are exact to 2^-30 turns for any int32 position. */
+dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_plan* plan,
+                           const void* q_dev, int64_t q_stride, int32_t Hq, const void* k_dev, const void* v_dev,
+                           int64_t kv_stride, const int32_t* positions_dev, void* q_out_dev, void* stream);
+
+/* Attention of the new tokens over the cache (which already holds their keys and values).
+ * Query head h reads KV head h / (Hq / H).  Token i at cache position c = kv_len - q_len + i sees position j if
+ *   0 <= j < kv_len,  j <= c where causal = 1,  j >= c - window where window >= 0 (needs causal = 1).
+ *   out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j),   lse = log sum_j w_j.
+ * A row that sees nothing (kv_len 0, or c < 0 under the causal mask) gives out = 0, lse = -inf.
+ * What stands in positions a row does not see never reaches that row: unwritten page rows, infinities and NaN past
+ * kv_len and behind the masks, and table entries of pages no new token sees (they need not name a block). */
+typedef struct dcp_attn_config {
+  float scale;                 /* finite */
+  int32_t causal;              /* 0 or 1 */
+  int32_t window;              /* -1: none */
+  int32_t reserved;            /* 0 */
+} dcp_attn_config;
+
+/* Workspace bytes dcp_paged_attention needs (256-byte aligned, zeroed once with dcp_workspace_init); 0 for invalid
+ * arguments.  It depends on the sizes in pool, batch and cfg, not on what their arrays hold. */
+size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
+                                    int32_t Hq);
+
+/*   q_dev [total_q][Hq][D] of the pool's type, tokens q_stride elements apart; out_dev [total_q][Hq][D] contiguous;
+ *   lse_dev (nullable): fp32 [total_q][Hq].  q, out 16-byte aligned, q_stride a multiple of 16 bytes.  Hq: a multiple
+ *   of H.  Rows of q that belong to no sequence are not written.
+ * Device error DCP_ETIMEOUT: a wait inside the kernel ran out (the result is unspecified). */
+dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
+                               const void* q_dev, int64_t q_stride, int32_t Hq, void* out_dev, float* lse_dev,
+                               void* workspace_dev, size_t ws_bytes, void* stream);
+
+/* Pages of every layer's pool, handled whole: k and v are [L][n_blocks][page], page_bytes = H * block_size * D *
+ * element size (either layout of dcp_paged_cache).  ref[b] counts the table entries that name block b (and any other
+ * holder); a block with ref 0 is free.  Entries < 0 of a table row are empty.  Table rows hold `stride` entries. */
+typedef struct dcp_page_pool {
+  void* k;                     /* device, 16-byte aligned */
+  void* v;
+  int32_t L;
+  int32_t block_size;
+  int64_t n_blocks;            /* < 2^31 */
+  int64_t page_bytes;          /* a multiple of 16 */
+  int32_t* status;
+} dcp_page_pool;
+
+/* Workspace bytes of the calls below for tables of n_rows x stride entries (zero it once with dcp_workspace_init). */
+size_t dcp_pages_workspace_size(const dcp_page_pool* pool, int32_t n_rows, int32_t stride);
+
+/* Block dst[i] = block src[i] in every layer, K and V.  Pairs with an entry outside [0, n_blocks) are skipped
+ * (DCP_EDEVICE).  The dst blocks must be distinct and none of them a src. */
+dcp_status dcp_pages_copy(const dcp_page_pool* pool, const int32_t* src_dev, const int32_t* dst_dev, int32_t n,
+                          void* stream);
+
+/* Branch sequences.  Child c continues row p = parent[c] of `tables`, whose len[p] positions fill its first
+ * ceil(len[p] / block_size) pages: the first shared[c] of them (null: the full ones, len[p] / block_size) are shared
+ * (their counts grow), the others are copied to fresh blocks, and further fresh blocks are reserved up to
+ * reserve[c] positions (null: none).  Fresh blocks are the lowest free ones, in the order of (child, page); their
+ * count becomes 1.  child_tables [n_children][stride] gets the children's rows (-1 past their pages).
+ * ref_in -> ref_out (may be the same array).  child_tables must not overlap `tables`.
+ * Device errors: DCP_ECAPACITY (not enough free blocks), DCP_EDEVICE (a parent outside [0, n_rows), a length or
+ * shared count outside its row, an entry of the parent's pages that names no live block): no page is copied then,
+ * ref_out = ref_in and every entry of child_tables is -1. */
+dcp_status dcp_pages_fork(const dcp_page_pool* pool, const int32_t* tables_dev, const int32_t* len_dev, int32_t n_rows,
+                          int32_t stride, const int32_t* parent_dev, const int32_t* shared_dev,
+                          const int32_t* reserve_dev, int32_t n_children, const int32_t* ref_in_dev,
+                          int32_t* child_tables_dev, int32_t* ref_out_dev, void* workspace_dev, size_t ws_bytes,
+                          void* stream);
+
+/* Drop table rows: every entry's block loses one count, tables_out gets -1 throughout (may be `tables`).
+ * ref_in -> ref_out (may be the same array).  DCP_EDEVICE: an entry past n_blocks (ignored) or a count that would
+ * fall below 0 (left at 0). */
+dcp_status dcp_pages_free(const dcp_page_pool* pool, const int32_t* tables_dev, int32_t n_rows, int32_t stride,
+                          const int32_t* ref_in_dev, int32_t* tables_out_dev, int32_t* ref_out_dev, void* stream);
+
+/* Pack the live blocks (ref > 0) to the front: the i-th live block at or past n_live moves into the i-th free block
+ * before it, in every layer; tables (all rows that name blocks of this pool) and counts follow.  tables_out and
+ * ref_out may be their inputs.  n_live_dev (nullable): number of live blocks.  DCP_EDEVICE: a table entry past
+ * n_blocks (kept as it is). */
+dcp_status dcp_pages_compact(const dcp_page_pool* pool, const int32_t* tables_dev, int32_t n_rows, int32_t stride,
+                             const int32_t* ref_in_dev, int32_t* tables_out_dev, int32_t* ref_out_dev,
+                             int32_t* n_live_dev, void* workspace_dev, size_t ws_bytes, void* stream);
+
+/* ABI check for bindings: sizes of the structs above, in the order dcp_kv_pool, dcp_seq_batch, dcp_rope_config,
+ * dcp_rope_plan, dcp_attn_config, dcp_page_pool (0 past the last). */
+uint32_t dcp_abi_serving_struct_size(int32_t which);
 
 /* Device addresses inside a prune-step workspace: l (fp32 [C]), the mask (uint8 [C]) and the index list
  * (int32 [C], first `kept` entries valid) of the last dcp_prune_step / dcp_compact_layers call. */
