@@ -1,0 +1,748 @@
+// Attention of the new tokens over the paged bf16 cache in tiles of 128 rows x 128 keys on the 5th-generation tensor
+// cores.
+//
+// Rows are (new token, query head of the KV head) pairs in that order, so the heads that share a KV head share its
+// tiles.  A CTA owns 256 rows (two tiles of 128) of one sequence and KV head and walks the keys they see:
+//   scores   S = Q K^T      Q, K in shared memory, S (fp32) in tensor memory
+//   softmax  P = exp(S - m) one thread a row, m a running maximum; P (bf16) goes back over S in tensor memory
+//   values   O += P V       P from tensor memory, V from shared memory, O (fp32) stays in tensor memory
+// Each 128-thread group works on its own row tile, so one tile's softmax runs under the other's matrix products.  m
+// moves only when a row's maximum has grown by more than 2^8 (weights stay below 256, sums in 32 bits), which leaves O
+// untouched in almost every step; m has moved or not, the quotient O / l is the same.
+//
+// Warps 0-3 and 4-7: softmax of row tile 0 and 1.  Warp 8: issues the matrix products.  Warp 9: copies pages with TMA
+// (a page of block_size positions is a box; 128-byte swizzle).  Warps 10, 11: the guard.  A weight of 0 times a value
+// of infinity or NaN is NaN, so in the tiles where some row must not see some key, the guard puts zeros for rows past
+// the sequence (page rows never written hold anything) and for infinities and NaN; rows that do see those get them
+// back in the epilogue, from the cache.
+#include <cuda.h>
+
+#include "serve.cuh"
+
+namespace dcp {
+
+namespace {
+
+constexpr int kRows = 128;             // rows of a tile (lanes of tensor memory)
+constexpr int kKeys = 128;             // keys of a tile
+constexpr int kTileThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows
+constexpr int kSpins = 1 << 22;        // limit of every wait
+
+struct Item {                          // what a CTA works on
+  int s, kh, lo, len;                  // sequence, KV head, first row of q, new tokens
+  int row0;                            // first (token, head) row
+  int kv;                              // cached positions
+  int rows[2];                         // rows of each tile
+  int t0[2], t1[2];                    // key tiles each row tile sees
+  int c0[2], c1[2];                    // cache positions of its first and last row
+};
+
+// How key tiles lie over pages: pages of up to 128 positions are gathered, pages_per_tile of them, each `box` rows
+// of the tile (a multiple of 8, so that the swizzle's 8-row groups line up; rows past block_size stay masked); larger
+// pages are cut into `subs` tiles.
+struct Tiling {
+  int bs, box, pages, subs;
+  __device__ __forceinline__ int tile_of(int pos) const {
+    return subs == 1 ? pos / (pages * bs) : pos / bs * subs + pos % bs / kKeys;
+  }
+  __device__ __forceinline__ int first(int t) const {
+    return subs == 1 ? t * pages * bs : t / subs * bs + t % subs * kKeys;
+  }
+  __device__ __forceinline__ int count(int t) const {
+    return subs == 1 ? pages * bs : min(kKeys, bs - t % subs * kKeys);
+  }
+  __device__ __forceinline__ bool gaps() const { return subs == 1 && box != bs; }
+  // position of column c relative to first(t), -1 where no position stands
+  __device__ __forceinline__ int place(int t, int c) const {
+    if (subs > 1) return c < count(t) ? c : -1;
+    const int g = c / box, r = c - g * box;
+    return g < pages && r < bs ? g * bs + r : -1;
+  }
+};
+
+struct TileParams {
+  AttendParams a;
+  Tiling tl;
+  int splits, q_tiles;
+  float scale_log2;                    // |scale| log2 e
+  uint32_t idesc_qk, idesc_pv;
+  float* part;                         // [item][split][256][D + 2] partial results
+  uint32_t* done;                      // [item] splits finished, 0 between calls
+};
+
+// ------------------------------------------------------------------------------------------ PTX
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+// False once any wait of the CTA has run out (`dead`): every role then leaves its loop.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  if (bar_try(bar, parity)) return true;
+  for (int i = 0; i < kSpins; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if (*dead) return false;
+  }
+  *dead = 1;
+  return false;
+}
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int row, int h, int blk,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(h), "r"(blk), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start and the two strides in units of 16 bytes, bits 46-48 = 1.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+template <int HALVES>
+struct Shape {
+  static constexpr int kD = 64 * HALVES;                 // head dims, padded with zeros
+  static constexpr int kHalf = kRows * 128;              // bytes of 128 rows x 64 dims
+  static constexpr int kTile = kHalf * HALVES;
+  static constexpr int kSlots = HALVES == 2 ? 5 : 10;    // ring of K and V tiles in turn
+  static constexpr int kSmem = 1024 + (2 + kSlots) * kTile + 1024;
+};
+
+__device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, int pos) {
+  return pos < kv && (!a.causal || pos <= c) && (a.window < 0 || pos >= c - a.window);
+}
+
+// Whether every row of positions c_lo .. c_hi sees every key of tile t.
+__device__ __forceinline__ bool tile_full(const AttendParams& a, const Tiling& tl, int t, int kv, int c_lo, int c_hi) {
+  const int p0 = tl.first(t), p1 = p0 + tl.count(t);
+  return !tl.gaps() && tl.count(t) == kKeys && p1 <= kv && (!a.causal || p1 - 1 <= c_lo) &&
+         (a.window < 0 || p0 >= c_hi - a.window);
+}
+
+template <int HALVES>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const __grid_constant__ TileParams p, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v) {
+  using Sh = Shape<HALVES>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bars[2 * Sh::kSlots + 4 + 2 + 2 + 2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead, s_poison, s_last;
+  const AttendParams& a = p.a;
+  const Tiling tl = p.tl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the item
+  Item it;
+  it.s = blockIdx.z / p.splits;
+  const int split = blockIdx.z % p.splits;
+  it.kh = blockIdx.y;
+  const int qt = p.q_tiles - 1 - blockIdx.x;  // the rows that see most keys first
+  if (!seq_rows(a.b, it.s, it.lo, it.len)) return;
+  const int n_rows = it.len * a.G;
+  it.row0 = qt * 2 * kRows;
+  if (it.row0 >= n_rows) return;
+  int64_t kv64;
+  if (!seq_kv(a.b, tl.bs, a.pool.H, it.s, it.kh, kv64)) return;
+  it.kv = (int)kv64;
+  const int32_t* table = a.b.tables + (int64_t)it.s * a.b.table_stride;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r0 = it.row0 + i * kRows;
+    it.rows[i] = max(0, min(kRows, n_rows - r0));
+    it.t0[i] = it.t1[i] = 0;
+    it.c0[i] = it.kv - it.len + r0 / a.G;
+    it.c1[i] = it.kv - it.len + (r0 + max(it.rows[i], 1) - 1) / a.G;
+    if (!it.rows[i]) continue;
+    const int end = a.causal ? min(it.kv, it.c1[i] + 1) : it.kv;
+    const int begin = a.window >= 0 ? max(0, it.c0[i] - a.window) : 0;
+    if (begin < end) {
+      it.t0[i] = tl.tile_of(begin);
+      it.t1[i] = tl.tile_of(end - 1) + 1;
+    }
+  }
+  if (p.splits > 1) {  // this split's share of the tiles the item's rows see
+    const bool one = it.t1[1] <= it.t0[1];
+    const int lo = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], hi = one ? it.t1[0] : it.t1[1];
+    const int per = (max(hi - lo, 0) + p.splits - 1) / p.splits;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      it.t0[i] = max(it.t0[i], lo + split * per);
+      it.t1[i] = max(it.t0[i], min(it.t1[i], lo + (split + 1) * per));
+    }
+  }
+  const bool act0 = it.t0[0] < it.t1[0], act1 = it.t0[1] < it.t1[1];
+  const int tb = act0 ? it.t0[0] : it.t0[1];                // tiles of either
+  const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : it.t1[0];
+  const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
+
+  // ---- set-up
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_smem = base, ring = base + 2 * Sh::kTile;
+  uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t bars = smem_u32(s_bars);
+  auto full = [&](int i) { return bars + 8 * i; };
+  auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
+  auto guarded = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
+  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
+  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
+  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 8), finished = bars + 8 * (2 * Sh::kSlots + 9);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kSlots; ++i) {
+      bar_init(full(i), 1);
+      bar_init(empty(i), 1);
+    }
+    for (int i = 0; i < 4; ++i) bar_init(guarded(i), 64);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(s_full(i), 1);
+      bar_init(p_full(i), kRows);
+    }
+    bar_init(q_full, 256);
+    bar_init(finished, 1);
+    s_dead = 0;
+    s_poison = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int i = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t t_s = tmem + lanes + i * kKeys, t_o = tmem + lanes + 256 + i * 128;
+    const int D = a.pool.D, rows_i = i ? it.rows[1] : it.rows[0];
+    {  // the rows of q into shared memory, zeros past the rows and past D
+      for (int u = r; u < kRows * 8 * HALVES; u += kRows) {
+        const int row = u / (8 * HALVES), ch = u % (8 * HALVES);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < rows_i && ch * 8 < D) {
+          const int R = it.row0 + i * kRows + row, tok = R / a.G, g = R - tok * a.G;
+          x = *reinterpret_cast<const uint4*>(a.q + ((int64_t)(it.lo + tok) * a.q_stride +
+                                                     (int64_t)(it.kh * a.G + g) * D + ch * 8) * 2);
+        }
+        *reinterpret_cast<uint4*>(gbase + i * Sh::kTile + (ch >> 3) * Sh::kHalf + row * 128 +
+                                  (((ch & 7) ^ (row & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();
+      bar_arrive(q_full);
+    }
+    const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
+    const int c = it.kv - it.len + tok;
+    const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
+    const int cmin = i ? it.c0[1] : it.c0[0], cmax = i ? it.c1[1] : it.c1[0];
+    const int seen_end = a.causal ? min(it.kv, c + 1) : it.kv;
+    const int seen_begin = a.window >= 0 ? c - a.window : 0;
+    const float sc = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int t = t0; t < t1 && ok; ++t) {
+      ok = bar_wait(s_full(i), (t - t0) & 1, &s_dead);
+      if (!ok) break;
+      fence_after();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tm_ld32(x[e], t_s + 32 * e);
+      wait_ld();
+      if (!tile_full(a, tl, t, it.kv, cmin, cmax)) {
+        const int p0 = tl.first(t);
+        if (!tl.gaps()) {
+          const int hi = min(seen_end - p0, tl.count(t)), lo = seen_begin - p0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e < lo || e >= hi) x[e >> 5][e & 31] = 0xFF800000u;
+        } else {
+          int g0 = 0, row = 0;  // page within the tile, row within the page
+#pragma unroll
+          for (int e = 0; e < 128; ++e) {
+            const int pos = p0 + g0 * tl.bs + row;
+            if (row >= tl.bs || g0 >= tl.pages || pos < seen_begin || pos >= seen_end) x[e >> 5][e & 31] = 0xFF800000u;
+            if (++row == tl.box) {
+              row = 0;
+              ++g0;
+            }
+          }
+        }
+      }
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e >> 5][e & 31]));
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const bool grow = mx > m && (m == -INFINITY || (mx - m) * sc > kGrow);
+      if (__any_sync(~0u, grow)) {
+        const float m2 = grow ? mx : m;
+        const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
+        m = m2;
+        l *= keep;
+        if (t > t0) {
+#pragma unroll
+          for (int e = 0; e < Sh::kD / 32; ++e) {
+            uint32_t o[32];
+            tm_ld32(o, t_o + 32 * e);
+            wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+            tm_st32(t_o + 32 * e, o);
+          }
+        }
+      }
+      const float off = m == -INFINITY ? 0.f : m * sc;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int k = 64 * e + 2 * u;
+          const float y0 = exp2_fast(fmaf(__uint_as_float(x[k >> 5][k & 31]), sc, -off));
+          const float y1 = exp2_fast(fmaf(__uint_as_float(x[(k + 1) >> 5][(k + 1) & 31]), sc, -off));
+          sum[(2 * u) & 3] += y0;
+          sum[(2 * u + 1) & 3] += y1;
+          w[u] = pack_bf16x2(y0, y1);
+        }
+        tm_st32(t_s + 32 * e, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      wait_st();
+      fence_before();
+      bar_arrive(p_full(i));
+    }
+    // ---- result of the row
+    if (ok && t0 < t1) {
+      ok = bar_wait(s_full(i), (t1 - t0) & 1, &s_dead);
+      fence_after();
+    }
+    if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
+    const bool mine = r < rows_i;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
+    float* part = p.part + ((((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt) * p.splits + split) *
+                               (2 * kRows) * (D + 2) + (int64_t)(i * kRows + r) * (D + 2);
+#pragma unroll 1
+    for (int e = 0; e < Sh::kD / 32 && ok; ++e) {
+      uint32_t o[32];
+      if (t0 < t1) {
+        tm_ld32(o, t_o + 32 * e);
+        wait_ld();
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; ++u) o[u] = 0;
+      }
+      if (s_poison && mine) {  // infinities and NaN this row sees in the guarded tiles
+        for (int t = t0; t < t1; ++t) {
+          if (tile_full(a, tl, t, it.kv, c_lo, c_hi)) continue;
+          for (int col = 0; col < kKeys; ++col) {
+            const int at = tl.place(t, col), pos = tl.first(t) + at;
+            if (at < 0 || !visible(a, it.kv, c, pos)) continue;
+            const int blk = table[pos / tl.bs];
+            if (blk < 0 || blk >= a.pool.n_blocks) continue;
+            const __nv_bfloat16* v = (const __nv_bfloat16*)a.pool.v + blk * a.pool.s_block +
+                                     (int64_t)it.kh * a.pool.s_head + (int64_t)(pos % tl.bs) * a.pool.s_row;
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const float y = 32 * e + u < D ? __bfloat162float(v[32 * e + u]) : 0.f;
+              if (!isfinite(y)) o[u] = __float_as_uint(__uint_as_float(o[u]) + y);
+            }
+          }
+        }
+      }
+      if (!mine) continue;
+      if (p.splits > 1) {
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+          if (32 * e + u < D) part[2 + 32 * e + u] = __uint_as_float(o[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; u += 8) {
+          if (32 * e + u >= D) continue;
+          uint4 y;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            w[b] = pack_bf16x2(__uint_as_float(o[u + 2 * b]) * inv, __uint_as_float(o[u + 2 * b + 1]) * inv);
+          *reinterpret_cast<uint4*>(a.out + (row * D + 32 * e + u) * 2) = y;
+        }
+      }
+    }
+    if (mine && ok) {
+      if (p.splits > 1) {
+        part[0] = m == -INFINITY ? m : m * sc;
+        part[1] = l;
+      } else if (a.lse) {
+        a.lse[row] = l != 0.f ? (m * sc + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 9) {
+      // ---------------------------------------------------------------------------------- pages
+      const int n_pages = tl.subs == 1 ? tl.pages : 1;
+      const uint32_t bytes = (uint32_t)tl.box * 128 * HALVES;
+      const int last_page = it.kv > 0 ? (it.kv - 1) / tl.bs : -1;
+      // pages some row of the item sees: these must name a block
+      const int see_lo = a.window >= 0 ? max(0, c_lo - a.window) : 0, see_hi = a.causal ? min(it.kv, c_hi + 1) : it.kv;
+      bool ok = true;
+      int n = 0;
+      for (int t = tb; t < te && ok; ++t) {
+        const int pg0 = tl.subs == 1 ? t * tl.pages : t / tl.subs;
+        const int row = tl.subs == 1 ? 0 : t % tl.subs * kKeys;
+        const int here = min(n_pages, last_page + 1 - pg0);  // pages of the tile that the sequence has
+        int blk = 0;
+        if (lane < here) {
+          blk = table[pg0 + lane];
+          if (blk < 0 || blk >= a.pool.n_blocks) {
+            const int q0 = (pg0 + lane) * tl.bs;
+            if (q0 < see_hi && q0 + tl.bs > see_lo) set_status(a.b.status, DCP_EDEVICE);
+            blk = (int)a.pool.n_blocks;  // outside the tensor map: zeros
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int slot = n % Sh::kSlots;
+          if (n >= Sh::kSlots) ok = ok && bar_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &s_dead);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          if (lane == 0) bar_expect(full(slot), here * bytes);
+          __syncwarp();
+          for (int pg = lane; pg < here; pg += 32) {
+            const uint32_t dst = ring + slot * Sh::kTile + pg * tl.box * 128;
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+              tma_page(dst + hf * Sh::kHalf, kv ? &map_v : &map_k, 64 * hf, row, it.kh, blk, full(slot));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // copies in flight end by themselves: leave when they have
+        for (int k = max(0, n - Sh::kSlots); k < n; ++k)
+          for (int u = 0; u < kSpins && !bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1); ++u) {
+          }
+      }
+    } else if (warp == 8) {
+      // ---------------------------------------------------------------------------------- matrix products
+      bool ok = te > tb ? bar_wait(q_full, 0, &s_dead) : true;
+      int masked = 0;
+      int seen[2] = {0, 0};
+      fence_after();
+      auto scores = [&](int i, int t) {  // S_i of tile t
+        const int slot = 2 * (t - tb) % Sh::kSlots;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < 4 * HALVES; ++k)
+            mma_ss(tmem + i * kKeys,
+                   smem_desc(q_smem + i * Sh::kTile + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024),
+                   smem_desc(ring + slot * Sh::kTile + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024), p.idesc_qk,
+                   k > 0);
+          mma_commit(s_full(i));
+        }
+        __syncwarp();
+      };
+      auto key_wait = [&](int t) {
+        const int n = 2 * (t - tb);
+        ok = ok && bar_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &s_dead);
+        fence_after();
+      };
+      auto active = [&](int i, int t) {
+        return i ? t >= it.t0[1] && t < it.t1[1] : t >= it.t0[0] && t < it.t1[0];
+      };
+      if (ok && tb < te) {
+        key_wait(tb);
+        for (int i = 0; i < 2 && ok; ++i)
+          if (active(i, tb)) scores(i, tb);
+        if (lane == 0) mma_commit(empty(0));
+      }
+      for (int t = tb; t < te && ok; ++t) {
+        const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
+        if (!tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
+          ok = bar_wait(guarded(masked & 3), (masked >> 2) & 1, &s_dead);
+          ++masked;
+        }
+        ok = ok && bar_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+        bool have_keys = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
+          if (ok && active(i, t)) {
+            ok = bar_wait(p_full(i), seen[i] & 1, &s_dead);
+            ++seen[i];
+            fence_after();
+            if (ok && lane == 0) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 8 * k,
+                       smem_desc(ring + slot * Sh::kTile + k * 2048, Sh::kHalf, 1024), p.idesc_pv, t > t0 || k > 0);
+              if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
+            }
+            __syncwarp();
+          }
+          if (ok && t + 1 < te && active(i, t + 1)) {
+            if (!have_keys) key_wait(t + 1);
+            have_keys = true;
+            if (ok) scores(i, t + 1);
+          }
+        }
+        if (ok && lane == 0) {
+          mma_commit(empty(slot));
+          if (t + 1 < te) mma_commit(empty((n + 1) % Sh::kSlots));
+        }
+        __syncwarp();
+      }
+      if (!ok) {  // products in flight end by themselves: leave when they have
+        if (lane == 0) mma_commit(finished);
+        __syncwarp();
+        for (int u = 0; u < kSpins && !bar_try(finished, 0); ++u) {
+        }
+        set_status(a.b.status, DCP_ETIMEOUT);
+      }
+    } else {
+      // ---------------------------------------------------------------------------------- guard
+      const int me = threadIdx.x - 320;
+      int masked = 0;
+      bool ok = true;
+      for (int t = tb; t < te && ok; ++t) {
+        if (tile_full(a, tl, t, it.kv, c_lo, c_hi)) continue;
+        const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
+        ok = bar_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+        if (!ok) break;
+        const int p0 = tl.first(t);
+        uint8_t* v = gbase + (2 + slot) * Sh::kTile;
+        bool found = false;
+        for (int u = me; u < kKeys * 8 * HALVES; u += 64) {
+          const int row = (u >> 3) & (kKeys - 1);
+          uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
+          const int place = tl.place(t, row);
+          if (place < 0 || p0 + place >= it.kv) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          uint4 x = *at;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+          bool bad = false;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if ((w[b] & 0x7F80u) == 0x7F80u) {
+              w[b] &= 0xFFFF0000u;
+              bad = true;
+            }
+            if ((w[b] & 0x7F800000u) == 0x7F800000u) {
+              w[b] &= 0xFFFFu;
+              bad = true;
+            }
+          }
+          if (bad) *at = x;
+          found |= bad;
+        }
+        if (found) s_poison = 1;
+        fence_proxy_async_smem();
+        bar_arrive(guarded(masked & 3));
+        ++masked;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+
+  // ---- the item's last split joins the parts
+  if (p.splits > 1) {
+    const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const uint32_t before = atomicAdd(p.done + item, 1);
+      s_last = before == (uint32_t)p.splits - 1;
+      if (s_last) p.done[item] = 0;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const int D = a.pool.D, rows = it.rows[0] + it.rows[1];
+    const float* part = p.part + item * p.splits * (2 * kRows) * (D + 2);
+    const int64_t step = (int64_t)2 * kRows * (D + 2);
+    for (int u = threadIdx.x; u < rows * (D / 8); u += kTileThreads) {
+      const int r = u / (D / 8), d = u % (D / 8) * 8;
+      const float* at = part + (int64_t)r * (D + 2);
+      float top = -INFINITY;
+      for (int k = 0; k < p.splits; ++k) top = fmaxf(top, __ldcg(at + k * step));
+      float l = 0.f, o[8] = {};
+      for (int k = 0; k < p.splits; ++k) {
+        const float* x = at + k * step;
+        const float lk = __ldcg(x + 1), w = __ldcg(x) == -INFINITY && lk == 0.f ? 0.f : exp2_fast(__ldcg(x) - top);
+        if (w == 0.f && lk == 0.f) continue;
+        l += w * lk;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) o[b] += w * __ldcg(x + 2 + d + b);
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int R = it.row0 + r, tok = R / a.G, g = R - tok * a.G;
+      const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
+      uint4 y;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w[b] = pack_bf16x2(o[2 * b] * inv, o[2 * b + 1] * inv);
+      *reinterpret_cast<uint4*>(a.out + (row * D + d) * 2) = y;
+      if (a.lse && d == 0) a.lse[row] = l != 0.f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess || found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeTiled)f;
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* map, const Pool& c, void* base, int box) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.bs, (cuuint64_t)c.H, (cuuint64_t)c.n_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.s_row * 2, (cuuint64_t)c.s_head * 2, (cuuint64_t)c.s_block * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of 128 x 128 (or 128 x D) in fp32 from bf16: format bits, N / 8 and M / 16.
+uint32_t idesc(int n, bool b_by_rows, bool negate) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (negate ? 1u << 13 : 0u) | (b_by_rows ? 1u << 16 : 0u) |
+         ((uint32_t)(n / 8) << 17) | ((uint32_t)(kRows / 16) << 24);
+}
+
+LaunchCache g_tile_launch[2];
+
+template <int HALVES>
+cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  int blocks;
+  const cudaError_t e = launch_setup(g_tile_launch[HALVES - 1], tile_kernel<HALVES>, kTileThreads,
+                                     Shape<HALVES>::kSmem, &blocks);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.q_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
+  tile_kernel<HALVES><<<grid, kTileThreads, Shape<HALVES>::kSmem, s>>>(p, k, v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
+  TilePlan t;
+  t.q_tiles = (int)(((int64_t)a.b.max_q * a.G + 2 * kRows - 1) / (2 * kRows));
+  const int64_t items = (int64_t)t.q_tiles * a.pool.H * a.b.n_seqs;
+  const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
+  // fewer items than SMs: the keys are split so that the SMs have one item each, at least 4 key tiles a split
+  int64_t splits = items < 152 ? 152 / items : 1;
+  if (splits > key_tiles / 4) splits = key_tiles / 4;
+  if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;
+  t.splits = splits < 1 ? 1 : (int)splits;
+  t.done_bytes = t.splits > 1 ? ((size_t)items * 4 + 255) & ~(size_t)255 : 0;
+  t.bytes = t.splits > 1 ? t.done_bytes + (size_t)items * t.splits * 2 * kRows * (a.pool.D + 2) * 4 : 0;
+  return t;
+}
+
+cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws, cudaStream_t s) {
+  const TilePlan t = plan_tiles(a, max_kv);
+  TileParams p{};
+  p.a = a;
+  const int bs = a.pool.bs;
+  p.tl.bs = bs;
+  p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
+  p.tl.pages = kKeys / p.tl.box;
+  p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
+  p.splits = t.splits;
+  p.q_tiles = t.q_tiles;
+  // a scale below 0 negates the products (the running maximum then is of what is exponentiated); one near 0 is held
+  // where masked scores of -inf still scale to -inf
+  const float mag = a.scale < 0.f ? -a.scale : a.scale;
+  p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
+  p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
+  p.idesc_pv = idesc(a.pool.D <= 64 ? 64 : 128, true, false);
+  p.done = (uint32_t*)ws;
+  p.part = (float*)((char*)ws + t.done_bytes);
+  CUtensorMap mk, mv;
+  if (!encode(&mk, a.pool, a.pool.k, p.tl.box) || !encode(&mv, a.pool, a.pool.v, p.tl.box))
+    return cudaErrorInvalidValue;
+  return a.pool.D <= 64 ? launch<1>(p, mk, mv, s) : launch<2>(p, mk, mv, s);
+}
+
+}  // namespace dcp

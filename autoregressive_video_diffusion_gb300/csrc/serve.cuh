@@ -60,6 +60,15 @@ struct PageParams {
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t s);
+
+// How the tiled attention divides its work, and the workspace that takes (counters first, zero between calls).
+struct TilePlan {
+  int q_tiles, splits;
+  size_t done_bytes, bytes;
+};
+TilePlan plan_tiles(const AttendParams& p, int64_t max_kv);
+cudaError_t launch_attend_tiles(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);
+
 cudaError_t launch_pages_copy(const PageParams& p, const int32_t* src, const int32_t* dst, int32_t n, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const int32_t* len, int32_t n_rows,
                               int32_t stride, const int32_t* parent, const int32_t* shared, const int32_t* reserve,

@@ -65,6 +65,18 @@ dcp_status check_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
   return DCP_OK;
 }
 
+AttendParams attend_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg, int32_t Hq) {
+  AttendParams p{};
+  p.pool = pool_of(pool);
+  p.b = batch_of(batch);
+  p.Hq = Hq;
+  p.G = Hq / pool->H;
+  p.causal = cfg->causal;
+  p.window = cfg->window;
+  p.scale = cfg->scale;
+  return p;
+}
+
 dcp_status check_pages(const dcp_page_pool* p) {
   if (!p || !p->k || !p->v || !p->status || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->status, 4))
     return DCP_EINVAL;
@@ -169,7 +181,7 @@ dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
 size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                                     int32_t Hq) {
   if (check_attention(pool, batch, cfg, Hq) != DCP_OK) return 0;
-  return 256;
+  return 256 + (plan_tiles(attend_of(pool, batch, cfg, Hq), batch->max_kv).bytes + 255) / 256 * 256;
 }
 
 dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
@@ -178,18 +190,12 @@ dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* bat
   if (!ws_ok(ws, ws_bytes, dcp_attention_workspace_size(pool, batch, cfg, Hq))) return DCP_EINVAL;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DCP_EINVAL;
   if (!token_stride_ok(q_stride, Hq, pool->D, elem_size(pool->dtype))) return DCP_EINVAL;
-  AttendParams p{};
-  p.pool = pool_of(pool);
-  p.b = batch_of(batch);
+  AttendParams p = attend_of(pool, batch, cfg, Hq);
   p.q = (const char*)q;
   p.out = (char*)out;
   p.lse = lse;
   p.q_stride = q_stride;
-  p.Hq = Hq;
-  p.G = Hq / pool->H;
-  p.causal = cfg->causal;
-  p.window = cfg->window;
-  p.scale = cfg->scale;
+  if (pool->dtype == DCP_BF16) return cuda_ok(launch_attend_tiles(p, batch->max_kv, ws, (cudaStream_t)stream));
   return cuda_ok(launch_attend_rows(p, (cudaStream_t)stream));
 }
 
