@@ -28,7 +28,8 @@ constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows
-constexpr int kSpins = 1 << 22;        // limit of every wait
+constexpr int kSpins = 1 << 24;        // limits of every wait: tries, and nanoseconds
+constexpr uint64_t kPatience = 2000000000ull;
 
 struct Item {                          // what a CTA works on
   int s, kh, lo, len;                  // sequence, KV head, first row of q, new tokens
@@ -91,15 +92,29 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
-// False once any wait of the CTA has run out (`dead`): every role then leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-  if (bar_try(bar, parity)) return true;
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
+  const uint64_t start = now_ns();
   for (int i = 0; i < kSpins; ++i) {
     if (bar_try(bar, parity)) return true;
-    if (*dead) return false;
+    if (*dead || now_ns() - start > kPatience) break;
   }
   *dead = 1;
   return false;
+}
+// False once any wait of the CTA has run out (`dead`): every role then leaves its loop.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  for (int i = 0; i < 64; ++i)
+    if (bar_try(bar, parity)) return true;
+  return bar_wait_long(bar, parity, dead);
+}
+// The same for a whole warp: its lanes agree.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  return __all_sync(~0u, bar_wait(bar, parity, dead));
 }
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int row, int h, int blk,
                                          uint32_t bar) {
@@ -148,10 +163,32 @@ __device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&r)[32]) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void tm_ld16(uint32_t (&r)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The n lowest bits (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+// x = -inf where keep is 0, in place: a select over 128 registers in two branches costs the compiler copies.
+__device__ __forceinline__ void hide_unless(uint32_t& x, uint32_t keep) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mov.b32 %0, 0xFF800000;\n\t}" : "+r"(x) : "r"(keep));
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start and the two strides in units of 16 bytes, bits 46-48 = 1.
@@ -234,7 +271,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   const bool act0 = it.t0[0] < it.t1[0], act1 = it.t0[1] < it.t1[1];
   const int tb = act0 ? it.t0[0] : it.t0[1];                // tiles of either
-  const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : it.t1[0];
+  const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : act0 ? it.t1[0] : tb;
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
 
   // ---- set-up
@@ -276,7 +313,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int i = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t t_s = tmem + lanes + i * kKeys, t_o = tmem + lanes + 256 + i * 128;
@@ -306,7 +343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int t = t0; t < t1 && ok; ++t) {
-      ok = bar_wait(s_full(i), (t - t0) & 1, &s_dead);
+      ok = warp_wait(s_full(i), (t - t0) & 1, &s_dead);
       if (!ok) break;
       fence_after();
       uint32_t x[4][32];
@@ -314,24 +351,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int e = 0; e < 4; ++e) tm_ld32(x[e], t_s + 32 * e);
       wait_ld();
       if (!tile_full(a, tl, t, it.kv, cmin, cmax)) {
+        uint32_t see[4];  // columns the row sees
         const int p0 = tl.first(t);
         if (!tl.gaps()) {
           const int hi = min(seen_end - p0, tl.count(t)), lo = seen_begin - p0;
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e < lo || e >= hi) x[e >> 5][e & 31] = 0xFF800000u;
+          for (int w = 0; w < 4; ++w) see[w] = low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w);
         } else {
-          int g0 = 0, row = 0;  // page within the tile, row within the page
 #pragma unroll
-          for (int e = 0; e < 128; ++e) {
-            const int pos = p0 + g0 * tl.bs + row;
-            if (row >= tl.bs || g0 >= tl.pages || pos < seen_begin || pos >= seen_end) x[e >> 5][e & 31] = 0xFF800000u;
-            if (++row == tl.box) {
-              row = 0;
-              ++g0;
+          for (int w = 0; w < 4; ++w) {
+            see[w] = 0;
+#pragma unroll 1
+            for (int b = 0; b < 32; ++b) {
+              const int at = tl.place(t, 32 * w + b);
+              if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[w] |= 1u << b;
             }
           }
         }
+#pragma unroll
+        for (int e = 0; e < 128; ++e) hide_unless(x[e >> 5][e & 31], see[e >> 5] & (1u << (e & 31)));
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -344,14 +382,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         m = m2;
         l *= keep;
         if (t > t0) {
-#pragma unroll
-          for (int e = 0; e < Sh::kD / 32; ++e) {
-            uint32_t o[32];
-            tm_ld32(o, t_o + 32 * e);
+#pragma unroll 1
+          for (int e = 0; e < Sh::kD / 16; ++e) {
+            uint32_t o[16];
+            tm_ld16(o, t_o + 16 * e);
             wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-            tm_st32(t_o + 32 * e, o);
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+            tm_st16(t_o + 16 * e, o);
           }
         }
       }
@@ -378,7 +416,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // ---- result of the row
     if (ok && t0 < t1) {
-      ok = bar_wait(s_full(i), (t1 - t0) & 1, &s_dead);
+      ok = warp_wait(s_full(i), (t1 - t0) & 1, &s_dead);
       fence_after();
     }
     if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
@@ -442,7 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 9) {
       // ---------------------------------------------------------------------------------- pages
       const int n_pages = tl.subs == 1 ? tl.pages : 1;
@@ -468,8 +506,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const int slot = n % Sh::kSlots;
-          if (n >= Sh::kSlots) ok = ok && bar_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &s_dead);
-          ok = __all_sync(~0u, ok);
+          if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &s_dead);
           if (!ok) break;
           if (lane == 0) bar_expect(full(slot), here * bytes);
           __syncwarp();
@@ -483,13 +520,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!ok) {  // copies in flight end by themselves: leave when they have
+        const uint64_t start = now_ns();
         for (int k = max(0, n - Sh::kSlots); k < n; ++k)
-          for (int u = 0; u < kSpins && !bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1); ++u) {
+          while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && now_ns() - start < kPatience) {
           }
       }
     } else if (warp == 8) {
       // ---------------------------------------------------------------------------------- matrix products
-      bool ok = te > tb ? bar_wait(q_full, 0, &s_dead) : true;
+      bool ok = te > tb ? warp_wait(q_full, 0, &s_dead) : true;
       int masked = 0;
       int seen[2] = {0, 0};
       fence_after();
@@ -508,7 +546,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       auto key_wait = [&](int t) {
         const int n = 2 * (t - tb);
-        ok = ok && bar_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &s_dead);
+        ok = ok && warp_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &s_dead);
         fence_after();
       };
       auto active = [&](int i, int t) {
@@ -523,16 +561,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int t = tb; t < te && ok; ++t) {
         const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
         if (!tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
-          ok = bar_wait(guarded(masked & 3), (masked >> 2) & 1, &s_dead);
+          ok = warp_wait(guarded(masked & 3), (masked >> 2) & 1, &s_dead);
           ++masked;
         }
-        ok = ok && bar_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+        ok = ok && warp_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
         bool have_keys = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
           if (ok && active(i, t)) {
-            ok = bar_wait(p_full(i), seen[i] & 1, &s_dead);
+            ok = warp_wait(p_full(i), seen[i] & 1, &s_dead);
             ++seen[i];
             fence_after();
             if (ok && lane == 0) {
@@ -550,6 +588,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (ok) scores(i, t + 1);
           }
         }
+        if (ok && t + 1 < te && !have_keys) key_wait(t + 1);
         if (ok && lane == 0) {
           mma_commit(empty(slot));
           if (t + 1 < te) mma_commit(empty((n + 1) % Sh::kSlots));
@@ -559,7 +598,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) {  // products in flight end by themselves: leave when they have
         if (lane == 0) mma_commit(finished);
         __syncwarp();
-        for (int u = 0; u < kSpins && !bar_try(finished, 0); ++u) {
+        const uint64_t start = now_ns();
+        while (!bar_try(finished, 0) && now_ns() - start < kPatience) {
         }
         set_status(a.b.status, DCP_ETIMEOUT);
       }
@@ -607,7 +647,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++masked;
       }
     }
+    __syncwarp();
   }
+  // every warp back to the registers it was launched with
+  if (warp < 8)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   fence_before();
   __syncthreads();
   fence_after();

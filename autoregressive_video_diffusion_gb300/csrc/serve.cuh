@@ -23,6 +23,8 @@ struct Pool {
   int64_t n_blocks, s_block, s_head, s_row;  // strides in elements
 };
 
+constexpr int32_t kMaxKv = 1 << 30;  // cached positions of a sequence: differences of positions fit 32 bits
+
 struct AppendParams {
   Pool pool;
   Batch b;
@@ -98,7 +100,7 @@ __device__ __forceinline__ bool seq_rows(const Batch& b, int s, int& lo, int& n)
 // Cached positions of sequence s as head h sees them, checked against the table row.
 __device__ __forceinline__ bool seq_kv(const Batch& b, int bs, int H, int s, int h, int64_t& kv) {
   kv = (int64_t)b.kv_len[b.kv_per_head ? (int64_t)s * H + h : s] + b.kv_add;
-  if (kv < 0 || kv > b.table_stride * bs || kv > INT32_MAX) {
+  if (kv < 0 || kv > b.table_stride * bs || kv > kMaxKv) {
     set_status(b.status, DCP_EDEVICE);
     return false;
   }

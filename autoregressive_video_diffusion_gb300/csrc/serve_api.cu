@@ -61,7 +61,7 @@ dcp_status check_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
   if (Hq < 1 || Hq > 65535 || Hq % pool->H) return DCP_EINVAL;
   if (!std::isfinite(cfg->scale) || (cfg->causal != 0 && cfg->causal != 1) || cfg->reserved != 0) return DCP_EINVAL;
   if (cfg->window < -1 || (cfg->window >= 0 && !cfg->causal)) return DCP_EINVAL;
-  if ((int64_t)batch->max_q * Hq > INT32_MAX) return DCP_EINVAL;
+  if ((int64_t)batch->max_q * Hq > kMaxKv) return DCP_EINVAL;
   return DCP_OK;
 }
 
@@ -72,7 +72,7 @@ AttendParams attend_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, cons
   p.Hq = Hq;
   p.G = Hq / pool->H;
   p.causal = cfg->causal;
-  p.window = cfg->window;
+  p.window = cfg->window < kMaxKv ? cfg->window : kMaxKv;
   p.scale = cfg->scale;
   return p;
 }

@@ -335,8 +335,8 @@ dcp_status dcp_restore(const dcp_cache* cache, const dcp_config* cfg, const void
  * A history that ends inside a page comes last in the table; the order of earlier regions is free where no causal
  * mask is asked for (the keys carry their phase).
  * Device errors shared by the calls: DCP_EDEVICE for a q_start that decreases, leaves [0, total_q] or gives a
- * sequence more than max_q new tokens, a kv_len outside [0, table_stride * block_size], or a table entry outside
- * [0, n_blocks) where a visible or new position lives.  Nothing out of bounds is read or written then; what the call
+ * sequence more than max_q new tokens, a kv_len outside [0, table_stride * block_size] or past 2^30, or a table entry
+ * outside [0, n_blocks) where a visible or new position lives.  Nothing out of bounds is read or written then; what the call
  * computes for that sequence is unspecified.
  * --------------------------------------------------------------------------------------------------------------- */
 typedef struct dcp_kv_pool {
@@ -438,7 +438,7 @@ size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch
 
 /*   q_dev [total_q][Hq][D] of the pool's type, tokens q_stride elements apart; out_dev [total_q][Hq][D] contiguous;
  *   lse_dev (nullable): fp32 [total_q][Hq].  q, out 16-byte aligned, q_stride a multiple of 16 bytes.  Hq: a multiple
- *   of H.  Rows of q that belong to no sequence are not written.
+ *   of H, max_q * Hq <= 2^30.  Rows of q that belong to no sequence are not written.
  * Device error DCP_ETIMEOUT: a wait inside the kernel ran out (the result is unspecified). */
 dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                                const void* q_dev, int64_t q_stride, int32_t Hq, void* out_dev, float* lse_dev,
