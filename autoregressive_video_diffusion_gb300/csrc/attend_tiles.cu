@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       bar_init(full(i), 1);
-      bar_init(empty(i), 1);
+      bar_init(empty(i), 3);  // the matrix products' commit, and both guard warps
     }
     for (int i = 0; i < 4; ++i) bar_init(guarded(i), 64);
     for (int i = 0; i < 2; ++i) {
@@ -605,46 +605,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else {
       // ---------------------------------------------------------------------------------- guard
+      // It follows every fill of the ring (a wait can only tell a phase from the one before it), so a slot is free
+      // once it has passed too.
       const int me = threadIdx.x - 320;
       int masked = 0;
       bool ok = true;
-      for (int t = tb; t < te && ok; ++t) {
-        if (tile_full(a, tl, t, it.kv, c_lo, c_hi)) continue;
-        const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
-        ok = bar_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+      for (int n = 0; n < 2 * (te - tb) && ok; ++n) {
+        const int t = tb + (n >> 1), slot = n % Sh::kSlots;
+        ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
         if (!ok) break;
-        const int p0 = tl.first(t);
-        uint8_t* v = gbase + (2 + slot) * Sh::kTile;
-        bool found = false;
-        for (int u = me; u < kKeys * 8 * HALVES; u += 64) {
-          const int row = (u >> 3) & (kKeys - 1);
-          uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
-          const int place = tl.place(t, row);
-          if (place < 0 || p0 + place >= it.kv) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 x = *at;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-          bool bad = false;
+        if ((n & 1) && !tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
+          const int p0 = tl.first(t);
+          uint8_t* v = gbase + (2 + slot) * Sh::kTile;
+          bool found = false;
+          for (int u = me; u < kKeys * 8 * HALVES; u += 64) {
+            const int row = (u >> 3) & (kKeys - 1);
+            uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
+            const int place = tl.place(t, row);
+            if (place < 0 || p0 + place >= it.kv) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 x = *at;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+            bool bad = false;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if ((w[b] & 0x7F80u) == 0x7F80u) {
-              w[b] &= 0xFFFF0000u;
-              bad = true;
+            for (int b = 0; b < 4; ++b) {
+              if ((w[b] & 0x7F80u) == 0x7F80u) {
+                w[b] &= 0xFFFF0000u;
+                bad = true;
+              }
+              if ((w[b] & 0x7F800000u) == 0x7F800000u) {
+                w[b] &= 0xFFFFu;
+                bad = true;
+              }
             }
-            if ((w[b] & 0x7F800000u) == 0x7F800000u) {
-              w[b] &= 0xFFFFu;
-              bad = true;
-            }
+            if (bad) *at = x;
+            found |= bad;
           }
-          if (bad) *at = x;
-          found |= bad;
+          if (found) s_poison = 1;
+          fence_proxy_async_smem();
+          bar_arrive(guarded(masked & 3));
+          ++masked;
         }
-        if (found) s_poison = 1;
-        fence_proxy_async_smem();
-        bar_arrive(guarded(masked & 3));
-        ++masked;
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty(slot));
       }
     }
     __syncwarp();
