@@ -27,6 +27,7 @@ constexpr int kRows = 128;             // rows of a tile (lanes of tensor memory
 constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows
 constexpr int kSpins = 1 << 24;        // limits of every wait: tries, and nanoseconds
 constexpr uint64_t kPatience = 2000000000ull;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const __grid_constant__ CUtensorMap map_v) {
   using Sh = Shape<HALVES>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bars[2 * Sh::kSlots + 4 + 2 + 2 + 2];
+  __shared__ __align__(8) uint64_t s_bars[2 * Sh::kSlots + kGuards + 6];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_poison, s_last;
   const AttendParams& a = p.a;
@@ -282,15 +283,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto full = [&](int i) { return bars + 8 * i; };
   auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
   auto guarded = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
-  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
-  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
-  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 8), finished = bars + 8 * (2 * Sh::kSlots + 9);
+  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + i); };
+  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + 2 + i); };
+  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + kGuards + 4), finished = bars + 8 * (2 * Sh::kSlots + kGuards + 5);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       bar_init(full(i), 1);
       bar_init(empty(i), 3);  // the matrix products' commit, and both guard warps
     }
-    for (int i = 0; i < 4; ++i) bar_init(guarded(i), 64);
+    for (int i = 0; i < kGuards; ++i) bar_init(guarded(i), 64);
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
       bar_init(p_full(i), kRows);
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int t = tb; t < te && ok; ++t) {
         const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
         if (!tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
-          ok = warp_wait(guarded(masked & 3), (masked >> 2) & 1, &s_dead);
+          ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &s_dead);
           ++masked;
         }
         ok = ok && warp_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           if (found) s_poison = 1;
           fence_proxy_async_smem();
-          bar_arrive(guarded(masked & 3));
+          bar_arrive(guarded(masked % kGuards));
           ++masked;
         }
         __syncwarp();
