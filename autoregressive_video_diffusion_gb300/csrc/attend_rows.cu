@@ -1,0 +1,516 @@
+// Attention of few rows a KV head (single tokens, drafts) over a bf16 cache, and of any number of rows over an fp32
+// cache, in warp-level matrix products (16 rows a warp).
+//
+// Rows are (new token, query head of the KV head) pairs.  Four warps share tiles of keys that travel page row by page
+// row through shared memory (asynchronous copies, several tiles in flight).  With MW = 4 each warp has 16 rows of its
+// own and sees every key; with MW = 1 the four warps have the same 16 rows and a quarter of each tile's keys, and
+// join their results at the end.  Few rows read every key once, so the bound is HBM and the work is spread over the
+// keys: an item's keys are split over CTAs, the last of which joins the parts.
+//
+// fp32: each factor x is x_hi + x_lo, both with 11 significant bits, and x y = x_hi y_hi + x_hi y_lo + x_lo y_hi up
+// to 2^-22: three tensor products for one.  The large and the small products of a score are summed apart, and a
+// tile's weighted values start from 0 and are added to the running ones by one fma, so that the tensor cores'
+// accumulation (which may truncate) never runs over more than a tile.
+#include <type_traits>
+
+#include "attend_join.cuh"
+
+namespace dcp {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRowThreads = 32 * kWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct RowParams {
+  AttendParams a;
+  int splits, span, row_tiles;  // keys of an item are cut into pieces of `span`
+  float scale_log2;             // |scale| log2 e
+  uint32_t flip;                // sign bit of a scale below 0, put into q
+  float* part;
+  uint32_t* done;
+};
+
+template <typename T, int DP, int MW>
+struct Rows {
+  static constexpr bool kHalf = sizeof(T) == 2;
+  static constexpr int kKeys = kHalf ? 64 : 32;         // keys of a tile
+  static constexpr int kMine = kKeys * MW / kWarps;     // of them, a warp's
+  static constexpr int kTiles = kMine / 8;              // in columns of 8
+  static constexpr int kRow = DP * sizeof(T) + 16;      // bytes of a row in shared memory: no bank is hit twice
+  static constexpr int kStages = 3;
+  static constexpr int kStage = 2 * kKeys * kRow;
+  static constexpr int kQ = kHalf ? 0 : 2 * 16 * MW * kRow;
+  static constexpr int kJoin = MW == 1 ? kWarps * 16 * (DP + 2) * 4 : 0;
+  static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
+  static constexpr int kSmem = kBuffers + kQ;
+  static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * kRow, "a tile's weights fit where its keys were");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+// x = hi + lo.  Infinities and NaN stay in hi alone.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = to_tf32(x);
+  const float rest = x - __uint_as_float(hi);
+  lo = to_tf32(rest == rest && fabsf(rest) < INFINITY ? rest : 0.f);
+}
+
+template <typename T, int DP, int MW>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
+  using R = Rows<T, DP, MW>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t s_off[4][R::kKeys];  // element offset of a key's row in the pool, -1: not read
+  __shared__ int s_last;
+  const AttendParams& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int s = blockIdx.z / p.splits, split = blockIdx.z % p.splits, kh = blockIdx.y;
+  const int tile = p.row_tiles - 1 - blockIdx.x;
+  const int D = a.pool.D, bs = a.pool.bs;
+
+  int lo, len;
+  int64_t kv64;
+  const bool sound = seq_rows(a.b, s, lo, len) & seq_kv(a.b, bs, a.pool.H, s, kh, kv64);
+  if (!sound) return;
+  const int kv = (int)kv64, n_rows = len * a.G, row0 = tile * 16 * MW;
+  if (row0 >= n_rows) return;
+  const int rows = min(16 * MW, n_rows - row0);
+  const int c_lo = kv - len + row0 / a.G, c_hi = kv - len + (row0 + rows - 1) / a.G;  // first and last row's position
+  // the keys some row of the item sees, and this split's piece of them
+  const int see_lo = a.window >= 0 ? max(0, c_lo - a.window) : 0, see_hi = a.causal ? min(kv, c_hi + 1) : kv;
+  int begin = see_lo, end = max(see_hi, see_lo);
+  if (p.splits > 1) {
+    // as even pieces of whole tiles as the splits allow (a longer sequence than max_kv has longer pieces)
+    const int span = max((int64_t)p.span, ((int64_t)(end - begin) + p.splits - 1) / p.splits);
+    const int whole = (span + R::kKeys - 1) / R::kKeys * R::kKeys;
+    begin = (int)min((int64_t)end, begin + (int64_t)split * whole);
+    end = (int)min((int64_t)end, (int64_t)begin + whole);
+  }
+  const int n_tiles = (end - begin + R::kKeys - 1) / R::kKeys;
+  const int32_t* table = a.b.tables + (int64_t)s * a.b.table_stride;
+
+  auto find = [&](int t) -> int64_t {
+    const int pos = begin + t * R::kKeys + threadIdx.x;
+    if (threadIdx.x >= R::kKeys || pos >= end) return -1;
+    const int page = pos / bs, blk = table[page];
+    if (blk < 0 || blk >= a.pool.n_blocks) {
+      set_status(a.b.status, DCP_EDEVICE);
+      return -1;
+    }
+    return blk * a.pool.s_block + kh * a.pool.s_head + (int64_t)(pos - page * bs) * a.pool.s_row;
+  };
+  const uint32_t base = smem_u32(smem);
+  const int chunks = D * (int)sizeof(T) / 16;
+  constexpr int kChunks = DP * sizeof(T) / 16;
+  auto fetch = [&](int t) {
+    if (t < n_tiles) {
+      const uint32_t k_at = base + (t % R::kStages) * R::kStage, v_at = k_at + R::kKeys * R::kRow;
+#pragma unroll
+      for (int j = 0; j < R::kKeys * kChunks / kRowThreads; ++j) {
+        const int u = threadIdx.x + j * kRowThreads, row = u / kChunks, ch = u % kChunks;
+        const int64_t off = s_off[t & 3][row];
+        const bool real = off >= 0 && ch < chunks;
+        const int64_t at = real ? off * (int64_t)sizeof(T) + ch * 16 : 0;
+        copy16(k_at + row * R::kRow + ch * 16, a.pool.k + at, real);
+        copy16(v_at + row * R::kRow + ch * 16, a.pool.v + at, real);
+      }
+    }
+    cp_async_commit();
+  };
+  {
+    int64_t f[R::kStages];
+#pragma unroll
+    for (int t = 0; t < R::kStages; ++t) f[t] = find(t);
+    if (threadIdx.x < R::kKeys)
+#pragma unroll
+      for (int t = 0; t < R::kStages; ++t) s_off[t][threadIdx.x] = f[t];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < R::kStages - 1; ++t) fetch(t);
+
+  // ---- q: bf16 in registers as the products want it, fp32 in shared memory as its two parts
+  const int first = MW == 1 ? 0 : warp * 16;  // the warp's first row of the item
+  uint32_t qa[R::kHalf ? DP / 16 : 1][4];
+  auto q_row = [&](int r) {
+    const int tok = (row0 + r) / a.G;
+    return a.q + ((int64_t)(lo + tok) * a.q_stride + (int64_t)(kh * a.G + (row0 + r) - tok * a.G) * D) *
+                     (int64_t)sizeof(T);
+  };
+  if constexpr (R::kHalf) {
+    const char* q0 = first + g < rows ? q_row(first + g) : nullptr;
+    const char* q1 = first + g + 8 < rows ? q_row(first + g + 8) : nullptr;
+    const uint32_t flip = p.flip | p.flip >> 16;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const char* q = e & 1 ? q1 : q0;
+        const int d = 16 * k + 2 * c + (e >> 1) * 8;
+        qa[k][e] = q && d < D ? *reinterpret_cast<const uint32_t*>(q + d * 2) ^ flip : 0;
+      }
+    }
+  } else {
+    uint8_t* qs = smem + R::kBuffers;
+    for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += kRowThreads) {
+      const int r = u / (DP / 4), d = u % (DP / 4) * 4;
+      uint4 x = make_uint4(0, 0, 0, 0), y = x;
+      if (r < rows && d < D) x = *reinterpret_cast<const uint4*>(q_row(r) + d * 4);
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+      uint32_t* v = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(w[e] ^ (r < rows ? p.flip : 0u)), w[e], v[e]);
+      *reinterpret_cast<uint4*>(qs + r * R::kRow + d * 4) = x;
+      *reinterpret_cast<uint4*>(qs + (16 * MW + r) * R::kRow + d * 4) = y;
+    }
+  }
+
+  // ---- the keys
+  float o[DP / 8][4];
+#pragma unroll
+  for (int j = 0; j < DP / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g and g + 8; l is this lane's share
+  int pos_of[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) pos_of[e] = kv - len + (row0 + first + g + 8 * e) / a.G;
+  const int k0 = MW == 1 ? warp * R::kMine : 0;  // the warp's first key of a tile
+  const bool idle = first >= rows;
+
+  for (int t = 0; t < n_tiles; ++t) {
+    const int64_t ahead = t + R::kStages < n_tiles ? find(t + R::kStages) : -1;
+    cp_async_wait<R::kStages - 2>();
+    __syncthreads();
+    fetch(t + R::kStages - 1);
+    const uint32_t k_at = base + (t % R::kStages) * R::kStage, v_at = k_at + R::kKeys * R::kRow;
+    const uint8_t* kp = smem + (t % R::kStages) * R::kStage;
+    const uint8_t* vp = kp + R::kKeys * R::kRow;
+    const int p0 = begin + t * R::kKeys;
+    const bool all = p0 + R::kKeys <= end && (!a.causal || p0 + R::kKeys - 1 <= c_lo) &&
+                     (a.window < 0 || p0 >= c_hi - a.window);
+    // a masked tile whose values hold infinities or NaN: 0 times those must not reach a row that does not see them
+    bool poison = false;
+    if (!all) {
+      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += kRowThreads) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vp + u / kChunks * R::kRow + u % kChunks * 16);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          poison |= (w[e] & 0x7F800000u) == 0x7F800000u || (R::kHalf && (w[e] & 0x7F80u) == 0x7F80u);
+      }
+      poison = __syncthreads_or(poison);
+    }
+    float x[R::kTiles][4], keep[2];
+#pragma unroll
+    for (int n = 0; n < R::kTiles; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+    if (!idle) {
+      if constexpr (R::kHalf) {
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int k = 0; k < DP / 32; ++k) {
+            uint32_t b[4];
+            ldm4(b, k_at + (k0 + 8 * n + (lane & 7)) * R::kRow + k * 64 + (lane >> 3) * 16);
+            mma_bf16(x[n], qa[2 * k], b[0], b[1]);
+            mma_bf16(x[n], qa[2 * k + 1], b[2], b[3]);
+          }
+      } else {
+        float y[R::kTiles][4];
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
+        const uint8_t* qh = smem + R::kBuffers + (first + g) * R::kRow + c * 4;
+        const uint8_t* ql = qh + 16 * MW * R::kRow;
+#pragma unroll
+        for (int k = 0; k < DP / 8; ++k) {
+          uint32_t ah[4], al[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = (e & 1) * 8 * R::kRow + (8 * k + (e >> 1) * 4) * 4;
+            ah[e] = *reinterpret_cast<const uint32_t*>(qh + at);
+            al[e] = *reinterpret_cast<const uint32_t*>(ql + at);
+          }
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) {
+            const float* kr = reinterpret_cast<const float*>(kp + (k0 + 8 * n + g) * R::kRow) + 8 * k + c;
+            uint32_t h0, h1, l0, l1;
+            split_tf32(kr[0], h0, l0);
+            split_tf32(kr[4], h1, l1);
+            mma_tf32(x[n], ah, h0, h1);
+            mma_tf32(y[n], ah, l0, l1);
+            mma_tf32(y[n], al, h0, h1);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] += y[n][e];
+      }
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = p0 + k0 + 8 * n + 2 * c + (e & 1), at = pos_of[e >> 1];
+            if (pos >= end || (a.causal && pos > at) || (a.window >= 0 && pos < at - a.window)) x[n][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = m[e];
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n) top = fmaxf(top, fmaxf(x[n][2 * e], x[n][2 * e + 1]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        keep[e] = m[e] == top ? 1.f : exp2_fast((m[e] - top) * p.scale_log2);
+        m[e] = top;
+        const float off = top == -INFINITY ? 0.f : top * p.scale_log2;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int b = 2 * e; b < 2 * e + 2; ++b) {
+            const bool hidden = x[n][b] == -INFINITY;
+            x[n][b] = exp2_fast(fmaf(x[n][b], p.scale_log2, -off));
+            sum += x[n][b];
+            if (poison && hidden) x[n][b] = -1.f;
+          }
+        l[e] = l[e] * keep[e] + sum;
+      }
+    }
+    if (poison) __syncthreads();  // every warp is done with the keys: the weights take their place
+    if (!idle) {
+      if (poison) {  // in plain arithmetic, skipping what a row does not see
+        T* ps = reinterpret_cast<T*>(smem + (t % R::kStages) * R::kStage) + warp * 16 * R::kMine;
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ps[(g + 8 * (e >> 1)) * R::kMine + 8 * n + 2 * c + (e & 1)] = (T)x[n][e];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float sum = o[j][e] * keep[e >> 1];
+            for (int n = 0; n < R::kMine; ++n) {
+              const float w = (float)ps[(g + 8 * (e >> 1)) * R::kMine + n];
+              if (w < 0.f) continue;
+              sum = fmaf(w, (float)*reinterpret_cast<const T*>(vp + (k0 + n) * R::kRow +
+                                                               (8 * j + 2 * c + (e & 1)) * (int)sizeof(T)), sum);
+            }
+            o[j][e] = sum;
+          }
+        }
+      } else if constexpr (R::kHalf) {
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] *= keep[e >> 1];
+#pragma unroll
+        for (int n = 0; n < R::kTiles; n += 2) {
+          const uint32_t w[4] = {pack_bf16x2(x[n][0], x[n][1]), pack_bf16x2(x[n][2], x[n][3]),
+                                 pack_bf16x2(x[n + 1][0], x[n + 1][1]), pack_bf16x2(x[n + 1][2], x[n + 1][3])};
+#pragma unroll
+          for (int j = 0; j < DP / 8; j += 2) {
+            uint32_t b[4];
+            ldm4t(b, v_at + (k0 + 8 * n + (lane & 15)) * R::kRow + (j + (lane >> 4)) * 16);
+            mma_bf16(o[j], w, b[0], b[1]);
+            mma_bf16(o[j + 1], w, b[2], b[3]);
+          }
+        }
+      } else {
+        // weight columns in the order (0, 2, 4, 6, 1, 3, 5, 7): a lane's own scores are its factors
+        uint32_t wh[R::kTiles][4], wl[R::kTiles][4];
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n) {
+          split_tf32(x[n][0], wh[n][0], wl[n][0]);
+          split_tf32(x[n][2], wh[n][1], wl[n][1]);
+          split_tf32(x[n][1], wh[n][2], wl[n][2]);
+          split_tf32(x[n][3], wh[n][3], wl[n][3]);
+        }
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) {
+            const float* v0 = reinterpret_cast<const float*>(vp + (k0 + 8 * n + 2 * c) * R::kRow) + 8 * j + g;
+            uint32_t h0, h1, l0, l1;
+            split_tf32(v0[0], h0, l0);
+            split_tf32(v0[R::kRow / 4], h1, l1);
+            mma_tf32(y, wl[n], h0, h1);
+            mma_tf32(y, wh[n], l0, l1);
+            mma_tf32(y, wh[n], h0, h1);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] = fmaf(o[j][e], keep[e >> 1], y[e]);
+        }
+      }
+    }
+    if (threadIdx.x < R::kKeys) s_off[(t + R::kStages) & 3][threadIdx.x] = ahead;
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(~0u, l[e], 1);
+    l[e] += __shfl_xor_sync(~0u, l[e], 2);
+    if (m[e] != -INFINITY) m[e] *= p.scale_log2;
+  }
+
+  // ---- results
+  const int64_t item = ((int64_t)s * a.pool.H + kh) * p.row_tiles + tile;
+  auto put = [&](int r, int d, float y0, float y1, float mr, float lr) {  // two dims of a row of the item
+    if (d >= D) return;
+    if (p.splits > 1) {
+      float* part = part_of(p.part, item, p.splits, split, 16 * MW, D, r);
+      if (d == 0) *reinterpret_cast<float2*>(part) = make_float2(mr, lr);
+      *reinterpret_cast<float2*>(part + 2 + d) = make_float2(y0, y1);
+      return;
+    }
+    const float inv = lr != 0.f ? 1.f / lr : 0.f;
+    const int tok = (row0 + r) / a.G;
+    const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (row0 + r) - tok * a.G;
+    if constexpr (R::kHalf)
+      *reinterpret_cast<uint32_t*>(a.out + (row * D + d) * 2) = pack_bf16x2(y0 * inv, y1 * inv);
+    else
+      *reinterpret_cast<float2*>(a.out + (row * D + d) * 4) = make_float2(y0 * inv, y1 * inv);
+    if (a.lse && d == 0) a.lse[row] = row_lse(mr, lr);
+  };
+  if constexpr (MW > 1) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = first + g + 8 * e;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int j = 0; j < DP / 8; ++j) put(r, 8 * j + 2 * c, o[j][2 * e], o[j][2 * e + 1], m[e], l[e]);
+    }
+  } else {
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(smem);  // [warp][16][DP + 2]
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = g + 8 * e;
+      if (r >= rows) continue;
+      float* at = join + (warp * 16 + r) * (DP + 2);
+      if (c == 0) *reinterpret_cast<float2*>(at) = make_float2(m[e], l[e]);
+#pragma unroll
+      for (int j = 0; j < DP / 8; ++j)
+        *reinterpret_cast<float2*>(at + 2 + 8 * j + 2 * c) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < rows * (DP / 2); u += kRowThreads) {
+      const int r = u / (DP / 2), d = u % (DP / 2) * 2;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join[(w * 16 + r) * (DP + 2)]);
+      float sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* at = join + (w * 16 + r) * (DP + 2);
+        if (at[1] == 0.f) continue;
+        const float k = exp2_fast(at[0] - top);
+        sum += k * at[1];
+        y0 += k * at[2 + d];
+        y1 += k * at[3 + d];
+      }
+      put(r, d, y0, y1, top, sum);
+    }
+  }
+  if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
+    join_parts<T>(a, part_of(p.part, item, p.splits, 0, 16 * MW, D, 0), p.splits, 16 * MW, rows, row0, lo, kh);
+}
+
+template <typename T, int DP, int MW>
+cudaError_t launch(const RowParams& p, cudaStream_t s) {
+  static LaunchCache lc;
+  int blocks;
+  const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, kRowThreads, Rows<T, DP, MW>::kSmem, &blocks);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
+  rows_kernel<T, DP, MW><<<grid, kRowThreads, Rows<T, DP, MW>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Rows of one CTA: all of a KV head's rows where they fit 16, else 64.
+int rows_a_cta(const AttendParams& a) { return (int64_t)a.b.max_q * a.G <= 16 ? 16 : 64; }
+
+}  // namespace
+
+bool attend_by_rows(const AttendParams& a) {
+  return a.pool.dtype == DCP_F32 || (int64_t)a.b.max_q * a.G <= 64;
+}
+
+RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
+  RowPlan r;
+  const int per = rows_a_cta(a), keys = a.pool.dtype == DCP_BF16 ? 64 : 32;
+  const int64_t seen = (int64_t)a.window + per / a.G + 2;  // of a tile's rows under a window
+  if (a.window >= 0 && max_kv > seen) max_kv = seen;
+  r.tiles = (int)(((int64_t)a.b.max_q * a.G + per - 1) / per);
+  const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
+  // Two CTAs of an SM at a time: one round of pieces for a few sequences, several rounds of shorter ones where their
+  // lengths may differ, but no piece under a tile (or four, in several rounds) and at most 64 pieces of an item.
+  const int64_t slots = 304, rounds = a.b.n_seqs >= 8 ? 8 : 1;
+  int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
+  const int64_t least = rounds > 1 ? 4 * keys : keys;
+  if (span < least) span = least;
+  if (span < (max_kv + 63) / 64) span = (max_kv + 63) / 64;
+  span = (span + keys - 1) / keys * keys;
+  int64_t splits = (max_kv + span - 1) / span;
+  if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;
+  r.splits = splits < 1 ? 1 : (int)splits;
+  r.span = (int)(span < kMaxKv ? span : kMaxKv);
+  r.done_bytes = r.splits > 1 ? ((size_t)items * 4 + 255) & ~(size_t)255 : 0;
+  r.bytes = r.splits > 1 ? r.done_bytes + (size_t)items * r.splits * per * (a.pool.D + 2) * 4 : 0;
+  return r;
+}
+
+cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, cudaStream_t s) {
+  const RowPlan r = plan_rows(a, max_kv);
+  RowParams p{};
+  p.a = a;
+  p.splits = r.splits;
+  p.span = r.span;
+  p.row_tiles = r.tiles;
+  // a scale below 0 negates q (the running maximum then is of what is exponentiated); one near 0 is held where masked
+  // scores of -inf still scale to -inf
+  const float mag = a.scale < 0.f ? -a.scale : a.scale;
+  p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
+  p.flip = a.scale < 0.f ? 0x80000000u : 0u;
+  p.done = (uint32_t*)ws;
+  p.part = (float*)((char*)ws + r.done_bytes);
+  const bool one = rows_a_cta(a) == 16, wide = a.pool.D > 64;
+  if (a.pool.dtype == DCP_BF16) {
+    if (one) return wide ? launch<__nv_bfloat16, 128, 1>(p, s) : launch<__nv_bfloat16, 64, 1>(p, s);
+    return wide ? launch<__nv_bfloat16, 128, 4>(p, s) : launch<__nv_bfloat16, 64, 4>(p, s);
+  }
+  if (one) return wide ? launch<float, 128, 1>(p, s) : launch<float, 64, 1>(p, s);
+  return wide ? launch<float, 128, 4>(p, s) : launch<float, 64, 4>(p, s);
+}
+
+}  // namespace dcp

@@ -17,7 +17,7 @@
 // back in the epilogue, from the cache.
 #include <cuda.h>
 
-#include "serve.cuh"
+#include "attend_join.cuh"
 
 namespace dcp {
 
@@ -179,12 +179,6 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The n lowest bits (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 // x = -inf where keep is 0, in place: a select over 128 registers in two branches costs the compiler copies.
@@ -274,6 +268,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tb = act0 ? it.t0[0] : it.t0[1];                // tiles of either
   const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : act0 ? it.t1[0] : tb;
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
+
+  const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
 
   // ---- set-up
   const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
@@ -424,8 +420,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const bool mine = r < rows_i;
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
-    float* part = p.part + ((((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt) * p.splits + split) *
-                               (2 * kRows) * (D + 2) + (int64_t)(i * kRows + r) * (D + 2);
+    float* part = part_of(p.part, item, p.splits, split, 2 * kRows, D, i * kRows + r);
 #pragma unroll 1
     for (int e = 0; e < Sh::kD / 32 && ok; ++e) {
       uint32_t o[32];
@@ -457,8 +452,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!mine) continue;
       if (p.splits > 1) {
 #pragma unroll
-        for (int u = 0; u < 32; ++u)
-          if (32 * e + u < D) part[2 + 32 * e + u] = __uint_as_float(o[u]);
+        for (int u = 0; u < 32; u += 2)
+          if (32 * e + u < D)
+            *reinterpret_cast<float2*>(part + 2 + 32 * e + u) =
+                make_float2(__uint_as_float(o[u]), __uint_as_float(o[u + 1]));
       } else {
 #pragma unroll
         for (int u = 0; u < 32; u += 8) {
@@ -477,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         part[0] = m == -INFINITY ? m : m * sc;
         part[1] = l;
       } else if (a.lse) {
-        a.lse[row] = l != 0.f ? (m * sc + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        a.lse[row] = row_lse(m * sc, l);
       }
     }
   } else {
@@ -667,46 +664,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 
   // ---- the item's last split joins the parts
-  if (p.splits > 1) {
-    const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const uint32_t before = atomicAdd(p.done + item, 1);
-      s_last = before == (uint32_t)p.splits - 1;
-      if (s_last) p.done[item] = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const int D = a.pool.D, rows = it.rows[0] + it.rows[1];
-    const float* part = p.part + item * p.splits * (2 * kRows) * (D + 2);
-    const int64_t step = (int64_t)2 * kRows * (D + 2);
-    for (int u = threadIdx.x; u < rows * (D / 8); u += kTileThreads) {
-      const int r = u / (D / 8), d = u % (D / 8) * 8;
-      const float* at = part + (int64_t)r * (D + 2);
-      float top = -INFINITY;
-      for (int k = 0; k < p.splits; ++k) top = fmaxf(top, __ldcg(at + k * step));
-      float l = 0.f, o[8] = {};
-      for (int k = 0; k < p.splits; ++k) {
-        const float* x = at + k * step;
-        const float lk = __ldcg(x + 1), w = __ldcg(x) == -INFINITY && lk == 0.f ? 0.f : exp2_fast(__ldcg(x) - top);
-        if (w == 0.f && lk == 0.f) continue;
-        l += w * lk;
-#pragma unroll
-        for (int b = 0; b < 8; ++b) o[b] += w * __ldcg(x + 2 + d + b);
-      }
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int R = it.row0 + r, tok = R / a.G, g = R - tok * a.G;
-      const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
-      uint4 y;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) w[b] = pack_bf16x2(o[2 * b] * inv, o[2 * b + 1] * inv);
-      *reinterpret_cast<uint4*>(a.out + (row * D + d) * 2) = y;
-      if (a.lse && d == 0) a.lse[row] = l != 0.f ? (top + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-    }
-  }
+  if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
+    join_parts<__nv_bfloat16>(a, part_of(p.part, item, p.splits, 0, 2 * kRows, a.pool.D, 0), p.splits, 2 * kRows,
+                              it.rows[0] + it.rows[1], it.row0, it.lo, it.kh);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -761,6 +721,8 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   TilePlan t;
   t.q_tiles = (int)(((int64_t)a.b.max_q * a.G + 2 * kRows - 1) / (2 * kRows));
   const int64_t items = (int64_t)t.q_tiles * a.pool.H * a.b.n_seqs;
+  const int64_t seen = (int64_t)a.window + 2 * kRows / a.G + 2;  // of an item's rows under a window
+  if (a.window >= 0 && max_kv > seen) max_kv = seen;
   const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
   // fewer items than SMs: the keys are split so that the SMs have one item each, at least 4 key tiles a split
   int64_t splits = items < 152 ? 152 / items : 1;

@@ -61,9 +61,17 @@ struct PageParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
-cudaError_t launch_attend_rows(const AttendParams& p, cudaStream_t s);
+// How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes (counters first,
+// zero between calls).
+struct RowPlan {
+  int tiles, splits, span;
+  size_t done_bytes, bytes;
+};
+bool attend_by_rows(const AttendParams& p);
+RowPlan plan_rows(const AttendParams& p, int64_t max_kv);
+cudaError_t launch_attend_rows(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);
 
-// How the tiled attention divides its work, and the workspace that takes (counters first, zero between calls).
+// The same for the tiled attention.
 struct TilePlan {
   int q_tiles, splits;
   size_t done_bytes, bytes;

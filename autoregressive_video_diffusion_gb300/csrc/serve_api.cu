@@ -181,7 +181,9 @@ dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
 size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                                     int32_t Hq) {
   if (check_attention(pool, batch, cfg, Hq) != DCP_OK) return 0;
-  return 256 + (plan_tiles(attend_of(pool, batch, cfg, Hq), batch->max_kv).bytes + 255) / 256 * 256;
+  const AttendParams p = attend_of(pool, batch, cfg, Hq);
+  const size_t bytes = attend_by_rows(p) ? plan_rows(p, batch->max_kv).bytes : plan_tiles(p, batch->max_kv).bytes;
+  return 256 + (bytes + 255) / 256 * 256;
 }
 
 dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
@@ -195,8 +197,8 @@ dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* bat
   p.out = (char*)out;
   p.lse = lse;
   p.q_stride = q_stride;
-  if (pool->dtype == DCP_BF16) return cuda_ok(launch_attend_tiles(p, batch->max_kv, ws, (cudaStream_t)stream));
-  return cuda_ok(launch_attend_rows(p, (cudaStream_t)stream));
+  return cuda_ok(attend_by_rows(p) ? launch_attend_rows(p, batch->max_kv, ws, (cudaStream_t)stream)
+                                   : launch_attend_tiles(p, batch->max_kv, ws, (cudaStream_t)stream));
 }
 
 size_t dcp_pages_workspace_size(const dcp_page_pool* pool, int32_t n_rows, int32_t stride) {
