@@ -4,14 +4,14 @@
 // Rows are (new token, query head of the KV head) pairs in that order, so the heads that share a KV head share its
 // tiles.  A CTA owns 256 rows (two tiles of 128) of one sequence and KV head and walks the keys they see:
 //   scores   S = Q K^T      Q, K in shared memory, S (fp32) in tensor memory
-//   softmax  P = exp(S - m) one thread a row, m a running maximum; P (bf16) goes back over S in tensor memory
+//   softmax  P = exp(S - m), m a running maximum; P (bf16) goes back over S in tensor memory
 //   values   O += P V       P from tensor memory, V from shared memory, O (fp32) stays in tensor memory
-// Each 128-thread group works on its own row tile, so one tile's softmax runs under the other's matrix products.  m
-// moves only when a row's maximum has grown by more than 2^8 (weights stay below 256, sums in 32 bits), which leaves O
+// Each row tile has its own 8 warps, so one tile's softmax runs under the other's matrix products; a row is two threads'
+// work, half of its scores each, so that an SM quarter always has several warps to choose from.  m moves only when a row's maximum has grown by more than 2^8 (weights stay below 256, sums in 32 bits), which leaves O
 // untouched in almost every step; m has moved or not, the quotient O / l is the same.
 //
-// Warps 0-3 and 4-7: softmax of row tile 0 and 1.  Warp 8: issues the matrix products.  Warp 9: copies pages with TMA
-// (a page of block_size positions is a box; 128-byte swizzle).  Warps 10, 11: the guard.  A weight of 0 times a value
+// Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warp 16: issues the matrix products.  Warp 17: copies pages with TMA
+// (a page of block_size positions is a box; 128-byte swizzle).  Warps 18, 19: the guard.  A weight of 0 times a value
 // of infinity or NaN is NaN, so in the tiles where some row must not see some key, the guard puts zeros for rows past
 // the sequence (page rows never written hold anything) and for infinities and NaN; rows that do see those get them
 // back in the epilogue, from the cache.
@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a tile (lanes of tensor memory)
 constexpr int kKeys = 128;             // keys of a tile
-constexpr int kTileThreads = 384;
+constexpr int kTileThreads = 640;
+constexpr int kSoftWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows
@@ -154,16 +155,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t at) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
-__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
-      : "memory");
-}
 __device__ __forceinline__ void tm_ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -178,6 +169,30 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
+}
+// Two fp32 in a register pair.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ void unpair(uint64_t z, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t w;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  return w;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t w;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  return w;
+}
+__device__ __forceinline__ float max3(float x, uint32_t y, uint32_t z) {
+  float w;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(w) : "f"(x), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
+  return w;
 }
 // The n lowest bits (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
@@ -221,6 +236,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ __align__(8) uint64_t s_bars[2 * Sh::kSlots + kGuards + 6];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_poison, s_last;
+  __shared__ float s_swap[2][2][kRows];  // what the two threads of a row tell each other
   const AttendParams& a = p.a;
   const Tiling tl = p.tl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,15 +306,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < kGuards; ++i) bar_init(guarded(i), 64);
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
-      bar_init(p_full(i), kRows);
+      bar_init(p_full(i), kSoftWarps / 2);
     }
-    bar_init(q_full, 256);
+    bar_init(q_full, 32 * kSoftWarps);
     bar_init(finished, 1);
     s_dead = 0;
     s_poison = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -308,15 +324,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   fence_after();
   const uint32_t tmem = s_tmem;
 
-  if (warp < 8) {
+  if (warp < kSoftWarps) {
     // ------------------------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int i = warp >> 2, r = threadIdx.x & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int i = warp >> 3, hf = warp >> 2 & 1, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-    const uint32_t t_s = tmem + lanes + i * kKeys, t_o = tmem + lanes + 256 + i * 128;
+    const uint32_t t_s = tmem + lanes + i * kKeys, t_o = tmem + lanes + 256 + i * 128 + hf * (Sh::kD / 2);
     const int D = a.pool.D, rows_i = i ? it.rows[1] : it.rows[0];
     {  // the rows of q into shared memory, zeros past the rows and past D
-      for (int u = r; u < kRows * 8 * HALVES; u += kRows) {
+      for (int u = threadIdx.x & 255; u < kRows * 8 * HALVES; u += 256) {
         const int row = u / (8 * HALVES), ch = u % (8 * HALVES);
         uint4 x = make_uint4(0, 0, 0, 0);
         if (row < rows_i && ch * 8 < D) {
@@ -330,6 +346,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_proxy_async_smem();
       bar_arrive(q_full);
     }
+    // the other thread of the row: this thread's value for its own
+    auto swap = [&](float y) {
+      s_swap[i][hf][r] = y;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory");
+      return s_swap[i][hf ^ 1][r];
+    };
     const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
     const int c = it.kv - it.len + tok;
     const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
@@ -343,35 +365,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = warp_wait(s_full(i), (t - t0) & 1, &s_dead);
       if (!ok) break;
       fence_after();
-      uint32_t x[4][32];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tm_ld32(x[e], t_s + 32 * e);
+      uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
+      tm_ld32(x[0], t_s + 64 * hf);
+      tm_ld32(x[1], t_s + 64 * hf + 32);
       wait_ld();
       if (!tile_full(a, tl, t, it.kv, cmin, cmax)) {
-        uint32_t see[4];  // columns the row sees
+        uint32_t see[2];  // columns the row sees
         const int p0 = tl.first(t);
         if (!tl.gaps()) {
-          const int hi = min(seen_end - p0, tl.count(t)), lo = seen_begin - p0;
+          const int hi = min(seen_end - p0, tl.count(t)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) see[w] = low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w);
+          for (int w = 0; w < 2; ++w) see[w] = low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w);
         } else {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < 2; ++w) {
             see[w] = 0;
 #pragma unroll 1
             for (int b = 0; b < 32; ++b) {
-              const int at = tl.place(t, 32 * w + b);
+              const int at = tl.place(t, 64 * hf + 32 * w + b);
               if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[w] |= 1u << b;
             }
           }
         }
 #pragma unroll
-        for (int e = 0; e < 128; ++e) hide_unless(x[e >> 5][e & 31], see[e >> 5] & (1u << (e & 31)));
+        for (int e = 0; e < 64; ++e) hide_unless(x[e >> 5][e & 31], see[e >> 5] & (1u << (e & 31)));
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e >> 5][e & 31]));
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      for (int e = 0; e < 32; ++e) top[e & 3] = max3(top[e & 3], x[0][e], x[1][e]);
+      float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      mx = fmaxf(mx, swap(mx));  // both have read their scores: weights may go over them
       const bool grow = mx > m && (m == -INFINITY || (mx - m) * sc > kGrow);
       if (__any_sync(~0u, grow)) {
         const float m2 = grow ? mx : m;
@@ -380,7 +403,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         l *= keep;
         if (t > t0) {
 #pragma unroll 1
-          for (int e = 0; e < Sh::kD / 16; ++e) {
+          for (int e = 0; e < Sh::kD / 32; ++e) {
             uint32_t o[16];
             tm_ld16(o, t_o + 16 * e);
             wait_ld();
@@ -390,39 +413,49 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      const float off = m == -INFINITY ? 0.f : m * sc;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float off = m == -INFINITY ? 0.f : -m * sc;
+      const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        uint32_t w[32];
+        uint32_t w[16];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const int k = 64 * e + 2 * u;
-          const float y0 = exp2_fast(fmaf(__uint_as_float(x[k >> 5][k & 31]), sc, -off));
-          const float y1 = exp2_fast(fmaf(__uint_as_float(x[(k + 1) >> 5][(k + 1) & 31]), sc, -off));
-          sum[(2 * u) & 3] += y0;
-          sum[(2 * u + 1) & 3] += y1;
+        for (int u = 0; u < 16; ++u) {
+          float y0, y1;
+          unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y0, y1);
+          y0 = exp2_fast(y0);
+          y1 = exp2_fast(y1);
+          sum[u & 1] = add2(sum[u & 1], pair(y0, y1));
           w[u] = pack_bf16x2(y0, y1);
         }
-        tm_st32(t_s + 32 * e, w);
+        tm_st16(t_s + 32 * hf + 16 * e, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float y0, y1;
+      unpair(add2(sum[0], sum[1]), y0, y1);
+      l += y0 + y1;
       wait_st();
       fence_before();
-      bar_arrive(p_full(i));
+      __syncwarp();
+      if (lane == 0) bar_arrive(p_full(i));
     }
     // ---- result of the row
     if (ok && t0 < t1) {
       ok = warp_wait(s_full(i), (t1 - t0) & 1, &s_dead);
       fence_after();
     }
-    if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
+    if (ok) {
+      l += swap(l);
+    } else {  // the row's other warp may have come one exchange further: it must not wait
+      asm volatile("bar.arrive %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory");
+      set_status(a.b.status, DCP_ETIMEOUT);
+    }
     const bool mine = r < rows_i;
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
     float* part = part_of(p.part, item, p.splits, split, 2 * kRows, D, i * kRows + r);
 #pragma unroll 1
-    for (int e = 0; e < Sh::kD / 32 && ok; ++e) {
+    for (int e = 0; e < Sh::kD / 64 && ok; ++e) {
+      const int d0 = hf * (Sh::kD / 2) + 32 * e;
       uint32_t o[32];
       if (t0 < t1) {
         tm_ld32(o, t_o + 32 * e);
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                      (int64_t)it.kh * a.pool.s_head + (int64_t)(pos % tl.bs) * a.pool.s_row;
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              const float y = 32 * e + u < D ? __bfloat162float(v[32 * e + u]) : 0.f;
+              const float y = d0 + u < D ? __bfloat162float(v[d0 + u]) : 0.f;
               if (!isfinite(y)) o[u] = __float_as_uint(__uint_as_float(o[u]) + y);
             }
           }
@@ -453,23 +486,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (p.splits > 1) {
 #pragma unroll
         for (int u = 0; u < 32; u += 2)
-          if (32 * e + u < D)
-            *reinterpret_cast<float2*>(part + 2 + 32 * e + u) =
+          if (d0 + u < D)
+            *reinterpret_cast<float2*>(part + 2 + d0 + u) =
                 make_float2(__uint_as_float(o[u]), __uint_as_float(o[u + 1]));
       } else {
 #pragma unroll
         for (int u = 0; u < 32; u += 8) {
-          if (32 * e + u >= D) continue;
+          if (d0 + u >= D) continue;
           uint4 y;
           uint32_t* w = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
           for (int b = 0; b < 4; ++b)
             w[b] = pack_bf16x2(__uint_as_float(o[u + 2 * b]) * inv, __uint_as_float(o[u + 2 * b + 1]) * inv);
-          *reinterpret_cast<uint4*>(a.out + (row * D + 32 * e + u) * 2) = y;
+          *reinterpret_cast<uint4*>(a.out + (row * D + d0 + u) * 2) = y;
         }
       }
     }
-    if (mine && ok) {
+    if (mine && ok && hf == 0) {
       if (p.splits > 1) {
         part[0] = m == -INFINITY ? m : m * sc;
         part[1] = l;
@@ -478,8 +511,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kSoftWarps + 1) {
       // ---------------------------------------------------------------------------------- pages
       const int n_pages = tl.subs == 1 ? tl.pages : 1;
       const uint32_t bytes = (uint32_t)tl.box * 128 * HALVES;
@@ -523,7 +556,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && now_ns() - start < kPatience) {
           }
       }
-    } else if (warp == 8) {
+    } else if (warp == kSoftWarps) {
       // ---------------------------------------------------------------------------------- matrix products
       bool ok = te > tb ? warp_wait(q_full, 0, &s_dead) : true;
       int masked = 0;
@@ -605,7 +638,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // ---------------------------------------------------------------------------------- guard
       // It follows every fill of the ring (a wait can only tell a phase from the one before it), so a slot is free
       // once it has passed too.
-      const int me = threadIdx.x - 320;
+      const int me = threadIdx.x - 32 * (kSoftWarps + 2);
       int masked = 0;
       bool ok = true;
       for (int n = 0; n < 2 * (te - tb) && ok; ++n) {
@@ -653,14 +686,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
   }
   // every warp back to the registers it was launched with
-  if (warp < 8)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+  if (warp < kSoftWarps)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 8)
+  if (warp == kSoftWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 
   // ---- the item's last split joins the parts
