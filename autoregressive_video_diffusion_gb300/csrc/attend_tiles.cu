@@ -213,7 +213,8 @@ struct Shape {
   static constexpr int kHalf = kRows * 128;              // bytes of 128 rows x 64 dims
   static constexpr int kTile = kHalf * HALVES;
   static constexpr int kSlots = HALVES == 2 ? 5 : 10;    // ring of K and V tiles in turn
-  static constexpr int kSmem = 1024 + (2 + kSlots) * kTile + 1024;
+  static constexpr int kHead = 3072;                     // barriers and the like, before the tiles
+  static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
 };
 
 __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, int pos) {
@@ -232,11 +233,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ TileParams p, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
   using Sh = Shape<HALVES>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bars[2 * Sh::kSlots + kGuards + 6];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_dead, s_poison, s_last;
-  __shared__ float s_swap[2][2][kRows];  // what the two threads of a row tell each other
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  struct Head {
+    uint64_t bars[2 * Sh::kSlots + kGuards + 6];
+    float swap[2][2][kRows];  // what the two threads of a row tell each other
+    uint32_t tmem;
+    int dead, poison, last;
+  };
+  static_assert(sizeof(Head) <= Sh::kHead, "the head fits before the tiles");
+  Head& sh = *reinterpret_cast<Head*>(smem_raw);
   const AttendParams& a = p.a;
   const Tiling tl = p.tl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,10 +293,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
 
   // ---- set-up
-  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t base = smem_u32(smem_raw) + Sh::kHead;
   const uint32_t q_smem = base, ring = base + 2 * Sh::kTile;
-  uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t bars = smem_u32(s_bars);
+  uint8_t* const gbase = smem_raw + Sh::kHead;
+  const uint32_t bars = smem_u32(sh.bars);
   auto full = [&](int i) { return bars + 8 * i; };
   auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
   auto guarded = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
@@ -310,19 +315,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     bar_init(q_full, 32 * kSoftWarps);
     bar_init(finished, 1);
-    s_dead = 0;
-    s_poison = 0;
+    sh.dead = 0;
+    sh.poison = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kSoftWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = sh.tmem;
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------------------------ softmax
@@ -348,9 +353,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // the other thread of the row: this thread's value for its own
     auto swap = [&](float y) {
-      s_swap[i][hf][r] = y;
+      sh.swap[i][hf][r] = y;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory");
-      return s_swap[i][hf ^ 1][r];
+      return sh.swap[i][hf ^ 1][r];
     };
     const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
     const int c = it.kv - it.len + tok;
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int t = t0; t < t1 && ok; ++t) {
-      ok = warp_wait(s_full(i), (t - t0) & 1, &s_dead);
+      ok = warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
       if (!ok) break;
       fence_after();
       uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // ---- result of the row
     if (ok && t0 < t1) {
-      ok = warp_wait(s_full(i), (t1 - t0) & 1, &s_dead);
+      ok = warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
       fence_after();
     }
     if (ok) {
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int u = 0; u < 32; ++u) o[u] = 0;
       }
-      if (s_poison && mine) {  // infinities and NaN this row sees in the guarded tiles
+      if (sh.poison && mine) {  // infinities and NaN this row sees in the guarded tiles
         for (int t = t0; t < t1; ++t) {
           if (tile_full(a, tl, t, it.kv, c_lo, c_hi)) continue;
           for (int col = 0; col < kKeys; ++col) {
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const int slot = n % Sh::kSlots;
-          if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &s_dead);
+          if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &sh.dead);
           if (!ok) break;
           if (lane == 0) bar_expect(full(slot), here * bytes);
           __syncwarp();
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else if (warp == kSoftWarps) {
       // ---------------------------------------------------------------------------------- matrix products
-      bool ok = te > tb ? warp_wait(q_full, 0, &s_dead) : true;
+      bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
       int masked = 0;
       int seen[2] = {0, 0};
       fence_after();
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       auto key_wait = [&](int t) {
         const int n = 2 * (t - tb);
-        ok = ok && warp_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &s_dead);
+        ok = ok && warp_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &sh.dead);
         fence_after();
       };
       auto active = [&](int i, int t) {
@@ -592,16 +597,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int t = tb; t < te && ok; ++t) {
         const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
         if (!tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
-          ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &s_dead);
+          ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &sh.dead);
           ++masked;
         }
-        ok = ok && warp_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+        ok = ok && warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
         bool have_keys = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
           if (ok && active(i, t)) {
-            ok = warp_wait(p_full(i), seen[i] & 1, &s_dead);
+            ok = warp_wait(p_full(i), seen[i] & 1, &sh.dead);
             ++seen[i];
             fence_after();
             if (ok && lane == 0) {
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       for (int n = 0; n < 2 * (te - tb) && ok; ++n) {
         const int t = tb + (n >> 1), slot = n % Sh::kSlots;
-        ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &s_dead);
+        ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
         if (!ok) break;
         if ((n & 1) && !tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
           const int p0 = tl.first(t);
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (bad) *at = x;
             found |= bad;
           }
-          if (found) s_poison = 1;
+          if (found) sh.poison = 1;
           fence_proxy_async_smem();
           bar_arrive(guarded(masked % kGuards));
           ++masked;
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 
   // ---- the item's last split joins the parts
-  if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
+  if (p.splits > 1 && last_of(p.done + item, p.splits, &sh.last))
     join_parts<__nv_bfloat16>(a, part_of(p.part, item, p.splits, 0, 2 * kRows, a.pool.D, 0), p.splits, 2 * kRows,
                               it.rows[0] + it.rows[1], it.row0, it.lo, it.kh);
 }
