@@ -125,20 +125,30 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
       ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(h), "r"(blk), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// The products are issued by one lane, chosen inside the instruction sequence: the warp's control flow stays uniform and
+// the operands stay in uniform registers (a branch on the lane made eight products take 720 cycles to issue).
+// Descriptors share their high word; `a`, `b` are the low words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                       uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi),
+      "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(b_hi),
+      "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -201,11 +211,12 @@ __device__ __forceinline__ void hide_unless(uint32_t& x, uint32_t keep) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mov.b32 %0, 0xFF800000;\n\t}" : "+r"(x) : "r"(keep));
 }
 
-// Shared-memory matrix descriptor, 128-byte swizzle: start and the two strides in units of 16 bytes, bits 46-48 = 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptor, 128-byte swizzle: low word the start and the leading stride in units of 16 bytes,
+// high word the other stride, bit 46 = 1 and the swizzle at bits 61-63.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading) {
+  return (addr >> 4 & 0x3FFF) | (leading >> 4) << 16;
 }
+constexpr uint32_t kDescHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 
 template <int HALVES>
 struct Shape {
@@ -569,16 +580,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_after();
       auto scores = [&](int i, int t) {  // S_i of tile t
         const int slot = 2 * (t - tb) % Sh::kSlots;
-        if (lane == 0) {
+        const uint32_t q = desc_lo(q_smem + i * Sh::kTile, 16), k = desc_lo(ring + slot * Sh::kTile, 16);
 #pragma unroll
-          for (int k = 0; k < 4 * HALVES; ++k)
-            mma_ss(tmem + i * kKeys,
-                   smem_desc(q_smem + i * Sh::kTile + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024),
-                   smem_desc(ring + slot * Sh::kTile + (k >> 2) * Sh::kHalf + (k & 3) * 32, 16, 1024), p.idesc_qk,
-                   k > 0);
-          mma_commit(s_full(i));
+        for (int e = 0; e < 4 * HALVES; ++e) {
+          const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
+          mma_ss(tmem + i * kKeys, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
         }
-        __syncwarp();
+        mma_commit(s_full(i));
       };
       auto key_wait = [&](int t) {
         const int n = 2 * (t - tb);
@@ -592,7 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         key_wait(tb);
         for (int i = 0; i < 2 && ok; ++i)
           if (active(i, tb)) scores(i, tb);
-        if (lane == 0) mma_commit(empty(0));
+        mma_commit(empty(0));
       }
       for (int t = tb; t < te && ok; ++t) {
         const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
@@ -609,14 +617,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ok = warp_wait(p_full(i), seen[i] & 1, &sh.dead);
             ++seen[i];
             fence_after();
-            if (ok && lane == 0) {
+            if (ok) {
+              const uint32_t v = desc_lo(ring + slot * Sh::kTile, Sh::kHalf);
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 8 * k,
-                       smem_desc(ring + slot * Sh::kTile + k * 2048, Sh::kHalf, 1024), p.idesc_pv, t > t0 || k > 0);
+                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 8 * k, v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
+                       t > t0 || k > 0);
               if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
             }
-            __syncwarp();
           }
           if (ok && t + 1 < te && active(i, t + 1)) {
             if (!have_keys) key_wait(t + 1);
@@ -625,15 +633,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (ok && t + 1 < te && !have_keys) key_wait(t + 1);
-        if (ok && lane == 0) {
+        if (ok) {
           mma_commit(empty(slot));
           if (t + 1 < te) mma_commit(empty((n + 1) % Sh::kSlots));
         }
-        __syncwarp();
       }
       if (!ok) {  // products in flight end by themselves: leave when they have
-        if (lane == 0) mma_commit(finished);
-        __syncwarp();
+        mma_commit(finished);
         const uint64_t start = now_ns();
         while (!bar_try(finished, 0) && now_ns() - start < kPatience) {
         }
