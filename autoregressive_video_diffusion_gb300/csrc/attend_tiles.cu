@@ -7,14 +7,17 @@
 //   softmax  P = exp(S - m), m a running maximum; P (bf16) goes back over S in tensor memory
 //   values   O += P V       P from tensor memory, V from shared memory, O (fp32) stays in tensor memory
 // Each row tile has its own 8 warps, so one tile's softmax runs under the other's matrix products; a row is two threads'
-// work, half of its scores each, so that an SM quarter always has several warps to choose from.  m moves only when a row's maximum has grown by more than 2^8 (weights stay below 256, sums in 32 bits), which leaves O
-// untouched in almost every step; m has moved or not, the quotient O / l is the same.
+// work, half of its scores each, so that an SM quarter always has several warps to choose from.  The weights are taken
+// relative to the maximum of the earlier tiles: the tile's own maximum is found alongside, and only a row that has
+// outgrown m by 2^64 takes its weights again.  m follows at the next tile, and only when the maximum has grown by more
+// than 2^8, which leaves O untouched in almost every step; m has moved or not, the quotient O / l is the same (weights
+// keep their relative precision in bf16, sums are held in 32 bits).
 //
-// Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warp 16: issues the matrix products.  Warp 17: copies pages with TMA
-// (a page of block_size positions is a box; 128-byte swizzle).  Warps 18, 19: the guard.  A weight of 0 times a value
-// of infinity or NaN is NaN, so in the tiles where some row must not see some key, the guard puts zeros for rows past
-// the sequence (page rows never written hold anything) and for infinities and NaN; rows that do see those get them
-// back in the epilogue, from the cache.
+// Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warp 16: issues the matrix products.  Warps 17, 18: copy the pages
+// of the keys and of the values with TMA (a page of block_size positions is a box; 128-byte swizzle).  Warp 19: the
+// guard.  A weight of 0 times a value of infinity or NaN is NaN, so in the tiles where some row must not see some key,
+// the guard puts zeros for rows past the sequence (page rows never written hold anything) and for infinities and NaN;
+// rows that do see those get them back in the epilogue, from the cache.
 #include <cuda.h>
 
 #include "attend_join.cuh"
@@ -29,7 +32,8 @@ constexpr int kTileThreads = 640;
 constexpr int kSoftWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
-constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows
+constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows after the tile,
+constexpr float kFar = 64.f;           // and before m follows at once
 constexpr int kSpins = 1 << 24;        // limits of every wait: tries, and nanoseconds
 constexpr uint64_t kPatience = 2000000000ull;
 
@@ -118,11 +122,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
   return __all_sync(~0u, bar_wait(bar, parity, dead));
 }
+// Issued by one lane of a converged warp.
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int row, int h, int blk,
                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(h), "r"(blk), "r"(bar)
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n\t}" ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(h), "r"(blk), "r"(bar)
       : "memory");
 }
 // The products are issued by one lane, chosen inside the instruction sequence: the warp's control flow stays uniform and
@@ -152,9 +158,26 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The loaded registers pass through the wait, so that nothing reads them before it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -247,7 +270,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   struct Head {
     uint64_t bars[2 * Sh::kSlots + kGuards + 6];
-    float swap[2][2][kRows];  // what the two threads of a row tell each other
+    union {                   // what the two threads of a row tell each other
+      __nv_bfloat16 top[2][2][2][kRows];
+      float sum[2][2][kRows];
+    } swap;
     uint32_t tmem;
     int dead, poison, last;
   };
@@ -317,9 +343,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       bar_init(full(i), 1);
-      bar_init(empty(i), 3);  // the matrix products' commit, and both guard warps
+      bar_init(empty(i), 2);  // the matrix products' commit, and the guard
     }
-    for (int i = 0; i < kGuards; ++i) bar_init(guarded(i), 64);
+    for (int i = 0; i < kGuards; ++i) bar_init(guarded(i), 32);
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
       bar_init(p_full(i), kSoftWarps / 2);
@@ -362,11 +388,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_proxy_async_smem();
       bar_arrive(q_full);
     }
-    // the other thread of the row: this thread's value for its own
-    auto swap = [&](float y) {
-      sh.swap[i][hf][r] = y;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory");
-      return sh.swap[i][hf ^ 1][r];
+    // The two threads of a row meet.  Both always meet equally often, even after a wait has run out: how often depends
+    // on nothing but the maxima they have exchanged (two buffers in turn, so neither can overwrite what the other has
+    // yet to read).
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory"); };
+    int swaps = 0;
+    auto swap_max = [&](float y) {  // of both threads' values, rounded to bf16: m need only be near the maximum
+      const __nv_bfloat16 z = __float2bfloat16_rn(y);
+      sh.swap.top[i][swaps & 1][hf][r] = z;
+      meet();
+      return fmaxf(__bfloat162float(z), __bfloat162float(sh.swap.top[i][swaps++ & 1][hf ^ 1][r]));
     };
     const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
     const int c = it.kv - it.len + tok;
@@ -375,77 +406,89 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int seen_end = a.causal ? min(it.kv, c + 1) : it.kv;
     const int seen_begin = a.window >= 0 ? c - a.window : 0;
     const float sc = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, seen = -INFINITY;  // seen: the row's maximum so far
+    auto move_to = [&](float m2, bool rescale) {     // the row's sums relative to m2
+      const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
+      m = m2;
+      l *= keep;
+      if (!rescale) return;
+#pragma unroll 1
+      for (int e = 0; e < Sh::kD / 32; ++e) {
+        uint32_t o[16];
+        tm_ld16(o, t_o + 16 * e);
+        wait_ld(o);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+        tm_st16(t_o + 16 * e, o);
+      }
+    };
     bool ok = true;
-    for (int t = t0; t < t1 && ok; ++t) {
-      ok = warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
-      if (!ok) break;
+    for (int t = t0; t < t1; ++t) {
+      ok &= warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
       fence_after();
-      uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
-      tm_ld32(x[0], t_s + 64 * hf);
-      tm_ld32(x[1], t_s + 64 * hf + 32);
-      wait_ld();
-      if (!tile_full(a, tl, t, it.kv, cmin, cmax)) {
-        uint32_t see[2];  // columns the row sees
+      uint32_t see[2] = {~0u, ~0u};  // columns the row sees
+      const bool masked = !tile_full(a, tl, t, it.kv, cmin, cmax);
+      if (masked) {
         const int p0 = tl.first(t);
         if (!tl.gaps()) {
           const int hi = min(seen_end - p0, tl.count(t)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) see[w] = low_bits(hi - 32 * w) & ~low_bits(lo - 32 * w);
+          for (int e = 0; e < 2; ++e) see[e] = low_bits(hi - 32 * e) & ~low_bits(lo - 32 * e);
         } else {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            see[w] = 0;
+          for (int e = 0; e < 2; ++e) {
+            see[e] = 0;
 #pragma unroll 1
             for (int b = 0; b < 32; ++b) {
-              const int at = tl.place(t, 64 * hf + 32 * w + b);
-              if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[w] |= 1u << b;
+              const int at = tl.place(t, 64 * hf + 32 * e + b);
+              if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[e] |= 1u << b;
             }
           }
         }
-#pragma unroll
-        for (int e = 0; e < 64; ++e) hide_unless(x[e >> 5][e & 31], see[e >> 5] & (1u << (e & 31)));
       }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      // m follows what the earlier tiles held
+      if (__any_sync(~0u, m != -INFINITY && (seen - m) * sc > kGrow)) move_to((seen - m) * sc > kGrow ? seen : m, true);
+      uint32_t w[2][16];
+      uint64_t sum[2];
+      for (bool settled = false;; settled = true) {
+        uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const float off = m == -INFINITY ? 0.f : -m * sc;
+        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+        sum[0] = sum[1] = 0;
+        tm_ld32(x[0], t_s + 64 * hf);
+        wait_ld(x[0]);
+        tm_ld32(x[1], t_s + 64 * hf + 32);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) top[e & 3] = max3(top[e & 3], x[0][e], x[1][e]);
-      float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      mx = fmaxf(mx, swap(mx));  // both have read their scores: weights may go over them
-      const bool grow = mx > m && (m == -INFINITY || (mx - m) * sc > kGrow);
-      if (__any_sync(~0u, grow)) {
-        const float m2 = grow ? mx : m;
-        const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
-        m = m2;
-        l *= keep;
-        if (t > t0) {
-#pragma unroll 1
-          for (int e = 0; e < Sh::kD / 32; ++e) {
-            uint32_t o[16];
-            tm_ld16(o, t_o + 16 * e);
-            wait_ld();
+        for (int e = 0; e < 2; ++e) {
+          if (e) wait_ld(x[1]);
+          if (masked) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-            tm_st16(t_o + 16 * e, o);
+            for (int u = 0; u < 32; ++u) hide_unless(x[e][u], see[e] & (1u << u));
+          }
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            top[u & 3] = max3(top[u & 3], x[e][2 * u], x[e][2 * u + 1]);
+            float y0, y1;
+            unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y0, y1);
+            y0 = exp2_fast(y0);
+            y1 = exp2_fast(y1);
+            sum[u & 1] = add2(sum[u & 1], pair(y0, y1));
+            w[e][u] = pack_bf16x2(y0, y1);
           }
         }
-      }
-      const float off = m == -INFINITY ? 0.f : -m * sc;
-      const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t w[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          float y0, y1;
-          unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y0, y1);
-          y0 = exp2_fast(y0);
-          y1 = exp2_fast(y1);
-          sum[u & 1] = add2(sum[u & 1], pair(y0, y1));
-          w[u] = pack_bf16x2(y0, y1);
+        // both threads of the row have read their scores: weights may go over them
+        if (settled) {
+          meet();
+          break;
         }
-        tm_st16(t_s + 32 * hf + 16 * e, w);
+        seen = fmaxf(seen, swap_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+        const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kFar;
+        if (!__any_sync(~0u, far)) break;
+        move_to(far ? seen : m, t > t0);
       }
+      tm_st16(t_s + 32 * hf, w[0]);
+      tm_st16(t_s + 32 * hf + 16, w[1]);
       float y0, y1;
       unpair(add2(sum[0], sum[1]), y0, y1);
       l += y0 + y1;
@@ -455,16 +498,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) bar_arrive(p_full(i));
     }
     // ---- result of the row
-    if (ok && t0 < t1) {
-      ok = warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
+    if (t0 < t1) {
+      ok &= warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
       fence_after();
     }
-    if (ok) {
-      l += swap(l);
-    } else {  // the row's other warp may have come one exchange further: it must not wait
-      asm volatile("bar.arrive %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory");
-      set_status(a.b.status, DCP_ETIMEOUT);
-    }
+    sh.swap.sum[i][hf][r] = l;
+    meet();
+    l += sh.swap.sum[i][hf ^ 1][r];
+    if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
     const bool mine = r < rows_i;
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
@@ -475,7 +516,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t o[32];
       if (t0 < t1) {
         tm_ld32(o, t_o + 32 * e);
-        wait_ld();
+        wait_ld(o);
       } else {
 #pragma unroll
         for (int u = 0; u < 32; ++u) o[u] = 0;
@@ -528,47 +569,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == kSoftWarps + 1) {
+    if (warp == kSoftWarps + 1 || warp == kSoftWarps + 2) {
       // ---------------------------------------------------------------------------------- pages
+      const bool values = warp == kSoftWarps + 2;
+      const CUtensorMap* map = values ? &map_v : &map_k;
       const int n_pages = tl.subs == 1 ? tl.pages : 1;
       const uint32_t bytes = (uint32_t)tl.box * 128 * HALVES;
       const int last_page = it.kv > 0 ? (it.kv - 1) / tl.bs : -1;
       // pages some row of the item sees: these must name a block
       const int see_lo = a.window >= 0 ? max(0, c_lo - a.window) : 0, see_hi = a.causal ? min(it.kv, c_hi + 1) : it.kv;
+      auto entry = [&](int t) {  // this lane's page of tile t
+        const int pg = (tl.subs == 1 ? t * tl.pages : t / tl.subs) + lane;
+        if (t >= te || lane >= n_pages || pg > last_page) return 0;
+        const int blk = table[pg];
+        if (blk >= 0 && blk < a.pool.n_blocks) return blk;
+        if (pg * tl.bs < see_hi && (pg + 1) * tl.bs > see_lo) set_status(a.b.status, DCP_EDEVICE);
+        return (int)a.pool.n_blocks;  // outside the tensor map: zeros
+      };
       bool ok = true;
-      int n = 0;
-      for (int t = tb; t < te && ok; ++t) {
-        const int pg0 = tl.subs == 1 ? t * tl.pages : t / tl.subs;
+      int n = values, next = entry(tb);
+      for (int t = tb; t < te; ++t, n += 2) {
+        const int blk = next, slot = n % Sh::kSlots;
+        next = entry(t + 1);
         const int row = tl.subs == 1 ? 0 : t % tl.subs * kKeys;
-        const int here = min(n_pages, last_page + 1 - pg0);  // pages of the tile that the sequence has
-        int blk = 0;
-        if (lane < here) {
-          blk = table[pg0 + lane];
-          if (blk < 0 || blk >= a.pool.n_blocks) {
-            const int q0 = (pg0 + lane) * tl.bs;
-            if (q0 < see_hi && q0 + tl.bs > see_lo) set_status(a.b.status, DCP_EDEVICE);
-            blk = (int)a.pool.n_blocks;  // outside the tensor map: zeros
-          }
-        }
+        const int here = min(n_pages, last_page + 1 - (tl.subs == 1 ? t * tl.pages : t / tl.subs));
+        if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &sh.dead);
+        if (!ok) break;
+        if (lane == 0) bar_expect(full(slot), here * bytes);
+        __syncwarp();
+        const uint32_t dst = ring + slot * Sh::kTile, bar = full(slot);
+        for (int pg = 0; pg < here; ++pg) {
+          const int b = __shfl_sync(~0u, blk, pg);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int slot = n % Sh::kSlots;
-          if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &sh.dead);
-          if (!ok) break;
-          if (lane == 0) bar_expect(full(slot), here * bytes);
-          __syncwarp();
-          for (int pg = lane; pg < here; pg += 32) {
-            const uint32_t dst = ring + slot * Sh::kTile + pg * tl.box * 128;
-#pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf)
-              tma_page(dst + hf * Sh::kHalf, kv ? &map_v : &map_k, 64 * hf, row, it.kh, blk, full(slot));
-          }
-          __syncwarp();
+          for (int e = 0; e < HALVES; ++e)
+            tma_page(dst + pg * tl.box * 128 + e * Sh::kHalf, map, 64 * e, row, it.kh, b, bar);
         }
       }
       if (!ok) {  // copies in flight end by themselves: leave when they have
         const uint64_t start = now_ns();
-        for (int k = max(0, n - Sh::kSlots); k < n; ++k)
+        for (int k = max((int)values, n - 2 * Sh::kSlots); k < n; k += 2)
           while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && now_ns() - start < kPatience) {
           }
       }
@@ -649,7 +688,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // ---------------------------------------------------------------------------------- guard
       // It follows every fill of the ring (a wait can only tell a phase from the one before it), so a slot is free
       // once it has passed too.
-      const int me = threadIdx.x - 32 * (kSoftWarps + 2);
       int masked = 0;
       bool ok = true;
       for (int n = 0; n < 2 * (te - tb) && ok; ++n) {
@@ -660,7 +698,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int p0 = tl.first(t);
           uint8_t* v = gbase + (2 + slot) * Sh::kTile;
           bool found = false;
-          for (int u = me; u < kKeys * 8 * HALVES; u += 64) {
+          for (int u = lane; u < kKeys * 8 * HALVES; u += 32) {
             const int row = (u >> 3) & (kKeys - 1);
             uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
             const int place = tl.place(t, row);
