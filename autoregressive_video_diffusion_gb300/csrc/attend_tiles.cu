@@ -34,8 +34,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows after the tile,
 constexpr float kFar = 64.f;           // and before m follows at once
-constexpr int kSpins = 1 << 24;        // limits of every wait: tries, and nanoseconds
-constexpr uint64_t kPatience = 2000000000ull;
+constexpr long long kPatience = 4000000000ll;  // limit of every wait, in SM clocks (two seconds)
 
 struct Item {                          // what a CTA works on
   int s, kh, lo, len;                  // sequence, KV head, first row of q, new tokens
@@ -98,25 +97,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
-  const uint64_t start = now_ns();
-  for (int i = 0; i < kSpins; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if (*dead || now_ns() - start > kPatience) break;
-  }
-  *dead = 1;
-  return false;
-}
-// False once any wait of the CTA has run out (`dead`): every role then leaves its loop.
+// False once any wait of the CTA has run out (`dead`).  (The limit goes by the SM's clock: reading the global timer
+// between tries cost hundreds of cycles a wait.)
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-  for (int i = 0; i < 64; ++i)
-    if (bar_try(bar, parity)) return true;
-  return bar_wait_long(bar, parity, dead);
+  if (bar_try(bar, parity)) return true;
+  const long long start = clock64();
+  while (!bar_try(bar, parity)) {
+    if (*dead) return false;
+    if (clock64() - start > kPatience) {
+      *dead = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // The same for a whole warp: its lanes agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
@@ -269,7 +262,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Sh = Shape<HALVES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   struct Head {
-    uint64_t bars[2 * Sh::kSlots + kGuards + 6];
+    uint64_t bars[2 * Sh::kSlots + kGuards + 14];
     union {                   // what the two threads of a row tell each other
       __nv_bfloat16 top[2][2][2][kRows];
       float sum[2][2][kRows];
@@ -338,6 +331,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
   auto guarded = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
   auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + i); };
+  auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + 6 + i); };
   auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + 2 + i); };
   const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + kGuards + 4), finished = bars + 8 * (2 * Sh::kSlots + kGuards + 5);
   if (threadIdx.x == 0) {
@@ -350,6 +344,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bar_init(s_full(i), 1);
       bar_init(p_full(i), kSoftWarps / 2);
     }
+    for (int i = 0; i < 8; ++i) bar_init(pair_met(i), 2);
     bar_init(q_full, 32 * kSoftWarps);
     bar_init(finished, 1);
     sh.dead = 0;
@@ -388,17 +383,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_proxy_async_smem();
       bar_arrive(q_full);
     }
-    // The two threads of a row meet.  Both always meet equally often, even after a wait has run out: how often depends
-    // on nothing but the maxima they have exchanged (two buffers in turn, so neither can overwrite what the other has
-    // yet to read).
-    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory"); };
+    // The two threads of a row tell each other their maxima through two buffers in turn: neither can overwrite what the
+    // other has yet to read.  They are rounded to bf16 (m need only be near the maximum).
+    const uint32_t met = pair_met(i * 4 + (warp & 3));
     int swaps = 0;
-    auto swap_max = [&](float y) {  // of both threads' values, rounded to bf16: m need only be near the maximum
-      const __nv_bfloat16 z = __float2bfloat16_rn(y);
-      sh.swap.top[i][swaps & 1][hf][r] = z;
-      meet();
-      return fmaxf(__bfloat162float(z), __bfloat162float(sh.swap.top[i][swaps++ & 1][hf ^ 1][r]));
-    };
     const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
     const int c = it.kv - it.len + tok;
     const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
@@ -423,9 +411,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     };
     bool ok = true;
-    for (int t = t0; t < t1; ++t) {
-      ok &= warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
-      fence_after();
+    for (int t = t0; t < t1 && ok; ++t) {
       uint32_t see[2] = {~0u, ~0u};  // columns the row sees
       const bool masked = !tile_full(a, tl, t, it.kv, cmin, cmax);
       if (masked) {
@@ -447,48 +433,65 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       // m follows what the earlier tiles held
-      if (__any_sync(~0u, m != -INFINITY && (seen - m) * sc > kGrow)) move_to((seen - m) * sc > kGrow ? seen : m, true);
+      const bool grown = m != -INFINITY && (seen - m) * sc > kGrow, move = __any_sync(~0u, grown);
+      ok = warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
+      if (!ok) break;
+      fence_after();
+      if (move) move_to(grown ? seen : m, true);
       uint32_t w[2][16];
       uint64_t sum[2];
       for (bool settled = false;; settled = true) {
         uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const float off = m == -INFINITY ? 0.f : -m * sc;
         const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
         sum[0] = sum[1] = 0;
         tm_ld32(x[0], t_s + 64 * hf);
-        wait_ld(x[0]);
         tm_ld32(x[1], t_s + 64 * hf + 32);
+        wait_ld(x[0]);
+        wait_ld(x[1]);
+        if (masked) {
+#pragma unroll
+          for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
+        }
+        if (!settled) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int u = 0; u < 32; ++u) top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
+          const __nv_bfloat16 mine = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          sh.swap.top[i][swaps & 1][hf][r] = mine;
+          __syncwarp();
+          if (lane == 0) bar_arrive(met);
+          seen = fmaxf(seen, __bfloat162float(mine));
+        }
+        // in steps over a chunk of scores, so that the exponentials follow one another without waiting
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (e) wait_ld(x[1]);
-          if (masked) {
+          float y[32];
 #pragma unroll
-            for (int u = 0; u < 32; ++u) hide_unless(x[e][u], see[e] & (1u << u));
-          }
+          for (int u = 0; u < 16; ++u)
+            unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y[2 * u],
+                   y[2 * u + 1]);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) y[u] = exp2_fast(y[u]);
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            top[u & 3] = max3(top[u & 3], x[e][2 * u], x[e][2 * u + 1]);
-            float y0, y1;
-            unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y0, y1);
-            y0 = exp2_fast(y0);
-            y1 = exp2_fast(y1);
-            sum[u & 1] = add2(sum[u & 1], pair(y0, y1));
-            w[e][u] = pack_bf16x2(y0, y1);
+            sum[u & 1] = add2(sum[u & 1], pair(y[2 * u], y[2 * u + 1]));
+            w[e][u] = pack_bf16x2(y[2 * u], y[2 * u + 1]);
           }
         }
-        // both threads of the row have read their scores: weights may go over them
-        if (settled) {
-          meet();
-          break;
-        }
-        seen = fmaxf(seen, swap_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+        if (settled) break;
+        ok = warp_wait(met, swaps & 1, &sh.dead);
+        if (!ok) break;
+        seen = fmaxf(seen, __bfloat162float(sh.swap.top[i][swaps & 1][hf ^ 1][r]));
+        ++swaps;
         const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kFar;
         if (!__any_sync(~0u, far)) break;
         move_to(far ? seen : m, t > t0);
       }
-      tm_st16(t_s + 32 * hf, w[0]);
-      tm_st16(t_s + 32 * hf + 16, w[1]);
+      if (!ok) break;
+      // each half over its own scores
+      tm_st16(t_s + 64 * hf, w[0]);
+      tm_st16(t_s + 64 * hf + 16, w[1]);
       float y0, y1;
       unpair(add2(sum[0], sum[1]), y0, y1);
       l += y0 + y1;
@@ -498,13 +501,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) bar_arrive(p_full(i));
     }
     // ---- result of the row
-    if (t0 < t1) {
-      ok &= warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
+    if (ok && t0 < t1) {
+      ok = warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
       fence_after();
     }
-    sh.swap.sum[i][hf][r] = l;
-    meet();
-    l += sh.swap.sum[i][hf ^ 1][r];
+    if (ok) {
+      sh.swap.sum[i][hf][r] = l;
+      __syncwarp();
+      if (lane == 0) bar_arrive(met);
+      ok = warp_wait(met, swaps & 1, &sh.dead);
+      l += sh.swap.sum[i][hf ^ 1][r];
+    }
     if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
     const bool mine = r < rows_i;
     const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -606,9 +613,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!ok) {  // copies in flight end by themselves: leave when they have
-        const uint64_t start = now_ns();
+        const long long start = clock64();
         for (int k = max((int)values, n - 2 * Sh::kSlots); k < n; k += 2)
-          while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && now_ns() - start < kPatience) {
+          while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && clock64() - start < kPatience) {
           }
       }
     } else if (warp == kSoftWarps) {
@@ -660,7 +667,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               const uint32_t v = desc_lo(ring + slot * Sh::kTile, Sh::kHalf);
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 8 * k, v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
+                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
                        t > t0 || k > 0);
               if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
             }
@@ -679,8 +686,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) {  // products in flight end by themselves: leave when they have
         mma_commit(finished);
-        const uint64_t start = now_ns();
-        while (!bar_try(finished, 0) && now_ns() - start < kPatience) {
+        const long long start = clock64();
+        while (!bar_try(finished, 0) && clock64() - start < kPatience) {
         }
         set_status(a.b.status, DCP_ETIMEOUT);
       }
