@@ -9,8 +9,8 @@
 // Each row tile has its own 8 warps, so one tile's softmax runs under the other's matrix products; a row is two threads'
 // work, half of its scores each, so that an SM quarter always has several warps to choose from.  The weights are taken
 // relative to the maximum of the earlier tiles: the tile's own maximum is found alongside, and only a row that has
-// outgrown m by 2^64 takes its weights again.  m follows at the next tile, and only when the maximum has grown by more
-// than 2^8, which leaves O untouched in almost every step; m has moved or not, the quotient O / l is the same (weights
+// outgrown m by 2^64 within one tile needs more care: its item is then done again with the tile's own maximum.  m
+// follows at the next tile, and only when the maximum has grown by more than 2^8, which leaves O untouched in almost every step; m has moved or not, the quotient O / l is the same (weights
 // keep their relative precision in bf16, sums are held in 32 bits).
 //
 // Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warp 16: issues the matrix products.  Warps 17, 18: copy the pages
@@ -32,8 +32,8 @@ constexpr int kTileThreads = 640;
 constexpr int kSoftWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
-constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows after the tile,
-constexpr float kFar = 64.f;           // and before m follows at once
+constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
+constexpr float kFar = 64.f;           // and within one tile before the item is done again
 constexpr long long kPatience = 4000000000ll;  // limit of every wait, in SM clocks (two seconds)
 
 struct Item {                          // what a CTA works on
@@ -50,6 +50,7 @@ struct Item {                          // what a CTA works on
 // pages are cut into `subs` tiles.
 struct Tiling {
   int bs, box, pages, subs;
+  bool whole;                          // every tile is 128 consecutive positions, tile t from 128 t on
   __device__ __forceinline__ int tile_of(int pos) const {
     return subs == 1 ? pos / (pages * bs) : pos / bs * subs + pos % bs / kKeys;
   }
@@ -248,12 +249,32 @@ __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, in
   return pos < kv && (!a.causal || pos <= c) && (a.window < 0 || pos >= c - a.window);
 }
 
-// Whether every row of positions c_lo .. c_hi sees every key of tile t.
-__device__ __forceinline__ bool tile_full(const AttendParams& a, const Tiling& tl, int t, int kv, int c_lo, int c_hi) {
-  const int p0 = tl.first(t), p1 = p0 + tl.count(t);
-  return !tl.gaps() && tl.count(t) == kKeys && p1 <= kv && (!a.causal || p1 - 1 <= c_lo) &&
-         (a.window < 0 || p0 >= c_hi - a.window);
+// The key tiles [x, y) of which every row at cache positions c_lo .. c_hi sees every key.
+__device__ __forceinline__ int2 open_tiles(const AttendParams& a, const Tiling& tl, int kv, int c_lo, int c_hi) {
+  if (!tl.whole) return make_int2(0, 0);
+  const int end = a.causal ? min(kv, c_lo + 1) : kv, begin = a.window >= 0 ? max(0, c_hi - a.window) : 0;
+  return make_int2((begin + kKeys - 1) / kKeys, max(end, 0) / kKeys);
 }
+__device__ __forceinline__ bool within(int2 range, int t) { return t >= range.x && t < range.y; }
+
+// A place in the ring and the parity of its fill.
+template <int SLOTS>
+struct Ring {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ void step() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void back() {
+    if (slot-- == 0) {
+      slot = SLOTS - 1;
+      phase ^= 1;
+    }
+  }
+};
 
 template <int HALVES>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -268,7 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float sum[2][2][kRows];
     } swap;
     uint32_t tmem;
-    int dead, poison, last;
+    int dead, poison, last, far;
   };
   static_assert(sizeof(Head) <= Sh::kHead, "the head fits before the tiles");
   Head& sh = *reinterpret_cast<Head*>(smem_raw);
@@ -320,6 +341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : act0 ? it.t1[0] : tb;
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
 
+  const int2 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
   const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
 
   // ---- set-up
@@ -349,6 +371,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bar_init(finished, 1);
     sh.dead = 0;
     sh.poison = 0;
+    sh.far = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kSoftWarps) {
@@ -386,14 +409,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // The two threads of a row tell each other their maxima through two buffers in turn: neither can overwrite what the
     // other has yet to read.  They are rounded to bf16 (m need only be near the maximum).
     const uint32_t met = pair_met(i * 4 + (warp & 3));
-    int swaps = 0;
     const int R = it.row0 + i * kRows + r, tok = R / a.G, g = R - tok * a.G;
     const int c = it.kv - it.len + tok;
     const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
     const int cmin = i ? it.c0[1] : it.c0[0], cmax = i ? it.c1[1] : it.c1[0];
-    const int seen_end = a.causal ? min(it.kv, c + 1) : it.kv;
-    const int seen_begin = a.window >= 0 ? c - a.window : 0;
+    const bool mine = r < rows_i;  // rows past the sequence's take part unmasked, and nothing of theirs is kept
+    const int seen_end = a.causal && mine ? min(it.kv, c + 1) : it.kv;
+    const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
     const float sc = p.scale_log2;
+    const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
     float m = -INFINITY, l = 0.f, seen = -INFINITY;  // seen: the row's maximum so far
     auto move_to = [&](float m2, bool rescale) {     // the row's sums relative to m2
       const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
@@ -410,101 +434,125 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tm_st16(t_o + 16 * e, o);
       }
     };
-    bool ok = true;
-    for (int t = t0; t < t1 && ok; ++t) {
-      uint32_t see[2] = {~0u, ~0u};  // columns the row sees
-      const bool masked = !tile_full(a, tl, t, it.kv, cmin, cmax);
-      if (masked) {
-        const int p0 = tl.first(t);
-        if (!tl.gaps()) {
-          const int hi = min(seen_end - p0, tl.count(t)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
+    uint32_t scored = 0, swaps = 0;  // parities: score tiles received, exchanges received
+    bool ok = true, pending = false;
+    auto hear = [&] {  // the other thread's maximum of the last exchange
+      ok = warp_wait(met, swaps & 1, &sh.dead);
+      seen = fmaxf(seen, __bfloat162float(sh.swap.top[i][swaps & 1][hf ^ 1][r]));
+      ++swaps;
+      pending = false;
+    };
+    for (bool careful = false;; careful = true) {
+      for (int t = t0; t < t1 && ok; ++t) {
+        uint32_t see[2] = {~0u, ~0u};  // columns the row sees
+        const bool masked = !within(mine_open, t);
+        if (masked) {
+          const int p0 = tl.first(t);
+          if (!tl.gaps()) {
+            const int hi = min(seen_end - p0, tl.count(t)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) see[e] = low_bits(hi - 32 * e) & ~low_bits(lo - 32 * e);
-        } else {
+            for (int e = 0; e < 2; ++e) see[e] = low_bits(hi - 32 * e) & ~low_bits(lo - 32 * e);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            see[e] = 0;
+            for (int e = 0; e < 2; ++e) {
+              see[e] = 0;
 #pragma unroll 1
-            for (int b = 0; b < 32; ++b) {
-              const int at = tl.place(t, 64 * hf + 32 * e + b);
-              if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[e] |= 1u << b;
+              for (int b = 0; b < 32; ++b) {
+                const int at = tl.place(t, 64 * hf + 32 * e + b);
+                if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[e] |= 1u << b;
+              }
             }
           }
         }
-      }
-      // m follows what the earlier tiles held
-      const bool grown = m != -INFINITY && (seen - m) * sc > kGrow, move = __any_sync(~0u, grown);
-      ok = warp_wait(s_full(i), (t - t0) & 1, &sh.dead);
-      if (!ok) break;
-      fence_after();
-      if (move) move_to(grown ? seen : m, true);
-      uint32_t w[2][16];
-      uint64_t sum[2];
-      for (bool settled = false;; settled = true) {
-        uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
-        const float off = m == -INFINITY ? 0.f : -m * sc;
-        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-        sum[0] = sum[1] = 0;
-        tm_ld32(x[0], t_s + 64 * hf);
-        tm_ld32(x[1], t_s + 64 * hf + 32);
-        wait_ld(x[0]);
-        wait_ld(x[1]);
-        if (masked) {
-#pragma unroll
-          for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
-        }
-        if (!settled) {
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int u = 0; u < 32; ++u) top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
-          const __nv_bfloat16 mine = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-          sh.swap.top[i][swaps & 1][hf][r] = mine;
-          __syncwarp();
-          if (lane == 0) bar_arrive(met);
-          seen = fmaxf(seen, __bfloat162float(mine));
-        }
-        // in steps over a chunk of scores, so that the exponentials follow one another without waiting
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y[32];
-#pragma unroll
-          for (int u = 0; u < 16; ++u)
-            unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y[2 * u],
-                   y[2 * u + 1]);
-#pragma unroll
-          for (int u = 0; u < 32; ++u) y[u] = exp2_fast(y[u]);
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            sum[u & 1] = add2(sum[u & 1], pair(y[2 * u], y[2 * u + 1]));
-            w[e][u] = pack_bf16x2(y[2 * u], y[2 * u + 1]);
-          }
-        }
-        if (settled) break;
-        ok = warp_wait(met, swaps & 1, &sh.dead);
+        // m follows what the earlier tiles held
+        if (pending) hear();
+        // before a row has seen a key there is no maximum to go by: the tile's own, of both threads, comes first
+        const bool exact = careful || __any_sync(~0u, seen == -INFINITY);
+        const bool grown = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow, move = __any_sync(~0u, grown);
+        ok = ok && warp_wait(s_full(i), scored & 1, &sh.dead);
         if (!ok) break;
-        seen = fmaxf(seen, __bfloat162float(sh.swap.top[i][swaps & 1][hf ^ 1][r]));
-        ++swaps;
-        const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kFar;
-        if (!__any_sync(~0u, far)) break;
-        move_to(far ? seen : m, t > t0);
+        ++scored;
+        fence_after();
+        if (move) move_to(grown ? seen : m, t > t0);
+        uint32_t w[2][16];
+        uint64_t sum[2];
+        for (bool settled = false;; settled = true) {
+          uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
+          const float off = m == -INFINITY ? 0.f : -m * sc;
+          const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+          sum[0] = sum[1] = 0;
+          tm_ld32(x[0], t_s + 64 * hf);
+          tm_ld32(x[1], t_s + 64 * hf + 32);
+          wait_ld(x[0]);
+          wait_ld(x[1]);
+          if (masked) {
+#pragma unroll
+            for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
+          }
+          if (!settled) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
+            const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            sh.swap.top[i][swaps & 1][hf][r] = own;
+            __syncwarp();
+            if (lane == 0) bar_arrive(met);
+            pending = true;
+            seen = fmaxf(seen, __bfloat162float(own));
+          }
+          // in steps over a chunk of scores, so that the exponentials follow one another without waiting
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y[32];
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y[2 * u],
+                     y[2 * u + 1]);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) y[u] = exp2_fast(y[u]);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              sum[u & 1] = add2(sum[u & 1], pair(y[2 * u], y[2 * u + 1]));
+              w[e][u] = pack_bf16x2(y[2 * u], y[2 * u + 1]);
+            }
+          }
+          if (settled) break;
+          if (!exact) {
+            if ((seen - m) * sc > kFar) sh.far = 1;
+            break;
+          }
+          hear();
+          const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
+          if (!ok || !__any_sync(~0u, far)) break;
+          move_to(far ? seen : m, t > t0);
+        }
+        if (!ok) break;
+        // each half over its own scores
+        tm_st16(t_s + 64 * hf, w[0]);
+        tm_st16(t_s + 64 * hf + 16, w[1]);
+        float y0, y1;
+        unpair(add2(sum[0], sum[1]), y0, y1);
+        l += y0 + y1;
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full(i));
       }
-      if (!ok) break;
-      // each half over its own scores
-      tm_st16(t_s + 64 * hf, w[0]);
-      tm_st16(t_s + 64 * hf + 16, w[1]);
-      float y0, y1;
-      unpair(add2(sum[0], sum[1]), y0, y1);
-      l += y0 + y1;
-      wait_st();
+      if (ok && t0 < t1) {  // the last product
+        ok = warp_wait(s_full(i), scored & 1, &sh.dead);
+        ++scored;
+        fence_after();
+      }
+      if (ok && pending) hear();
       fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(p_full(i));
+      __syncthreads();
+      fence_after();
+      if (careful || !sh.far) break;
+      m = seen = -INFINITY;
+      l = 0.f;
     }
     // ---- result of the row
-    if (ok && t0 < t1) {
-      ok = warp_wait(s_full(i), (t1 - t0) & 1, &sh.dead);
-      fence_after();
-    }
     if (ok) {
       sh.swap.sum[i][hf][r] = l;
       __syncwarp();
@@ -513,7 +561,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       l += sh.swap.sum[i][hf ^ 1][r];
     }
     if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
-    const bool mine = r < rows_i;
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
     float* part = part_of(p.part, item, p.splits, split, 2 * kRows, D, i * kRows + r);
@@ -530,7 +577,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (sh.poison && mine) {  // infinities and NaN this row sees in the guarded tiles
         for (int t = t0; t < t1; ++t) {
-          if (tile_full(a, tl, t, it.kv, c_lo, c_hi)) continue;
+          if (within(open, t)) continue;
           for (int col = 0; col < kKeys; ++col) {
             const int at = tl.place(t, col), pos = tl.first(t) + at;
             if (at < 0 || !visible(a, it.kv, c, pos)) continue;
@@ -594,39 +641,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return (int)a.pool.n_blocks;  // outside the tensor map: zeros
       };
       bool ok = true;
-      int n = values, next = entry(tb);
-      for (int t = tb; t < te; ++t, n += 2) {
-        const int blk = next, slot = n % Sh::kSlots;
-        next = entry(t + 1);
-        const int row = tl.subs == 1 ? 0 : t % tl.subs * kKeys;
-        const int here = min(n_pages, last_page + 1 - (tl.subs == 1 ? t * tl.pages : t / tl.subs));
-        if (n >= Sh::kSlots) ok = warp_wait(empty(slot), (n / Sh::kSlots - 1) & 1, &sh.dead);
-        if (!ok) break;
-        if (lane == 0) bar_expect(full(slot), here * bytes);
-        __syncwarp();
-        const uint32_t dst = ring + slot * Sh::kTile, bar = full(slot);
-        for (int pg = 0; pg < here; ++pg) {
-          const int b = __shfl_sync(~0u, blk, pg);
+      Ring<Sh::kSlots> at{values, 0};
+      int issued = 0;
+      for (bool careful = false;; careful = true) {
+        int next = entry(tb);
+        for (int t = tb; t < te && ok; ++t) {
+          const int blk = next;
+          next = entry(t + 1);
+          const int row = tl.subs == 1 ? 0 : t % tl.subs * kKeys;
+          const int here = min(n_pages, last_page + 1 - (tl.subs == 1 ? t * tl.pages : t / tl.subs));
+          ok = warp_wait(empty(at.slot), at.phase ^ 1, &sh.dead);  // at once in the first round
+          if (!ok) break;
+          const uint32_t dst = ring + at.slot * Sh::kTile, bar = full(at.slot);
+          if (lane == 0) bar_expect(bar, here * bytes);
+          __syncwarp();
+          for (int pg = 0; pg < here; ++pg) {
+            const int b = __shfl_sync(~0u, blk, pg);
 #pragma unroll
-          for (int e = 0; e < HALVES; ++e)
-            tma_page(dst + pg * tl.box * 128 + e * Sh::kHalf, map, 64 * e, row, it.kh, b, bar);
-        }
-      }
-      if (!ok) {  // copies in flight end by themselves: leave when they have
-        const long long start = clock64();
-        for (int k = max((int)values, n - 2 * Sh::kSlots); k < n; k += 2)
-          while (!bar_try(full(k % Sh::kSlots), (k / Sh::kSlots) & 1) && clock64() - start < kPatience) {
+            for (int e = 0; e < HALVES; ++e)
+              tma_page(dst + pg * tl.box * 128 + e * Sh::kHalf, map, 64 * e, row, it.kh, b, bar);
           }
+          at.step();
+          at.step();
+          ++issued;
+        }
+        if (!ok) {  // copies in flight end by themselves: leave when they have
+          const long long start = clock64();
+          for (int k = 0; k < (Sh::kSlots + 1) / 2 && k < issued; ++k) {
+            at.back();
+            at.back();
+            while (!bar_try(full(at.slot), at.phase) && clock64() - start < kPatience) {
+            }
+          }
+          issued = 0;
+        }
+        __syncthreads();
+        if (careful || !sh.far) break;
       }
     } else if (warp == kSoftWarps) {
       // ---------------------------------------------------------------------------------- matrix products
       bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
-      int masked = 0;
-      int seen[2] = {0, 0};
-      fence_after();
-      auto scores = [&](int i, int t) {  // S_i of tile t
-        const int slot = 2 * (t - tb) % Sh::kSlots;
-        const uint32_t q = desc_lo(q_smem + i * Sh::kTile, 16), k = desc_lo(ring + slot * Sh::kTile, 16);
+      uint32_t masked = 0, weighed[2] = {0, 0};
+      Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
+      auto scores = [&](int i) {  // S_i of the keys at `at`
+        const uint32_t q = desc_lo(q_smem + i * Sh::kTile, 16), k = desc_lo(ring + at.slot * Sh::kTile, 16);
 #pragma unroll
         for (int e = 0; e < 4 * HALVES; ++e) {
           const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
@@ -634,109 +692,121 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         mma_commit(s_full(i));
       };
-      auto key_wait = [&](int t) {
-        const int n = 2 * (t - tb);
-        ok = ok && warp_wait(full(n % Sh::kSlots), (n / Sh::kSlots) & 1, &sh.dead);
-        fence_after();
-      };
       auto active = [&](int i, int t) {
         return i ? t >= it.t0[1] && t < it.t1[1] : t >= it.t0[0] && t < it.t1[0];
       };
-      if (ok && tb < te) {
-        key_wait(tb);
-        for (int i = 0; i < 2 && ok; ++i)
-          if (active(i, tb)) scores(i, tb);
-        mma_commit(empty(0));
-      }
-      for (int t = tb; t < te && ok; ++t) {
-        const int n = 2 * (t - tb) + 1, slot = n % Sh::kSlots;
-        if (!tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
-          ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &sh.dead);
-          ++masked;
+      for (bool careful = false;; careful = true) {
+        if (ok && tb < te) {
+          ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+          fence_after();
+          for (int i = 0; i < 2 && ok; ++i)
+            if (active(i, tb)) scores(i);
+          mma_commit(empty(at.slot));
+          at.step();
         }
-        ok = ok && warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
-        bool have_keys = false;
+        for (int t = tb; t < te && ok; ++t) {
+          const uint32_t v = desc_lo(ring + at.slot * Sh::kTile, Sh::kHalf), v_empty = empty(at.slot);
+          if (!within(open, t)) {
+            ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &sh.dead);
+            ++masked;
+          }
+          ok = ok && warp_wait(full(at.slot), at.phase, &sh.dead);
+          at.step();
+          bool keys = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
-          if (ok && active(i, t)) {
-            ok = warp_wait(p_full(i), seen[i] & 1, &sh.dead);
-            ++seen[i];
-            fence_after();
-            if (ok) {
-              const uint32_t v = desc_lo(ring + slot * Sh::kTile, Sh::kHalf);
+          for (int i = 0; i < 2; ++i) {
+            const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
+            if (ok && active(i, t)) {
+              ok = warp_wait(p_full(i), weighed[i] & 1, &sh.dead);
+              ++weighed[i];
+              fence_after();
+              if (ok) {
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
-                       t > t0 || k > 0);
-              if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4),
+                         kDescHi, p.idesc_pv, t > t0 || k > 0);
+                if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
+              }
+            }
+            if (ok && t + 1 < te && active(i, t + 1)) {
+              if (!keys) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+              fence_after();
+              keys = true;
+              if (ok) scores(i);
             }
           }
-          if (ok && t + 1 < te && active(i, t + 1)) {
-            if (!have_keys) key_wait(t + 1);
-            have_keys = true;
-            if (ok) scores(i, t + 1);
+          if (ok && t + 1 < te && !keys) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+          if (ok) {
+            mma_commit(v_empty);
+            if (t + 1 < te) {
+              mma_commit(empty(at.slot));
+              at.step();
+            }
           }
         }
-        if (ok && t + 1 < te && !have_keys) key_wait(t + 1);
-        if (ok) {
-          mma_commit(empty(slot));
-          if (t + 1 < te) mma_commit(empty((n + 1) % Sh::kSlots));
+        if (!ok) {  // products in flight end by themselves: leave when they have
+          mma_commit(finished);
+          const long long start = clock64();
+          while (!bar_try(finished, 0) && clock64() - start < kPatience) {
+          }
+          set_status(a.b.status, DCP_ETIMEOUT);
         }
-      }
-      if (!ok) {  // products in flight end by themselves: leave when they have
-        mma_commit(finished);
-        const long long start = clock64();
-        while (!bar_try(finished, 0) && clock64() - start < kPatience) {
-        }
-        set_status(a.b.status, DCP_ETIMEOUT);
+        fence_before();
+        __syncthreads();
+        fence_after();
+        if (careful || !sh.far) break;
       }
     } else {
       // ---------------------------------------------------------------------------------- guard
       // It follows every fill of the ring (a wait can only tell a phase from the one before it), so a slot is free
       // once it has passed too.
-      int masked = 0;
+      uint32_t masked = 0;
       bool ok = true;
-      for (int n = 0; n < 2 * (te - tb) && ok; ++n) {
-        const int t = tb + (n >> 1), slot = n % Sh::kSlots;
-        ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
-        if (!ok) break;
-        if ((n & 1) && !tile_full(a, tl, t, it.kv, c_lo, c_hi)) {
-          const int p0 = tl.first(t);
-          uint8_t* v = gbase + (2 + slot) * Sh::kTile;
-          bool found = false;
-          for (int u = lane; u < kKeys * 8 * HALVES; u += 32) {
-            const int row = (u >> 3) & (kKeys - 1);
-            uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
-            const int place = tl.place(t, row);
-            if (place < 0 || p0 + place >= it.kv) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *at;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool bad = false;
+      Ring<Sh::kSlots> at{0, 0};
+      for (bool careful = false;; careful = true) {
+        for (int n = 0; n < 2 * (te - tb) && ok; ++n, at.step()) {
+          const int t = tb + (n >> 1), slot = at.slot;
+          ok = warp_wait(full(slot), at.phase, &sh.dead);
+          if (!ok) break;
+          if ((n & 1) && !within(open, t)) {
+            const int p0 = tl.first(t);
+            uint8_t* v = gbase + (2 + slot) * Sh::kTile;
+            bool found = false;
+            for (int u = lane; u < kKeys * 8 * HALVES; u += 32) {
+              const int row = (u >> 3) & (kKeys - 1);
+              uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
+              const int place = tl.place(t, row);
+              if (place < 0 || p0 + place >= it.kv) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 x = *at;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              bool bad = false;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              if ((w[b] & 0x7F80u) == 0x7F80u) {
-                w[b] &= 0xFFFF0000u;
-                bad = true;
+              for (int b = 0; b < 4; ++b) {
+                if ((w[b] & 0x7F80u) == 0x7F80u) {
+                  w[b] &= 0xFFFF0000u;
+                  bad = true;
+                }
+                if ((w[b] & 0x7F800000u) == 0x7F800000u) {
+                  w[b] &= 0xFFFFu;
+                  bad = true;
+                }
               }
-              if ((w[b] & 0x7F800000u) == 0x7F800000u) {
-                w[b] &= 0xFFFFu;
-                bad = true;
-              }
+              if (bad) *at = x;
+              found |= bad;
             }
-            if (bad) *at = x;
-            found |= bad;
+            if (found) sh.poison = 1;
+            fence_proxy_async_smem();
+            bar_arrive(guarded(masked % kGuards));
+            ++masked;
           }
-          if (found) sh.poison = 1;
-          fence_proxy_async_smem();
-          bar_arrive(guarded(masked % kGuards));
-          ++masked;
+          __syncwarp();
+          if (lane == 0) bar_arrive(empty(slot));
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(empty(slot));
+        __syncthreads();
+        if (careful || !sh.far) break;
       }
     }
     __syncwarp();
@@ -832,6 +902,7 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
   p.tl.pages = kKeys / p.tl.box;
   p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
+  p.tl.whole = bs % kKeys == 0 || (p.tl.box == bs && p.tl.pages * bs == kKeys);
   p.splits = t.splits;
   p.q_tiles = t.q_tiles;
   // a scale below 0 negates the products (the running maximum then is of what is exponentiated); one near 0 is held
