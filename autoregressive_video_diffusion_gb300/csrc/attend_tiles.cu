@@ -13,11 +13,13 @@
 // follows at the next tile, and only when the maximum has grown by more than 2^8, which leaves O untouched in almost every step; m has moved or not, the quotient O / l is the same (weights
 // keep their relative precision in bf16, sums are held in 32 bits).
 //
-// Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warp 16: issues the matrix products.  Warps 17, 18: copy the pages
-// of the keys and of the values with TMA (a page of block_size positions is a box; 128-byte swizzle).  Warp 19: the
-// guard.  A weight of 0 times a value of infinity or NaN is NaN, so in the tiles where some row must not see some key,
-// the guard puts zeros for rows past the sequence (page rows never written hold anything) and for infinities and NaN;
-// rows that do see those get them back in the epilogue, from the cache.
+// Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warps 16, 17: issue the matrix products of row tile 0 and 1 (one
+// warp for both was busy for 3600 clocks a step of 2048 clocks of products).  Warps 18, 19: copy the pages of the keys
+// and of the values with TMA (a page of block_size positions is a box; 128-byte swizzle).
+//
+// A weight of 0 times a value of infinity or NaN is NaN.  So in the tiles where some row must not see some key, the
+// softmax warps put zeros for rows past the sequence (page rows never written hold anything) and for infinities and
+// NaN before they hand over their weights; rows that do see those get them back in the epilogue, from the cache.
 #include <cuda.h>
 
 #include "attend_join.cuh"
@@ -31,7 +33,6 @@ constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileThreads = 640;
 constexpr int kSoftWarps = 16;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kGuards = 8;              // guarded value tiles ahead of the products: at most half the ring
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
 constexpr float kFar = 64.f;           // and within one tile before the item is done again
 constexpr long long kPatience = 4000000000ll;  // limit of every wait, in SM clocks (two seconds)
@@ -245,6 +246,16 @@ struct Shape {
   static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
 };
 
+// Two bf16: whether one is an infinity or NaN, and with 0 in such a place.
+__device__ __forceinline__ bool any_special(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t no_special(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+  return w;
+}
+
 __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, int pos) {
   return pos < kv && (!a.causal || pos <= c) && (a.window < 0 || pos >= c - a.window);
 }
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Sh = Shape<HALVES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   struct Head {
-    uint64_t bars[2 * Sh::kSlots + kGuards + 14];
+    uint64_t bars[2 * Sh::kSlots + 15];
     union {                   // what the two threads of a row tell each other
       __nv_bfloat16 top[2][2][2][kRows];
       float sum[2][2][kRows];
@@ -351,24 +362,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t bars = smem_u32(sh.bars);
   auto full = [&](int i) { return bars + 8 * i; };
   auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
-  auto guarded = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
-  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + i); };
-  auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + 6 + i); };
-  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + kGuards + 2 + i); };
-  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + kGuards + 4), finished = bars + 8 * (2 * Sh::kSlots + kGuards + 5);
+  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
+  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 2 + i); };
+  auto finished = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
+  auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
+  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 14);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       bar_init(full(i), 1);
-      bar_init(empty(i), 2);  // the matrix products' commit, and the guard
+      bar_init(empty(i), 2);  // the products of both row tiles
     }
-    for (int i = 0; i < kGuards; ++i) bar_init(guarded(i), 32);
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
       bar_init(p_full(i), kSoftWarps / 2);
+      bar_init(finished(i), 1);
     }
     for (int i = 0; i < 8; ++i) bar_init(pair_met(i), 2);
     bar_init(q_full, 32 * kSoftWarps);
-    bar_init(finished, 1);
     sh.dead = 0;
     sh.poison = 0;
     sh.far = 0;
@@ -534,6 +544,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float y0, y1;
         unpair(add2(sum[0], sum[1]), y0, y1);
         l += y0 + y1;
+        if (masked) {  // guard the values: see the top of the file
+          const int n = 2 * (t - tb + (careful ? te - tb : 0)) + 1, slot = n % Sh::kSlots;
+          ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
+          if (!ok) break;
+          uint8_t* v = gbase + (2 + slot) * Sh::kTile;
+          bool found = false;
+          for (int u = threadIdx.x & 255; u < kKeys * 8 * HALVES; u += 256) {
+            const int row = (u >> 3) & (kKeys - 1), place = tl.place(t, row);
+            uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
+            if (place < 0 || tl.first(t) + place >= it.kv) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 y = *at;
+            if (any_special(y.x) | any_special(y.y) | any_special(y.z) | any_special(y.w)) {
+              *at = make_uint4(no_special(y.x), no_special(y.y), no_special(y.z), no_special(y.w));
+              found = true;
+            }
+          }
+          if (found) sh.poison = 1;
+          fence_proxy_async_smem();
+        }
         wait_st();
         fence_before();
         __syncwarp();
@@ -623,9 +655,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == kSoftWarps + 1 || warp == kSoftWarps + 2) {
+    if (warp >= kSoftWarps + 2) {
       // ---------------------------------------------------------------------------------- pages
-      const bool values = warp == kSoftWarps + 2;
+      const bool values = warp == kSoftWarps + 3;
       const CUtensorMap* map = values ? &map_v : &map_k;
       const int n_pages = tl.subs == 1 ? tl.pages : 1;
       const uint32_t bytes = (uint32_t)tl.box * 128 * HALVES;
@@ -678,134 +710,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncthreads();
         if (careful || !sh.far) break;
       }
-    } else if (warp == kSoftWarps) {
+    } else {
       // ---------------------------------------------------------------------------------- matrix products
+      const int i = warp - kSoftWarps;
+      const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
+      const uint32_t t_s = tmem + i * kKeys, t_o = tmem + 256 + i * 128, q = desc_lo(q_smem + i * Sh::kTile, 16);
       bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
-      uint32_t masked = 0, weighed[2] = {0, 0};
+      uint32_t weighed = 0;
       Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
-      auto scores = [&](int i) {  // S_i of the keys at `at`
-        const uint32_t q = desc_lo(q_smem + i * Sh::kTile, 16), k = desc_lo(ring + at.slot * Sh::kTile, 16);
+      auto scores = [&](int t) {
+        ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+        if (!ok) return;
+        fence_after();
+        if (t >= t0 && t < t1) {
+          const uint32_t k = desc_lo(ring + at.slot * Sh::kTile, 16);
 #pragma unroll
-        for (int e = 0; e < 4 * HALVES; ++e) {
-          const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
-          mma_ss(tmem + i * kKeys, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
+          for (int e = 0; e < 4 * HALVES; ++e) {
+            const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
+            mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
+          }
+          mma_commit(s_full(i));
         }
-        mma_commit(s_full(i));
-      };
-      auto active = [&](int i, int t) {
-        return i ? t >= it.t0[1] && t < it.t1[1] : t >= it.t0[0] && t < it.t1[0];
       };
       for (bool careful = false;; careful = true) {
         if (ok && tb < te) {
-          ok = warp_wait(full(at.slot), at.phase, &sh.dead);
-          fence_after();
-          for (int i = 0; i < 2 && ok; ++i)
-            if (active(i, tb)) scores(i);
+          scores(tb);
           mma_commit(empty(at.slot));
           at.step();
         }
         for (int t = tb; t < te && ok; ++t) {
           const uint32_t v = desc_lo(ring + at.slot * Sh::kTile, Sh::kHalf), v_empty = empty(at.slot);
-          if (!within(open, t)) {
-            ok = warp_wait(guarded(masked % kGuards), (masked / kGuards) & 1, &sh.dead);
-            ++masked;
-          }
-          ok = ok && warp_wait(full(at.slot), at.phase, &sh.dead);
+          ok = warp_wait(full(at.slot), at.phase, &sh.dead);
           at.step();
-          bool keys = false;
+          if (t >= t0 && t < t1) {
+            ok = ok && warp_wait(p_full(i), weighed & 1, &sh.dead);
+            if (!ok) break;
+            ++weighed;
+            fence_after();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
-            if (ok && active(i, t)) {
-              ok = warp_wait(p_full(i), weighed[i] & 1, &sh.dead);
-              ++weighed[i];
-              fence_after();
-              if (ok) {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_ts(tmem + 256 + i * 128, tmem + i * kKeys + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4),
-                         kDescHi, p.idesc_pv, t > t0 || k > 0);
-                if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
-              }
-            }
-            if (ok && t + 1 < te && active(i, t + 1)) {
-              if (!keys) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
-              fence_after();
-              keys = true;
-              if (ok) scores(i);
-            }
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(t_o, t_s + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
+                     t > t0 || k > 0);
+            if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
           }
-          if (ok && t + 1 < te && !keys) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
-          if (ok) {
+          if (!ok) break;
+          if (t + 1 < te) {
+            scores(t + 1);
+            if (!ok) break;
             mma_commit(v_empty);
-            if (t + 1 < te) {
-              mma_commit(empty(at.slot));
-              at.step();
-            }
+            mma_commit(empty(at.slot));
+            at.step();
+          } else {
+            mma_commit(v_empty);
           }
         }
         if (!ok) {  // products in flight end by themselves: leave when they have
-          mma_commit(finished);
+          mma_commit(finished(i));
           const long long start = clock64();
-          while (!bar_try(finished, 0) && clock64() - start < kPatience) {
+          while (!bar_try(finished(i), 0) && clock64() - start < kPatience) {
           }
           set_status(a.b.status, DCP_ETIMEOUT);
         }
         fence_before();
         __syncthreads();
         fence_after();
-        if (careful || !sh.far) break;
-      }
-    } else {
-      // ---------------------------------------------------------------------------------- guard
-      // It follows every fill of the ring (a wait can only tell a phase from the one before it), so a slot is free
-      // once it has passed too.
-      uint32_t masked = 0;
-      bool ok = true;
-      Ring<Sh::kSlots> at{0, 0};
-      for (bool careful = false;; careful = true) {
-        for (int n = 0; n < 2 * (te - tb) && ok; ++n, at.step()) {
-          const int t = tb + (n >> 1), slot = at.slot;
-          ok = warp_wait(full(slot), at.phase, &sh.dead);
-          if (!ok) break;
-          if ((n & 1) && !within(open, t)) {
-            const int p0 = tl.first(t);
-            uint8_t* v = gbase + (2 + slot) * Sh::kTile;
-            bool found = false;
-            for (int u = lane; u < kKeys * 8 * HALVES; u += 32) {
-              const int row = (u >> 3) & (kKeys - 1);
-              uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
-              const int place = tl.place(t, row);
-              if (place < 0 || p0 + place >= it.kv) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 x = *at;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-              bool bad = false;
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                if ((w[b] & 0x7F80u) == 0x7F80u) {
-                  w[b] &= 0xFFFF0000u;
-                  bad = true;
-                }
-                if ((w[b] & 0x7F800000u) == 0x7F800000u) {
-                  w[b] &= 0xFFFFu;
-                  bad = true;
-                }
-              }
-              if (bad) *at = x;
-              found |= bad;
-            }
-            if (found) sh.poison = 1;
-            fence_proxy_async_smem();
-            bar_arrive(guarded(masked % kGuards));
-            ++masked;
-          }
-          __syncwarp();
-          if (lane == 0) bar_arrive(empty(slot));
-        }
-        __syncthreads();
         if (careful || !sh.far) break;
       }
     }
