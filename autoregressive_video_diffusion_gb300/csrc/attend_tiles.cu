@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using Sh = Shape<HALVES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   struct Head {
-    uint64_t bars[2 * Sh::kSlots + 15];
+    uint64_t bars[2 * Sh::kSlots + 17];
     union {                   // what the two threads of a row tell each other
       __nv_bfloat16 top[2][2][2][kRows];
       float sum[2][2][kRows];
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto finished = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
   auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
   const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 14);
+  auto turn = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 15 + i); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       bar_init(full(i), 1);
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bar_init(s_full(i), 1);
       bar_init(p_full(i), kSoftWarps / 2);
       bar_init(finished(i), 1);
+      bar_init(turn(i), 1);
     }
     for (int i = 0; i < 8; ++i) bar_init(pair_met(i), 2);
     bar_init(q_full, 32 * kSoftWarps);
@@ -716,52 +718,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
       const uint32_t t_s = tmem + i * kKeys, t_o = tmem + 256 + i * 128, q = desc_lo(q_smem + i * Sh::kTile, 16);
       bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
-      uint32_t weighed = 0;
+      uint32_t weighed = 0, turns = 0;
       Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
       auto scores = [&](int t) {
-        ok = warp_wait(full(at.slot), at.phase, &sh.dead);
-        if (!ok) return;
-        fence_after();
-        if (t >= t0 && t < t1) {
-          const uint32_t k = desc_lo(ring + at.slot * Sh::kTile, 16);
+        if (t < t0 || t >= t1) return;
+        const uint32_t k = desc_lo(ring + at.slot * Sh::kTile, 16);
 #pragma unroll
-          for (int e = 0; e < 4 * HALVES; ++e) {
-            const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
-            mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
-          }
-          mma_commit(s_full(i));
+        for (int e = 0; e < 4 * HALVES; ++e) {
+          const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
+          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
         }
+        mma_commit(s_full(i));
       };
       for (bool careful = false;; careful = true) {
         if (ok && tb < te) {
-          scores(tb);
-          mma_commit(empty(at.slot));
-          at.step();
+          ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+          if (ok) {
+            fence_after();
+            scores(tb);
+            mma_commit(empty(at.slot));
+            at.step();
+          }
         }
         for (int t = tb; t < te && ok; ++t) {
           const uint32_t v = desc_lo(ring + at.slot * Sh::kTile, Sh::kHalf), v_empty = empty(at.slot);
+          const bool weigh = t >= t0 && t < t1;
           ok = warp_wait(full(at.slot), at.phase, &sh.dead);
           at.step();
-          if (t >= t0 && t < t1) {
-            ok = ok && warp_wait(p_full(i), weighed & 1, &sh.dead);
-            if (!ok) break;
-            ++weighed;
-            fence_after();
+          if (ok && t + 1 < te) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
+          if (ok && weigh) ok = warp_wait(p_full(i), weighed++ & 1, &sh.dead);
+          // The row tiles take turns, values of a tile and scores of the next at a time: one's softmax runs under the
+          // other's products.  (Products in the order of their readiness brought both softmaxes into step.)
+          ok = ok && warp_wait(turn(i), (turns++ & 1) ^ (i ^ 1), &sh.dead);
+          if (!ok) break;
+          fence_after();
+          if (weigh) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
               mma_ts(t_o, t_s + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
                      t > t0 || k > 0);
             if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
           }
-          if (!ok) break;
+          if (t + 1 < te) scores(t + 1);
+          if (lane == 0) bar_arrive(turn(i ^ 1));
+          __syncwarp();
+          mma_commit(v_empty);
           if (t + 1 < te) {
-            scores(t + 1);
-            if (!ok) break;
-            mma_commit(v_empty);
             mma_commit(empty(at.slot));
             at.step();
-          } else {
-            mma_commit(v_empty);
           }
         }
         if (!ok) {  // products in flight end by themselves: leave when they have
