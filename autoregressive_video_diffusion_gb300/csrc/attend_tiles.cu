@@ -126,30 +126,38 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
       "[%6];\n\t}" ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(h), "r"(blk), "r"(bar)
       : "memory");
 }
-// The products are issued by one lane, chosen inside the instruction sequence: the warp's control flow stays uniform and
+// The products are issued by the lane with `lead`, inside the instruction sequence: the warp's control flow stays uniform and
 // the operands stay in uniform registers (a branch on the lane made eight products take 720 cycles to issue).
 // Descriptors share their high word; `a`, `b` are the low words.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
-                                       uint32_t idesc, bool add) {
+                                       uint32_t idesc, bool add, uint32_t lead) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
-      "setp.ne.b32 p, %6, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi),
-      "r"(idesc), "r"((uint32_t)add)
+      "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, bool add,
+                                       uint32_t lead) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(b_hi),
-      "r"(idesc), "r"((uint32_t)add)
+      "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+      : "memory");
+}
+// 1 in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(x));
+  return x;
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -197,25 +205,6 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
-}
-// Two fp32 in a register pair.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t z;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
-  return z;
-}
-__device__ __forceinline__ void unpair(uint64_t z, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t w;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
-  return w;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t w;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
-  return w;
 }
 __device__ __forceinline__ float max3(float x, uint32_t y, uint32_t z) {
   float w;
@@ -487,12 +476,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_after();
         if (move) move_to(grown ? seen : m, t > t0);
         uint32_t w[2][16];
-        uint64_t sum[2];
+        float sum[4];
         for (bool settled = false;; settled = true) {
           uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
           const float off = m == -INFINITY ? 0.f : -m * sc;
-          const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-          sum[0] = sum[1] = 0;
+          sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
           tm_ld32(x[0], t_s + 64 * hf);
           tm_ld32(x[1], t_s + 64 * hf + 32);
           wait_ld(x[0]);
@@ -513,39 +501,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             pending = true;
             seen = fmaxf(seen, __bfloat162float(own));
           }
-          // in steps over a chunk of scores, so that the exponentials follow one another without waiting
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y[32];
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-              unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y[2 * u],
-                     y[2 * u + 1]);
-#pragma unroll
-            for (int u = 0; u < 32; ++u) y[u] = exp2_fast(y[u]);
+            for (int u = 0; u < 32; ++u) x[e][u] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(x[e][u]), sc, off)));
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-              sum[u & 1] = add2(sum[u & 1], pair(y[2 * u], y[2 * u + 1]));
-              w[e][u] = pack_bf16x2(y[2 * u], y[2 * u + 1]);
+              const float y0 = __uint_as_float(x[e][2 * u]), y1 = __uint_as_float(x[e][2 * u + 1]);
+              sum[(2 * u) & 3] += y0;
+              sum[(2 * u + 1) & 3] += y1;
+              w[e][u] = pack_bf16x2(y0, y1);
             }
+            if (!exact) tm_st16(t_s + 64 * hf + 16 * e, w[e]);  // each half over its own scores
           }
-          if (settled) break;
-          if (!exact) {
-            if ((seen - m) * sc > kFar) sh.far = 1;
-            break;
-          }
+          if (settled || !exact) break;
           hear();
           const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
           if (!ok || !__any_sync(~0u, far)) break;
           move_to(far ? seen : m, t > t0);
         }
         if (!ok) break;
-        // each half over its own scores
-        tm_st16(t_s + 64 * hf, w[0]);
-        tm_st16(t_s + 64 * hf + 16, w[1]);
-        float y0, y1;
-        unpair(add2(sum[0], sum[1]), y0, y1);
-        l += y0 + y1;
+        if (exact) {
+          tm_st16(t_s + 64 * hf, w[0]);
+          tm_st16(t_s + 64 * hf + 16, w[1]);
+        }
         if (masked) {  // guard the values: see the top of the file
           const int n = 2 * (t - tb + (careful ? te - tb : 0)) + 1, slot = n % Sh::kSlots;
           ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
@@ -572,6 +551,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(i));
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (!exact && (seen - m) * sc > kFar) sh.far = 1;
       }
       if (ok && t0 < t1) {  // the last product
         ok = warp_wait(s_full(i), scored & 1, &sh.dead);
@@ -718,6 +699,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int t0 = i ? it.t0[1] : it.t0[0], t1 = i ? it.t1[1] : it.t1[0];
       const uint32_t t_s = tmem + i * kKeys, t_o = tmem + 256 + i * 128, q = desc_lo(q_smem + i * Sh::kTile, 16);
       bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
+      const uint32_t lead = elected();
       uint32_t weighed = 0, turns = 0;
       Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
       auto scores = [&](int t) {
@@ -726,9 +708,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4 * HALVES; ++e) {
           const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
-          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0);
+          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, lead);
         }
-        mma_commit(s_full(i));
+        mma_commit(s_full(i), lead);
       };
       for (bool careful = false;; careful = true) {
         if (ok && tb < te) {
@@ -736,7 +718,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (ok) {
             fence_after();
             scores(tb);
-            mma_commit(empty(at.slot));
+            mma_commit(empty(at.slot), lead);
             at.step();
           }
         }
@@ -746,30 +728,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = warp_wait(full(at.slot), at.phase, &sh.dead);
           at.step();
           if (ok && t + 1 < te) ok = warp_wait(full(at.slot), at.phase, &sh.dead);
-          if (ok && weigh) ok = warp_wait(p_full(i), weighed++ & 1, &sh.dead);
           // The row tiles take turns, values of a tile and scores of the next at a time: one's softmax runs under the
           // other's products.  (Products in the order of their readiness brought both softmaxes into step.)
           ok = ok && warp_wait(turn(i), (turns++ & 1) ^ (i ^ 1), &sh.dead);
+          if (ok && weigh) ok = warp_wait(p_full(i), weighed++ & 1, &sh.dead);
           if (!ok) break;
           fence_after();
           if (weigh) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
               mma_ts(t_o, t_s + 64 * (k >> 2) + 8 * (k & 3), v + (k * 2048 >> 4), kDescHi, p.idesc_pv,
-                     t > t0 || k > 0);
-            if (t + 1 == t1) mma_commit(s_full(i));  // the row tile's O is done
+                     t > t0 || k > 0, lead);
+            if (t + 1 == t1) mma_commit(s_full(i), lead);  // the row tile's O is done
           }
           if (t + 1 < te) scores(t + 1);
-          if (lane == 0) bar_arrive(turn(i ^ 1));
+          if (lead) bar_arrive(turn(i ^ 1));
           __syncwarp();
-          mma_commit(v_empty);
+          mma_commit(v_empty, lead);
           if (t + 1 < te) {
-            mma_commit(empty(at.slot));
+            mma_commit(empty(at.slot), lead);
             at.step();
           }
         }
         if (!ok) {  // products in flight end by themselves: leave when they have
-          mma_commit(finished(i));
+          mma_commit(finished(i), lead);
           const long long start = clock64();
           while (!bar_try(finished(i), 0) && clock64() - start < kPatience) {
           }
