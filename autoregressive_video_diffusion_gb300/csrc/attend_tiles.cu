@@ -475,12 +475,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++scored;
         fence_after();
         if (move) move_to(grown ? seen : m, t > t0);
-        uint32_t w[2][16];
-        float sum[4];
-        for (bool settled = false;; settled = true) {
-          uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
-          const float off = m == -INFINITY ? 0.f : -m * sc;
-          sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+        uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
+        auto take = [&] {
           tm_ld32(x[0], t_s + 64 * hf);
           tm_ld32(x[1], t_s + 64 * hf + 32);
           wait_ld(x[0]);
@@ -489,41 +485,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
           }
-          if (!settled) {
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        };
+        auto tell = [&] {  // this thread's maximum
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
-            const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-            sh.swap.top[i][swaps & 1][hf][r] = own;
-            __syncwarp();
-            if (lane == 0) bar_arrive(met);
-            pending = true;
-            seen = fmaxf(seen, __bfloat162float(own));
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) x[e][u] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(x[e][u]), sc, off)));
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const float y0 = __uint_as_float(x[e][2 * u]), y1 = __uint_as_float(x[e][2 * u + 1]);
-              sum[(2 * u) & 3] += y0;
-              sum[(2 * u + 1) & 3] += y1;
-              w[e][u] = pack_bf16x2(y0, y1);
-            }
-            if (!exact) tm_st16(t_s + 64 * hf + 16 * e, w[e]);  // each half over its own scores
-          }
-          if (settled || !exact) break;
+          for (int u = 0; u < 32; ++u)
+            top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
+          const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          sh.swap.top[i][swaps & 1][hf][r] = own;
+          __syncwarp();
+          if (lane == 0) bar_arrive(met);
+          pending = true;
+          seen = fmaxf(seen, __bfloat162float(own));
+        };
+        if (exact) {
+          take();
+          tell();
           hear();
           const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
-          if (!ok || !__any_sync(~0u, far)) break;
-          move_to(far ? seen : m, t > t0);
+          if (__any_sync(~0u, far)) move_to(far ? seen : m, t > t0);
         }
-        if (!ok) break;
-        if (exact) {
-          tm_st16(t_s + 64 * hf, w[0]);
-          tm_st16(t_s + 64 * hf + 16, w[1]);
+        take();
+        if (!exact) tell();
+        const float off = m == -INFINITY ? 0.f : -m * sc;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t w[16];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[e][u] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(x[e][u]), sc, off)));
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float y0 = __uint_as_float(x[e][2 * u]), y1 = __uint_as_float(x[e][2 * u + 1]);
+            sum[(2 * u) & 3] += y0;
+            sum[(2 * u + 1) & 3] += y1;
+            w[u] = pack_bf16x2(y0, y1);
+          }
+          tm_st16(t_s + 64 * hf + 16 * e, w);  // each half over its own scores
         }
         if (masked) {  // guard the values: see the top of the file
           const int n = 2 * (t - tb + (careful ? te - tb : 0)) + 1, slot = n % Sh::kSlots;
