@@ -206,6 +206,25 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
+// Two fp32 in a register pair.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ void unpair(uint64_t z, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t w;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  return w;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t w;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  return w;
+}
 __device__ __forceinline__ float max3(float x, uint32_t y, uint32_t z) {
   float w;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(w) : "f"(x), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
@@ -486,39 +505,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
           }
         };
-        auto tell = [&] {  // this thread's maximum
+        auto highest = [&] {  // of this thread's scores, rounded to what the other one hears
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int u = 0; u < 32; ++u)
             top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
-          const __nv_bfloat16 own = __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          return __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        };
+        auto tell = [&](__nv_bfloat16 own) {
           sh.swap.top[i][swaps & 1][hf][r] = own;
           __syncwarp();
           if (lane == 0) bar_arrive(met);
           pending = true;
           seen = fmaxf(seen, __bfloat162float(own));
         };
+        take();
+        const __nv_bfloat16 own = highest();
         if (exact) {
-          take();
-          tell();
+          tell(own);
           hear();
           const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
           if (__any_sync(~0u, far)) move_to(far ? seen : m, t > t0);
         }
-        take();
-        if (!exact) tell();
         const float off = m == -INFINITY ? 0.f : -m * sc;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t w[16];
 #pragma unroll
-          for (int u = 0; u < 32; ++u) x[e][u] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(x[e][u]), sc, off)));
+          for (int u = 0; u < 16; ++u) {
+            float y0, y1;
+            unpair(fma2(pair(__uint_as_float(x[e][2 * u]), __uint_as_float(x[e][2 * u + 1])), sc2, off2), y0, y1);
+            x[e][2 * u] = __float_as_uint(exp2_fast(y0));
+            x[e][2 * u + 1] = __float_as_uint(exp2_fast(y1));
+          }
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
             const float y0 = __uint_as_float(x[e][2 * u]), y1 = __uint_as_float(x[e][2 * u + 1]);
-            sum[(2 * u) & 3] += y0;
-            sum[(2 * u + 1) & 3] += y1;
+            sum[u & 1] = add2(sum[u & 1], pair(y0, y1));
             w[u] = pack_bf16x2(y0, y1);
           }
           tm_st16(t_s + 64 * hf + 16 * e, w);  // each half over its own scores
@@ -549,8 +574,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(i));
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (!exact && (seen - m) * sc > kFar) sh.far = 1;
+        float y0, y1;
+        unpair(add2(sum[0], sum[1]), y0, y1);
+        l += y0 + y1;
+        if (!exact) {
+          tell(own);
+          if ((seen - m) * sc > kFar) sh.far = 1;
+        }
       }
       if (ok && t0 < t1) {  // the last product
         ok = warp_wait(s_full(i), scored & 1, &sh.dead);
