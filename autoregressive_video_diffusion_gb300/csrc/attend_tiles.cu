@@ -74,6 +74,7 @@ struct TileParams {
   AttendParams a;
   Tiling tl;
   int splits, q_tiles;
+  int whole;                           // items of one CTA each before those that are split
   float scale_log2;                    // |scale| log2 e
   uint32_t idesc_qk, idesc_pv;
   float* part;                         // [item][split][256][D + 2] partial results
@@ -112,6 +113,21 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
   }
   return true;
+}
+// The same by polling, for the two warps everything waits for: a try that suspends its thread wakes it late.
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, volatile int* dead) {
+  const long long start = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(~0u, ok)) return true;
+    if (__any_sync(~0u, *dead)) return false;
+    if (clock64() - start > kPatience) *dead = 1;
+  }
 }
 // The same for a whole warp: its lanes agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
@@ -318,10 +334,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   // ---- the item
   Item it;
-  it.s = blockIdx.z / p.splits;
-  const int split = blockIdx.z % p.splits;
-  it.kh = blockIdx.y;
-  const int qt = p.q_tiles - 1 - blockIdx.x;  // the rows that see most keys first
+  // blocks in the order: row tile, KV head, sequence; the first `whole` items are one CTA's, the others are split
+  const int cut = max(0, (int)blockIdx.x - p.whole), item = cut ? p.whole + cut / p.splits : min(blockIdx.x, p.whole);
+  const int splits = item < p.whole ? 1 : p.splits, split = item < p.whole ? 0 : cut % p.splits;
+  const int qt = p.q_tiles - 1 - item % p.q_tiles;  // the rows that see most keys first
+  it.kh = item / p.q_tiles % a.pool.H;
+  it.s = item / p.q_tiles / a.pool.H;
   if (!seq_rows(a.b, it.s, it.lo, it.len)) return;
   const int n_rows = it.len * a.G;
   it.row0 = qt * 2 * kRows;
@@ -345,10 +363,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       it.t1[i] = tl.tile_of(end - 1) + 1;
     }
   }
-  if (p.splits > 1) {  // this split's share of the tiles the item's rows see
+  if (splits > 1) {  // this split's share of the tiles the item's rows see
     const bool one = it.t1[1] <= it.t0[1];
     const int lo = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], hi = one ? it.t1[0] : it.t1[1];
-    const int per = (max(hi - lo, 0) + p.splits - 1) / p.splits;
+    const int per = (max(hi - lo, 0) + splits - 1) / splits;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       it.t0[i] = max(it.t0[i], lo + split * per);
@@ -361,7 +379,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
 
   const int2 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
-  const int64_t item = ((int64_t)it.s * a.pool.H + it.kh) * p.q_tiles + qt;
 
   // ---- set-up
   const uint32_t base = smem_u32(smem_raw) + Sh::kHead;
@@ -606,7 +623,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
-    float* part = part_of(p.part, item, p.splits, split, 2 * kRows, D, i * kRows + r);
+    float* part = part_of(p.part, item - p.whole, p.splits, split, 2 * kRows, D, i * kRows + r);
 #pragma unroll 1
     for (int e = 0; e < Sh::kD / 64 && ok; ++e) {
       const int d0 = hf * (Sh::kD / 2) + 32 * e;
@@ -637,7 +654,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!mine) continue;
-      if (p.splits > 1) {
+      if (splits > 1) {
 #pragma unroll
         for (int u = 0; u < 32; u += 2)
           if (d0 + u < D)
@@ -657,7 +674,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     if (mine && ok && hf == 0) {
-      if (p.splits > 1) {
+      if (splits > 1) {
         part[0] = m == -INFINITY ? m : m * sc;
         part[1] = l;
       } else if (a.lse) {
@@ -759,7 +776,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // The row tiles take turns, values of a tile and scores of the next at a time: one's softmax runs under the
           // other's products.  (Products in the order of their readiness brought both softmaxes into step.)
           ok = ok && warp_wait(turn(i), (turns++ & 1) ^ (i ^ 1), &sh.dead);
-          if (ok && weigh) ok = warp_wait(p_full(i), weighed++ & 1, &sh.dead);
+          if (ok && weigh) ok = warp_poll(p_full(i), weighed++ & 1, &sh.dead);
           if (!ok) break;
           fence_after();
           if (weigh) {
@@ -805,8 +822,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 
   // ---- the item's last split joins the parts
-  if (p.splits > 1 && last_of(p.done + item, p.splits, &sh.last))
-    join_parts<__nv_bfloat16>(a, part_of(p.part, item, p.splits, 0, 2 * kRows, a.pool.D, 0), p.splits, 2 * kRows,
+  if (splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
+    join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0), splits, 2 * kRows,
                               it.rows[0] + it.rows[1], it.row0, it.lo, it.kh);
 }
 
@@ -851,8 +868,10 @@ cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap&
   const cudaError_t e = launch_setup(g_tile_launch[HALVES - 1], tile_kernel<HALVES>, kTileThreads,
                                      Shape<HALVES>::kSmem, &blocks);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.q_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
-  tile_kernel<HALVES><<<grid, kTileThreads, Shape<HALVES>::kSmem, s>>>(p, k, v);
+  const int64_t items = (int64_t)p.q_tiles * p.a.pool.H * p.a.b.n_seqs;
+  const int64_t grid = p.whole + (items - p.whole) * p.splits;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  tile_kernel<HALVES><<<(unsigned)grid, kTileThreads, Shape<HALVES>::kSmem, s>>>(p, k, v);
   return cudaGetLastError();
 }
 
@@ -865,18 +884,24 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   const int64_t seen = (int64_t)a.window + 2 * kRows / a.G + 2;  // of an item's rows under a window
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
   const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
-  // fewer items than SMs: the keys are split so that the SMs have one item each, at least 4 key tiles a split
-  int64_t splits = items < 152 ? 152 / items : 1;
+  // Fewer items than SMs: their keys are split so that the SMs have one part each.  Items of equal work (one sequence
+  // without a causal mask) in a few rounds: those of the last, incomplete round are split over the SMs it has.  At least
+  // 4 key tiles a part.
+  const int64_t sms = sm_count(), rounds = items / sms, left = items % sms;
+  const bool tail = rounds > 0 && rounds < 16 && left && a.b.n_seqs == 1 && !a.causal;
+  int64_t splits = items < sms ? sms / items : tail ? sms / left : 1;
   if (splits > key_tiles / 4) splits = key_tiles / 4;
-  if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;
   t.splits = splits < 1 ? 1 : (int)splits;
-  t.done_bytes = t.splits > 1 ? ((size_t)items * 4 + 255) & ~(size_t)255 : 0;
-  t.bytes = t.splits > 1 ? t.done_bytes + (size_t)items * t.splits * 2 * kRows * (a.pool.D + 2) * 4 : 0;
+  t.whole = t.splits == 1 ? items : rounds * sms;
+  const size_t cut = (size_t)(items - t.whole);
+  t.done_bytes = (cut * 4 + 255) & ~(size_t)255;
+  t.bytes = t.done_bytes + cut * t.splits * 2 * kRows * (a.pool.D + 2) * 4;
   return t;
 }
 
 cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws, cudaStream_t s) {
   const TilePlan t = plan_tiles(a, max_kv);
+  if (t.whole > INT32_MAX) return cudaErrorInvalidValue;
   TileParams p{};
   p.a = a;
   const int bs = a.pool.bs;
@@ -886,6 +911,7 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
   p.tl.whole = bs % kKeys == 0 || (p.tl.box == bs && p.tl.pages * bs == kKeys);
   p.splits = t.splits;
+  p.whole = (int)t.whole;
   p.q_tiles = t.q_tiles;
   // a scale below 0 negates the products (the running maximum then is of what is exponentiated); one near 0 is held
   // where masked scores of -inf still scale to -inf

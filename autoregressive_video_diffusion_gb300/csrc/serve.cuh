@@ -74,6 +74,7 @@ cudaError_t launch_attend_rows(const AttendParams& p, int64_t max_kv, void* ws, 
 // The same for the tiled attention.
 struct TilePlan {
   int q_tiles, splits;
+  int64_t whole;  // items that are not split, the first ones
   size_t done_bytes, bytes;
 };
 TilePlan plan_tiles(const AttendParams& p, int64_t max_kv);
