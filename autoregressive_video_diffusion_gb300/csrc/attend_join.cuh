@@ -38,39 +38,61 @@ __device__ __forceinline__ bool last_of(uint32_t* done, int splits, int* s_last)
 }
 
 // Joins `splits` parts of `rows` rows (`stride` rows a part) whose first is row `row0` of (token, head of the KV
-// head) rows, sequence start lo.
+// head) rows, sequence start lo.  Called by a whole CTA; scratch: join_scratch(rows, splits) bytes of shared memory.
+// First every part's maximum and sum, all at once, then the weights of the parts, then the values with many loads in
+// flight: a loop that reads a part after the other pays a memory latency for each.
+__host__ __device__ constexpr int64_t join_scratch(int rows, int splits) { return ((int64_t)rows * splits * 2 + rows) * 4; }
+
 template <typename T>
 __device__ __forceinline__ void join_parts(const AttendParams& a, const float* part, int splits, int stride, int rows,
-                                           int row0, int lo, int kh) {
+                                           int row0, int lo, int kh, float* scratch) {
   const int D = a.pool.D, quads = D / 4;
   const int64_t step = (int64_t)stride * (D + 2);
+  float* const weight = scratch;                 // [rows][splits]: the maximum, then the part's weight
+  float* const sum = weight + rows * splits;     // [rows][splits]
+  float* const inv = sum + rows * splits;        // [rows]
+  __syncthreads();
+  for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
+    const int r = u / splits, k = u - r * splits;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + k * step + (int64_t)r * (D + 2)));
+    weight[u] = ml.x;
+    sum[u] = ml.y;
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    float top = -INFINITY, l = 0.f;
+    for (int k = 0; k < splits; ++k) top = fmaxf(top, weight[r * splits + k]);
+    for (int k = 0; k < splits; ++k) {
+      // a split that saw no key of this row has the sum 0
+      const float w = sum[r * splits + k] == 0.f ? 0.f : exp2_fast(weight[r * splits + k] - top);
+      weight[r * splits + k] = w;
+      if (w != 0.f) l += w * sum[r * splits + k];
+    }
+    inv[r] = l != 0.f ? 1.f / l : 0.f;
+    const int R = row0 + r, tok = R / a.G;
+    if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(top, l);
+  }
+  __syncthreads();
   for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
     const int r = u / quads, d = (u - r * quads) * 4;
-    const float* at = part + (int64_t)r * (D + 2);
-    float top = -INFINITY;
-    for (int k = 0; k < splits; ++k) top = fmaxf(top, __ldcg(at + k * step));
-    float l = 0.f, o[4] = {};
-#pragma unroll 4
+    const float* at = part + (int64_t)r * (D + 2) + 2 + d;
+    const float* w = weight + r * splits;
+    float o[4] = {};
+#pragma unroll 8
     for (int k = 0; k < splits; ++k) {
-      const float* x = at + k * step;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(x));
-      if (ml.y == 0.f) continue;  // the split saw no key of this row
-      const float w = exp2_fast(ml.x - top);
-      const float2 x0 = __ldcg(reinterpret_cast<const float2*>(x + 2 + d));
-      const float2 x1 = __ldcg(reinterpret_cast<const float2*>(x + 4 + d));
-      l += w * ml.y;
-      o[0] += w * x0.x, o[1] += w * x0.y, o[2] += w * x1.x, o[3] += w * x1.y;
+      const float2 x0 = __ldcg(reinterpret_cast<const float2*>(at + k * step));
+      const float2 x1 = __ldcg(reinterpret_cast<const float2*>(at + k * step + 2));
+      const float wk = w[k];
+      if (wk != 0.f) o[0] += wk * x0.x, o[1] += wk * x0.y, o[2] += wk * x1.x, o[3] += wk * x1.y;
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
     const int R = row0 + r, tok = R / a.G;
     const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G);
+    const float n = inv[r];
     if (sizeof(T) == 2)
       *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) =
-          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+          make_uint2(pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n));
     else
-      *reinterpret_cast<float4*>(a.out + (row * D + d) * 4) =
-          make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    if (a.lse && d == 0) a.lse[row] = row_lse(top, l);
+      *reinterpret_cast<float4*>(a.out + (row * D + d) * 4) = make_float4(o[0] * n, o[1] * n, o[2] * n, o[3] * n);
   }
 }
 

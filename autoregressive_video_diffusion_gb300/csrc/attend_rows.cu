@@ -8,7 +8,8 @@
 // keys: an item's keys are split over CTAs, the last of which joins the parts.
 //
 // fp32: each factor x is x_hi + x_lo, both with 11 significant bits, and x y = x_hi y_hi + x_hi y_lo + x_lo y_hi up
-// to 2^-22: three tensor products for one.  The large and the small products of a score are summed apart, and a
+// to 2^-22: three tensor products for one.  A tile is taken apart once, for all warps (each warp doing it for itself
+// made the conversions the bound: 331 us for what now takes a fraction).  The large and the small products of a score are summed apart, and a
 // tile's weighted values start from 0 and are added to the running ones by one fma, so that the tensor cores'
 // accumulation (which may truncate) never runs over more than a tile.
 #include <type_traits>
@@ -21,6 +22,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kRowThreads = 32 * kWarps;
+constexpr int kMaxSplits = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct RowParams {
@@ -39,12 +41,16 @@ struct Rows {
   static constexpr int kMine = kKeys * MW / kWarps;     // of them, a warp's
   static constexpr int kTiles = kMine / 8;              // in columns of 8
   static constexpr int kRow = DP * sizeof(T) + 16;      // bytes of a row in shared memory: no bank is hit twice
-  static constexpr int kStages = 3;
+  static constexpr int kStages = kHalf || DP == 64 ? 3 : 2;
   static constexpr int kStage = 2 * kKeys * kRow;
-  static constexpr int kQ = kHalf ? 0 : 2 * 16 * MW * kRow;
+  // fp32 taken apart: (hi, lo) pairs, rows padded so that a product's operands hit every bank once
+  static constexpr int kPairK = DP * 8 + 32, kPairV = DP * 8 + 16;
+  static constexpr int kQ = kHalf ? 0 : 16 * MW * kPairK;
+  static constexpr int kPairs = kHalf ? 0 : kKeys * (kPairK + kPairV);
   static constexpr int kJoin = MW == 1 ? kWarps * 16 * (DP + 2) * 4 : 0;
   static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
-  static constexpr int kSmem = kBuffers + kQ;
+  static constexpr int kSmem = kBuffers + kQ + kPairs;
+  static_assert(join_scratch(16 * MW, kMaxSplits) <= kSmem, "the join's scratch fits where the tiles were");
   static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * kRow, "a tile's weights fit where its keys were");
 };
 
@@ -73,16 +79,18 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t to_tf32(float x) {
-  uint32_t y;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
-  return y;
+// x = hi + lo: hi the upper 11 significant bits, lo the rest, rounded where the products cut it (they read 11 bits).
+// Infinities and NaN stay in hi alone.
+__device__ __forceinline__ uint2 halves(uint32_t x) {
+  if ((x & 0x7F800000u) == 0x7F800000u) return make_uint2(x, 0);
+  const uint32_t hi = x & 0xFFFFE000u;
+  return make_uint2(hi, __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u);
 }
-// x = hi + lo.  Infinities and NaN stay in hi alone.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = to_tf32(x);
-  const float rest = x - __uint_as_float(hi);
-  lo = to_tf32(rest == rest && fabsf(rest) < INFINITY ? rest : 0.f);
+// Four consecutive values taken apart.
+__device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
+  const uint2 a = halves(x.x), b = halves(x.y), c = halves(x.z), d = halves(x.w);
+  *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<uint4*>(to + 16) = make_uint4(c.x, c.y, d.x, d.y);
 }
 
 template <typename T, int DP, int MW>
@@ -183,14 +191,12 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     uint8_t* qs = smem + R::kBuffers;
     for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += kRowThreads) {
       const int r = u / (DP / 4), d = u % (DP / 4) * 4;
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
-      if (r < rows && d < D) x = *reinterpret_cast<const uint4*>(q_row(r) + d * 4);
-      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-      uint32_t* v = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(w[e] ^ (r < rows ? p.flip : 0u)), w[e], v[e]);
-      *reinterpret_cast<uint4*>(qs + r * R::kRow + d * 4) = x;
-      *reinterpret_cast<uint4*>(qs + (16 * MW + r) * R::kRow + d * 4) = y;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < rows && d < D) {
+        x = *reinterpret_cast<const uint4*>(q_row(r) + d * 4);
+        x = make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip);
+      }
+      store_halves(qs + r * R::kPairK + d * 8, x);
     }
   }
 
@@ -218,6 +224,17 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
                      (a.window < 0 || p0 >= c_hi - a.window);
     // a masked tile whose values hold infinities or NaN: 0 times those must not reach a row that does not see them
     bool poison = false;
+    uint8_t* const pk = smem + R::kBuffers + R::kQ;
+    uint8_t* const pv = pk + R::kKeys * R::kPairK;
+    if constexpr (!R::kHalf) {
+#pragma unroll 4
+      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += kRowThreads) {
+        const int row = u / kChunks, ch = u % kChunks;
+        store_halves(pk + row * R::kPairK + ch * 32, *reinterpret_cast<const uint4*>(kp + row * R::kRow + ch * 16));
+        store_halves(pv + row * R::kPairV + ch * 32, *reinterpret_cast<const uint4*>(vp + row * R::kRow + ch * 16));
+      }
+      __syncthreads();
+    }
     if (!all) {
       for (int u = threadIdx.x; u < R::kKeys * kChunks; u += kRowThreads) {
         const uint4 x = *reinterpret_cast<const uint4*>(vp + u / kChunks * R::kRow + u % kChunks * 16);
@@ -246,26 +263,24 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         float y[R::kTiles][4];
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
-        const uint8_t* qh = smem + R::kBuffers + (first + g) * R::kRow + c * 4;
-        const uint8_t* ql = qh + 16 * MW * R::kRow;
+        const uint8_t* qp = smem + R::kBuffers + (first + g) * R::kPairK + c * 8;
+        const uint8_t* kq = pk + (k0 + g) * R::kPairK + c * 8;
 #pragma unroll
         for (int k = 0; k < DP / 8; ++k) {
           uint32_t ah[4], al[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int at = (e & 1) * 8 * R::kRow + (8 * k + (e >> 1) * 4) * 4;
-            ah[e] = *reinterpret_cast<const uint32_t*>(qh + at);
-            al[e] = *reinterpret_cast<const uint32_t*>(ql + at);
+            const uint2 f = *reinterpret_cast<const uint2*>(qp + (e & 1) * 8 * R::kPairK + (8 * k + (e >> 1) * 4) * 8);
+            ah[e] = f.x;
+            al[e] = f.y;
           }
 #pragma unroll
           for (int n = 0; n < R::kTiles; ++n) {
-            const float* kr = reinterpret_cast<const float*>(kp + (k0 + 8 * n + g) * R::kRow) + 8 * k + c;
-            uint32_t h0, h1, l0, l1;
-            split_tf32(kr[0], h0, l0);
-            split_tf32(kr[4], h1, l1);
-            mma_tf32(x[n], ah, h0, h1);
-            mma_tf32(y[n], ah, l0, l1);
-            mma_tf32(y[n], al, h0, h1);
+            const uint2 f0 = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k);
+            const uint2 f1 = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k + 32);
+            mma_tf32(x[n], ah, f0.x, f1.x);
+            mma_tf32(y[n], ah, f0.y, f1.y);
+            mma_tf32(y[n], al, f0.x, f1.x);
           }
         }
 #pragma unroll
@@ -350,23 +365,24 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         uint32_t wh[R::kTiles][4], wl[R::kTiles][4];
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n) {
-          split_tf32(x[n][0], wh[n][0], wl[n][0]);
-          split_tf32(x[n][2], wh[n][1], wl[n][1]);
-          split_tf32(x[n][1], wh[n][2], wl[n][2]);
-          split_tf32(x[n][3], wh[n][3], wl[n][3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint2 f = halves(__float_as_uint(x[n][(e & 1) * 2 + (e >> 1)]));
+            wh[n][e] = f.x;
+            wl[n][e] = f.y;
+          }
         }
+        const uint8_t* vq = pv + (k0 + 2 * c) * R::kPairV + g * 8;
 #pragma unroll
         for (int j = 0; j < DP / 8; ++j) {
           float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int n = 0; n < R::kTiles; ++n) {
-            const float* v0 = reinterpret_cast<const float*>(vp + (k0 + 8 * n + 2 * c) * R::kRow) + 8 * j + g;
-            uint32_t h0, h1, l0, l1;
-            split_tf32(v0[0], h0, l0);
-            split_tf32(v0[R::kRow / 4], h1, l1);
-            mma_tf32(y, wl[n], h0, h1);
-            mma_tf32(y, wh[n], l0, l1);
-            mma_tf32(y, wh[n], h0, h1);
+            const uint2 f0 = *reinterpret_cast<const uint2*>(vq + 8 * n * R::kPairV + 64 * j);
+            const uint2 f1 = *reinterpret_cast<const uint2*>(vq + (8 * n + 1) * R::kPairV + 64 * j);
+            mma_tf32(y, wl[n], f0.x, f1.x);
+            mma_tf32(y, wh[n], f0.y, f1.y);
+            mma_tf32(y, wh[n], f0.x, f1.x);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[j][e] = fmaf(o[j][e], keep[e >> 1], y[e]);
@@ -443,7 +459,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     }
   }
   if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
-    join_parts<T>(a, part_of(p.part, item, p.splits, 0, 16 * MW, D, 0), p.splits, 16 * MW, rows, row0, lo, kh);
+    join_parts<T>(a, part_of(p.part, item, p.splits, 0, 16 * MW, D, 0), p.splits, 16 * MW, rows, row0, lo, kh,
+                  reinterpret_cast<float*>(smem));
 }
 
 template <typename T, int DP, int MW>
@@ -474,12 +491,12 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   r.tiles = (int)(((int64_t)a.b.max_q * a.G + per - 1) / per);
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
   // Two CTAs of an SM at a time: one round of pieces for a few sequences, several rounds of shorter ones where their
-  // lengths may differ, but no piece under a tile (or four, in several rounds) and at most 64 pieces of an item.
-  const int64_t slots = 304, rounds = a.b.n_seqs >= 8 ? 8 : 1;
+  // lengths may differ, but no piece under two tiles (or four, in several rounds) and at most kMaxSplits of an item.
+  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 8 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
-  const int64_t least = rounds > 1 ? 4 * keys : keys;
+  const int64_t least = (rounds > 1 ? 4 : 2) * keys;
   if (span < least) span = least;
-  if (span < (max_kv + 63) / 64) span = (max_kv + 63) / 64;
+  if (span < (max_kv + kMaxSplits - 1) / kMaxSplits) span = (max_kv + kMaxSplits - 1) / kMaxSplits;
   span = (span + keys - 1) / keys * keys;
   int64_t splits = (max_kv + span - 1) / span;
   if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;

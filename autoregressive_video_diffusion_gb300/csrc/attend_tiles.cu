@@ -32,6 +32,7 @@ constexpr int kRows = 128;             // rows of a tile (lanes of tensor memory
 constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileThreads = 640;
 constexpr int kSoftWarps = 16;
+constexpr int kMaxSplits = 92;         // of an item: what the join's scratch holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
 constexpr float kFar = 64.f;           // and within one tile before the item is done again
@@ -268,6 +269,7 @@ struct Shape {
   static constexpr int kSlots = HALVES == 2 ? 5 : 10;    // ring of K and V tiles in turn
   static constexpr int kHead = 3072;                     // barriers and the like, before the tiles
   static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
+  static_assert(join_scratch(2 * kRows, kMaxSplits) <= kSmem - kHead, "the join's scratch fits where the tiles were");
 };
 
 // Two bf16: whether one is an infinity or NaN, and with 0 in such a place.
@@ -824,7 +826,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // ---- the item's last split joins the parts
   if (splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
     join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0), splits, 2 * kRows,
-                              it.rows[0] + it.rows[1], it.row0, it.lo, it.kh);
+                              it.rows[0] + it.rows[1], it.row0, it.lo, it.kh,
+                              reinterpret_cast<float*>(gbase));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -891,6 +894,7 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   const bool tail = rounds > 0 && rounds < 16 && left && a.b.n_seqs == 1 && !a.causal;
   int64_t splits = items < sms ? sms / items : tail ? sms / left : 1;
   if (splits > key_tiles / 4) splits = key_tiles / 4;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   t.splits = splits < 1 ? 1 : (int)splits;
   t.whole = t.splits == 1 ? items : rounds * sms;
   const size_t cut = (size_t)(items - t.whole);
