@@ -250,15 +250,22 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     for (int n = 0; n < R::kTiles; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
     if (!idle) {
       if constexpr (R::kHalf) {
+        float y[R::kTiles][4];  // every other step's products, so that none waits for the one before it
 #pragma unroll
-        for (int n = 0; n < R::kTiles; ++n)
+        for (int n = 0; n < R::kTiles; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < DP / 32; ++k) {
+        for (int k = 0; k < DP / 32; ++k)
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) {
             uint32_t b[4];
             ldm4(b, k_at + (k0 + 8 * n + (lane & 7)) * R::kRow + k * 64 + (lane >> 3) * 16);
             mma_bf16(x[n], qa[2 * k], b[0], b[1]);
-            mma_bf16(x[n], qa[2 * k + 1], b[2], b[3]);
+            mma_bf16(y[n], qa[2 * k + 1], b[2], b[3]);
           }
+#pragma unroll
+        for (int n = 0; n < R::kTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] += y[n][e];
       } else {
         float y[R::kTiles][4];
 #pragma unroll
@@ -274,14 +281,19 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
             ah[e] = f.x;
             al[e] = f.y;
           }
+          uint2 f[R::kTiles][2];
 #pragma unroll
           for (int n = 0; n < R::kTiles; ++n) {
-            const uint2 f0 = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k);
-            const uint2 f1 = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k + 32);
-            mma_tf32(x[n], ah, f0.x, f1.x);
-            mma_tf32(y[n], ah, f0.y, f1.y);
-            mma_tf32(y[n], al, f0.x, f1.x);
+            f[n][0] = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k);
+            f[n][1] = *reinterpret_cast<const uint2*>(kq + 8 * n * R::kPairK + 64 * k + 32);
           }
+          // no product right behind one it adds to: it would wait for it
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) mma_tf32(y[n], ah, f[n][0].y, f[n][1].y);
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) mma_tf32(x[n], ah, f[n][0].x, f[n][1].x);
+#pragma unroll
+          for (int n = 0; n < R::kTiles; ++n) mma_tf32(y[n], al, f[n][0].x, f[n][1].x);
         }
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n)
@@ -374,18 +386,29 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         }
         const uint8_t* vq = pv + (k0 + 2 * c) * R::kPairV + g * 8;
 #pragma unroll
-        for (int j = 0; j < DP / 8; ++j) {
-          float y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < DP / 8; j += 4) {
+          float y[4][4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) y[b][0] = y[b][1] = y[b][2] = y[b][3] = 0.f;
 #pragma unroll
           for (int n = 0; n < R::kTiles; ++n) {
-            const uint2 f0 = *reinterpret_cast<const uint2*>(vq + 8 * n * R::kPairV + 64 * j);
-            const uint2 f1 = *reinterpret_cast<const uint2*>(vq + (8 * n + 1) * R::kPairV + 64 * j);
-            mma_tf32(y, wl[n], f0.x, f1.x);
-            mma_tf32(y, wh[n], f0.y, f1.y);
-            mma_tf32(y, wh[n], f0.x, f1.x);
+            uint2 f[4][2];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              f[b][0] = *reinterpret_cast<const uint2*>(vq + 8 * n * R::kPairV + 64 * (j + b));
+              f[b][1] = *reinterpret_cast<const uint2*>(vq + (8 * n + 1) * R::kPairV + 64 * (j + b));
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mma_tf32(y[b], wl[n], f[b][0].x, f[b][1].x);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mma_tf32(y[b], wh[n], f[b][0].y, f[b][1].y);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mma_tf32(y[b], wh[n], f[b][0].x, f[b][1].x);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][e] = fmaf(o[j][e], keep[e >> 1], y[e]);
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j + b][e] = fmaf(o[j + b][e], keep[e >> 1], y[b][e]);
         }
       }
     }
@@ -492,7 +515,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
   // Two CTAs of an SM at a time: one round of pieces for a few sequences, several rounds of shorter ones where their
   // lengths may differ, but no piece under two tiles (or four, in several rounds) and at most kMaxSplits of an item.
-  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 8 : 1;
+  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 16 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
   const int64_t least = (rounds > 1 ? 4 : 2) * keys;
   if (span < least) span = least;
