@@ -187,9 +187,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object, where torch offers that (a few microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_index = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and _device_index is not None and torch.cuda.is_initialized():
+        return _raw_stream(_device_index())
+    return torch.cuda.current_stream().cuda_stream
 
 
 @dataclass

@@ -77,26 +77,40 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   // units of a token a thread holds at once; whole heads where they pass through shared memory
   const int batch = PAIRS == kHalfAny ? kUnits * kThreads / per_head * per_head : kUnits * kThreads;
 
-  uint4 x[kUnits], y[kUnits];
-  auto source = [&](int t, int h) {
-    return h < p.Hq ? (const uint4*)((const T*)p.q + (t0 + t) * p.q_stride + (int64_t)h * D)
-           : h < p.Hq + p.pool.H
-               ? (const uint4*)((const T*)p.k + (t0 + t) * p.kv_stride + (int64_t)(h - p.Hq) * D)
-               : (const uint4*)((const T*)p.v + (t0 + t) * p.kv_stride + (int64_t)(h - p.Hq - p.pool.H) * D);
+  // A thread's units are kThreads apart: their head and place follow one another without a division.
+  const int head_step = kThreads / per_head, unit_step = kThreads - head_step * per_head;
+  uint4 x[2][kUnits], y[2][kUnits];
+  struct Unit {
+    int i, h, e;  // place in the batch, head (q, then k, then v), unit of the head
   };
-  auto load = [&](int t, int u0) {
+  auto first = [&](int u0) {
+    const int u = u0 + threadIdx.x, h = u / per_head;
+    return Unit{(int)threadIdx.x, h, u - h * per_head};
+  };
+  auto next = [&](Unit& u) {
+    u.i += kThreads;
+    u.h += head_step;
+    u.e += unit_step;
+    if (u.e >= per_head) {
+      u.e -= per_head;
+      ++u.h;
+    }
+  };
+  auto there = [&](const Unit& u) { return u.i < batch && u.h < heads; };
+  auto load = [&](int t, Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
+    const T* q = (const T*)p.q + (t0 + t) * p.q_stride;
+    const T* k = (const T*)p.k + (t0 + t) * p.kv_stride - p.Hq * D;
+    const T* v = (const T*)p.v + (t0 + t) * p.kv_stride - (p.Hq + p.pool.H) * D;
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int i = threadIdx.x + j * kThreads, u = u0 + i;
-      if (i >= batch || u >= per_token) continue;
-      const int h = u / per_head, e = u - h * per_head;
-      const uint4* src = source(t, h);
-      x[j] = src[e < pair_vecs ? e : e + pair_vecs];
-      if (e < pair_vecs) y[j] = src[e + pair_vecs];
+    for (int j = 0; j < kUnits; ++j, next(u)) {
+      if (!there(u)) continue;
+      const uint4* src = (const uint4*)((u.h < p.Hq ? q : u.h < p.Hq + p.pool.H ? k : v) + u.h * D);
+      a[j] = src[u.e < pair_vecs ? u.e : u.e + pair_vecs];
+      if (PAIRS == kHalfVec && u.e < pair_vecs) b[j] = src[u.e + pair_vecs];
     }
   };
 
-  load(0, 0);
+  load(0, first(0), x[0], y[0]);
   if (threadIdx.x < TOK) where[threadIdx.x].seq = -1;
   __syncthreads();
   for (int s = threadIdx.x; s < p.b.n_seqs; s += kThreads) {
@@ -129,77 +143,99 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
   __syncthreads();
 
-  for (int t = 0; t < n; ++t) {
+  const int batches = (per_token + batch - 1) / batch;
+  auto turn_and_store = [&](int t, Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
     const Where w = where[t];
-    for (int u0 = 0; u0 < per_token; u0 += batch) {
-      if (t || u0) load(t, u0);
-      if (PAIRS == kHalfAny) {
-        __syncthreads();
+    if (PAIRS == kHalfAny) {
+      __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kUnits; ++j)
-          if (threadIdx.x + j * kThreads < batch) rows[threadIdx.x + j * kThreads] = x[j];
-        __syncthreads();
-      }
+      for (int j = 0; j < kUnits; ++j)
+        if (threadIdx.x + j * kThreads < batch) rows[threadIdx.x + j * kThreads] = a[j];
+      __syncthreads();
+    }
+    if (w.seq < 0) return;
+    T* const q_to = (T*)p.q_out + (int64_t)(t0 + t) * p.Hq * D;
 #pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int i = threadIdx.x + j * kThreads, u = u0 + i;
-        if (i >= batch || u >= per_token || w.seq < 0) continue;
-        const int h = u / per_head, e = u - h * per_head;
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.pool.H;
-        if (!is_q && w.off < 0) continue;
-        T* to = is_q ? (T*)p.q_out + (int64_t)(t0 + t) * p.Hq * D + (int64_t)h * D
-                     : is_v ? (T*)p.pool.v + w.off + (h - p.Hq - p.pool.H) * p.pool.s_head
-                            : (T*)p.pool.k + w.off + (h - p.Hq) * p.pool.s_head;
-        uint4* dst = (uint4*)to;
-        if (PAIRS == kHalfVec && e < pair_vecs) {
-          if (!is_v) {
-            float a[N], b[N];
-            E::get(x[j], a);
-            E::get(y[j], b);
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-              const float2 r = cs[t][e * N + k];
-              const float a2 = a[k] * r.x - b[k] * r.y;
-              b[k] = a[k] * r.y + b[k] * r.x;
-              a[k] = a2;
-            }
-            x[j] = E::put(a);
-            y[j] = E::put(b);
-          }
-          dst[e] = x[j];
-          dst[e + pair_vecs] = y[j];
-          continue;
-        }
-        const int v = e + pair_vecs;
-        if (PAIRS == kInterleaved && !is_v && v * N < 2 * half) {
-          float a[N];
-          E::get(x[j], a);
-#pragma unroll
-          for (int k = 0; k < N; k += 2) {
-            const int q = v * (N / 2) + k / 2;
-            if (q >= half) continue;
-            const float2 r = cs[t][q];
-            const float a2 = a[k] * r.x - a[k + 1] * r.y;
-            a[k + 1] = a[k] * r.y + a[k + 1] * r.x;
-            a[k] = a2;
-          }
-          x[j] = E::put(a);
-        }
-        if (PAIRS == kHalfAny && !is_v && v * N < 2 * half) {
-          float a[N];
-          E::get(x[j], a);
-          const uint4* row = rows + i - e;
+    for (int j = 0; j < kUnits; ++j, next(u)) {
+      if (!there(u)) continue;
+      const int h = u.h, e = u.e;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.pool.H;
+      if (!is_q && w.off < 0) continue;
+      uint4* dst = (uint4*)(is_q ? q_to + h * D
+                                 : (T*)(is_v ? p.pool.v : p.pool.k) + w.off +
+                                       (h - (is_v ? p.Hq + p.pool.H : p.Hq)) * p.pool.s_head);
+      const int v = e + pair_vecs;  // of a unit of one vector
+      if (PAIRS == kHalfVec && e < pair_vecs) {
+        if (!is_v) {
+          float f[N], g[N];
+          E::get(a[j], f);
+          E::get(b[j], g);
 #pragma unroll
           for (int k = 0; k < N; ++k) {
-            const int d = v * N + k;
-            if (d >= 2 * half) continue;
-            const float2 r = cs[t][d < half ? d : d - half];
-            a[k] = d < half ? a[k] * r.x - E::one(row, d + half) * r.y : a[k] * r.x + E::one(row, d - half) * r.y;
+            const float2 r = cs[t][e * N + k];
+            const float f2 = f[k] * r.x - g[k] * r.y;
+            g[k] = f[k] * r.y + g[k] * r.x;
+            f[k] = f2;
           }
-          x[j] = E::put(a);
+          a[j] = E::put(f);
+          b[j] = E::put(g);
         }
-        dst[v] = x[j];
+        dst[e] = a[j];
+        dst[v] = b[j];
+        continue;
       }
+      if (PAIRS == kInterleaved && !is_v && v * N < 2 * half) {
+        float f[N];
+        E::get(a[j], f);
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+          const int q = v * (N / 2) + k / 2;
+          if (q >= half) continue;
+          const float2 r = cs[t][q];
+          const float f2 = f[k] * r.x - f[k + 1] * r.y;
+          f[k + 1] = f[k] * r.y + f[k + 1] * r.x;
+          f[k] = f2;
+        }
+        a[j] = E::put(f);
+      }
+      if (PAIRS == kHalfAny && !is_v && v * N < 2 * half) {
+        float f[N];
+        E::get(a[j], f);
+        const uint4* row = rows + u.i - e;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int d = v * N + k;
+          if (d >= 2 * half) continue;
+          const float2 r = cs[t][d < half ? d : d - half];
+          f[k] = d < half ? f[k] * r.x - E::one(row, d + half) * r.y : f[k] * r.x + E::one(row, d - half) * r.y;
+        }
+        a[j] = E::put(f);
+      }
+      dst[v] = a[j];
+    }
+  };
+  // the next batch's loads are in flight while a batch is turned and stored
+  Unit u = first(0);
+  int t = 0, left = batches;
+  bool more = true;
+#pragma unroll 2
+  for (int k = 0; more; k ^= 1) {
+    const Unit now = u;
+    const int t_now = t;
+    if (--left == 0) {
+      left = batches;
+      ++t;
+      u = first(0);
+    } else {
+      u = first((batches - left) * batch);
+    }
+    more = t < n;
+    if (k == 0) {
+      if (more) load(t, u, x[1], y[1]);
+      turn_and_store(t_now, now, x[0], y[0]);
+    } else {
+      if (more) load(t, u, x[0], y[0]);
+      turn_and_store(t_now, now, x[1], y[1]);
     }
   }
 }

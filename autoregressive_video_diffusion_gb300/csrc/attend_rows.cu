@@ -37,15 +37,15 @@ struct RowParams {
 template <typename T, int DP, int MW>
 struct Rows {
   static constexpr bool kHalf = sizeof(T) == 2;
-  static constexpr int kKeys = kHalf ? 64 : 32;         // keys of a tile
+  static constexpr int kKeys = kHalf ? 64 : DP == 128 && MW == 4 ? 16 : 32;  // keys of a tile
   static constexpr int kMine = kKeys * MW / kWarps;     // of them, a warp's
   static constexpr int kTiles = kMine / 8;              // in columns of 8
   static constexpr int kRow = DP * sizeof(T) + 16;      // bytes of a row in shared memory: no bank is hit twice
-  static constexpr int kStages = kHalf || DP == 64 ? 3 : 2;
+  static constexpr int kStages = kHalf ? 3 : 2;  // with 2, two CTAs of an fp32 kernel fit an SM
   static constexpr int kStage = 2 * kKeys * kRow;
   // fp32 taken apart: (hi, lo) pairs, rows padded so that a product's operands hit every bank once
   static constexpr int kPairK = DP * 8 + 32, kPairV = DP * 8 + 16;
-  static constexpr int kQ = kHalf ? 0 : 16 * MW * kPairK;
+  static constexpr int kQ = kHalf ? 0 : 16 * MW * kRow;
   static constexpr int kPairs = kHalf ? 0 : kKeys * (kPairK + kPairV);
   static constexpr int kJoin = MW == 1 ? kWarps * 16 * (DP + 2) * 4 : 0;
   static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 #pragma unroll
   for (int t = 0; t < R::kStages - 1; ++t) fetch(t);
 
-  // ---- q: bf16 in registers as the products want it, fp32 in shared memory as its two parts
+  // ---- q: bf16 in registers as the products want it, fp32 in shared memory
   const int first = MW == 1 ? 0 : warp * 16;  // the warp's first row of the item
   uint32_t qa[R::kHalf ? DP / 16 : 1][4];
   auto q_row = [&](int r) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         x = *reinterpret_cast<const uint4*>(q_row(r) + d * 4);
         x = make_uint4(x.x ^ p.flip, x.y ^ p.flip, x.z ^ p.flip, x.w ^ p.flip);
       }
-      store_halves(qs + r * R::kPairK + d * 8, x);
+      *reinterpret_cast<uint4*>(qs + r * R::kRow + d * 4) = x;
     }
   }
 
@@ -270,14 +270,15 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         float y[R::kTiles][4];
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
-        const uint8_t* qp = smem + R::kBuffers + (first + g) * R::kPairK + c * 8;
+        const uint8_t* qp = smem + R::kBuffers + (first + g) * R::kRow + c * 4;
         const uint8_t* kq = pk + (k0 + g) * R::kPairK + c * 8;
 #pragma unroll
         for (int k = 0; k < DP / 8; ++k) {
           uint32_t ah[4], al[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint2 f = *reinterpret_cast<const uint2*>(qp + (e & 1) * 8 * R::kPairK + (8 * k + (e >> 1) * 4) * 8);
+            const uint2 f = halves(*reinterpret_cast<const uint32_t*>(qp + (e & 1) * 8 * R::kRow +
+                                                                      (8 * k + (e >> 1) * 4) * 4));
             ah[e] = f.x;
             al[e] = f.y;
           }
@@ -513,9 +514,11 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
   r.tiles = (int)(((int64_t)a.b.max_q * a.G + per - 1) / per);
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
-  // Two CTAs of an SM at a time: one round of pieces for a few sequences, several rounds of shorter ones where their
-  // lengths may differ, but no piece under two tiles (or four, in several rounds) and at most kMaxSplits of an item.
-  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 16 : 1;
+  // Two CTAs of an SM at a time: one round of pieces for a few sequences; several rounds of shorter ones where their
+  // lengths may differ (6 rounds: 48 sequences of 200 .. 16000 positions take 369 us, 374 with 4, 386 with 12, 425 with
+  // 2) or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 213 us with 4 rounds,
+  // 251 with 1, 236 with 16).  No piece under two tiles (or four, in several rounds), at most kMaxSplits of an item.
+  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 6 : per == 64 && a.pool.dtype == DCP_F32 ? 4 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
   const int64_t least = (rounds > 1 ? 4 : 2) * keys;
   if (span < least) span = least;

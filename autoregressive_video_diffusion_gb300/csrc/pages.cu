@@ -36,22 +36,35 @@ __device__ int block_scan(int x, int* s_warp, int* total) {
   return v - x + (warp ? before : 0);
 }
 
-// Moves the listed pages: an item is one page of one layer and tensor, blockIdx.x strides over all of them.
+// Moves the listed pages: an item is a piece of one page of one layer and tensor, taken in turn by the CTAs.  Each
+// thread has kMoves vectors in flight; nothing that is moved is read again, so it passes the caches by.
+constexpr int kMoves = 8;
+constexpr int kPiece = kThreads * kMoves * 16;
+
 __global__ void __launch_bounds__(kThreads) move_kernel(PageParams p, const int32_t* src, const int32_t* dst,
                                                         int step, const int32_t* count, int32_t n) {
-  const int64_t items = (int64_t)(count ? *count : n) * p.L * 2;
+  wait_for_predecessor();
+  const int pieces = (int)((p.page_bytes + kPiece - 1) / kPiece), per_pair = 2 * p.L * pieces;
+  const int64_t items = (int64_t)(count ? *count : n) * per_pair;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t pair = it / (2 * p.L);
-    const int layer = (int)(it / 2 % p.L);
+    const int64_t pair = it / per_pair;
+    const int rest = (int)(it - pair * per_pair), layer = rest / (2 * pieces), part = rest - layer * 2 * pieces;
     const int64_t a = src[pair * step], b = dst[pair * step];
     if (a < 0 || b < 0 || a >= p.n_blocks || b >= p.n_blocks) {
       if (threadIdx.x == 0) set_status(p.status, DCP_EDEVICE);
       continue;
     }
-    char* base = (it & 1 ? p.v : p.k) + layer * p.n_blocks * p.page_bytes;
-    const uint4* from = (const uint4*)(base + a * p.page_bytes);
-    uint4* to = (uint4*)(base + b * p.page_bytes);
-    for (int64_t i = threadIdx.x; i < p.page_bytes / 16; i += blockDim.x) to[i] = from[i];
+    char* const base = (part >= pieces ? p.v : p.k) + layer * p.n_blocks * p.page_bytes;
+    const int64_t at = (int64_t)(part >= pieces ? part - pieces : part) * kPiece + threadIdx.x * 16;
+    const char* from = base + a * p.page_bytes;
+    char* to = base + b * p.page_bytes;
+    Vec<4> x[kMoves];
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k)
+      if (at + k * kThreads * 16 < p.page_bytes) ld_stream(x[k], from + at + k * kThreads * 16);
+#pragma unroll
+    for (int k = 0; k < kMoves; ++k)
+      if (at + k * kThreads * 16 < p.page_bytes) st_stream(to + at + k * kThreads * 16, x[k]);
   }
 }
 
@@ -60,6 +73,7 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
                                                      const int32_t* shared, const int32_t* reserve,
                                                      int32_t n_children, const int32_t* ref_in, int32_t* child,
                                                      int32_t* ref_out, int32_t* ws) {
+  allow_dependents();
   __shared__ int s_warp[32];
   __shared__ int s_bad, s_moves;
   int2* moves = (int2*)(ws + kHead);
@@ -84,10 +98,6 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
           s_bad = 1;
         } else {
           want = (int)(total - ns);
-          for (int j = 0; j < np; ++j) {
-            const int b = tables[(int64_t)r * stride + j];
-            if (b < 0 || b >= p.n_blocks || ref_in[b] <= 0) s_bad = 1;
-          }
         }
       }
     }
@@ -95,6 +105,13 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
     const int at = block_scan(want, s_warp, &sum) + need;
     if (c < n_children) first[c] = at;
     need += sum;
+  }
+  // every page of a parent names a live block
+  for (int64_t i = threadIdx.x; i < (int64_t)n_children * stride; i += kPlan) {
+    const int c = (int)(i / stride), j = (int)(i - (int64_t)c * stride), r = parent[c];
+    if (r < 0 || r >= n_rows || (int64_t)j * p.bs >= len[r]) continue;
+    const int b = tables[(int64_t)r * stride + j];
+    if (b < 0 || b >= p.n_blocks || ref_in[b] <= 0) s_bad = 1;
   }
   // the lowest free blocks, as many as are needed
   int found = 0;
@@ -160,6 +177,7 @@ __global__ void __launch_bounds__(kPlan) free_kernel(PageParams p, const int32_t
 __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int32_t* tables, int64_t n,
                                                         const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out,
                                                         int32_t* n_live, int32_t* ws) {
+  allow_dependents();
   __shared__ int s_warp[32];
   int2* moves = (int2*)(ws + kHead);
   int32_t* to = ws + kHead + 2 * p.n_blocks;  // where every block goes
@@ -202,17 +220,31 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
   }
 }
 
+// The copy kernel; behind a bookkeeping kernel it is launched while that one runs, and waits for it.
+cudaError_t move(const PageParams& p, const int32_t* src, const int32_t* dst, int step, const int32_t* count, int32_t n,
+                 cudaStream_t s) {
+  const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, most = (int64_t)sm_count() * 6;
+  const int64_t items = (int64_t)n * p.L * 2 * pieces;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(count || items > most ? most : items));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = count ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, move_kernel, p, src, dst, step, count, n);
+}
+
 cudaError_t move_listed(const PageParams& p, int32_t* ws, cudaStream_t s) {
-  move_kernel<<<sm_count() * 8, kThreads, 0, s>>>(p, ws + kHead, ws + kHead + 1, 2, ws, 0);
-  return cudaGetLastError();
+  return move(p, ws + kHead, ws + kHead + 1, 2, ws, 0, s);
 }
 
 }  // namespace
 
 cudaError_t launch_pages_copy(const PageParams& p, const int32_t* src, const int32_t* dst, int32_t n, cudaStream_t s) {
-  const int64_t items = (int64_t)n * p.L * 2;
-  move_kernel<<<(int)(items < sm_count() * 8 ? items : sm_count() * 8), kThreads, 0, s>>>(p, src, dst, 1, nullptr, n);
-  return cudaGetLastError();
+  return move(p, src, dst, 1, nullptr, n, s);
 }
 
 cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const int32_t* len, int32_t n_rows,
