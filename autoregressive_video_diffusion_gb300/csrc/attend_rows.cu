@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   const int tile = p.row_tiles - 1 - blockIdx.x;
   const int D = a.pool.D, bs = a.pool.bs;
 
+  allow_dependents();
+  wait_for_predecessor();
   int lo, len;
   int64_t kv64;
   const bool sound = seq_rows(a.b, s, lo, len) & seq_kv(a.b, bs, a.pool.H, s, kh, kv64);
@@ -494,8 +496,7 @@ cudaError_t launch(const RowParams& p, cudaStream_t s) {
   const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, kRowThreads, Rows<T, DP, MW>::kSmem, &blocks);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
-  rows_kernel<T, DP, MW><<<grid, kRowThreads, Rows<T, DP, MW>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(rows_kernel<T, DP, MW>, grid, kRowThreads, Rows<T, DP, MW>::kSmem, s, p);
 }
 
 // Rows of one CTA: all of a KV head's rows where they fit 16, else 64.

@@ -342,6 +342,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int qt = p.q_tiles - 1 - item % p.q_tiles;  // the rows that see most keys first
   it.kh = item / p.q_tiles % a.pool.H;
   it.s = item / p.q_tiles / a.pool.H;
+  allow_dependents();
+  wait_for_predecessor();
   if (!seq_rows(a.b, it.s, it.lo, it.len)) return;
   const int n_rows = it.len * a.G;
   it.row0 = qt * 2 * kRows;
@@ -874,8 +876,7 @@ cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap&
   const int64_t items = (int64_t)p.q_tiles * p.a.pool.H * p.a.b.n_seqs;
   const int64_t grid = p.whole + (items - p.whole) * p.splits;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  tile_kernel<HALVES><<<(unsigned)grid, kTileThreads, Shape<HALVES>::kSmem, s>>>(p, k, v);
-  return cudaGetLastError();
+  return launch_behind(tile_kernel<HALVES>, dim3((unsigned)grid), kTileThreads, Shape<HALVES>::kSmem, s, p, k, v);
 }
 
 }  // namespace

@@ -43,6 +43,7 @@ constexpr int kPiece = kThreads * kMoves * 16;
 
 __global__ void __launch_bounds__(kThreads) move_kernel(PageParams p, const int32_t* src, const int32_t* dst,
                                                         int step, const int32_t* count, int32_t n) {
+  allow_dependents();
   wait_for_predecessor();
   const int pieces = (int)((p.page_bytes + kPiece - 1) / kPiece), per_pair = 2 * p.L * pieces;
   const int64_t items = (int64_t)(count ? *count : n) * per_pair;
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
                                                      int32_t n_children, const int32_t* ref_in, int32_t* child,
                                                      int32_t* ref_out, int32_t* ws) {
   allow_dependents();
+  wait_for_predecessor();
   __shared__ int s_warp[32];
   __shared__ int s_bad, s_moves;
   int2* moves = (int2*)(ws + kHead);
@@ -158,6 +160,8 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
 
 __global__ void __launch_bounds__(kPlan) free_kernel(PageParams p, const int32_t* tables, int64_t n,
                                                      const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out) {
+  allow_dependents();
+  wait_for_predecessor();
   if (ref_in != ref_out)
     for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) ref_out[b] = ref_in[b];
   __syncthreads();
@@ -178,6 +182,7 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
                                                         const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out,
                                                         int32_t* n_live, int32_t* ws) {
   allow_dependents();
+  wait_for_predecessor();
   __shared__ int s_warp[32];
   int2* moves = (int2*)(ws + kHead);
   int32_t* to = ws + kHead + 2 * p.n_blocks;  // where every block goes
@@ -220,21 +225,12 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
   }
 }
 
-// The copy kernel; behind a bookkeeping kernel it is launched while that one runs, and waits for it.
 cudaError_t move(const PageParams& p, const int32_t* src, const int32_t* dst, int step, const int32_t* count, int32_t n,
                  cudaStream_t s) {
   const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, most = (int64_t)sm_count() * 6;
   const int64_t items = (int64_t)n * p.L * 2 * pieces;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(count || items > most ? most : items));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = count ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, move_kernel, p, src, dst, step, count, n);
+  return launch_behind(move_kernel, dim3((unsigned)(count || items > most ? most : items)), kThreads, 0, s, p, src, dst,
+                       step, count, n);
 }
 
 cudaError_t move_listed(const PageParams& p, int32_t* ws, cudaStream_t s) {
@@ -251,23 +247,22 @@ cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const 
                               int32_t stride, const int32_t* parent, const int32_t* shared, const int32_t* reserve,
                               int32_t n_children, const int32_t* ref_in, int32_t* child_tables, int32_t* ref_out,
                               int32_t* ws, cudaStream_t s) {
-  fork_kernel<<<1, kPlan, 0, s>>>(p, tables, len, n_rows, stride, parent, shared, reserve, n_children, ref_in,
-                                  child_tables, ref_out, ws);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(fork_kernel, dim3(1), kPlan, 0, s, p, tables, len, n_rows, stride, parent, shared,
+                                      reserve, n_children, ref_in, child_tables, ref_out, ws);
   return e != cudaSuccess ? e : move_listed(p, ws, s);
 }
 
 cudaError_t launch_pages_free(const PageParams& p, const int32_t* tables, int32_t n_rows, int32_t stride,
                               const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out, cudaStream_t s) {
-  free_kernel<<<1, kPlan, 0, s>>>(p, tables, (int64_t)n_rows * stride, ref_in, tables_out, ref_out);
-  return cudaGetLastError();
+  return launch_behind(free_kernel, dim3(1), kPlan, 0, s, p, tables, (int64_t)n_rows * stride, ref_in, tables_out,
+                       ref_out);
 }
 
 cudaError_t launch_pages_compact(const PageParams& p, const int32_t* tables, int32_t n_rows, int32_t stride,
                                  const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out, int32_t* n_live,
                                  int32_t* ws, cudaStream_t s) {
-  compact_kernel<<<1, kPlan, 0, s>>>(p, tables, (int64_t)n_rows * stride, ref_in, tables_out, ref_out, n_live, ws);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(compact_kernel, dim3(1), kPlan, 0, s, p, tables, (int64_t)n_rows * stride, ref_in,
+                                      tables_out, ref_out, n_live, ws);
   return e != cudaSuccess ? e : move_listed(p, ws, s);
 }
 

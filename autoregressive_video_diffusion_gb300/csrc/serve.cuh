@@ -2,6 +2,8 @@
 // kernels.
 #pragma once
 
+#include <utility>
+
 #include "dcp_internal.cuh"
 
 namespace dcp {
@@ -92,6 +94,24 @@ cudaError_t launch_pages_compact(const PageParams& p, const int32_t* tables, int
                                  int32_t* ws, cudaStream_t s);
 
 #ifdef __CUDACC__
+
+// Launch with programmatic stream serialization: the kernel's CTAs may take their places while its predecessor on the
+// stream drains.  Every kernel launched so waits for its predecessor before it touches global memory and lets its own
+// successor come at once (a call of a few microseconds is mostly launch).
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // Sequence s of the batch: its first row of q and its length, checked.  False (and the status word) where they are
 // inconsistent: the caller then leaves the sequence alone.
