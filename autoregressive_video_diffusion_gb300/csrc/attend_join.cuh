@@ -5,10 +5,12 @@
 
 namespace dcp {
 
-// A split leaves for each of its rows [m, l, o_0 .. o_{D-1}] in fp32: the running maximum in units of log2, and the
-// sums of weights and weighted values relative to it.  An item's parts are [split][rows][D + 2].
+// A split leaves for each of its rows [m, l, -, -, o_0 .. o_{D-1}] in fp32: the running maximum in units of log2, and
+// the sums of weights and weighted values relative to it.  An item's parts are [split][rows][kPartHead + D].
+constexpr int kPartHead = 4;
+
 __device__ __forceinline__ float* part_of(float* parts, int64_t item, int splits, int split, int rows, int D, int r) {
-  return parts + ((item * splits + split) * rows + r) * (int64_t)(D + 2);
+  return parts + ((item * splits + split) * rows + r) * (int64_t)(kPartHead + D);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -25,65 +27,91 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // Called by a whole CTA after its part is written; true for the item's last CTA.  The parts are read in the order of
 // the splits, so the result does not depend on which CTA comes last.
 __device__ __forceinline__ bool last_of(uint32_t* done, int splits, int* s_last) {
-  __threadfence();
-  __syncthreads();
+  __syncthreads();  // the other threads' writes are ordered before this thread's release
   if (threadIdx.x == 0) {
-    const uint32_t before = atomicAdd(done, 1);
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(done) : "memory");
     *s_last = before == (uint32_t)splits - 1;
     if (*s_last) *done = 0;
-    __threadfence();
   }
   __syncthreads();
   return *s_last;
 }
 
 // Joins `splits` parts of `rows` rows (`stride` rows a part) whose first is row `row0` of (token, head of the KV
-// head) rows, sequence start lo.  Called by a whole CTA; scratch: join_scratch(rows, splits) bytes of shared memory.
-// First every part's maximum and sum, all at once, then the weights of the parts, then the values with many loads in
-// flight: a loop that reads a part after the other pays a memory latency for each.
-__host__ __device__ constexpr int64_t join_scratch(int rows, int splits) { return ((int64_t)rows * splits * 2 + rows) * 4; }
+// head) rows, sequence start lo.  Called by a whole CTA; scratch: `room` bytes of shared memory, at least
+// join_scratch(rows, splits).  Everything is fetched at once where it fits the scratch (a loop over the parts in global
+// memory pays a memory latency every few of them: 5 us for 12 parts of 5 rows, 1 us this way), else the maxima and sums
+// first and the values with several loads in flight.
+__host__ __device__ constexpr int64_t join_scratch(int rows, int splits) { return (int64_t)rows * (splits + 1) * 4; }
 
 template <typename T>
 __device__ __forceinline__ void join_parts(const AttendParams& a, const float* part, int splits, int stride, int rows,
-                                           int row0, int lo, int kh, float* scratch) {
-  const int D = a.pool.D, quads = D / 4;
-  const int64_t step = (int64_t)stride * (D + 2);
-  float* const weight = scratch;                 // [rows][splits]: the maximum, then the part's weight
-  float* const sum = weight + rows * splits;     // [rows][splits]
-  float* const inv = sum + rows * splits;        // [rows]
+                                           int row0, int lo, int kh, uint8_t* scratch, int64_t room) {
+  const int D = a.pool.D, quads = D / 4, width = kPartHead + D;
+  int64_t step = (int64_t)stride * width;
+  float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]
+  float* const inv = weight + rows * splits;                // [rows]
+  const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
   __syncthreads();
-  for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
-    const int r = u / splits, k = u - r * splits;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + k * step + (int64_t)r * (D + 2)));
-    weight[u] = ml.x;
-    sum[u] = ml.y;
-  }
-  __syncthreads();
-  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-    float top = -INFINITY, l = 0.f;
-    for (int k = 0; k < splits; ++k) top = fmaxf(top, weight[r * splits + k]);
-    for (int k = 0; k < splits; ++k) {
-      // a split that saw no key of this row has the sum 0
-      const float w = sum[r * splits + k] == 0.f ? 0.f : exp2_fast(weight[r * splits + k] - top);
-      weight[r * splits + k] = w;
-      if (w != 0.f) l += w * sum[r * splits + k];
+  const bool local = used + (int64_t)rows * splits * width * 4 <= room;
+  if (local) {
+    const int chunks = rows * width / 4;
+    const uint32_t to = smem_u32(scratch + used);
+    for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
+      const int k = u / chunks;
+      cp_async16(to + u * 16, part + k * step + (u - k * chunks) * 4);
     }
-    inv[r] = l != 0.f ? 1.f / l : 0.f;
-    const int R = row0 + r, tok = R / a.G;
-    if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(top, l);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    part = reinterpret_cast<const float*>(scratch + used);
+    step = (int64_t)rows * width;
+  }
+  // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
+  for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+    const int lane = threadIdx.x & 31;
+    float2 ml[3];
+    float top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int k = lane + 32 * j;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (k < splits) {
+        const float2* at = reinterpret_cast<const float2*>(part + k * step + (int64_t)r * width);
+        ml[j] = local ? *at : __ldcg(at);
+      }
+      if (ml[j].y != 0.f) top = fmaxf(top, ml[j].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int k = lane + 32 * j;
+      const float w = ml[j].y == 0.f ? 0.f : exp2_fast(ml[j].x - top);
+      if (k < splits) weight[r * splits + k] = w;
+      if (w != 0.f) l += w * ml[j].y;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    if (lane == 0) {
+      inv[r] = l != 0.f ? 1.f / l : 0.f;
+      const int R = row0 + r, tok = R / a.G;
+      if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(top, l);
+    }
   }
   __syncthreads();
   for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
     const int r = u / quads, d = (u - r * quads) * 4;
-    const float* at = part + (int64_t)r * (D + 2) + 2 + d;
+    const float* at = part + (int64_t)r * width + kPartHead + d;
     const float* w = weight + r * splits;
     float o[4] = {};
 #pragma unroll 8
     for (int k = 0; k < splits; ++k) {
-      const float2 x0 = __ldcg(reinterpret_cast<const float2*>(at + k * step));
-      const float2 x1 = __ldcg(reinterpret_cast<const float2*>(at + k * step + 2));
+      const float4* from = reinterpret_cast<const float4*>(at + k * step);
+      const float4 x = local ? *from : __ldcg(from);
       const float wk = w[k];
-      if (wk != 0.f) o[0] += wk * x0.x, o[1] += wk * x0.y, o[2] += wk * x1.x, o[3] += wk * x1.y;
+      if (wk != 0.f) o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;
     }
     const int R = row0 + r, tok = R / a.G;
     const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G);

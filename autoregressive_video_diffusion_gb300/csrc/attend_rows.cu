@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     if (p.splits > 1) {
       float* part = part_of(p.part, item, p.splits, split, 16 * MW, D, r);
       if (d == 0) *reinterpret_cast<float2*>(part) = make_float2(mr, lr);
-      *reinterpret_cast<float2*>(part + 2 + d) = make_float2(y0, y1);
+      *reinterpret_cast<float2*>(part + kPartHead + d) = make_float2(y0, y1);
       return;
     }
     const float inv = lr != 0.f ? 1.f / lr : 0.f;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   }
   if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
     join_parts<T>(a, part_of(p.part, item, p.splits, 0, 16 * MW, D, 0), p.splits, 16 * MW, rows, row0, lo, kh,
-                  reinterpret_cast<float*>(smem));
+                  smem, R::kSmem);
 }
 
 template <typename T, int DP, int MW>
@@ -530,7 +530,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   r.splits = splits < 1 ? 1 : (int)splits;
   r.span = (int)(span < kMaxKv ? span : kMaxKv);
   r.done_bytes = r.splits > 1 ? ((size_t)items * 4 + 255) & ~(size_t)255 : 0;
-  r.bytes = r.splits > 1 ? r.done_bytes + (size_t)items * r.splits * per * (a.pool.D + 2) * 4 : 0;
+  r.bytes = r.splits > 1 ? r.done_bytes + (size_t)items * r.splits * per * (kPartHead + a.pool.D) * 4 : 0;
   return r;
 }
 

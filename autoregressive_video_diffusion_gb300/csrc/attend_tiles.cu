@@ -52,7 +52,7 @@ struct Item {                          // what a CTA works on
 // pages are cut into `subs` tiles.
 struct Tiling {
   int bs, box, pages, subs;
-  bool whole;                          // every tile is 128 consecutive positions, tile t from 128 t on
+  int span;                            // positions of every tile where they are consecutive and as many, else 0
   __device__ __forceinline__ int tile_of(int pos) const {
     return subs == 1 ? pos / (pages * bs) : pos / bs * subs + pos % bs / kKeys;
   }
@@ -62,6 +62,7 @@ struct Tiling {
   __device__ __forceinline__ int count(int t) const {
     return subs == 1 ? pages * bs : min(kKeys, bs - t % subs * kKeys);
   }
+  __device__ __forceinline__ int columns() const { return pages * box; }  // of a tile, the rest stays empty
   __device__ __forceinline__ bool gaps() const { return subs == 1 && box != bs; }
   // position of column c relative to first(t), -1 where no position stands
   __device__ __forceinline__ int place(int t, int c) const {
@@ -78,7 +79,7 @@ struct TileParams {
   int whole;                           // items of one CTA each before those that are split
   float scale_log2;                    // |scale| log2 e
   uint32_t idesc_qk, idesc_pv;
-  float* part;                         // [item][split][256][D + 2] partial results
+  float* part;                         // [item][split][256][kPartHead + D] partial results
   uint32_t* done;                      // [item] splits finished, 0 between calls
 };
 
@@ -288,9 +289,9 @@ __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, in
 
 // The key tiles [x, y) of which every row at cache positions c_lo .. c_hi sees every key.
 __device__ __forceinline__ int2 open_tiles(const AttendParams& a, const Tiling& tl, int kv, int c_lo, int c_hi) {
-  if (!tl.whole) return make_int2(0, 0);
+  if (!tl.span) return make_int2(0, 0);
   const int end = a.causal ? min(kv, c_lo + 1) : kv, begin = a.window >= 0 ? max(0, c_hi - a.window) : 0;
-  return make_int2((begin + kKeys - 1) / kKeys, max(end, 0) / kKeys);
+  return make_int2((begin + tl.span - 1) / tl.span, max(end, 0) / tl.span);
 }
 __device__ __forceinline__ bool within(int2 range, int t) { return t >= range.x && t < range.y; }
 
@@ -415,6 +416,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     sh.far = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // rows of the ring no page ever fills: a weight of 0 must meet a value of 0 there
+  if (tl.columns() < kKeys) {
+    const int rows = kKeys - tl.columns();
+    for (int u = threadIdx.x; u < Sh::kSlots * HALVES * rows * 8; u += kTileThreads) {
+      const int tile = u / (rows * 8), at = u - tile * rows * 8;
+      *reinterpret_cast<uint4*>(gbase + 2 * Sh::kTile + tile * Sh::kHalf + (tl.columns() * 8 + at) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+  }
   if (warp == kSoftWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
                  : "memory");
@@ -485,7 +496,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     for (bool careful = false;; careful = true) {
       for (int t = t0; t < t1 && ok; ++t) {
-        uint32_t see[2] = {~0u, ~0u};  // columns the row sees
+        // columns the row sees: those that stand for keys, in a masked tile those it may see
+        uint32_t see[2] = {low_bits(tl.columns() - 64 * hf), low_bits(tl.columns() - 64 * hf - 32)};
         const bool masked = !within(mine_open, t);
         if (masked) {
           const int p0 = tl.first(t);
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tm_ld32(x[1], t_s + 64 * hf + 32);
           wait_ld(x[0]);
           wait_ld(x[1]);
-          if (masked) {
+          if (masked || tl.columns() < kKeys) {
 #pragma unroll
             for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
           }
@@ -662,7 +674,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int u = 0; u < 32; u += 2)
           if (d0 + u < D)
-            *reinterpret_cast<float2*>(part + 2 + d0 + u) =
+            *reinterpret_cast<float2*>(part + kPartHead + d0 + u) =
                 make_float2(__uint_as_float(o[u]), __uint_as_float(o[u + 1]));
       } else {
 #pragma unroll
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4 * HALVES; ++e) {
           const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
-          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, lead);
+          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, 16 * e < a.pool.D ? lead : 0);
         }
         mma_commit(s_full(i), lead);
       };
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
     join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0), splits, 2 * kRows,
                               it.rows[0] + it.rows[1], it.row0, it.lo, it.kh,
-                              reinterpret_cast<float*>(gbase));
+                              gbase, Sh::kSmem - Sh::kHead);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -900,7 +912,7 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   t.whole = t.splits == 1 ? items : rounds * sms;
   const size_t cut = (size_t)(items - t.whole);
   t.done_bytes = (cut * 4 + 255) & ~(size_t)255;
-  t.bytes = t.done_bytes + cut * t.splits * 2 * kRows * (a.pool.D + 2) * 4;
+  t.bytes = t.done_bytes + cut * t.splits * 2 * kRows * (kPartHead + a.pool.D) * 4;
   return t;
 }
 
@@ -914,7 +926,7 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
   p.tl.pages = kKeys / p.tl.box;
   p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
-  p.tl.whole = bs % kKeys == 0 || (p.tl.box == bs && p.tl.pages * bs == kKeys);
+  p.tl.span = bs % kKeys == 0 ? kKeys : bs < kKeys && p.tl.box == bs ? p.tl.pages * bs : 0;
   p.splits = t.splits;
   p.whole = (int)t.whole;
   p.q_tiles = t.q_tiles;
@@ -923,7 +935,7 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   const float mag = a.scale < 0.f ? -a.scale : a.scale;
   p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
   p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
-  p.idesc_pv = idesc(a.pool.D <= 64 ? 64 : 128, true, false);
+  p.idesc_pv = idesc((a.pool.D + 15) / 16 * 16, true, false);
   p.done = (uint32_t*)ws;
   p.part = (float*)((char*)ws + t.done_bytes);
   CUtensorMap mk, mv;
