@@ -470,6 +470,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
     const float sc = p.scale_log2;
     const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
+    const bool narrow = tl.columns() < kKeys;
+    const uint32_t see_open[2] = {low_bits(tl.columns() - 64 * hf), low_bits(tl.columns() - 64 * hf - 32)};
     float m = -INFINITY, l = 0.f, seen = -INFINITY;  // seen: the row's maximum so far
     auto move_to = [&](float m2, bool rescale) {     // the row's sums relative to m2
       const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
@@ -496,9 +498,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     for (bool careful = false;; careful = true) {
       for (int t = t0; t < t1 && ok; ++t) {
-        // columns the row sees: those that stand for keys, in a masked tile those it may see
-        uint32_t see[2] = {low_bits(tl.columns() - 64 * hf), low_bits(tl.columns() - 64 * hf - 32)};
-        const bool masked = !within(mine_open, t);
+        // columns the row sees: in a masked tile those it may see, else those that stand for keys
+        uint32_t see[2] = {see_open[0], see_open[1]};
+        const bool masked = !within(mine_open, t), hide = masked || narrow;
         if (masked) {
           const int p0 = tl.first(t);
           if (!tl.gaps()) {
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tm_ld32(x[1], t_s + 64 * hf + 32);
           wait_ld(x[0]);
           wait_ld(x[1]);
-          if (masked || tl.columns() < kKeys) {
+          if (hide) {
 #pragma unroll
             for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
           }
@@ -761,15 +763,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t t_s = tmem + i * kKeys, t_o = tmem + 256 + i * 128, q = desc_lo(q_smem + i * Sh::kTile, 16);
       bool ok = te > tb ? warp_wait(q_full, 0, &sh.dead) : true;
       const uint32_t lead = elected();
+      const bool every_dim = a.pool.D > Sh::kD - 16;
       uint32_t weighed = 0, turns = 0;
       Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
       auto scores = [&](int t) {
         if (t < t0 || t >= t1) return;
         const uint32_t k = desc_lo(ring + at.slot * Sh::kTile, 16);
+        if (every_dim) {
 #pragma unroll
-        for (int e = 0; e < 4 * HALVES; ++e) {
-          const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
-          mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, 16 * e < a.pool.D ? lead : 0);
+          for (int e = 0; e < 4 * HALVES; ++e) {
+            const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
+            mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, lead);
+          }
+        } else {
+#pragma unroll 1
+          for (int e = 0; 16 * e < a.pool.D; ++e) {
+            const uint32_t step = ((e >> 2) * Sh::kHalf + (e & 3) * 32) >> 4;
+            mma_ss(t_s, q + step, kDescHi, k + step, kDescHi, p.idesc_qk, e > 0, lead);
+          }
         }
         mma_commit(s_full(i), lead);
       };
