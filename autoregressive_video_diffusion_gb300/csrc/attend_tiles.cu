@@ -8,10 +8,12 @@
 //   values   O += P V       P from tensor memory, V from shared memory, O (fp32) stays in tensor memory
 // Each row tile has its own 8 warps, so one tile's softmax runs under the other's matrix products; a row is two threads'
 // work, half of its scores each, so that an SM quarter always has several warps to choose from.  The weights are taken
-// relative to the maximum of the earlier tiles: the tile's own maximum is found alongside, and only a row that has
-// outgrown m by 2^64 within one tile needs more care: its item is then done again with the tile's own maximum.  m
-// follows at the next tile, and only when the maximum has grown by more than 2^8, which leaves O untouched in almost every step; m has moved or not, the quotient O / l is the same (weights
-// keep their relative precision in bf16, sums are held in 32 bits).
+// relative to a level m that the earlier tiles have set: the maximum of the first tile, and from then on what the sums
+// of the weights say (a sum of 64 weights is within 2^6 of its largest).  m follows at the next tile, and only when a
+// tile's weights have added up to more than 2^8, which leaves O untouched in almost every step; m has moved or not, the
+// quotient O / l is the same (weights keep their relative precision in bf16, sums are held in 32 bits).  Only a row
+// whose scores rise by more than 2^64 within one tile needs more care: its item is then done again with each tile's own
+// maximum.
 //
 // Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warps 16, 17: issue the matrix products of row tile 0 and 1 (one
 // warp for both was busy for 3600 clocks a step of 2048 clocks of products).  Warps 18, 19: copy the pages of the keys
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const bool mine = r < rows_i;  // rows past the sequence's take part unmasked, and nothing of theirs is kept
     const int seen_end = a.causal && mine ? min(it.kv, c + 1) : it.kv;
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
-    const float sc = p.scale_log2;
+    const float sc = p.scale_log2, per_log2 = 1.f / sc;
     const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
     const bool narrow = tl.columns() < kKeys;
     const uint32_t see_open[2] = {low_bits(tl.columns() - 64 * hf), low_bits(tl.columns() - 64 * hf - 32)};
@@ -530,43 +532,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_after();
         if (move) move_to(grown ? seen : m, t > t0);
         uint32_t x[2][32];  // the row's scores of keys 64 hf .. 64 hf + 63
-        auto take = [&] {
-          tm_ld32(x[0], t_s + 64 * hf);
-          tm_ld32(x[1], t_s + 64 * hf + 32);
-          wait_ld(x[0]);
-          wait_ld(x[1]);
-          if (hide) {
+        auto cover = [&](int e) {
 #pragma unroll
-            for (int u = 0; u < 64; ++u) hide_unless(x[u >> 5][u & 31], see[u >> 5] & (1u << (u & 31)));
-          }
+          for (int u = 0; u < 32; ++u) hide_unless(x[e][u], see[e] & (1u << u));
         };
-        auto highest = [&] {  // of this thread's scores, rounded to what the other one hears
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int u = 0; u < 32; ++u)
-            top[u & 3] = max3(top[u & 3], x[u >> 4][2 * (u & 15)], x[u >> 4][2 * (u & 15) + 1]);
-          return __float2bfloat16_rn(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-        };
-        auto tell = [&](__nv_bfloat16 own) {
+        auto tell = [&](float y) {
+          const __nv_bfloat16 own = __float2bfloat16_rn(y);
           sh.swap.top[i][swaps & 1][hf][r] = own;
           __syncwarp();
           if (lane == 0) bar_arrive(met);
           pending = true;
           seen = fmaxf(seen, __bfloat162float(own));
         };
-        take();
-        const __nv_bfloat16 own = highest();
+        tm_ld32(x[0], t_s + 64 * hf);
+        wait_ld(x[0]);
+        tm_ld32(x[1], t_s + 64 * hf + 32);
         if (exact) {
-          tell(own);
+          wait_ld(x[1]);
+          if (hide) {
+            cover(0);
+            cover(1);
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int u = 0; u < 32; ++u) top[u & 3] = max3(top[u & 3], x[0][u], x[1][u]);
+          tell(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
           hear();
           const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
           if (__any_sync(~0u, far)) move_to(far ? seen : m, t > t0);
+        } else if (hide) {
+          cover(0);
         }
         const float off = m == -INFINITY ? 0.f : -m * sc;
         const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          if (e && !exact) {
+            wait_ld(x[1]);
+            if (hide) cover(1);
+          }
           uint32_t w[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
@@ -611,9 +616,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) bar_arrive(p_full(i));
         float y0, y1;
         unpair(add2(sum[0], sum[1]), y0, y1);
-        l += y0 + y1;
-        if (!exact) {
-          tell(own);
+        y0 += y1;
+        l += y0;
+        if (!exact) {  // the largest weight is between a 64th of the sum and the sum
+          tell(m + __log2f(y0) * per_log2);
           if ((seen - m) * sc > kFar) sh.far = 1;
         }
       }
