@@ -1,9 +1,9 @@
 // Attention of few rows a KV head (single tokens, drafts) over a bf16 cache, and of any number of rows over an fp32
 // cache, in warp-level matrix products (16 rows a warp).
 //
-// Rows are (new token, query head of the KV head) pairs.  Four warps share tiles of keys that travel page row by page
-// row through shared memory (asynchronous copies, several tiles in flight).  With MW = 4 each warp has 16 rows of its
-// own and sees every key; with MW = 1 the four warps have the same 16 rows and a quarter of each tile's keys, and
+// Rows are (new token, query head of the KV head) pairs.  The warps share tiles of keys that travel page row by page
+// row through shared memory (asynchronous copies, several tiles in flight).  With MW = 4 or 8 each warp (of as many) has 16 rows
+// of its own and sees every key; with MW = 1 four warps have the same 16 rows and a quarter of each tile's keys, and
 // join their results at the end.  Few rows read every key once, so the bound is HBM and the work is spread over the
 // keys: an item's keys are split over CTAs, the last of which joins the parts.
 //
@@ -20,9 +20,8 @@ namespace dcp {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kRowThreads = 32 * kWarps;
 constexpr int kMaxSplits = 64;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct RowParams {
@@ -37,7 +36,9 @@ struct RowParams {
 template <typename T, int DP, int MW>
 struct Rows {
   static constexpr bool kHalf = sizeof(T) == 2;
-  static constexpr int kKeys = kHalf ? 64 : DP == 128 && MW == 4 ? 16 : 32;  // keys of a tile
+  static constexpr int kWarps = MW == 8 ? 8 : 4, kThreads = 32 * kWarps;
+  static constexpr int kCtas = MW == 8 && DP == 128 ? 1 : 2;  // of an SM, by shared memory
+  static constexpr int kKeys = kHalf ? 64 : 32;         // keys of a tile
   static constexpr int kMine = kKeys * MW / kWarps;     // of them, a warp's
   static constexpr int kTiles = kMine / 8;              // in columns of 8
   static constexpr int kRow = DP * sizeof(T) + 16;      // bytes of a row in shared memory: no bank is hit twice
@@ -51,7 +52,7 @@ struct Rows {
   static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
   static constexpr int kSmem = kBuffers + kQ + kPairs;
   static_assert(join_scratch(16 * MW, kMaxSplits) <= kSmem, "the join's scratch fits where the tiles were");
-  static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * kRow, "a tile's weights fit where its keys were");
+  static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * (kHalf ? kRow : kPairK), "a tile's weights fit where its keys were");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
@@ -94,7 +95,7 @@ __device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
 }
 
 template <typename T, int DP, int MW>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
+__global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kCtas) rows_kernel(const __grid_constant__ RowParams p) {
   using R = Rows<T, DP, MW>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_off[4][R::kKeys];  // element offset of a key's row in the pool, -1: not read
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     if (t < n_tiles) {
       const uint32_t k_at = base + (t % R::kStages) * R::kStage, v_at = k_at + R::kKeys * R::kRow;
 #pragma unroll
-      for (int j = 0; j < R::kKeys * kChunks / kRowThreads; ++j) {
-        const int u = threadIdx.x + j * kRowThreads, row = u / kChunks, ch = u % kChunks;
+      for (int j = 0; j < R::kKeys * kChunks / R::kThreads; ++j) {
+        const int u = threadIdx.x + j * R::kThreads, row = u / kChunks, ch = u % kChunks;
         const int64_t off = s_off[t & 3][row];
         const bool real = off >= 0 && ch < chunks;
         const int64_t at = real ? off * (int64_t)sizeof(T) + ch * 16 : 0;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     }
   } else {
     uint8_t* qs = smem + R::kBuffers;
-    for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += kRowThreads) {
+    for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += R::kThreads) {
       const int r = u / (DP / 4), d = u % (DP / 4) * 4;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (r < rows && d < D) {
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     uint8_t* const pv = pk + R::kKeys * R::kPairK;
     if constexpr (!R::kHalf) {
 #pragma unroll 4
-      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += kRowThreads) {
+      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += R::kThreads) {
         const int row = u / kChunks, ch = u % kChunks;
         store_halves(pk + row * R::kPairK + ch * 32, *reinterpret_cast<const uint4*>(kp + row * R::kRow + ch * 16));
         store_halves(pv + row * R::kPairV + ch * 32, *reinterpret_cast<const uint4*>(vp + row * R::kRow + ch * 16));
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
       __syncthreads();
     }
     if (!all) {
-      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += kRowThreads) {
+      for (int u = threadIdx.x; u < R::kKeys * kChunks; u += R::kThreads) {
         const uint4 x = *reinterpret_cast<const uint4*>(vp + u / kChunks * R::kRow + u % kChunks * 16);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     if (poison) __syncthreads();  // every warp is done with the keys: the weights take their place
     if (!idle) {
       if (poison) {  // in plain arithmetic, skipping what a row does not see
-        T* ps = reinterpret_cast<T*>(smem + (t % R::kStages) * R::kStage) + warp * 16 * R::kMine;
+        T* ps = reinterpret_cast<T*>(R::kHalf ? smem + (t % R::kStages) * R::kStage : pk) + warp * 16 * R::kMine;
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n)
 #pragma unroll
@@ -466,14 +467,14 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         *reinterpret_cast<float2*>(at + 2 + 8 * j + 2 * c) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < rows * (DP / 2); u += kRowThreads) {
+    for (int u = threadIdx.x; u < rows * (DP / 2); u += R::kThreads) {
       const int r = u / (DP / 2), d = u % (DP / 2) * 2;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join[(w * 16 + r) * (DP + 2)]);
+      for (int w = 0; w < R::kWarps; ++w) top = fmaxf(top, join[(w * 16 + r) * (DP + 2)]);
       float sum = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < R::kWarps; ++w) {
         const float* at = join + (w * 16 + r) * (DP + 2);
         if (at[1] == 0.f) continue;
         const float k = exp2_fast(at[0] - top);
@@ -493,14 +494,17 @@ template <typename T, int DP, int MW>
 cudaError_t launch(const RowParams& p, cudaStream_t s) {
   static LaunchCache lc;
   int blocks;
-  const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, kRowThreads, Rows<T, DP, MW>::kSmem, &blocks);
+  const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, &blocks);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
-  return launch_behind(rows_kernel<T, DP, MW>, grid, kRowThreads, Rows<T, DP, MW>::kSmem, s, p);
+  return launch_behind(rows_kernel<T, DP, MW>, grid, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, s, p);
 }
 
-// Rows of one CTA: all of a KV head's rows where they fit 16, else 64.
-int rows_a_cta(const AttendParams& a) { return (int64_t)a.b.max_q * a.G <= 16 ? 16 : 64; }
+// Rows of one CTA: all of a KV head's rows where they fit 16; else 64, and 128 for fp32 (8 warps share the taking apart
+// of a tile).
+int rows_a_cta(const AttendParams& a) {
+  return (int64_t)a.b.max_q * a.G <= 16 ? 16 : a.pool.dtype == DCP_BF16 ? 64 : 128;
+}
 
 }  // namespace
 
@@ -517,9 +521,9 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
   // Two CTAs of an SM at a time: one round of pieces for a few sequences; several rounds of shorter ones where their
   // lengths may differ (6 rounds: 48 sequences of 200 .. 16000 positions take 369 us, 374 with 4, 386 with 12, 425 with
-  // 2) or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 213 us with 4 rounds,
-  // 251 with 1, 236 with 16).  No piece under two tiles (or four, in several rounds), at most kMaxSplits of an item.
-  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 6 : per == 64 && a.pool.dtype == DCP_F32 ? 4 : 1;
+  // 2) or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 197 us with 4 rounds,
+  // 270 with 1, 198 with 8).  No piece under two tiles (or four, in several rounds), at most kMaxSplits of an item.
+  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 6 : per == 128 ? 4 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
   const int64_t least = (rounds > 1 ? 4 : 2) * keys;
   if (span < least) span = least;
@@ -554,7 +558,7 @@ cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, 
     return wide ? launch<__nv_bfloat16, 128, 4>(p, s) : launch<__nv_bfloat16, 64, 4>(p, s);
   }
   if (one) return wide ? launch<float, 128, 1>(p, s) : launch<float, 64, 1>(p, s);
-  return wide ? launch<float, 128, 4>(p, s) : launch<float, 64, 4>(p, s);
+  return wide ? launch<float, 128, 8>(p, s) : launch<float, 64, 8>(p, s);
 }
 
 }  // namespace dcp
