@@ -56,12 +56,15 @@ struct Tiling {
   int bs, box, pages, subs;
   int span;                            // positions of every tile where they are consecutive and as many, else 0
   __device__ __forceinline__ int tile_of(int pos) const {
+    if (span == kKeys) return pos / kKeys;
     return subs == 1 ? pos / (pages * bs) : pos / bs * subs + pos % bs / kKeys;
   }
   __device__ __forceinline__ int first(int t) const {
+    if (span) return t * span;
     return subs == 1 ? t * pages * bs : t / subs * bs + t % subs * kKeys;
   }
   __device__ __forceinline__ int count(int t) const {
+    if (span) return span;
     return subs == 1 ? pages * bs : min(kKeys, bs - t % subs * kKeys);
   }
   __device__ __forceinline__ int columns() const { return pages * box; }  // of a tile, the rest stays empty
@@ -337,6 +340,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const Tiling tl = p.tl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // ---- set-up that needs nothing of the predecessor's
+  const uint32_t base = smem_u32(smem_raw) + Sh::kHead;
+  const uint32_t q_smem = base, ring = base + 2 * Sh::kTile;
+  uint8_t* const gbase = smem_raw + Sh::kHead;
+  const uint32_t bars = smem_u32(sh.bars);
+  auto full = [&](int i) { return bars + 8 * i; };
+  auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
+  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
+  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 2 + i); };
+  auto finished = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
+  auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
+  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 14);
+  auto turn = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 15 + i); };
+  if (warp == 0) {
+    for (int i = lane; i < 2 * Sh::kSlots + 17; i += 32) {
+      const int own = i - 2 * Sh::kSlots;  // past the ring: the order of the functions above
+      // an empty slot: the products of both row tiles; weights of a row tile: its 8 warps; a pair: its two
+      const int count = own < -Sh::kSlots ? 1 : own < 0 ? 2 : own < 2 ? 1 : own < 4 ? kSoftWarps / 2 : own < 6 ? 1
+                        : own < 14 ? 2 : own < 15 ? 32 * kSoftWarps : 1;
+      bar_init(bars + 8 * i, count);
+    }
+    if (lane == 0) sh.dead = sh.poison = sh.far = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
   // ---- the item
   Item it;
   // blocks in the order: row tile, KV head, sequence; the first `whole` items are one CTA's, the others are split
@@ -347,12 +375,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   it.s = item / p.q_tiles / a.pool.H;
   allow_dependents();
   wait_for_predecessor();
-  if (!seq_rows(a.b, it.s, it.lo, it.len)) return;
+  int64_t kv64;
+  const bool sound = seq_rows(a.b, it.s, it.lo, it.len) & seq_kv(a.b, tl.bs, a.pool.H, it.s, it.kh, kv64);
+  if (!sound) return;
   const int n_rows = it.len * a.G;
   it.row0 = qt * 2 * kRows;
   if (it.row0 >= n_rows) return;
-  int64_t kv64;
-  if (!seq_kv(a.b, tl.bs, a.pool.H, it.s, it.kh, kv64)) return;
   it.kv = (int)kv64;
   const int32_t* table = a.b.tables + (int64_t)it.s * a.b.table_stride;
 #pragma unroll
@@ -387,37 +415,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   const int2 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
 
-  // ---- set-up
-  const uint32_t base = smem_u32(smem_raw) + Sh::kHead;
-  const uint32_t q_smem = base, ring = base + 2 * Sh::kTile;
-  uint8_t* const gbase = smem_raw + Sh::kHead;
-  const uint32_t bars = smem_u32(sh.bars);
-  auto full = [&](int i) { return bars + 8 * i; };
-  auto empty = [&](int i) { return bars + 8 * (Sh::kSlots + i); };
-  auto s_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + i); };
-  auto p_full = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 2 + i); };
-  auto finished = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 4 + i); };
-  auto pair_met = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 6 + i); };
-  const uint32_t q_full = bars + 8 * (2 * Sh::kSlots + 14);
-  auto turn = [&](int i) { return bars + 8 * (2 * Sh::kSlots + 15 + i); };
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Sh::kSlots; ++i) {
-      bar_init(full(i), 1);
-      bar_init(empty(i), 2);  // the products of both row tiles
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(s_full(i), 1);
-      bar_init(p_full(i), kSoftWarps / 2);
-      bar_init(finished(i), 1);
-      bar_init(turn(i), 1);
-    }
-    for (int i = 0; i < 8; ++i) bar_init(pair_met(i), 2);
-    bar_init(q_full, 32 * kSoftWarps);
-    sh.dead = 0;
-    sh.poison = 0;
-    sh.far = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
+  // ---- the rest of the set-up
   // rows of the ring no page ever fills: a weight of 0 must meet a value of 0 there
   if (tl.columns() < kKeys) {
     const int rows = kKeys - tl.columns();
@@ -445,17 +443,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t t_s = tmem + lanes + i * kKeys, t_o = tmem + lanes + 256 + i * 128 + hf * (Sh::kD / 2);
     const int D = a.pool.D, rows_i = i ? it.rows[1] : it.rows[0];
-    {  // the rows of q into shared memory, zeros past the rows and past D
-      for (int u = threadIdx.x & 255; u < kRows * 8 * HALVES; u += 256) {
-        const int row = u / (8 * HALVES), ch = u % (8 * HALVES);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows_i && ch * 8 < D) {
-          const int R = it.row0 + i * kRows + row, tok = R / a.G, g = R - tok * a.G;
-          x = *reinterpret_cast<const uint4*>(a.q + ((int64_t)(it.lo + tok) * a.q_stride +
-                                                     (int64_t)(it.kh * a.G + g) * D + ch * 8) * 2);
+    {  // the rows of q into shared memory, zeros past the rows and past D; every load before the first store
+      constexpr int kChunks = 8 * HALVES, kStep = 256 / kChunks, kEach = kRows / kStep;
+      const int ch = threadIdx.x % kChunks, row_a = (threadIdx.x & 255) / kChunks;
+      const int step_t = kStep / a.G, step_g = kStep - step_t * a.G;
+      const int Ra = it.row0 + i * kRows + row_a;
+      int tk = Ra / a.G, gk = Ra - tk * a.G;
+      uint4 x[kEach];
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (row_a + k * kStep < rows_i && ch * 8 < D)
+          x[k] = *reinterpret_cast<const uint4*>(a.q + ((int64_t)(it.lo + tk) * a.q_stride +
+                                                        (int64_t)(it.kh * a.G + gk) * D + ch * 8) * 2);
+        tk += step_t;
+        gk += step_g;
+        if (gk >= a.G) {
+          gk -= a.G;
+          ++tk;
         }
+      }
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int row = row_a + k * kStep;
         *reinterpret_cast<uint4*>(gbase + i * Sh::kTile + (ch >> 3) * Sh::kHalf + row * 128 +
-                                  (((ch & 7) ^ (row & 7)) << 4)) = x;
+                                  (((ch & 7) ^ (row & 7)) << 4)) = x[k];
       }
       fence_proxy_async_smem();
       bar_arrive(q_full);
@@ -592,18 +604,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int n = 2 * (t - tb + (careful ? te - tb : 0)) + 1, slot = n % Sh::kSlots;
           ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
           if (!ok) break;
-          uint8_t* v = gbase + (2 + slot) * Sh::kTile;
+          uint8_t* const v = gbase + (2 + slot) * Sh::kTile + (threadIdx.x & 255) * 16;
+          const int p0 = tl.first(t), row_a = (threadIdx.x & 255) >> 3, filled = min(tl.count(t), it.kv - p0);
           bool found = false;
-          for (int u = threadIdx.x & 255; u < kKeys * 8 * HALVES; u += 256) {
-            const int row = (u >> 3) & (kKeys - 1), place = tl.place(t, row);
-            uint4* at = reinterpret_cast<uint4*>(v + (u >> 10) * Sh::kHalf + (u & 1023) * 16);
-            if (place < 0 || tl.first(t) + place >= it.kv) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
+          uint4 y[4 * HALVES];
+#pragma unroll
+          for (int k = 0; k < 4 * HALVES; ++k) y[k] = *reinterpret_cast<const uint4*>(v + k * 4096);
+#pragma unroll
+          for (int k = 0; k < 4 * HALVES; ++k) {
+            const int row = row_a + 32 * (k & 3);  // of 128 rows of 64 dims, twice
+            bool stands = row < filled;
+            if (tl.gaps()) {
+              const int place = tl.place(t, row);
+              stands = place >= 0 && p0 + place < it.kv;
             }
-            uint4 y = *at;
-            if (any_special(y.x) | any_special(y.y) | any_special(y.z) | any_special(y.w)) {
-              *at = make_uint4(no_special(y.x), no_special(y.y), no_special(y.z), no_special(y.w));
+            if (!stands) {
+              *reinterpret_cast<uint4*>(v + k * 4096) = make_uint4(0, 0, 0, 0);
+            } else if (any_special(y[k].x) | any_special(y[k].y) | any_special(y[k].z) | any_special(y[k].w)) {
+              *reinterpret_cast<uint4*>(v + k * 4096) =
+                  make_uint4(no_special(y[k].x), no_special(y[k].y), no_special(y[k].z), no_special(y[k].w));
               found = true;
             }
           }
