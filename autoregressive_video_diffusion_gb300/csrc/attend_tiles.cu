@@ -121,21 +121,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   }
   return true;
 }
-// The same by polling, for the two warps everything waits for: a try that suspends its thread wakes it late.
-__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, volatile int* dead) {
-  const long long start = clock64();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (__all_sync(~0u, ok)) return true;
-    if (__any_sync(~0u, *dead)) return false;
-    if (clock64() - start > kPatience) *dead = 1;
-  }
-}
 // The same for a whole warp: its lanes agree.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
   return __all_sync(~0u, bar_wait(bar, parity, dead));
@@ -828,7 +813,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           // The row tiles take turns, values of a tile and scores of the next at a time: one's softmax runs under the
           // other's products.  (Products in the order of their readiness brought both softmaxes into step.)
           ok = ok && warp_wait(turn(i), (turns++ & 1) ^ (i ^ 1), &sh.dead);
-          if (ok && weigh) ok = warp_poll(p_full(i), weighed++ & 1, &sh.dead);
+          if (ok && weigh) ok = warp_wait(p_full(i), weighed++ & 1, &sh.dead);
           if (!ok) break;
           fence_after();
           if (weigh) {
