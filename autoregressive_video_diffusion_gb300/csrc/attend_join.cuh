@@ -38,18 +38,20 @@ __device__ __forceinline__ bool last_of(uint32_t* done, int splits, int* s_last)
   return *s_last;
 }
 
-// Joins `splits` parts of `rows` rows (`stride` rows a part) whose first is row `row0` of (token, head of the KV
+// Joins `splits` parts of `rows` rows whose first is row `row0` of (token, head of the KV
 // head) rows, sequence start lo.  Called by a whole CTA; scratch: `room` bytes of shared memory, at least
 // join_scratch(rows, splits).  Everything is fetched at once where it fits the scratch (a loop over the parts in global
 // memory pays a memory latency every few of them: 5 us for 12 parts of 5 rows, 1 us this way), else the maxima and sums
 // first and the values with several loads in flight.
 __host__ __device__ constexpr int64_t join_scratch(int rows, int splits) { return (int64_t)rows * (splits + 1) * 4; }
 
+// The first part is at `part0`, the others from `part1` on, `step` floats apart.
 template <typename T>
-__device__ __forceinline__ void join_parts(const AttendParams& a, const float* part, int splits, int stride, int rows,
-                                           int row0, int lo, int kh, uint8_t* scratch, int64_t room) {
+__device__ __forceinline__ void join_parts(const AttendParams& a, const float* part0, const float* part1, int64_t step,
+                                           int splits, int rows, int row0, int lo, int kh, uint8_t* scratch,
+                                           int64_t room) {
   const int D = a.pool.D, quads = D / 4, width = kPartHead + D;
-  int64_t step = (int64_t)stride * width;
+  auto part = [&](int k) { return k ? part1 + (k - 1) * step : part0; };
   float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]
   float* const inv = weight + rows * splits;                // [rows]
   const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
@@ -60,37 +62,34 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
     const uint32_t to = smem_u32(scratch + used);
     for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
       const int k = u / chunks;
-      cp_async16(to + u * 16, part + k * step + (u - k * chunks) * 4);
+      cp_async16(to + u * 16, part(k) + (u - k * chunks) * 4);
     }
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
-    part = reinterpret_cast<const float*>(scratch + used);
     step = (int64_t)rows * width;
+    part0 = reinterpret_cast<const float*>(scratch + used);
+    part1 = part0 + step;
   }
   // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
   for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
     const int lane = threadIdx.x & 31;
-    float2 ml[3];
+    auto head = [&](int k) {
+      const float2* at = reinterpret_cast<const float2*>(part(k) + (int64_t)r * width);
+      return local ? *at : __ldcg(at);
+    };
     float top = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const int k = lane + 32 * j;
-      ml[j] = make_float2(-INFINITY, 0.f);
-      if (k < splits) {
-        const float2* at = reinterpret_cast<const float2*>(part + k * step + (int64_t)r * width);
-        ml[j] = local ? *at : __ldcg(at);
-      }
-      if (ml[j].y != 0.f) top = fmaxf(top, ml[j].x);
+    for (int k = lane; k < splits; k += 32) {
+      const float2 ml = head(k);
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const int k = lane + 32 * j;
-      const float w = ml[j].y == 0.f ? 0.f : exp2_fast(ml[j].x - top);
-      if (k < splits) weight[r * splits + k] = w;
-      if (w != 0.f) l += w * ml[j].y;
+    for (int k = lane; k < splits; k += 32) {
+      const float2 ml = head(k);
+      const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);
+      weight[r * splits + k] = w;
+      if (w != 0.f) l += w * ml.y;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
@@ -103,12 +102,12 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
   __syncthreads();
   for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
     const int r = u / quads, d = (u - r * quads) * 4;
-    const float* at = part + (int64_t)r * width + kPartHead + d;
+    const int64_t at = (int64_t)r * width + kPartHead + d;
     const float* w = weight + r * splits;
     float o[4] = {};
 #pragma unroll 8
     for (int k = 0; k < splits; ++k) {
-      const float4* from = reinterpret_cast<const float4*>(at + k * step);
+      const float4* from = reinterpret_cast<const float4*>(part(k) + at);
       const float4 x = local ? *from : __ldcg(from);
       const float wk = w[k];
       if (wk != 0.f) o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;

@@ -21,12 +21,15 @@ namespace dcp {
 namespace {
 
 constexpr int kMaxSplits = 64;
+constexpr int kEvenItems = 512;  // items whose tiles can be shared evenly
 
+constexpr int kMaxSms = 160;       // the join's scratch holds a part of two CTAs on each
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct RowParams {
   AttendParams a;
-  int splits, span, row_tiles;  // keys of an item are cut into pieces of `span`
+  int even;                     // 1: the CTAs share all items' key tiles evenly
+  int splits, span, row_tiles;  // else keys of an item are cut into pieces of `span`
   float scale_log2;             // |scale| log2 e
   uint32_t flip;                // sign bit of a scale below 0, put into q
   float* part;
@@ -51,7 +54,7 @@ struct Rows {
   static constexpr int kJoin = MW == 1 ? kWarps * 16 * (DP + 2) * 4 : 0;
   static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
   static constexpr int kSmem = kBuffers + kQ + kPairs;
-  static_assert(join_scratch(16 * MW, kMaxSplits) <= kSmem, "the join's scratch fits where the tiles were");
+  static_assert(join_scratch(16 * MW, MW == 1 ? 2 * kMaxSms : kMaxSplits) <= kSmem, "the join's scratch fits where the tiles were");
   static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * (kHalf ? kRow : kPairK), "a tile's weights fit where its keys were");
 };
 
@@ -94,38 +97,17 @@ __device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
   *reinterpret_cast<uint4*>(to + 16) = make_uint4(c.x, c.y, d.x, d.y);
 }
 
+// Rows [row0, row0 + rows) of (token, head of the KV head) of sequence s, which has `len` new tokens from row lo of q on
+// and `kv` cached positions, against the keys [begin, end).  The result goes to out and lse, or to `part`.
 template <typename T, int DP, int MW>
-__global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kCtas) rows_kernel(const __grid_constant__ RowParams p) {
+__device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem, int64_t (*s_off)[Rows<T, DP, MW>::kKeys],
+                                             int s, int kh, int lo, int len, int kv, int row0, int rows, int begin,
+                                             int end, float* part) {
   using R = Rows<T, DP, MW>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t s_off[4][R::kKeys];  // element offset of a key's row in the pool, -1: not read
-  __shared__ int s_last;
   const AttendParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int s = blockIdx.z / p.splits, split = blockIdx.z % p.splits, kh = blockIdx.y;
-  const int tile = p.row_tiles - 1 - blockIdx.x;
   const int D = a.pool.D, bs = a.pool.bs;
-
-  allow_dependents();
-  wait_for_predecessor();
-  int lo, len;
-  int64_t kv64;
-  const bool sound = seq_rows(a.b, s, lo, len) & seq_kv(a.b, bs, a.pool.H, s, kh, kv64);
-  if (!sound) return;
-  const int kv = (int)kv64, n_rows = len * a.G, row0 = tile * 16 * MW;
-  if (row0 >= n_rows) return;
-  const int rows = min(16 * MW, n_rows - row0);
   const int c_lo = kv - len + row0 / a.G, c_hi = kv - len + (row0 + rows - 1) / a.G;  // first and last row's position
-  // the keys some row of the item sees, and this split's piece of them
-  const int see_lo = a.window >= 0 ? max(0, c_lo - a.window) : 0, see_hi = a.causal ? min(kv, c_hi + 1) : kv;
-  int begin = see_lo, end = max(see_hi, see_lo);
-  if (p.splits > 1) {
-    // as even pieces of whole tiles as the splits allow (a longer sequence than max_kv has longer pieces)
-    const int span = max((int64_t)p.span, ((int64_t)(end - begin) + p.splits - 1) / p.splits);
-    const int whole = (span + R::kKeys - 1) / R::kKeys * R::kKeys;
-    begin = (int)min((int64_t)end, begin + (int64_t)split * whole);
-    end = (int)min((int64_t)end, (int64_t)begin + whole);
-  }
   const int n_tiles = (end - begin + R::kKeys - 1) / R::kKeys;
   const int32_t* table = a.b.tables + (int64_t)s * a.b.table_stride;
 
@@ -427,13 +409,12 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
   }
 
   // ---- results
-  const int64_t item = ((int64_t)s * a.pool.H + kh) * p.row_tiles + tile;
   auto put = [&](int r, int d, float y0, float y1, float mr, float lr) {  // two dims of a row of the item
     if (d >= D) return;
-    if (p.splits > 1) {
-      float* part = part_of(p.part, item, p.splits, split, 16 * MW, D, r);
-      if (d == 0) *reinterpret_cast<float2*>(part) = make_float2(mr, lr);
-      *reinterpret_cast<float2*>(part + kPartHead + d) = make_float2(y0, y1);
+    if (part) {
+      float* at = part + (int64_t)r * (kPartHead + D);
+      if (d == 0) *reinterpret_cast<float2*>(at) = make_float2(mr, lr);
+      *reinterpret_cast<float2*>(at + kPartHead + d) = make_float2(y0, y1);
       return;
     }
     const float inv = lr != 0.f ? 1.f / lr : 0.f;
@@ -485,9 +466,127 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       put(r, d, y0, y1, top, sum);
     }
   }
-  if (p.splits > 1 && last_of(p.done + item, p.splits, &s_last))
-    join_parts<T>(a, part_of(p.part, item, p.splits, 0, 16 * MW, D, 0), p.splits, 16 * MW, rows, row0, lo, kh,
-                  smem, R::kSmem);
+}
+
+// The keys some of the rows see.
+__device__ __forceinline__ void seen_range(const AttendParams& a, int kv, int len, int row0, int rows, int& begin,
+                                           int& end) {
+  const int c_lo = kv - len + row0 / a.G, c_hi = kv - len + (row0 + rows - 1) / a.G;
+  begin = a.window >= 0 ? max(0, c_lo - a.window) : 0;
+  end = max(a.causal ? min(kv, c_hi + 1) : kv, begin);
+}
+
+// An item is a tile of rows of one sequence and KV head.
+template <typename T, int DP, int MW>
+__global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kCtas)
+    rows_kernel(const __grid_constant__ RowParams p) {
+  using R = Rows<T, DP, MW>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t s_off[4][R::kKeys];  // element offset of a key's row in the pool, -1: not read
+  __shared__ int s_last;
+  const AttendParams& a = p.a;
+  const int D = a.pool.D, width = kPartHead + D;
+  allow_dependents();
+  wait_for_predecessor();
+
+  if constexpr (MW == 1) {
+    if (p.even) {
+      // Every CTA takes the same number of consecutive key tiles of all items together: the sums of the items' tiles,
+      // then the pieces of the items that lie in the CTA's share.  At most its first and its last piece are parts.
+      __shared__ int64_t s_first[kEvenItems + 1];  // tiles before an item
+      __shared__ int64_t s_warp[R::kWarps];
+      const int items = a.b.n_seqs * a.pool.H, each = (items + R::kThreads - 1) / R::kThreads;
+      const int i0 = min(items, (int)threadIdx.x * each), i1 = min(items, i0 + each);
+      auto look = [&](int i, int& lo, int& len, int& kv, int& begin, int& end) -> int64_t {
+        int64_t kv64;
+        const bool sound = seq_rows(a.b, i / a.pool.H, lo, len) &
+                           seq_kv(a.b, a.pool.bs, a.pool.H, i / a.pool.H, i % a.pool.H, kv64);
+        if (!sound || len == 0) return 0;
+        kv = (int)kv64;
+        seen_range(a, kv, len, 0, len * a.G, begin, end);
+        return max(1, (end - begin + R::kKeys - 1) / R::kKeys);  // rows that see nothing have their result too
+      };
+      int lo, len, kv, begin, end;
+      int64_t mine = 0;
+      for (int i = i0; i < i1; ++i) {
+        s_first[i] = mine;
+        mine += look(i, lo, len, kv, begin, end);
+      }
+      int64_t before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, before, o);
+        if ((threadIdx.x & 31) >= o) before += y;
+      }
+      if ((threadIdx.x & 31) == 31) s_warp[threadIdx.x >> 5] = before;
+      __syncthreads();
+      int64_t total = 0;
+#pragma unroll
+      for (int w = 0; w < R::kWarps; ++w) {
+        if (w < threadIdx.x >> 5) before += s_warp[w];
+        total += s_warp[w];
+      }
+      for (int i = i0; i < i1; ++i) s_first[i] += before - mine;
+      if (threadIdx.x == 0) s_first[items] = total;
+      __syncthreads();
+      // two tiles a CTA at least
+      const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + 1) / 2));
+      if (blockIdx.x >= ctas) return;
+      int64_t at = blockIdx.x * total / ctas;
+      const int64_t to = (blockIdx.x + 1) * total / ctas;
+      int item = 0;
+      for (int step = kEvenItems; step; step >>= 1)  // the last item that begins at or before `at`
+        if (item + step < items && s_first[item + step] <= at) item += step;
+      for (; at < to; ++item) {
+        const int64_t f0 = s_first[item], f1 = s_first[item + 1];
+        if (f1 <= at) continue;
+        look(item, lo, len, kv, begin, end);
+        const int64_t stop = min(to, f1);
+        const bool opens = at == f0, closes = stop == f1;
+        const int s = item / a.pool.H, kh = item % a.pool.H, rows = len * a.G;
+        const int from = begin + (int)(at - f0) * R::kKeys, upto = min(end, begin + (int)(stop - f0) * R::kKeys);
+        const int64_t slot = (int64_t)16 * width;  // parts of a CTA: of an item it goes on with, of one it begins
+        float* const part = opens && closes ? nullptr : p.part + (2 * (int64_t)blockIdx.x + opens) * slot;
+        attend_piece<T, DP, 1>(p, smem, s_off, s, kh, lo, len, kv, 0, rows, from, upto, part);
+        if (part) {
+          const int64_t c0 = ((f0 + 1) * ctas - 1) / total, c1 = (f1 * ctas - 1) / total;
+          const int n = (int)(c1 - c0 + 1);
+          if (last_of(p.done + item, n, &s_last))
+            join_parts<T>(a, p.part + (2 * c0 + 1) * slot, p.part + 2 * (c0 + 1) * slot, 2 * slot, n, rows, 0, lo, kh,
+                          smem, R::kSmem);
+        }
+        at = stop;
+        __syncthreads();
+      }
+      return;
+    }
+  }
+
+  const int s = blockIdx.z / p.splits, split = blockIdx.z % p.splits, kh = blockIdx.y;
+  const int tile = p.row_tiles - 1 - blockIdx.x;
+  int lo, len;
+  int64_t kv64;
+  const bool sound = seq_rows(a.b, s, lo, len) & seq_kv(a.b, a.pool.bs, a.pool.H, s, kh, kv64);
+  if (!sound) return;
+  const int kv = (int)kv64, n_rows = len * a.G, row0 = tile * 16 * MW;
+  if (row0 >= n_rows) return;
+  const int rows = min(16 * MW, n_rows - row0);
+  int begin, end;
+  seen_range(a, kv, len, row0, rows, begin, end);
+  if (p.splits > 1) {
+    // as even pieces of whole tiles as the splits allow (a longer sequence than max_kv has longer pieces)
+    const int span = max((int64_t)p.span, ((int64_t)(end - begin) + p.splits - 1) / p.splits);
+    const int whole = (span + R::kKeys - 1) / R::kKeys * R::kKeys;
+    begin = (int)min((int64_t)end, begin + (int64_t)split * whole);
+    end = (int)min((int64_t)end, (int64_t)begin + whole);
+  }
+  const int64_t item = ((int64_t)s * a.pool.H + kh) * p.row_tiles + tile;
+  float* const parts = p.splits > 1 ? part_of(p.part, item, p.splits, 0, 16 * MW, D, 0) : nullptr;
+  const int64_t step = (int64_t)16 * MW * width;
+  attend_piece<T, DP, MW>(p, smem, s_off, s, kh, lo, len, kv, row0, rows, begin, end,
+                          parts ? parts + split * step : nullptr);
+  if (parts && last_of(p.done + item, p.splits, &s_last))
+    join_parts<T>(a, parts, parts + step, step, p.splits, rows, row0, lo, kh, smem, R::kSmem);
 }
 
 template <typename T, int DP, int MW>
@@ -496,7 +595,7 @@ cudaError_t launch(const RowParams& p, cudaStream_t s) {
   int blocks;
   const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, &blocks);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
+  const dim3 grid = p.even ? dim3(p.splits) : dim3(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
   return launch_behind(rows_kernel<T, DP, MW>, grid, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, s, p);
 }
 
@@ -519,10 +618,21 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
   r.tiles = (int)(((int64_t)a.b.max_q * a.G + per - 1) / per);
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
+  // Items that may differ in length: two CTAs of an SM at a time, each with the same number of key tiles (48 sequences
+  // of 200 .. 16000 positions: 324 us, against 354 in pieces of a fixed span; items alike are cut as well by a span,
+  // without the sums: one token over 1531 positions 12.3 us, against 14.0).
+  r.even = per == 16 && items <= kEvenItems && (a.b.n_seqs > 1 || a.b.kv_per_head);
+  if (r.even) {
+    r.splits = 2 * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
+    r.span = 0;
+    r.done_bytes = ((size_t)items * 4 + 255) & ~(size_t)255;
+    r.bytes = r.done_bytes + (size_t)r.splits * 2 * 16 * (kPartHead + a.pool.D) * 4;
+    return r;
+  }
   // Two CTAs of an SM at a time: one round of pieces for a few sequences; several rounds of shorter ones where their
-  // lengths may differ (6 rounds: 48 sequences of 200 .. 16000 positions take 369 us, 374 with 4, 386 with 12, 425 with
-  // 2) or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 197 us with 4 rounds,
-  // 270 with 1, 198 with 8).  No piece under two tiles (or four, in several rounds), at most kMaxSplits of an item.
+  // lengths may differ or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 197 us
+  // with 4 rounds, 270 with 1, 198 with 8).  No piece under two tiles (or four, in several rounds), at most kMaxSplits
+  // of an item.
   const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 6 : per == 128 ? 4 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
   const int64_t least = (rounds > 1 ? 4 : 2) * keys;
@@ -542,6 +652,7 @@ cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, 
   const RowPlan r = plan_rows(a, max_kv);
   RowParams p{};
   p.a = a;
+  p.even = r.even;
   p.splits = r.splits;
   p.span = r.span;
   p.row_tiles = r.tiles;

@@ -860,9 +860,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   // ---- the item's last split joins the parts
   if (splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
-    join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0), splits, 2 * kRows,
-                              it.rows[0] + it.rows[1], it.row0, it.lo, it.kh,
-                              gbase, Sh::kSmem - Sh::kHead);
+    join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0),
+                              part_of(p.part, item - p.whole, p.splits, 1, 2 * kRows, a.pool.D, 0),
+                              (int64_t)2 * kRows * (kPartHead + a.pool.D), splits, it.rows[0] + it.rows[1], it.row0,
+                              it.lo, it.kh, gbase, Sh::kSmem - Sh::kHead);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -66,7 +66,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 // How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes (counters first,
 // zero between calls).
 struct RowPlan {
-  int tiles, splits, span;
+  int tiles, splits, span, even;
   size_t done_bytes, bytes;
 };
 bool attend_by_rows(const AttendParams& p);
