@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
 
 cudaError_t move(const PageParams& p, const int32_t* src, const int32_t* dst, int step, const int32_t* count, int32_t n,
                  cudaStream_t s) {
-  const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, most = (int64_t)sm_count() * 6;
+  const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, most = (int64_t)sm_count() * 5;
   const int64_t items = (int64_t)n * p.L * 2 * pieces;
   return launch_behind(move_kernel, dim3((unsigned)(count || items > most ? most : items)), kThreads, 0, s, p, src, dst,
                        step, count, n);
