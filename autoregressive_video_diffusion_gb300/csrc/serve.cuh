@@ -63,11 +63,15 @@ struct PageParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
-// How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes (counters first,
-// zero between calls).
+// The attention's workspace: a counter for each item whose keys are split, zero between calls and in the same place
+// whatever the sizes (calls of different sizes may share a workspace), then the parts.
+constexpr int kDoneItems = 16384;
+constexpr size_t kDoneBytes = (size_t)kDoneItems * 4;
+
+// How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes.
 struct RowPlan {
   int tiles, splits, span, even;
-  size_t done_bytes, bytes;
+  size_t bytes;
 };
 bool attend_by_rows(const AttendParams& p);
 RowPlan plan_rows(const AttendParams& p, int64_t max_kv);
@@ -77,7 +81,7 @@ cudaError_t launch_attend_rows(const AttendParams& p, int64_t max_kv, void* ws, 
 struct TilePlan {
   int q_tiles, splits;
   int64_t whole;  // items that are not split, the first ones
-  size_t done_bytes, bytes;
+  size_t bytes;
 };
 TilePlan plan_tiles(const AttendParams& p, int64_t max_kv);
 cudaError_t launch_attend_tiles(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);

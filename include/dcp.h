@@ -432,7 +432,8 @@ typedef struct dcp_attn_config {
 } dcp_attn_config;
 
 /* Workspace bytes dcp_paged_attention needs (256-byte aligned, zeroed once with dcp_workspace_init); 0 for invalid
- * arguments.  It depends on the sizes in pool, batch and cfg, not on what their arrays hold. */
+ * arguments.  It depends on the sizes in pool, batch and cfg and on the current device, not on what the arrays hold.
+ * Calls of different sizes may share one workspace that is large enough for each. */
 size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                                     int32_t Hq);
 

@@ -206,6 +206,68 @@ def test_attention_lengths_by_head(gpu, dtype, nq):
     check_attention(c, q, out, lse, 0.125, False, -1, kv_of=lens)
 
 
+RAGGED = [
+    # dtype, hq, h, d, bs, q_lens, kv_lens: single tokens and drafts of ragged batches, with and without keys
+    ("bf16", 8, 2, 128, 16, [1] * 20, [1, 7000, 0, 64, 65, 3, 129, 2048, 1, 1, 900, 16, 0, 5000, 33, 64, 63, 1, 2, 700]),
+    ("bf16", 5, 5, 64, 24, [2, 3, 1, 0, 2, 1], [2, 500, 64, 9, 128, 4000]),
+    ("f32", 4, 4, 32, 8, [1] * 9, [1, 300, 0, 32, 31, 33, 2, 65, 700]),
+    ("f32", 6, 2, 128, 32, [4, 1, 0, 5], [4, 600, 5, 97]),
+    ("bf16", 64, 64, 64, 16, [1] * 9, [30, 1, 200, 64, 0, 128, 77, 5, 300]),  # more items than are shared evenly
+    ("bf16", 16, 2, 80, 16, [8, 3, 1, 7], [900, 70, 2000, 7]),                # 64 rows a head, keys cut by a span
+]
+
+
+@pytest.mark.parametrize("case", RAGGED, ids=[str(i) for i in range(len(RAGGED))])
+@pytest.mark.parametrize("window", [-1, 100])
+def test_attention_of_ragged_batches(gpu, case, window):
+    dtype, hq, h, d, bs, q_lens, kv_lens = case
+    c = Cache(dtype, NHD, h, d, bs, q_lens, kv_lens, seed=d + window).fill()
+    q = c.normal(c.start[-1], hq, d)
+    out, lse = attend(c, q, True, window)
+    assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
+    check_attention(c, q, out, lse, d ** -0.5, True, window)
+
+
+@pytest.mark.parametrize("nq,kv,hq,h", [(1100, 1600, 40, 40), (100, 20000, 2, 1), (300, 3000, 4, 2)])
+def test_attention_items_split_over_the_keys(gpu, nq, kv, hq, h):
+    """An incomplete last round of items, and fewer items than SMs."""
+    c = Cache("bf16", HND, h, 64, 32, [nq], [kv], seed=11).fill()
+    q = c.normal(nq, hq, 64)
+    out, lse = attend(c, q, False, -1)
+    check_attention(c, q, out, lse, 0.125, False, -1)
+
+
+def test_calls_of_different_sizes_share_a_workspace(gpu):
+    cases = [("bf16", [1] * 12, [3000] * 12, 8, 4), ("bf16", [300], [5000], 4, 2), ("f32", [200, 90], [900, 90], 4, 4),
+             ("bf16", [1], [9000], 8, 8)]
+    caches = [Cache(t, HND, h, 64, 16, ql, kl, seed=i).fill() for i, (t, ql, kl, hq, h) in enumerate(cases)]
+    cfg, size = dcp.AttnConfig(), 0
+    for c, (_, _, _, hq, _) in zip(caches, cases):
+        size = max(size, dcp.dcp_attention_workspace_size(c.pool(), c.batch(), cfg, hq))
+    ws = dcp.new_workspace(size)
+    for _ in range(2):
+        for c, (_, _, _, hq, _) in zip(caches, cases):
+            q = c.normal(c.start[-1], hq, 64)
+            out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+            dcp.dcp_paged_attention(c.pool(), c.batch(), cfg, q, out, lse, ws)
+            check_attention(c, q, out, lse, 0.125, True, -1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 130])
+@pytest.mark.parametrize("rise", [3.0, 40.0, 1000.0])
+def test_attention_scores_that_rise_along_the_keys(gpu, dtype, nq, rise):
+    """Later keys outweigh the earlier ones by far: running maxima move, by more than 2^64 within a tile for the last."""
+    c = Cache(dtype, HND, 1, 64, 16, [nq], [700], seed=12)
+    j = torch.arange(700, device="cuda")[:, None, None]
+    grow = torch.where(j >= 300, 1.0 + rise * (j // 150 - 1), 1.0)
+    c.keys[0] = (c.keys[0].float() * grow).to(c.dt)
+    c.fill()
+    q = c.normal(nq, 2, 64)
+    out, lse = attend(c, q, True, -1)
+    check_attention(c, q, out, lse, 0.125, True, -1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nq", [1, 200])
 def test_attention_large_scores_strided_q_no_lse(gpu, dtype, nq):
