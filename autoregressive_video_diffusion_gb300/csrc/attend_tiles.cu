@@ -263,7 +263,7 @@ struct Shape {
   static constexpr int kHalf = kRows * 128;              // bytes of 128 rows x 64 dims
   static constexpr int kTile = kHalf * HALVES;
   static constexpr int kSlots = HALVES == 2 ? 5 : 10;    // ring of K and V tiles in turn
-  static constexpr int kHead = 3072;                     // barriers and the like, before the tiles
+  static constexpr int kHead = 3 * 1024;                    // barriers and the like, before the tiles
   static constexpr int kSmem = kHead + (2 + kSlots) * kTile;
   static_assert(join_scratch(2 * kRows, kMaxSplits) <= kSmem - kHead, "the join's scratch fits where the tiles were");
 };
