@@ -581,12 +581,13 @@ def dcp_rope_plan(cfg: RopeConfig) -> DcpRopePlanC:
 
 def _rows_of(t: torch.Tensor, pool: KVPool, batch: SeqBatch, heads: int, what: str) -> int:
     """Token stride of a [total_q][heads][D] tensor of the pool's type whose heads are dense."""
-    if t.dtype != pool.dtype or t.shape != (batch.total_q, heads, pool.D):
+    n, D = batch.total_q, pool.D
+    if t.dtype is not pool.dtype or t.shape != (n, heads, D):
         raise DcpError(what, DCP_EINVAL)
-    s = t.stride()
-    if s[2] != 1 or (s[1] != pool.D and heads > 1):
+    token, head, dim = t.stride()
+    if dim != 1 or (head != D and heads > 1):
         raise DcpError(what, DCP_EINVAL)
-    return s[0] if batch.total_q > 1 else heads * pool.D
+    return token if n > 1 else heads * D
 
 
 def dcp_rope_append(pool: KVPool, batch: SeqBatch, plan: DcpRopePlanC, q, k: torch.Tensor, v: torch.Tensor,

@@ -1,19 +1,18 @@
 // Rotary turn of the new tokens' q and k, and k, v into the cache's pages, in one pass over the data.
 //
-// A CTA takes a few tokens: each thread first loads its first vectors of q, k, v (they depend on nothing), then the
-// CTA finds the tokens' sequences, phases and page rows and builds their cos/sin in shared memory, then turns and
-// stores.  The phase in turns is an integer product modulo 2^64, so whole turns drop out exactly at any distance; cos
+// A CTA takes a token: each thread first loads its first vectors of q, k, v (they depend on nothing), then the CTA finds
+// the token's sequence, phase and page row and builds its cos/sin in shared memory, then turns and stores.  The phase in turns is an integer product modulo 2^64, so whole turns drop out exactly at any distance; cos
 // and sin are taken of the remaining fraction, once per token and pair, and shared by all heads.
 // The bound is HBM (each of q, k, v read and written once); a few tokens are bound by the chain launch -> q_start,
-// kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 73 us (5.2 TB/s), 1900 tokens
-// of 32 + 8 + 8 fp32 heads of 96 28 us (4.4 TB/s), 32 tokens 3.6 us in a graph.
+// kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 67 us (5.7 TB/s), 1900 tokens
+// of 32 + 8 + 8 fp32 heads of 96 26 us (4.8 TB/s), 32 tokens 3.6 us in a graph.
 #include "serve.cuh"
 
 namespace dcp {
 
 namespace {
 
-constexpr int kUnits = 2;  // units (one or two 16-byte vectors) a thread has in flight
+constexpr int kTurners = 128;  // threads of a CTA
 
 struct Where {
   int64_t off;   // element offset of the token's row in head 0 of the pool, -1: not stored
@@ -63,23 +62,24 @@ enum Pairs {
   kHalfAny,      // any other half: partners are read from a copy of the rows in shared memory
 };
 
-template <typename T, int PAIRS, int TOK>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+template <typename T, int PAIRS>
+__global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant__ AppendParams p) {
   using E = Elems<T>;
   constexpr int N = E::kN;
-  __shared__ Where where[TOK];
-  __shared__ float2 cs[TOK][DCP_ROPE_MAX_PAIRS];
-  __shared__ uint4 rows[PAIRS == kHalfAny ? kUnits * kThreads : 1];
-  const int t0 = blockIdx.x * TOK, n = min(TOK, p.b.total_q - t0);
+  constexpr int kUnits = PAIRS == kHalfVec ? 2 : 4;  // units (one or two vectors) a thread has in flight, twice
+  __shared__ Where where;
+  __shared__ float2 cs[DCP_ROPE_MAX_PAIRS];
+  __shared__ uint4 rows[PAIRS == kHalfAny ? kUnits * kTurners : 1];
+  const int64_t tok = blockIdx.x;
   const int D = p.pool.D, vecs = D / N, half = p.half, heads = p.Hq + 2 * p.pool.H;
   const int pair_vecs = PAIRS == kHalfVec ? half / N : 0;   // units of two vectors in a head
   const int per_head = vecs - pair_vecs;
   const int per_token = heads * per_head;
   // units of a token a thread holds at once; whole heads where they pass through shared memory
-  const int batch = PAIRS == kHalfAny ? kUnits * kThreads / per_head * per_head : kUnits * kThreads;
+  const int batch = PAIRS == kHalfAny ? kUnits * kTurners / per_head * per_head : kUnits * kTurners;
 
-  // A thread's units are kThreads apart: their head and place follow one another without a division.
-  const int head_step = kThreads / per_head, unit_step = kThreads - head_step * per_head;
+  // A thread's units are kTurners apart: their head and place follow one another without a division.
+  const int head_step = kTurners / per_head, unit_step = kTurners - head_step * per_head;
   uint4 x[2][kUnits], y[2][kUnits];
   struct Unit {
     int i, h, e;  // place in the batch, head (q, then k, then v), unit of the head
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     return Unit{(int)threadIdx.x, h, u - h * per_head};
   };
   auto next = [&](Unit& u) {
-    u.i += kThreads;
+    u.i += kTurners;
     u.h += head_step;
     u.e += unit_step;
     if (u.e >= per_head) {
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
   };
   auto there = [&](const Unit& u) { return u.i < batch && u.h < heads; };
-  auto load = [&](int t, Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
-    const T* q = (const T*)p.q + (t0 + t) * p.q_stride;
-    const T* k = (const T*)p.k + (t0 + t) * p.kv_stride - p.Hq * D;
-    const T* v = (const T*)p.v + (t0 + t) * p.kv_stride - (p.Hq + p.pool.H) * D;
+  auto load = [&](Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
+    const T* q = (const T*)p.q + tok * p.q_stride;
+    const T* k = (const T*)p.k + tok * p.kv_stride - p.Hq * D;
+    const T* v = (const T*)p.v + tok * p.kv_stride - (p.Hq + p.pool.H) * D;
 #pragma unroll
     for (int j = 0; j < kUnits; ++j, next(u)) {
       if (!there(u)) continue;
@@ -113,51 +113,48 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 
   allow_dependents();
   wait_for_predecessor();
-  load(0, first(0), x[0], y[0]);
-  if (threadIdx.x < TOK) where[threadIdx.x].seq = -1;
+  load(first(0), x[0], y[0]);
+  if (threadIdx.x == 0) where.seq = -1;
   __syncthreads();
-  for (int s = threadIdx.x; s < p.b.n_seqs; s += kThreads) {
+  for (int s = threadIdx.x; s < p.b.n_seqs; s += kTurners) {
     int lo, len;
     int64_t kv;
     const bool sound = seq_rows(p.b, s, lo, len) & seq_kv(p.b, p.pool.bs, p.pool.H, s, 0, kv);
-    if (!sound) continue;
-    for (int t = max(lo, t0); t < min(lo + len, t0 + n); ++t) {
-      const int64_t c = kv - len + (t - lo);
-      Where w{-1, (int32_t)c, s};
-      if (c >= 0) {
-        const int64_t page = c / p.pool.bs;
-        const int64_t blk = p.b.tables[s * p.b.table_stride + page];
-        if (blk >= 0 && blk < p.pool.n_blocks)
-          w.off = blk * p.pool.s_block + (c - page * p.pool.bs) * p.pool.s_row;
-        else
-          set_status(p.b.status, DCP_EDEVICE);
-      }
-      where[t - t0] = w;
+    if (!sound || tok < lo || tok >= lo + len) continue;
+    const int64_t c = kv - len + (tok - lo);
+    Where w{-1, (int32_t)c, s};
+    if (c >= 0) {
+      const int64_t page = c / p.pool.bs;
+      const int64_t blk = p.b.tables[s * p.b.table_stride + page];
+      if (blk >= 0 && blk < p.pool.n_blocks)
+        w.off = blk * p.pool.s_block + (c - page * p.pool.bs) * p.pool.s_row;
+      else
+        set_status(p.b.status, DCP_EDEVICE);
     }
+    where = w;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int t = i / half, q = i - t * half;
-    const int32_t phase = p.positions ? p.positions[t0 + t] : where[t].phase;
-    const uint64_t turn = (uint64_t)(int64_t)phase * p.turns[q];
+  for (int i = threadIdx.x; i < half; i += kTurners) {
+    const int32_t phase = p.positions ? p.positions[tok] : where.phase;
+    const uint64_t turn = (uint64_t)(int64_t)phase * p.turns[i];
     float s, c;
     sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    cs[t][q] = make_float2(c * p.amplitude, s * p.amplitude);
+    cs[i] = make_float2(c * p.amplitude, s * p.amplitude);
   }
   __syncthreads();
 
   const int batches = (per_token + batch - 1) / batch;
-  auto turn_and_store = [&](int t, Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
-    const Where w = where[t];
+  auto turn_and_store = [&](Unit u, uint4 (&a)[kUnits], uint4 (&b)[kUnits]) {
+    const Where w = where;
     if (PAIRS == kHalfAny) {
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < kUnits; ++j)
-        if (threadIdx.x + j * kThreads < batch) rows[threadIdx.x + j * kThreads] = a[j];
+        if (threadIdx.x + j * kTurners < batch) rows[threadIdx.x + j * kTurners] = a[j];
       __syncthreads();
     }
     if (w.seq < 0) return;
-    T* const q_to = (T*)p.q_out + (int64_t)(t0 + t) * p.Hq * D;
+    T* const q_to = (T*)p.q_out + (int64_t)tok * p.Hq * D;
 #pragma unroll
     for (int j = 0; j < kUnits; ++j, next(u)) {
       if (!there(u)) continue;
@@ -175,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
           E::get(b[j], g);
 #pragma unroll
           for (int k = 0; k < N; ++k) {
-            const float2 r = cs[t][e * N + k];
+            const float2 r = cs[e * N + k];
             const float f2 = f[k] * r.x - g[k] * r.y;
             g[k] = f[k] * r.y + g[k] * r.x;
             f[k] = f2;
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         for (int k = 0; k < N; k += 2) {
           const int q = v * (N / 2) + k / 2;
           if (q >= half) continue;
-          const float2 r = cs[t][q];
+          const float2 r = cs[q];
           const float f2 = f[k] * r.x - f[k + 1] * r.y;
           f[k + 1] = f[k] * r.y + f[k + 1] * r.x;
           f[k] = f2;
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         for (int k = 0; k < N; ++k) {
           const int d = v * N + k;
           if (d >= 2 * half) continue;
-          const float2 r = cs[t][d < half ? d : d - half];
+          const float2 r = cs[d < half ? d : d - half];
           f[k] = d < half ? f[k] * r.x - E::one(row, d + half) * r.y : f[k] * r.x + E::one(row, d - half) * r.y;
         }
         a[j] = E::put(f);
@@ -218,39 +215,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
   };
   // the next batch's loads are in flight while a batch is turned and stored
-  Unit u = first(0);
-  int t = 0, left = batches;
-  bool more = true;
-#pragma unroll 2
-  for (int k = 0; more; k ^= 1) {
-    const Unit now = u;
-    const int t_now = t;
-    if (--left == 0) {
-      left = batches;
-      ++t;
-      u = first(0);
-    } else {
-      u = first((batches - left) * batch);
-    }
-    more = t < n;
-    if (k == 0) {
-      if (more) load(t, u, x[1], y[1]);
-      turn_and_store(t_now, now, x[0], y[0]);
-    } else {
-      if (more) load(t, u, x[0], y[0]);
-      turn_and_store(t_now, now, x[1], y[1]);
-    }
+  for (int b = 0; b < batches; b += 2) {
+    if (b + 1 < batches) load(first((b + 1) * batch), x[1], y[1]);
+    turn_and_store(first(b * batch), x[0], y[0]);
+    if (b + 1 == batches) break;
+    if (b + 2 < batches) load(first((b + 2) * batch), x[0], y[0]);
+    turn_and_store(first((b + 1) * batch), x[1], y[1]);
   }
 }
 
 template <typename T, int PAIRS>
 cudaError_t launch_tokens(const AppendParams& p, cudaStream_t s) {
-  // One token a CTA until the SMs have several CTAs each, then two, so that the look-up is shared.  (Two tokens and two
-  // units in flight: 6240 tokens of 120 heads 76 us, 2400 of 48 fp32 heads 31 us; four and four 79 and 39; four and two
-  // 81 and 35; one and four 80 and 44.)
-  if (p.b.total_q <= 8 * sm_count())
-    return launch_behind(append_kernel<T, PAIRS, 1>, dim3((unsigned)p.b.total_q), kThreads, 0, s, p);
-  return launch_behind(append_kernel<T, PAIRS, 2>, dim3((unsigned)((p.b.total_q + 1) / 2)), kThreads, 0, s, p);
+  // A token a CTA of 128 threads, so that many CTAs are at different places of their chain.  (6240 tokens of 120 heads /
+  // 1900 of 48 fp32 heads whose units are two vectors: 4 units a thread 67 / 35 us, 2 units 71 / 26; two tokens a CTA
+  // of 256 threads 74 / 29, four 81 / 35.)
+  return launch_behind(append_kernel<T, PAIRS>, dim3((unsigned)p.b.total_q), kTurners, 0, s, p);
 }
 
 template <typename T>

@@ -38,6 +38,19 @@ __device__ int block_scan(int x, int* s_warp, int* total) {
   return v - x + (warp ? before : 0);
 }
 
+// ref_out = ref_in by the whole CTA, four counts at a time where the arrays allow it.
+__device__ __forceinline__ void copy_counts(const int32_t* ref_in, int32_t* ref_out, int64_t n) {
+  if (ref_in == ref_out) return;
+  int64_t done = 0;
+  if ((((uintptr_t)ref_in | (uintptr_t)ref_out) & 15) == 0) {
+    done = n & ~(int64_t)3;
+#pragma unroll 4
+    for (int64_t b = threadIdx.x; b < n / 4; b += kPlan)
+      reinterpret_cast<int4*>(ref_out)[b] = reinterpret_cast<const int4*>(ref_in)[b];
+  }
+  for (int64_t b = done + threadIdx.x; b < n; b += kPlan) ref_out[b] = ref_in[b];
+}
+
 // Moves the listed pages: an item is a piece of one page of one layer and tensor, taken in turn by the CTAs.  Each
 // thread has kMoves vectors in flight; nothing that is moved is read again, so it passes the caches by.
 constexpr int kMoves = 8;
@@ -128,8 +141,7 @@ __global__ void __launch_bounds__(kPlan) fork_kernel(PageParams p, const int32_t
     found += sum;
   }
   __syncthreads();
-  if (ref_in != ref_out)
-    for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) ref_out[b] = ref_in[b];
+  copy_counts(ref_in, ref_out, p.n_blocks);
   const bool bad = s_bad, full = found < need;
   __syncthreads();
   if (bad || full) {
@@ -164,18 +176,23 @@ __global__ void __launch_bounds__(kPlan) free_kernel(PageParams p, const int32_t
                                                      const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out) {
   allow_dependents();
   wait_for_predecessor();
-  if (ref_in != ref_out)
-    for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) ref_out[b] = ref_in[b];
+  copy_counts(ref_in, ref_out, p.n_blocks);
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < n; i += kPlan) {
-    const int b = tables[i];
-    tables_out[i] = -1;
-    if (b < 0) continue;
-    if (b >= p.n_blocks) {
-      set_status(p.status, DCP_EDEVICE);
-    } else if (atomicSub(ref_out + b, 1) <= 0) {
-      atomicAdd(ref_out + b, 1);
-      set_status(p.status, DCP_EDEVICE);
+  // four entries a thread at a time: their reads, then their counts, in flight together
+  for (int64_t i0 = threadIdx.x; i0 < n; i0 += 4 * kPlan) {
+    int b[4], left[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t i = i0 + k * kPlan;
+      b[k] = i < n ? tables[i] : -1;
+      if (i < n) tables_out[i] = -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) left[k] = b[k] >= 0 && b[k] < p.n_blocks ? atomicSub(ref_out + b[k], 1) : 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (b[k] >= p.n_blocks || left[k] <= 0) set_status(p.status, DCP_EDEVICE);
+      if (left[k] <= 0) atomicAdd(ref_out + b[k], 1);
     }
   }
 }
