@@ -59,7 +59,7 @@ struct Item {                          // what a CTA works on
 // pages are cut into `subs` tiles.
 struct Tiling {
   int bs, box, pages, subs;
-  int span;                            // positions of every tile where they are consecutive and as many, else 0
+  int span;                            // positions of every tile where all have as many, else 0
   __device__ __forceinline__ int tile_of(int pos) const {
     if (span == kKeys) return pos / kKeys;
     return subs == 1 ? pos / (pages * bs) : pos / bs * subs + pos % bs / kKeys;
@@ -268,10 +268,9 @@ struct Shape {
   static_assert(join_scratch(2 * kRows, kMaxSplits) <= kSmem - kHead, "the join's scratch fits where the tiles were");
 };
 
-// Two bf16: whether one is an infinity or NaN, and with 0 in such a place.
-__device__ __forceinline__ bool any_special(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
+// Two bf16: bit 15 or 31 where one is an infinity or NaN (its exponent's bits all set carry into it); and the two with
+// 0 in such a place.
+__device__ __forceinline__ uint32_t specials(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 __device__ __forceinline__ uint32_t no_special(uint32_t w) {
   if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
@@ -474,8 +473,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
     const float sc = p.scale_log2, per_log2 = 1.f / sc;
     const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
-    const bool narrow = tl.columns() < kKeys;
-    const uint32_t see_open[2] = {low_bits(tl.columns() - 64 * hf), low_bits(tl.columns() - 64 * hf - 32)};
+    const bool narrow = tl.columns() < kKeys || tl.gaps();
+    uint32_t see_open[2];  // columns that stand for keys
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      see_open[e] = tl.gaps() ? __ballot_sync(~0u, tl.place(0, 64 * hf + 32 * e + lane) >= 0)
+                              : low_bits(tl.columns() - 64 * hf - 32 * e);
     float m = -INFINITY, l = 0.f, seen = -INFINITY;  // seen: the row's maximum so far
     auto move_to = [&](float m2, bool rescale) {     // the row's sums relative to m2
       const float keep = m == m2 ? 1.f : exp2_fast((m - m2) * sc);
@@ -512,14 +515,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) see[e] = low_bits(hi - 32 * e) & ~low_bits(lo - 32 * e);
           } else {
+            int page = 64 * hf / tl.box, row = 64 * hf - page * tl.box;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              see[e] = 0;
-#pragma unroll 1
+              uint32_t bits = 0;
+#pragma unroll 4
               for (int b = 0; b < 32; ++b) {
-                const int at = tl.place(t, 64 * hf + 32 * e + b);
-                if (at >= 0 && p0 + at >= seen_begin && p0 + at < seen_end) see[e] |= 1u << b;
+                const int pos = p0 + page * tl.bs + row;
+                bits |= (uint32_t)(pos >= seen_begin && pos < seen_end) << b;
+                if (++row == tl.box) {
+                  row = 0;
+                  ++page;
+                }
               }
+              see[e] = bits & see_open[e];
             }
           }
         }
@@ -596,28 +605,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           uint8_t* const v = gbase + (2 + slot) * Sh::kTile + (threadIdx.x & 255) * 16;
           const int p0 = tl.first(t), row_a = (threadIdx.x & 255) >> 3, filled = min(tl.count(t), it.kv - p0);
-          bool found = false;
           uint4 y[4 * HALVES];
+          uint32_t special = 0;
 #pragma unroll
           for (int k = 0; k < 4 * HALVES; ++k) y[k] = *reinterpret_cast<const uint4*>(v + k * 4096);
 #pragma unroll
-          for (int k = 0; k < 4 * HALVES; ++k) {
-            const int row = row_a + 32 * (k & 3);  // of 128 rows of 64 dims, twice
-            bool stands = row < filled;
-            if (tl.gaps()) {
-              const int place = tl.place(t, row);
-              stands = place >= 0 && p0 + place < it.kv;
+          for (int k = 0; k < 4 * HALVES; ++k)
+            special |= specials(y[k].x) | specials(y[k].y) | specials(y[k].z) | specials(y[k].w);
+          special &= 0x80008000u;
+          if (special || filled < kKeys || tl.gaps()) {
+#pragma unroll
+            for (int k = 0; k < 4 * HALVES; ++k) {
+              const int row = row_a + 32 * (k & 3);  // of 128 rows of 64 dims, twice
+              bool stands = row < filled;
+              if (tl.gaps()) {
+                const int place = tl.place(t, row);
+                stands = place >= 0 && p0 + place < it.kv;
+              }
+              if (!stands)
+                *reinterpret_cast<uint4*>(v + k * 4096) = make_uint4(0, 0, 0, 0);
+              else if ((specials(y[k].x) | specials(y[k].y) | specials(y[k].z) | specials(y[k].w)) & 0x80008000u) {
+                *reinterpret_cast<uint4*>(v + k * 4096) =
+                    make_uint4(no_special(y[k].x), no_special(y[k].y), no_special(y[k].z), no_special(y[k].w));
+                sh.poison = 1;
+              }
             }
-            if (!stands) {
-              *reinterpret_cast<uint4*>(v + k * 4096) = make_uint4(0, 0, 0, 0);
-            } else if (any_special(y[k].x) | any_special(y[k].y) | any_special(y[k].z) | any_special(y[k].w)) {
-              *reinterpret_cast<uint4*>(v + k * 4096) =
-                  make_uint4(no_special(y[k].x), no_special(y[k].y), no_special(y[k].z), no_special(y[k].w));
-              found = true;
-            }
+            fence_proxy_async_smem();
           }
-          if (found) sh.poison = 1;
-          fence_proxy_async_smem();
         }
         wait_st();
         fence_before();
@@ -929,11 +943,11 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
   // Fewer items than SMs: their keys are split so that the SMs have one part each.  Items of equal work (one sequence
   // without a causal mask) in a few rounds: those of the last, incomplete round are split over the SMs it has.  At least
-  // 4 key tiles a part.
+  // 2 key tiles a part.
   const int64_t sms = sm_count(), rounds = items / sms, left = items % sms;
   const bool tail = rounds > 0 && rounds < 16 && left && a.b.n_seqs == 1 && !a.causal;
   int64_t splits = items < sms ? sms / items : tail ? sms / left : 1;
-  if (splits > key_tiles / 4) splits = key_tiles / 4;
+  if (splits > key_tiles / 2) splits = key_tiles / 2;
   if (splits > kMaxSplits) splits = kMaxSplits;
   t.splits = splits < 1 ? 1 : (int)splits;
   t.whole = t.splits == 1 ? items : rounds * sms;
@@ -952,7 +966,7 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
   p.tl.pages = kKeys / p.tl.box;
   p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
-  p.tl.span = bs % kKeys == 0 ? kKeys : bs < kKeys && p.tl.box == bs ? p.tl.pages * bs : 0;
+  p.tl.span = bs % kKeys == 0 ? kKeys : bs < kKeys ? p.tl.pages * bs : 0;
   p.splits = t.splits;
   p.whole = (int)t.whole;
   p.q_tiles = t.q_tiles;
