@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       for (int i = i0; i < i1; ++i) s_first[i] += before - mine;
       if (threadIdx.x == 0) s_first[items] = total;
       __syncthreads();
-      // two tiles a CTA at least
-      const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + 1) / 2));
+      // Two tiles a CTA at least, and no fewer CTAs than items (a piece costs as much to begin as several tiles).
+      const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, max((total + 1) / 2, min((int64_t)items, total))));
       if (blockIdx.x >= ctas) return;
       int64_t at = blockIdx.x * total / ctas;
       const int64_t to = (blockIdx.x + 1) * total / ctas;
@@ -604,10 +604,15 @@ cudaError_t launch(const RowParams& p, cudaStream_t s) {
   return launch_behind(rows_kernel<T, DP, MW>, grid, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, s, p);
 }
 
-// Rows of one CTA: all of a KV head's rows where they fit 16; else 64, and 128 for fp32 (8 warps share the taking apart
-// of a tile).
-int rows_a_cta(const AttendParams& a) {
-  return (int64_t)a.b.max_q * a.G <= 16 ? 16 : a.pool.dtype == DCP_BF16 ? 64 : 128;
+// Rows of one CTA: all of a KV head's rows where they fit 16, and 16 too where up to 64 meet few keys and the CTAs still
+// run in one round: reading the keys again costs nothing then (in a graph, 28 rows of 12 sequences over a few keys 8.7
+// instead of 9.9 us, 40 fp32 rows of 4 sequences 9.4 instead of 12.0; 58 sequences of 28 rows in two rounds 15.9 instead
+// of 10.9).  Else 64, and 128 for fp32 (8 warps share the taking apart of a tile).
+int rows_a_cta(const AttendParams& a, bool few) {
+  const int64_t rows = (int64_t)a.b.max_q * a.G;
+  if (rows <= 16) return 16;
+  if (few && rows <= 64 && (rows + 15) / 16 * a.pool.H * a.b.n_seqs <= 2 * sm_count()) return 16;
+  return a.pool.dtype == DCP_BF16 ? 64 : 128;
 }
 
 }  // namespace
@@ -618,15 +623,19 @@ bool attend_by_rows(const AttendParams& a) {
 
 RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   RowPlan r;
-  const int per = rows_a_cta(a), keys = a.pool.dtype == DCP_BF16 ? 64 : 32;
-  const int64_t seen = (int64_t)a.window + per / a.G + 2;  // of a tile's rows under a window
+  const int keys = a.pool.dtype == DCP_BF16 ? 64 : 32;
+  const int64_t seen = (int64_t)a.window + 128 / a.G + 2;  // of a tile's rows under a window
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
+  // So few keys that an item in one go is over before parts of it would be joined (11 sequences' tokens over 10 keys in
+  // a graph: 6.3 us, against 12.4 in shares of two tiles).
+  const bool few = max_kv <= 6 * keys;
+  const int per = r.rows = rows_a_cta(a, few);
   r.tiles = (int)(((int64_t)a.b.max_q * a.G + per - 1) / per);
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
   // Items that may differ in length: two CTAs of an SM at a time, each with the same number of key tiles (48 sequences
   // of 200 .. 16000 positions: 324 us, against 354 in pieces of a fixed span; items alike are cut as well by a span,
   // without the sums: one token over 1531 positions 12.3 us, against 14.0).
-  r.even = per == 16 && items <= kEvenItems && (a.b.n_seqs > 1 || a.b.kv_per_head);
+  r.even = (int64_t)a.b.max_q * a.G <= 16 && items <= kEvenItems && (a.b.n_seqs > 1 || a.b.kv_per_head) && !few;
   if (r.even) {
     r.splits = 2 * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
     r.span = 0;
@@ -645,7 +654,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   span = (span + keys - 1) / keys * keys;
   int64_t splits = (max_kv + span - 1) / span;
   if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;
-  r.splits = splits < 1 || items > kDoneItems ? 1 : (int)splits;
+  r.splits = splits < 1 || few || items > kDoneItems ? 1 : (int)splits;
   r.span = (int)(span < kMaxKv ? span : kMaxKv);
   r.bytes = r.splits > 1 ? kDoneBytes + (size_t)items * r.splits * per * (kPartHead + a.pool.D) * 4 : 0;
   return r;
@@ -666,7 +675,7 @@ cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, 
   p.flip = a.scale < 0.f ? 0x80000000u : 0u;
   p.done = (uint32_t*)ws;
   p.part = (float*)((char*)ws + kDoneBytes);
-  const bool one = rows_a_cta(a) == 16, wide = a.pool.D > 64;
+  const bool one = r.rows == 16, wide = a.pool.D > 64;
   if (a.pool.dtype == DCP_BF16) {
     if (one) return wide ? launch<__nv_bfloat16, 128, 1>(p, s) : launch<__nv_bfloat16, 64, 1>(p, s);
     return wide ? launch<__nv_bfloat16, 128, 4>(p, s) : launch<__nv_bfloat16, 64, 4>(p, s);

@@ -70,7 +70,7 @@ constexpr size_t kDoneBytes = (size_t)kDoneItems * 4;
 
 // How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes.
 struct RowPlan {
-  int tiles, splits, span, even;
+  int rows, tiles, splits, span, even;  // rows of a CTA, tiles of them
   size_t bytes;
 };
 bool attend_by_rows(const AttendParams& p);
