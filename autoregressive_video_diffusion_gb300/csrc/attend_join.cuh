@@ -43,7 +43,9 @@ __device__ __forceinline__ bool last_of(uint32_t* done, int splits, int* s_last)
 // join_scratch(rows, splits).  Everything is fetched at once where it fits the scratch (a loop over the parts in global
 // memory pays a memory latency every few of them: 5 us for 12 parts of 5 rows, 1 us this way), else the maxima and sums
 // first and the values with several loads in flight.
-__host__ __device__ constexpr int64_t join_scratch(int rows, int splits) { return (int64_t)rows * (splits + 1) * 4; }
+__host__ __device__ constexpr int64_t join_scratch(int rows, int splits) {
+  return (int64_t)rows * (2 * splits + 1) * 4;
+}
 
 // The first part is at `part0`, the others from `part1` on, `step` floats apart.
 template <typename T>
@@ -52,8 +54,9 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
                                            int64_t room) {
   const int D = a.pool.D, quads = D / 4, width = kPartHead + D;
   auto part = [&](int k) { return k ? part1 + (k - 1) * step : part0; };
-  float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]
-  float* const inv = weight + rows * splits;                // [rows]
+  float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]: the maximum, then the part's weight
+  float* const sum = weight + rows * splits;                // [rows][splits]
+  float* const inv = sum + rows * splits;                   // [rows]
   const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
   __syncthreads();
   const bool local = used + (int64_t)rows * splits * width * 4 <= room;
@@ -71,25 +74,28 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
     part0 = reinterpret_cast<const float*>(scratch + used);
     part1 = part0 + step;
   }
+  for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
+    const int r = u / splits;
+    const float2* at = reinterpret_cast<const float2*>(part(u - r * splits) + (int64_t)r * width);
+    const float2 ml = local ? *at : __ldcg(at);
+    weight[u] = ml.x;
+    sum[u] = ml.y;
+  }
+  __syncthreads();
   // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
   for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
     const int lane = threadIdx.x & 31;
-    auto head = [&](int k) {
-      const float2* at = reinterpret_cast<const float2*>(part(k) + (int64_t)r * width);
-      return local ? *at : __ldcg(at);
-    };
+    float* const w = weight + r * splits;
+    const float* const ls = sum + r * splits;
     float top = -INFINITY, l = 0.f;
-    for (int k = lane; k < splits; k += 32) {
-      const float2 ml = head(k);
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
+    for (int k = lane; k < splits; k += 32)
+      if (ls[k] != 0.f) top = fmaxf(top, w[k]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     for (int k = lane; k < splits; k += 32) {
-      const float2 ml = head(k);
-      const float w = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);
-      weight[r * splits + k] = w;
-      if (w != 0.f) l += w * ml.y;
+      const float wk = ls[k] == 0.f ? 0.f : exp2_fast(w[k] - top);
+      w[k] = wk;
+      if (wk != 0.f) l += wk * ls[k];
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
