@@ -13,9 +13,9 @@
 // tile's weighted values start from 0 and are added to the running ones by one fma, so that the tensor cores'
 // accumulation (which may truncate) never runs over more than a tile.
 //
-// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 322-325 us,
-// 6.25 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
-// fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 197-201 us, bound by the tf32 products
+// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-313 us,
+// 6.5 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
+// fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 192-201 us, bound by the tf32 products
 // (40 % of their rate while a CTA runs).
 #include <type_traits>
 

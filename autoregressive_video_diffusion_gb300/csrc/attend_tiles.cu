@@ -24,7 +24,7 @@
 // NaN before they hand over their weights; rows that do see those get them back in the epilogue, from the cache.
 //
 // Measured: 6240 tokens, 40 query heads over 8 KV heads of 128, 25907 keys: 2133-2193 us, 1510-1550 TFLOP/s.  Causal
-// chunks of 130 .. 2048 tokens behind up to 12000 keys: 700-716 us, 1340-1370 TFLOP/s.  What bounds it is the chain of
+// chunks of 130 .. 2048 tokens behind up to 12000 keys: 672-716 us, 1340-1430 TFLOP/s.  What bounds it is the chain of
 // a row tile (products 1100 clocks, scores ready 300, weights 1150, products awake 300), of which the other row tile's
 // products cover 1100.
 #include <cuda.h>
