@@ -1,11 +1,12 @@
 // Rotary turn of the new tokens' q and k, and k, v into the cache's pages, in one pass over the data.
 //
-// A CTA takes a token: each thread first loads its first vectors of q, k, v (they depend on nothing), then the CTA finds
-// the token's sequence, phase and page row and builds its cos/sin in shared memory, then turns and stores.  The phase in turns is an integer product modulo 2^64, so whole turns drop out exactly at any distance; cos
-// and sin are taken of the remaining fraction, once per token and pair, and shared by all heads.
+// A CTA takes a token: each thread first loads its first vectors of q, k, v (they depend on nothing), then the CTA
+// finds the token's sequence, phase and page row and builds its cos/sin in shared memory, then turns and stores.  The
+// phase in turns is an integer product modulo 2^64, so whole turns drop out exactly at any distance; cos and sin are
+// taken of the remaining fraction, once per token and pair, and shared by all heads.
 // The bound is HBM (each of q, k, v read and written once); a few tokens are bound by the chain launch -> q_start,
-// kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 67 us (5.7 TB/s), 3375 tokens
-// of 32 + 8 + 8 fp32 heads of 96 26 us (4.8 TB/s), 32 tokens 3.6 us in a graph.
+// kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 68 us (5.7 TB/s), 3375 tokens
+// of 32 + 8 + 8 fp32 heads of 96 25 us (5.0 TB/s), 32 tokens 4.0 us in a graph.
 #include "serve.cuh"
 
 namespace dcp {
@@ -226,9 +227,9 @@ __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant_
 
 template <typename T, int PAIRS>
 cudaError_t launch_tokens(const AppendParams& p, cudaStream_t s) {
-  // A token a CTA of 128 threads, so that many CTAs are at different places of their chain.  (6240 tokens of 120 heads /
-  // 3375 of 48 fp32 heads whose units are two vectors: 4 units a thread 67 / 35 us, 2 units 71 / 26; two tokens a CTA
-  // of 256 threads 74 / 29, four 81 / 35.)
+  // A token a CTA of 128 threads, so that many CTAs are at different places of their chain.  (6240 tokens of 120
+  // heads / 3375 of 48 fp32 heads whose units are two vectors: 4 units a thread 67 / 35 us, 2 units 71 / 26; two
+  // tokens a CTA of 256 threads 74 / 29, four 81 / 35.)
   return launch_behind(append_kernel<T, PAIRS>, dim3((unsigned)p.b.total_q), kTurners, 0, s, p);
 }
 

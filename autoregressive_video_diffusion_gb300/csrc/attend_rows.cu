@@ -2,16 +2,16 @@
 // cache, in warp-level matrix products (16 rows a warp).
 //
 // Rows are (new token, query head of the KV head) pairs.  The warps share tiles of keys that travel page row by page
-// row through shared memory (asynchronous copies, several tiles in flight).  With MW = 4 or 8 each warp (of as many) has 16 rows
-// of its own and sees every key; with MW = 1 four warps have the same 16 rows and a quarter of each tile's keys, and
-// join their results at the end.  Few rows read every key once, so the bound is HBM and the work is spread over the
-// keys: an item's keys are split over CTAs, the last of which joins the parts.
+// row through shared memory (asynchronous copies, several tiles in flight).  With MW = 4 or 8 each warp (of as many)
+// has 16 rows of its own and sees every key; with MW = 1 four warps have the same 16 rows and a quarter of each tile's
+// keys, and join their results at the end.  Few rows read every key once, so the bound is HBM and the work is spread
+// over the keys: an item's keys are split over CTAs, the last of which joins the parts.
 //
 // fp32: each factor x is x_hi + x_lo, both with 11 significant bits, and x y = x_hi y_hi + x_hi y_lo + x_lo y_hi up
 // to 2^-22: three tensor products for one.  A tile is taken apart once, for all warps (each warp doing it for itself
-// made the conversions the bound: 331 us for what now takes a fraction).  The large and the small products of a score are summed apart, and a
-// tile's weighted values start from 0 and are added to the running ones by one fma, so that the tensor cores'
-// accumulation (which may truncate) never runs over more than a tile.
+// made the conversions the bound: 331 us for what now takes 200).  The large and the small products of a score are
+// summed apart, and a tile's weighted values start from 0 and are added to the running ones by one fma, so that the
+// tensor cores' accumulation (which may truncate) never runs over more than a tile.
 //
 // Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-313 us,
 // 6.5 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
@@ -59,8 +59,10 @@ struct Rows {
   static constexpr int kJoin = MW == 1 ? kWarps * 16 * (DP + 2) * 4 : 0;
   static constexpr int kBuffers = kStages * kStage > kJoin ? kStages * kStage : kJoin;
   static constexpr int kSmem = kBuffers + kQ + kPairs;
-  static_assert(join_scratch(16 * MW, MW == 1 ? 2 * kMaxSms : kMaxSplits) <= kSmem, "the join's scratch fits where the tiles were");
-  static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * (kHalf ? kRow : kPairK), "a tile's weights fit where its keys were");
+  static_assert(join_scratch(16 * MW, MW == 1 ? 2 * kMaxSms : kMaxSplits) <= kSmem,
+                "the join's scratch fits where the tiles were");
+  static_assert(kWarps * 16 * kMine * (int)sizeof(T) <= kKeys * (kHalf ? kRow : kPairK),
+                "a tile's weights fit where its keys were");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
@@ -102,11 +104,11 @@ __device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
   *reinterpret_cast<uint4*>(to + 16) = make_uint4(c.x, c.y, d.x, d.y);
 }
 
-// Rows [row0, row0 + rows) of (token, head of the KV head) of sequence s, which has `len` new tokens from row lo of q on
-// and `kv` cached positions, against the keys [begin, end).  The result goes to out and lse, or to `part`.
+// Rows [row0, row0 + rows) of (token, head of the KV head) of sequence s, which has `len` new tokens from row lo of q
+// on and `kv` cached positions, against the keys [begin, end).  The result goes to out and lse, or to `part`.
 template <typename T, int DP, int MW>
-__device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem, int64_t (*s_off)[Rows<T, DP, MW>::kKeys],
-                                             int s, int kh, int lo, int len, int kv, int row0, int rows, int begin,
+__device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
+                                             int64_t (*s_off)[Rows<T, DP, MW>::kKeys], int s, int kh, int lo, int len, int kv, int row0, int rows, int begin,
                                              int end, float* part) {
   using R = Rows<T, DP, MW>;
   const AttendParams& a = p.a;
@@ -598,10 +600,11 @@ template <typename T, int DP, int MW>
 cudaError_t launch(const RowParams& p, cudaStream_t s) {
   static LaunchCache lc;
   int blocks;
-  const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, &blocks);
+  using R = Rows<T, DP, MW>;
+  const cudaError_t e = launch_setup(lc, rows_kernel<T, DP, MW>, R::kThreads, R::kSmem, &blocks);
   if (e != cudaSuccess) return e;
   const dim3 grid = p.even ? dim3(p.splits) : dim3(p.row_tiles, p.a.pool.H, p.a.b.n_seqs * p.splits);
-  return launch_behind(rows_kernel<T, DP, MW>, grid, Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kSmem, s, p);
+  return launch_behind(rows_kernel<T, DP, MW>, grid, R::kThreads, R::kSmem, s, p);
 }
 
 // Rows of one CTA: all of a KV head's rows where they fit 16, and 16 too where up to 64 meet few keys and the CTAs still

@@ -12,8 +12,8 @@
 // of the weights say (a sum of 64 weights is within 2^6 of its largest).  m follows at the next tile, and only when a
 // tile's weights have added up to more than 2^8, which leaves O untouched in almost every step; m has moved or not, the
 // quotient O / l is the same (weights keep their relative precision in bf16, sums are held in 32 bits).  Only a row
-// whose scores rise by more than 2^64 within one tile needs more care: its item is then done again with each tile's own
-// maximum.
+// whose scores rise by more than 2^64 within one tile, or lie beyond 2^8192 (levels travel between a row's threads in
+// bf16), needs more care: its item is then done again with each tile's own maximum, told in two parts.
 //
 // Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warps 16, 17: issue the matrix products of row tile 0 and 1 (one
 // warp for both was busy for 3600 clocks a step of 2048 clocks of products).  Warps 18, 19: copy the pages of the keys
@@ -43,6 +43,7 @@ constexpr int kMaxSplits = 92;         // of an item: what the join's scratch ho
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
 constexpr float kFar = 64.f;           // and within one tile before the item is done again
+constexpr float kHuge = 8192.f;        // log2 of a weight whose level, heard in bf16, is too coarse for kFar
 constexpr long long kPatience = 4000000000ll;  // limit of every wait, in SM clocks (two seconds)
 
 struct Item {                          // what a CTA works on
@@ -567,8 +568,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int u = 0; u < 32; ++u) top[u & 3] = max3(top[u & 3], x[0][u], x[1][u]);
-          tell(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-          hear();
+          const float mine_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (careful) {
+            // both threads here, then the maximum in two bf16 parts through both buffers
+            if (lane == 0) bar_arrive(met);
+            ok = warp_wait(met, swaps++ & 1, &sh.dead);
+            const __nv_bfloat16 high = __float2bfloat16_rn(mine_top);
+            const float rest = mine_top - __bfloat162float(high);
+            const __nv_bfloat16 low = __float2bfloat16_rn(rest == rest ? rest : 0.f);
+            sh.swap.top[i][0][hf][r] = high;
+            sh.swap.top[i][1][hf][r] = low;
+            __syncwarp();
+            if (lane == 0) bar_arrive(met);
+            ok = ok && warp_wait(met, swaps++ & 1, &sh.dead);
+            seen = fmaxf(seen, fmaxf(__bfloat162float(high) + __bfloat162float(low),
+                                     __bfloat162float(sh.swap.top[i][0][hf ^ 1][r]) +
+                                         __bfloat162float(sh.swap.top[i][1][hf ^ 1][r])));
+          } else {
+            tell(mine_top);
+            hear();
+            if (fabsf(seen) * sc > kHuge && seen != -INFINITY) sh.far = 1;
+          }
           const bool far = m == -INFINITY ? seen > m : (seen - m) * sc > kGrow;
           if (__any_sync(~0u, far)) move_to(far ? seen : m, t > t0);
         } else if (hide) {
@@ -643,7 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         l += y0;
         if (!exact) {  // the largest weight is between a 64th of the sum and the sum
           tell(m + __log2f(y0) * per_log2);
-          if ((seen - m) * sc > kFar) sh.far = 1;
+          if ((seen - m) * sc > kFar || (fabsf(seen) * sc > kHuge && seen != -INFINITY)) sh.far = 1;
         }
       }
       if (ok && t0 < t1) {  // the last product

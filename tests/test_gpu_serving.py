@@ -270,6 +270,17 @@ def test_attention_scores_that_rise_along_the_keys(gpu, dtype, nq, rise):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nq", [1, 200])
+@pytest.mark.parametrize("scale", [60.0, 500.0, -900.0])
+def test_attention_scores_in_the_thousands(gpu, dtype, nq, scale):
+    """A row is its largest score's value; levels and maxima of 10^4 and more must still be told apart."""
+    c = Cache(dtype, HND, 2, 64, 16, [nq], [600], seed=13).fill()
+    q = c.normal(nq, 4, 64)
+    out, lse = attend(c, q, True, -1, scale=scale)
+    check_attention(c, q, out, lse, scale, True, -1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 200])
 def test_attention_large_scores_strided_q_no_lse(gpu, dtype, nq):
     """Scores in the hundreds (a softmax with almost one key), a fused projection's q, no lse; another stream."""
     c = Cache(dtype, NHD, 2, 128, 16, [nq], [300], seed=7).fill()
