@@ -13,8 +13,8 @@
 // summed apart, and a tile's weighted values start from 0 and are added to the running ones by one fma, so that the
 // tensor cores' accumulation (which may truncate) never runs over more than a tile.
 //
-// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-313 us,
-// 6.5 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
+// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-325 us,
+// 6.2-6.5 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
 // fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 192-201 us, bound by the tf32 products
 // (40 % of their rate while a CTA runs).
 #include <type_traits>
@@ -108,8 +108,8 @@ __device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
 // on and `kv` cached positions, against the keys [begin, end).  The result goes to out and lse, or to `part`.
 template <typename T, int DP, int MW>
 __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
-                                             int64_t (*s_off)[Rows<T, DP, MW>::kKeys], int s, int kh, int lo, int len, int kv, int row0, int rows, int begin,
-                                             int end, float* part) {
+                                             int64_t (*s_off)[Rows<T, DP, MW>::kKeys], int s, int kh, int lo,
+                                             int len, int kv, int row0, int rows, int begin, int end, float* part) {
   using R = Rows<T, DP, MW>;
   const AttendParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -607,10 +607,10 @@ cudaError_t launch(const RowParams& p, cudaStream_t s) {
   return launch_behind(rows_kernel<T, DP, MW>, grid, R::kThreads, R::kSmem, s, p);
 }
 
-// Rows of one CTA: all of a KV head's rows where they fit 16, and 16 too where up to 64 meet few keys and the CTAs still
-// run in one round: reading the keys again costs nothing then (in a graph, 28 rows of 12 sequences over a few keys 8.7
-// instead of 9.9 us, 40 fp32 rows of 4 sequences 9.4 instead of 12.0; 58 sequences of 28 rows in two rounds 15.9 instead
-// of 10.9).  Else 64, and 128 for fp32 (8 warps share the taking apart of a tile).
+// Rows of one CTA: all of a KV head's rows where they fit 16, and 16 too where up to 64 meet few keys and the CTAs
+// still run in one round: reading the keys again costs nothing then (in a graph, 28 rows of 12 sequences over a few
+// keys 8.7 instead of 9.9 us, 40 fp32 rows of 4 sequences 9.4 instead of 12.0; 58 sequences of 28 rows in two rounds
+// 15.9 instead of 10.9).  Else 64, and 128 for fp32 (8 warps share the taking apart of a tile).
 int rows_a_cta(const AttendParams& a, bool few) {
   const int64_t rows = (int64_t)a.b.max_q * a.G;
   if (rows <= 16) return 16;
