@@ -308,7 +308,7 @@ def dcp_prune_step(cache: KVCache, cfg: Config, x0hat: torch.Tensor, xref: torch
                               _ptr(kept_host_pinned), _ptr(ws), ws.numel(), _stream(stream)), "dcp_prune_step")
 
 
-DCP_NOALLOC_WORKSPACE_BYTES = 4 << 20
+DCP_NOALLOC_WORKSPACE_BYTES = (4 << 20) + (8 << 10)
 
 
 def dcp_prune_step_noalloc(cache: KVCache, cfg: Config, x0hat: torch.Tensor, xref: torch.Tensor, evict_slot: int,

@@ -642,7 +642,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   if (r.even) {
     r.splits = 2 * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
     r.span = 0;
-    r.bytes = kDoneBytes + (size_t)r.splits * 2 * 16 * (kPartHead + a.pool.D) * 4;
+    r.bytes = (size_t)r.splits * 2 * 16 * (kPartHead + a.pool.D) * 4;
     return r;
   }
   // Two CTAs of an SM at a time: one round of pieces for a few sequences; several rounds of shorter ones where their
@@ -659,7 +659,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   if (splits > 65535 / a.b.n_seqs) splits = 65535 / a.b.n_seqs;
   r.splits = splits < 1 || few || items > kDoneItems ? 1 : (int)splits;
   r.span = (int)(span < kMaxKv ? span : kMaxKv);
-  r.bytes = r.splits > 1 ? kDoneBytes + (size_t)items * r.splits * per * (kPartHead + a.pool.D) * 4 : 0;
+  r.bytes = r.splits > 1 ? (size_t)items * r.splits * per * (kPartHead + a.pool.D) * 4 : 0;
   return r;
 }
 
@@ -676,8 +676,8 @@ cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, 
   const float mag = a.scale < 0.f ? -a.scale : a.scale;
   p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
   p.flip = a.scale < 0.f ? 0x80000000u : 0u;
-  p.done = (uint32_t*)ws;
-  p.part = (float*)((char*)ws + kDoneBytes);
+  p.done = done_counters(ws);
+  p.part = (float*)((char*)ws + kScratch);
   const bool one = r.rows == 16, wide = a.pool.D > 64;
   if (a.pool.dtype == DCP_BF16) {
     if (one) return wide ? launch<__nv_bfloat16, 128, 1>(p, s) : launch<__nv_bfloat16, 64, 1>(p, s);

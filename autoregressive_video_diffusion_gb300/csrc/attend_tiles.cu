@@ -972,7 +972,7 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   t.splits = splits < 1 ? 1 : (int)splits;
   t.whole = t.splits == 1 ? items : rounds * sms;
   const size_t cut = (size_t)(items - t.whole);
-  t.bytes = cut == 0 ? 0 : kDoneBytes + cut * t.splits * 2 * kRows * (kPartHead + a.pool.D) * 4;
+  t.bytes = cut * t.splits * 2 * kRows * (kPartHead + a.pool.D) * 4;
   return t;
 }
 
@@ -996,8 +996,8 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
   p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
   p.idesc_pv = idesc((a.pool.D + 15) / 16 * 16, true, false);
-  p.done = (uint32_t*)ws;
-  p.part = (float*)((char*)ws + kDoneBytes);
+  p.done = done_counters(ws);
+  p.part = (float*)((char*)ws + kScratch);
   CUtensorMap mk, mv;
   if (!encode(&mk, a.pool, a.pool.k, p.tl.box) || !encode(&mv, a.pool, a.pool.v, p.tl.box))
     return cudaErrorInvalidValue;

@@ -43,6 +43,14 @@ struct Ctrl {
 };
 static_assert(sizeof(Ctrl) == 256, "ctrl block is one 256-byte line");
 
+// The start of every workspace is the same for all entry points, so that they can share one in any order: the control
+// block, then a counter for each attention item whose keys are split over CTAs.  What must be zero before a call is in
+// these (the scan's counter and accumulators, all of the attention's counters), is zero again after it, and is written
+// by no other call.  Behind them, from kScratch on, a call finds whatever the one before it left there.
+constexpr int kDoneItems = 2048;
+constexpr size_t kDoneBytes = (size_t)kDoneItems * 4;
+constexpr size_t kScratch = sizeof(Ctrl) + kDoneBytes;
+
 struct Layout {           // byte offsets inside the workspace
   size_t bits, ell, mask, idx, trig_g, rot_g, trig_h, rot_h, plane_off, dyn, total;
 };
@@ -51,7 +59,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline Layout make_layout(int64_t n_tok, int64_t n_planes, int64_t F, int64_t n_t, int64_t max_frames) {
   Layout L{};
-  size_t off = sizeof(Ctrl);
+  size_t off = kScratch;
   L.bits = off;       off = align256(off + 4 * (size_t)((n_tok + 31) / 32));
   L.ell = off;        off = align256(off + 4 * (size_t)n_tok);
   L.mask = off;       off = align256(off + (size_t)n_tok);

@@ -12,8 +12,10 @@ namespace {
 
 constexpr int kPlan = 1024;  // threads of a bookkeeping CTA
 
-// Workspace: [0] number of moves, then (from kHead on) the list of (source, destination) pairs.
+// A call's part of the workspace, from kScratch on: [0] number of moves, then (from kHead on) the list of (source,
+// destination) pairs.
 constexpr int kHead = 64;
+int32_t* scratch(int32_t* ws) { return ws + kScratch / 4; }
 
 // Exclusive sum of x over the CTA, *total the whole sum.
 __device__ int block_scan(int x, int* s_warp, int* total) {
@@ -266,6 +268,7 @@ cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const 
                               int32_t stride, const int32_t* parent, const int32_t* shared, const int32_t* reserve,
                               int32_t n_children, const int32_t* ref_in, int32_t* child_tables, int32_t* ref_out,
                               int32_t* ws, cudaStream_t s) {
+  ws = scratch(ws);
   const cudaError_t e = launch_behind(fork_kernel, dim3(1), kPlan, 0, s, p, tables, len, n_rows, stride, parent, shared,
                                       reserve, n_children, ref_in, child_tables, ref_out, ws);
   return e != cudaSuccess ? e : move_listed(p, ws, s);
@@ -280,6 +283,7 @@ cudaError_t launch_pages_free(const PageParams& p, const int32_t* tables, int32_
 cudaError_t launch_pages_compact(const PageParams& p, const int32_t* tables, int32_t n_rows, int32_t stride,
                                  const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out, int32_t* n_live,
                                  int32_t* ws, cudaStream_t s) {
+  ws = scratch(ws);
   const cudaError_t e = launch_behind(compact_kernel, dim3(1), kPlan, 0, s, p, tables, (int64_t)n_rows * stride, ref_in,
                                       tables_out, ref_out, n_live, ws);
   return e != cudaSuccess ? e : move_listed(p, ws, s);

@@ -63,12 +63,10 @@ struct PageParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
-// The attention's workspace: a counter for each item whose keys are split, zero between calls and in the same place
-// whatever the sizes (calls of different sizes may share a workspace), then the parts.
-constexpr int kDoneItems = 16384;
-constexpr size_t kDoneBytes = (size_t)kDoneItems * 4;
+// The attention's workspace: the counters at its start (kDoneItems of them), from kScratch on the parts.
+inline uint32_t* done_counters(void* ws) { return (uint32_t*)((char*)ws + sizeof(Ctrl)); }
 
-// How the attention of few rows (or of an fp32 cache) divides its work, and the workspace that takes.
+// How the attention of few rows (or of an fp32 cache) divides its work, and the bytes its parts take.
 struct RowPlan {
   int rows, tiles, splits, span, even;  // rows of a CTA, tiles of them
   size_t bytes;

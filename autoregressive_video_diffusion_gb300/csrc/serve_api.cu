@@ -183,7 +183,7 @@ size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch
   if (check_attention(pool, batch, cfg, Hq) != DCP_OK) return 0;
   const AttendParams p = attend_of(pool, batch, cfg, Hq);
   const size_t bytes = attend_by_rows(p) ? plan_rows(p, batch->max_kv).bytes : plan_tiles(p, batch->max_kv).bytes;
-  return 256 + (bytes + 255) / 256 * 256;
+  return kScratch + (bytes + 255) / 256 * 256;
 }
 
 dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
@@ -206,7 +206,7 @@ size_t dcp_pages_workspace_size(const dcp_page_pool* pool, int32_t n_rows, int32
   // the list of moves and the fresh blocks of a fork, or the list of moves and the map of a packing
   const size_t entries = (size_t)n_rows * stride;
   const size_t fork = 3 * entries + n_rows, pack = 3 * (size_t)pool->n_blocks;
-  return (256 + 4 * (fork > pack ? fork : pack) + 255) & ~(size_t)255;
+  return (kScratch + 256 + 4 * (fork > pack ? fork : pack) + 255) & ~(size_t)255;
 }
 
 dcp_status dcp_pages_copy(const dcp_page_pool* pool, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {

@@ -24,7 +24,8 @@
  *     and lengths as they were; a history frame outside [first non-sink frame, q0) is found while re-indexing, and
  *     only that row is left unturned.
  *   - The workspace is caller-owned device scratch of dcp_workspace_size() bytes, 256-byte aligned.  Zero it once
- *     with dcp_workspace_init() before its first use; every call leaves it ready for the next.  Calls that share a
+ *     with dcp_workspace_init() before its first use; every call leaves it ready for the next, whichever entry point
+ *     that is: one workspace of the largest size that any of them asks for serves them all.  Calls that share a
  *     workspace or a cache must be ordered on one stream (not thread-safe per workspace or cache).  Host threads
  *     may call the library at the same time on different caches and workspaces (on one or several devices).
  *
@@ -174,9 +175,9 @@ dcp_status dcp_prune_step(const dcp_cache* cache, const dcp_config* cfg, const f
  * Score inputs in page-locked host memory are read at replay time, so a serving loop can refill them between
  * replays. */
 
-/* Largest workspace dcp_prune_step_noalloc can use: 4 MiB (the full-depth 40 x 40 x 128 cache with 6240-token
- * chunks and max_frames 256 needs about 190 KB). */
-#define DCP_NOALLOC_WORKSPACE_BYTES (4u << 20)
+/* Largest workspace dcp_prune_step_noalloc can use: 4 MiB and the 8 KB of counters that every workspace begins with
+ * (the full-depth 40 x 40 x 128 cache with 6240-token chunks and max_frames 256 needs about 200 KB). */
+#define DCP_NOALLOC_WORKSPACE_BYTES ((4u << 20) + (8u << 10))
 
 /* dcp_prune_step for callers that cannot allocate device memory (for example code running inside a device
  * allocator's callback, or an engine that forbids allocation after start-up).  The paper has no counterpart: this
@@ -433,7 +434,7 @@ typedef struct dcp_attn_config {
 
 /* Workspace bytes dcp_paged_attention needs (256-byte aligned, zeroed once with dcp_workspace_init); 0 for invalid
  * arguments.  It depends on the sizes in pool, batch and cfg and on the current device, not on what the arrays hold.
- * Calls of different sizes may share one workspace that is large enough for each. */
+ * Calls of different sizes, and the other entry points, may share one workspace that is large enough for each. */
 size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                                     int32_t Hq);
 
