@@ -129,6 +129,8 @@ _SIGS = {
     "dcp_paged_workspace_size": ([ctypes.POINTER(DcpPagedCacheC), _pg], _sz),
     "dcp_paged_prune_step": ([ctypes.POINTER(DcpPagedCacheC), _pg, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
                               _vp, _vp, _sz, _vp], _i32),
+    "dcp_paged_prune_step_shared": ([ctypes.POINTER(DcpPagedCacheC), _pg, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "dcp_abi_paged_cache_size": ([], ctypes.c_uint32),
     "dcp_read_history_keys": ([_pc, _pg, _i32, _i32, _i32, _vp, _vp, _sz, _vp], _i32),
     "dcp_phase_table": ([_pg, _i32, _i32, _i32, _vp, _vp], _i32),
@@ -406,7 +408,9 @@ class PagedKVCache:
 
     Pools are [L][n_blocks][H][block_size][D] (HND) or [L][n_blocks][block_size][H][D] (NHD); hist_blocks and
     window_blocks are int32 device tensors the caller fills (block ids of the history positions and of the ring
-    slots, slot s owning entries [s * C / block_size, (s + 1) * C / block_size))."""
+    slots, slot s owning entries [s * C / block_size, (s + 1) * C / block_size)).  block_ref may be set to the blocks'
+    reference counts (int32 [n_blocks], as the dcp_pages_* calls keep them): a prune step that would write a history
+    block that another sequence holds too is then refused on the device (DCP_EDEVICE)."""
 
     def __init__(self, L: int, H: int, D: int, dtype: int, block_size: int, layout: int, n_blocks: int,
                  hist_cap: int, n_window_blocks: int, device="cuda"):
@@ -418,6 +422,7 @@ class PagedKVCache:
         self.v_pool = torch.empty(shape, dtype=tdt, device=device)
         self.hist_blocks = torch.zeros(max(hist_cap // block_size, 1), dtype=torch.int32, device=device)
         self.window_blocks = torch.zeros(max(n_window_blocks, 1), dtype=torch.int32, device=device)
+        self.block_ref = None
         self.hist_len = torch.zeros(L * H, dtype=torch.int32, device=device)
         self.hist_t = torch.zeros(max(hist_cap, 1), dtype=torch.int32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
@@ -439,10 +444,18 @@ def dcp_paged_workspace_size(cache: PagedKVCache, cfg: Config) -> int:
 def dcp_paged_prune_step(cache: PagedKVCache, cfg: Config, x0hat: torch.Tensor, xref: torch.Tensor, evict_slot: int,
                          evict_first_frame: int, q0_prev: int, q0: int, head_is_static, kept, kept_host,
                          ws: torch.Tensor, stream=None) -> None:
+    """With cache.block_ref set: dcp_paged_prune_step_shared, which refuses to write history blocks held in common."""
     cc, gc = cache.c(), cfg.c()
-    _check(lib.dcp_paged_prune_step(ctypes.byref(cc), ctypes.byref(gc), _ptr(x0hat), _ptr(xref), x0hat.shape[1],
-                                    evict_slot, evict_first_frame, q0_prev, q0, _ptr(head_is_static), _ptr(kept),
-                                    _ptr(kept_host), _ptr(ws), ws.numel(), _stream(stream)), "dcp_paged_prune_step")
+    args = (_ptr(x0hat), _ptr(xref), x0hat.shape[1], evict_slot, evict_first_frame, q0_prev, q0, _ptr(head_is_static),
+            _ptr(kept), _ptr(kept_host), _ptr(ws), ws.numel(), _stream(stream))
+    ref = cache.block_ref
+    if ref is None:
+        _check(lib.dcp_paged_prune_step(ctypes.byref(cc), ctypes.byref(gc), *args), "dcp_paged_prune_step")
+        return
+    if ref.dtype != torch.int32 or not ref.is_contiguous() or ref.numel() != cache.n_blocks:
+        raise DcpError("dcp_paged_prune_step", DCP_EINVAL)
+    _check(lib.dcp_paged_prune_step_shared(ctypes.byref(cc), ctypes.byref(gc), _ptr(ref), *args),
+           "dcp_paged_prune_step_shared")
 
 
 def paged_row_map(cfg: Config, hist_cap: int, block_size: int, sink_blocks: torch.Tensor, hist_blocks: torch.Tensor,
@@ -684,7 +697,9 @@ def dcp_pages_copy(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, stream=
 def dcp_pages_fork(pool: PagePool, tables: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor, shared, reserve,
                    ref: torch.Tensor, child_tables: torch.Tensor, ref_out: torch.Tensor, ws: torch.Tensor,
                    stream=None) -> None:
-    """Branch rows parent[c] of `tables` into child_tables; shared and reserve (int32 [n_children]) may be None."""
+    """Branch rows parent[c] of `tables` into child_tables; shared and reserve (int32 [n_children]) may be None.  Pages
+    that will be written must not be shared: of a cache whose prune steps turn the history's keys (reindex_mode 0, q0 - T_s
+    past the span) only those before the history are.  Set PagedKVCache.block_ref to `ref` to have this checked."""
     _ints("dcp_pages_fork", tables, lens, parent, shared, reserve, ref, child_tables, ref_out)
     (rows, stride), n = tables.shape, parent.numel()
     if child_tables.shape != (n, stride) or lens.numel() != rows or ref.numel() != pool.n_blocks or \

@@ -204,10 +204,14 @@ dcp_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ECUDA
 // delta_max = q0 - T_s <= span end, so t~(t) = t for every frame of the chunk (the chunk's oldest offset is
 // q0 - evict_first_frame, its largest).  The GPU sweep draws steps on both sides of each boundary
 // (q0 - evict_first_frame = R, R + 1; q0 - T_s = span end, span end + 1) and compares them with the oracle.
+bool inside_span(const dcp_config* g, const Derived& d, int32_t q0) {
+  const double span_end = g->g_mode == 0 ? g->g_span_S : g->g_recent_R + g->g_span_S;
+  return (double)(q0 - d.T_s) <= span_end;
+}
+
 bool chunk_keeps_phase(const dcp_config* g, const Derived& d, int32_t evict_first_frame, int32_t q0) {
   if (g->reindex_mode == 1 || g->n_temporal_pairs == 0) return true;
-  const double span_end = g->g_mode == 0 ? g->g_span_S : g->g_recent_R + g->g_span_S;
-  return (double)(q0 - d.T_s) <= span_end || (double)(q0 - evict_first_frame) <= g->g_recent_R;
+  return inside_span(g, d, q0) || (double)(q0 - evict_first_frame) <= g->g_recent_R;
 }
 
 // The turn of the leaving chunk's keys for a gather at q0: none (no_turn: the scan builds no table for the chunk), or
@@ -271,6 +275,7 @@ struct PagedView {
   Paging pg;
   const int32_t* window_blocks;
   int64_t n_blocks;
+  const int32_t* block_ref;  // nullable
 };
 
 // A paged cache seen as a dcp_cache (for the shared checks and parameters) plus its addressing.  The shadow's cap
@@ -316,6 +321,7 @@ dcp_status paged_view(const dcp_paged_cache* c, const dcp_config* g, dcp_cache* 
   pv->pg = pg;
   pv->window_blocks = c->window_blocks;
   pv->n_blocks = c->n_blocks;
+  pv->block_ref = nullptr;
   return DCP_OK;
 }
 
@@ -570,6 +576,19 @@ dcp_status dcp_paged_prune_step(const dcp_paged_cache* cache, const dcp_config* 
                          head_is_static, kept_dev, kept_host_pinned, ws, ws_bytes, stream);
 }
 
+dcp_status dcp_paged_prune_step_shared(const dcp_paged_cache* cache, const dcp_config* cfg, const int32_t* block_ref,
+                                       const float* x0hat, const float* xref, int32_t dd, int32_t evict_slot,
+                                       int32_t evict_first_frame, int32_t q0_prev, int32_t q0,
+                                       const uint8_t* head_is_static, int32_t* kept_dev, int32_t* kept_host_pinned,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  dcp_cache shadow;
+  PagedView pv;
+  if (paged_view(cache, cfg, &shadow, &pv) != DCP_OK || !block_ref || !aligned(block_ref, 4)) return DCP_EINVAL;
+  pv.block_ref = block_ref;
+  return prune_step_impl(&shadow, &pv, cfg, x0hat, xref, dd, evict_slot, evict_first_frame, q0_prev, q0,
+                         head_is_static, kept_dev, kept_host_pinned, ws, ws_bytes, stream);
+}
+
 uint32_t dcp_abi_paged_cache_size(void) { return (uint32_t)sizeof(dcp_paged_cache); }
 
 dcp_status dcp_phase_table(const dcp_config* g, int32_t q0, int32_t frame_lo, int32_t frame_hi, float* out,
@@ -675,6 +694,9 @@ dcp_status prune_step_impl(const dcp_cache* cache, const PagedView* pv, const dc
     sp.tbl_b = pg.src_blocks;
     sp.n_tbl_b = (int32_t)per_chunk;
     sp.n_blocks = pv->n_blocks;
+    sp.block_ref = pv->block_ref;
+    sp.block_size = pv->pg.bs;
+    sp.history_turns = rephase && !inside_span(cfg, d, q0);
     sp.n_tbl_slices = (sp.n_tbl_a + sp.n_tbl_b + kThreads - 1) / kThreads;
   }
   if (ws_clear_bytes && cudaMemsetAsync(ws, 0, ws_clear_bytes, st) != cudaSuccess) return DCP_ECUDA;

@@ -39,7 +39,9 @@ struct Ctrl {
   int32_t n_dyn;            // receiving planes in the list
   int64_t snap_rows;        // snapshot / restore: saved rows per tensor
   int64_t snap_data_off;    // snapshot / restore: byte offset of the K block in the image
-  int32_t pad[42];
+  int32_t acc_shared_end;   // max over history blocks held in common of their place in the table + 1
+  int32_t acc_shared_first_inv;  // max over them of INT32_MAX - place
+  int32_t pad[40];
 };
 static_assert(sizeof(Ctrl) == 256, "ctrl block is one 256-byte line");
 
@@ -108,6 +110,10 @@ struct ScanParams {
   const int32_t* tbl_b;
   int32_t n_tbl_a, n_tbl_b, n_tbl_slices;
   int64_t n_blocks;
+  // nullable: reference counts of the blocks.  A step that would write a history block (tbl_a) that more than one table
+  // entry names is refused: the blocks the kept rows enter, and every one in use when the history's keys turn.
+  const int32_t* block_ref;
+  int32_t block_size, history_turns;
   // phase tables, built by the CTAs numbered past the tiles (tbl_per entries each, at most kTableEntries)
   int32_t n_trig_blocks, tbl_per;
   float4* trig_g;          // [F][n_t]: turn from t to t~(t; q0) for the leaving chunk's frames

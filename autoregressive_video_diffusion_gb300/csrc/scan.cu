@@ -173,13 +173,18 @@ __device__ void plane_checks(const ScanParams& p, int slice, int* s_warp, int* s
 // before anything moves (the gather and re-index kernels read the tables only after the verdict).
 __device__ void table_checks(const ScanParams& p, int slice) {
   const int e = slice * kThreads + threadIdx.x;
-  int bad = 0;
+  int bad = 0, shared = 0;
   if (e < p.n_tbl_a + p.n_tbl_b) {
     const int32_t b = e < p.n_tbl_a ? p.tbl_a[e] : p.tbl_b[e - p.n_tbl_a];
     bad = b < 0 || (int64_t)b >= p.n_blocks;
+    shared = p.block_ref && e < p.n_tbl_a && !bad && p.block_ref[b] > 1;
   }
   bad = __reduce_max_sync(kFull, bad);
   if ((threadIdx.x & 31) == 0 && bad) atomicMax(&p.ctrl->acc_bad, 1);
+  if (shared) {
+    atomicMax(&p.ctrl->acc_shared_end, e + 1);
+    atomicMax(&p.ctrl->acc_shared_first_inv, INT32_MAX - e);
+  }
 }
 
 // theta_p = base^(-p / n_t) is evaluated as exp2(log2(base) * (-p / n_t)) (dev_turn_entry).
@@ -290,7 +295,12 @@ __device__ void finalize(const ScanParams& p, int* s_warp, int* s_pick) {
   const bool random = p.x0hat && p.keep_rule == 2;
   // the check accumulators (other CTAs' atomics), read now so their round trip overlaps the ballot words' loads
   int len1 = 0, min_inv = 0, first_inv = 0, longest = 0, bad = 0, all_min_inv = 0, n_dyn = 0;
+  int shared_end = 0, shared_first_inv = 0;
   if (threadIdx.x == 0) {
+    if (p.block_ref) {
+      shared_end = __ldcg(&c->acc_shared_end);
+      shared_first_inv = __ldcg(&c->acc_shared_first_inv);
+    }
     n_dyn = __ldcg(&c->acc_n_dyn);
     len1 = __ldcg(&c->acc_len_max1);
     min_inv = __ldcg(&c->acc_len_min_inv);
@@ -338,6 +348,15 @@ __device__ void finalize(const ScanParams& p, int* s_warp, int* s_pick) {
         set_status(p.status, DCP_ECAPACITY);
       }
     }
+    if (shared_end && !abort) {  // rows of the blocks held in common: [shared_lo, shared_hi) holds them all
+      const int64_t shared_lo = (int64_t)(INT32_MAX - shared_first_inv) * p.block_size;
+      const int64_t shared_hi = (int64_t)shared_end * p.block_size;
+      if ((p.history_turns && longest > shared_lo) ||
+          (has_dyn && common < shared_hi && (int64_t)common + k > shared_lo)) {
+        abort = 1;
+        set_status(p.status, DCP_EDEVICE);
+      }
+    }
     c->k = k;
     c->has_dyn = has_dyn ? 1 : 0;
     c->common_len = common;
@@ -353,6 +372,8 @@ __device__ void finalize(const ScanParams& p, int* s_warp, int* s_pick) {
     c->acc_rp_max = 0;
     c->acc_all_min_inv = 0;
     c->acc_bad = 0;
+    c->acc_shared_end = 0;
+    c->acc_shared_first_inv = 0;
     c->n_dyn = n_dyn;
     c->acc_n_dyn = 0;
     c->done = 0u;

@@ -21,7 +21,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import autoregressive_video_diffusion_gb300 as dcp  # noqa: E402
 
 LAYERS, HEADS, KV_HEADS, D, BS = 2, 8, 4, 64, 16
-# every phase offset stays in g's identity range, so history pages never change and branches can share them
+# Every phase offset stays in g's identity range, so history pages never change and branches can share the full ones.
+# (Past the span the prune steps turn the whole history: branches would then share the sink's pages only.)
 CFG = dcp.Config(gamma=0.10, sink_chunks=1, window_chunks=2, tokens_per_frame=16, frames_per_chunk=4,
                  n_temporal_pairs=8, g_recent_R=1000.0, g_span_S=1000.0, max_frames=128)
 C, SLOTS, HIST_CAP = CFG.C, CFG.window_chunks + 1, 512
@@ -129,6 +130,7 @@ def main() -> float:
     tables = perm[:n_table][None].contiguous()
     ref = torch.zeros(n_blocks, dtype=torch.int32, device="cuda")
     ref[tables[0].long()] = 1
+    cache.block_ref = ref  # a prune step that would write a shared page is refused
     root = Session(cache, tables[0])
     worst = 0.0
     for _ in range(6):

@@ -274,6 +274,20 @@ dcp_status dcp_paged_prune_step(const dcp_paged_cache* cache, const dcp_config* 
                                 int32_t q0_prev, int32_t q0, const uint8_t* head_is_static_dev, int32_t* kept_dev,
                                 int32_t* kept_host_pinned, void* workspace_dev, size_t ws_bytes, void* stream);
 
+/* dcp_paged_prune_step on a cache some of whose blocks other sequences hold too (branches made by dcp_pages_fork).
+ * block_ref_dev [n_blocks] holds the blocks' reference counts as the dcp_pages_* calls keep them.  The step writes the
+ * history blocks that the kept rows enter, and with reindex_mode 0, once the oldest non-sink offset q0 - T_s lies past
+ * the span (g_span_S in g_mode 0, g_recent_R + g_span_S in g_mode 1), the keys of every history block in use: turned in
+ * place, which each holder of a common block would do again.  Where a block with a count above 1 is among these (or
+ * between two such blocks), the step records DCP_EDEVICE and leaves the cache as it was.  dcp_paged_prune_step itself
+ * knows no counts: there the caller sees to it that no such block is shared.
+ * Host errors: those of dcp_paged_prune_step, and a null or misaligned block_ref_dev. */
+dcp_status dcp_paged_prune_step_shared(const dcp_paged_cache* cache, const dcp_config* cfg,
+                                       const int32_t* block_ref_dev, const float* x0hat_dev, const float* xref_dev,
+                                       int32_t d, int32_t evict_slot, int32_t evict_first_frame, int32_t q0_prev,
+                                       int32_t q0, const uint8_t* head_is_static_dev, int32_t* kept_dev,
+                                       int32_t* kept_host_pinned, void* workspace_dev, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------------------------------------------
  * Host snapshot and restore of the pruned cache.
  * Page "기술 요약: 생성형 월드 모델을 위한 지속적 계산 상태" (gist.science/ko/paper/2607.21686), section "PCS contract":
@@ -472,6 +486,12 @@ dcp_status dcp_pages_copy(const dcp_page_pool* pool, const int32_t* src_dev, con
  * (their counts grow), the others are copied to fresh blocks, and further fresh blocks are reserved up to
  * reserve[c] positions (null: none).  Fresh blocks are the lowest free ones, in the order of (child, page); their
  * count becomes 1.  child_tables [n_children][stride] gets the children's rows (-1 past their pages).
+ * A shared page may be read by all its holders and must be written by none: a page that will be written belongs past
+ * the shared ones.  The full pages, the default, suit rows that only grow.  dcp_rope_append writes the pages of the new
+ * tokens (a ring slot's pages are written again when the slot is), dcp_paged_prune_step the pages that its kept rows
+ * enter, and with reindex_mode 0, once q0 - T_s lies past the span, every page of the history: a cache in that state
+ * shares the pages before its history (its sink) and no more.  dcp_paged_prune_step_shared refuses a step that would
+ * write a shared page.
  * ref_in -> ref_out (may be the same array).  child_tables must not overlap `tables`.
  * Device errors: DCP_ECAPACITY (not enough free blocks), DCP_EDEVICE (a parent outside [0, n_rows), a length or
  * shared count outside its row, an entry of the parent's pages that names no live block): no page is copied then,
