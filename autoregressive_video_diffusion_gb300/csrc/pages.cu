@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(kPlan) free_kernel(PageParams p, const int32_t
   }
 }
 
+constexpr int kTaken = INT32_MIN;
+
 __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int32_t* tables, int64_t n,
                                                         const int32_t* ref_in, int32_t* tables_out, int32_t* ref_out,
                                                         int32_t* n_live, int32_t* ws) {
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
   wait_for_predecessor();
   __shared__ int s_warp[32];
   int2* moves = (int2*)(ws + kHead);
-  int32_t* to = ws + kHead + 2 * p.n_blocks;  // where every block goes
+  // where every block goes: itself or its hole; of a free block -1 - itself, or kTaken where a page moves into it
+  int32_t* to = ws + kHead + 2 * p.n_blocks;
   int mine = 0, live;
   for (int64_t b = threadIdx.x; b < p.n_blocks; b += kPlan) mine += ref_in[b] > 0;
   block_scan(mine, s_warp, &live);
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
     if (hole) moves[h].y = (int)b;
     if (mover) moves[m].x = (int)b;
     if (b < p.n_blocks) {
-      to[b] = (int)b;
+      to[b] = r > 0 ? (int)b : -1 - (int)b;
       ref_out[b] = r;
     }
   }
@@ -231,14 +234,24 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
   for (int i = threadIdx.x; i < movers; i += kPlan) {
     const int2 m = moves[i];
     to[m.x] = m.y;
+    to[m.y] = kTaken;
     ref_out[m.y] = ref_out[m.x];
     ref_out[m.x] = 0;
   }
   __syncthreads();
   for (int64_t i = threadIdx.x; i < n; i += kPlan) {
     const int b = tables[i];
-    if (b >= p.n_blocks) set_status(p.status, DCP_EDEVICE);
-    tables_out[i] = b < 0 ? -1 : b >= p.n_blocks ? b : to[b];
+    int now = b < 0 ? -1 : b;
+    if (b >= p.n_blocks) {
+      set_status(p.status, DCP_EDEVICE);
+    } else if (b >= 0) {
+      now = to[b];
+      if (now < 0) {  // a free block: nothing of the row's stands there
+        set_status(p.status, DCP_EDEVICE);
+        now = now == kTaken ? -1 : b;
+      }
+    }
+    tables_out[i] = now;
   }
   if (threadIdx.x == 0) {
     ws[0] = movers;

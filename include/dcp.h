@@ -511,7 +511,8 @@ dcp_status dcp_pages_free(const dcp_page_pool* pool, const int32_t* tables_dev, 
 /* Pack the live blocks (ref > 0) to the front: the i-th live block at or past n_live moves into the i-th free block
  * before it, in every layer; tables (all rows that name blocks of this pool) and counts follow.  tables_out and
  * ref_out may be their inputs.  n_live_dev (nullable): number of live blocks.  DCP_EDEVICE: a table entry past
- * n_blocks (kept as it is). */
+ * n_blocks (kept as it is), or one that names a free block (kept too, but -1 where a page moves into that block: it
+ * would come to name another row's page). */
 dcp_status dcp_pages_compact(const dcp_page_pool* pool, const int32_t* tables_dev, int32_t n_rows, int32_t stride,
                              const int32_t* ref_in_dev, int32_t* tables_out_dev, int32_t* ref_out_dev,
                              int32_t* n_live_dev, void* workspace_dev, size_t ws_bytes, void* stream);

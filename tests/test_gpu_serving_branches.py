@@ -13,7 +13,7 @@ from tests import devcache
 from tests.paged import PagedCopy
 from tests.serving import HND, NHD, ints
 from tests.test_gpu_parity import _cuda, assert_cache_parity
-from tests.test_gpu_serving import same
+from tests.test_gpu_serving import Pages, dev, same
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,23 @@ def test_prune_step_without_counts_and_with_bad_ones(gpu):
     m.block_ref = f.ref.long()
     with pytest.raises(dcp.DcpError):
         f.step(m)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_compact_entries_that_name_free_blocks(gpu, in_place):
+    """Reported; such an entry is emptied where a page moves into its block, so that it cannot come to name another
+    row's page, and kept where the block stays free."""
+    p = Pages(2, 40, (1, 1, 8), 1, [1], 6)
+    p.ref[:] = 0
+    p.ref[[1, 3, 30, 31]] = 1  # the 4 live blocks: 30 and 31 move into the free 0 and 2
+    t = np.array([[1, 3, 30, 31, -1, -1], [2, 35, 3, 0, 7, -1]], np.int32)
+    k0, v0 = p.k.clone(), p.v.clone()
+    td, rin, n = dev(t), dev(p.ref), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tout, rout = (td, rin) if in_place else (torch.zeros_like(td), torch.full_like(rin, 9))
+    ws = dcp.new_workspace(dcp.dcp_pages_workspace_size(p.pool, 2, 6))
+    dcp.dcp_pages_compact(p.pool, td, rin, tout, rout, n, ws)
+    assert dcp.dcp_get_status(p.status) == dcp.DCP_EDEVICE
+    assert tout.tolist() == [[1, 3, 0, 2, -1, -1], [-1, 35, 3, -1, 7, -1]]
+    assert n.item() == 4 and rout.tolist() == [1] * 4 + [0] * 36
+    for x, x0 in ((p.k, k0), (p.v, v0)):
+        assert same(x[:, :4], x0[:, [30, 1, 31, 3]])
