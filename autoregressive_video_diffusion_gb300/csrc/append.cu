@@ -3,7 +3,9 @@
 // A CTA takes a token: each thread first loads its first vectors of q, k, v (they depend on nothing), then the CTA
 // finds the token's sequence, phase and page row and builds its cos/sin in shared memory, then turns and stores.  The
 // phase in turns is an integer product modulo 2^64, so whole turns drop out exactly at any distance; cos and sin are
-// taken of the remaining fraction, once per token and pair, and shared by all heads.
+// taken of 32 bits of the remaining fraction, once per token and pair, and shared by all heads.  (The plan's fractions
+// are good to 2^-62 of a turn and the cut is one of 2^-32, so the phase is off by less than 2^-30 turns at the ends of
+// the int32 range.)
 // The bound is HBM (each of q, k, v read and written once); a few tokens are bound by the chain launch -> q_start,
 // kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 68 us (5.7 TB/s), 3375 tokens
 // of 32 + 8 + 8 fp32 heads of 96 25 us (5.0 TB/s), 32 tokens 4.0 us in a graph.
@@ -138,9 +140,13 @@ __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant_
   for (int i = threadIdx.x; i < half; i += kTurners) {
     const int32_t phase = p.positions ? p.positions[tok] : where.phase;
     const uint64_t turn = (uint64_t)(int64_t)phase * p.turns[i];
+    // the fraction of a turn, 32 bits: what fp32 holds of it, and the rest as a first-order correction
+    const int32_t fraction = (int32_t)(turn >> 32);
+    const float most = (float)fraction;
+    const float rest = (float)((int64_t)fraction - (int64_t)most) * (float)(3.14159265358979323846 * 0x1p-31);
     float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-    cs[i] = make_float2(c * p.amplitude, s * p.amplitude);
+    sincospif(most * 0x1p-31f, &s, &c);
+    cs[i] = make_float2(fmaf(-s, rest, c) * p.amplitude, fmaf(c, rest, s) * p.amplitude);
   }
   __syncthreads();
 

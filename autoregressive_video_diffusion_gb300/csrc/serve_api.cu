@@ -9,8 +9,69 @@ using namespace dcp;
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+// ------------------------------------------------------------------------------------------ frequencies
+// A phase of 2^-30 turns at positions up to 2^31 takes theta / (2 pi) to 2^-62, more than a double holds.  So the plan
+// computes in unevaluated sums of two doubles (Dekker 1971, Knuth's exact sum; products through fma), about 100 bits.
+struct Two {
+  double hi, lo;
+};
 
+Two quick_sum(double a, double b) {  // |a| >= |b|
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+Two exact_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Two exact_product(double a, double b) {
+  const double p = a * b;
+  return {p, std::fma(a, b, -p)};
+}
+Two operator+(Two x, Two y) {
+  const Two s = exact_sum(x.hi, y.hi), t = exact_sum(x.lo, y.lo);
+  const Two u = quick_sum(s.hi, s.lo + t.hi);
+  return quick_sum(u.hi, u.lo + t.lo);
+}
+Two operator-(Two x) { return {-x.hi, -x.lo}; }
+Two operator*(Two x, Two y) {
+  const Two p = exact_product(x.hi, y.hi);
+  return quick_sum(p.hi, p.lo + (x.hi * y.lo + x.lo * y.hi));
+}
+Two operator/(Two x, Two y) {  // long division in three digits
+  const double a = x.hi / y.hi;
+  const Two r = x + -(y * Two{a, 0.0});
+  const double b = r.hi / y.hi;
+  const Two s = r + -(y * Two{b, 0.0});
+  return quick_sum(a, b) + Two{s.hi / y.hi, 0.0};
+}
+constexpr Two kLn2{0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56};
+constexpr Two kTwoPi{0x1.921fb54442d18p+2, 0x1.1a62633145c07p-52};
+
+// e^x: x = k ln 2 + 256 r, the Taylor sum of e^r (|r| < 0.0014: ten terms reach 2^-110), squared eight times.
+Two exp_two(Two x) {
+  const double k = std::nearbyint(x.hi / kLn2.hi);
+  Two r = x + -(kLn2 * Two{k, 0.0});
+  r = {r.hi / 256, r.lo / 256};
+  Two sum{1.0, 0.0};
+  for (int n = 10; n; --n) sum = Two{1.0, 0.0} + r * sum / Two{(double)n, 0.0};
+  for (int i = 0; i < 8; ++i) sum = sum * sum;
+  return {std::ldexp(sum.hi, (int)k), std::ldexp(sum.lo, (int)k)};
+}
+// ln x: one Newton step from the double's logarithm.
+Two log_two(double x) {
+  const Two y{std::log(x), 0.0};
+  return y + (Two{x, 0.0} * exp_two(-y) + Two{-1.0, 0.0});
+}
+// x modulo 1 in steps of 2^-64, for 0 <= x.
+uint64_t fraction(Two x) {
+  const double whole = std::floor(x.hi), scaled = std::ldexp(x.hi - whole, 64), steps = std::floor(scaled);
+  // a low part of an eighth and more belongs to a double without a fraction: no phase is left to speak of
+  const double low = std::fabs(x.lo) < 0.125 ? std::floor((scaled - steps) + std::ldexp(x.lo, 64)) : 0.0;
+  return (uint64_t)steps + (uint64_t)(int64_t)low;
+}
+
+// ------------------------------------------------------------------------------------------ checks
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int elem_size(int32_t dtype) { return dtype == DCP_BF16 ? 2 : 4; }
@@ -119,23 +180,32 @@ dcp_status dcp_rope_plan_init(const dcp_rope_config* g, dcp_rope_plan* plan) {
       (!std::isfinite(g->orig_len) || !(g->orig_len > 0.0) || !std::isfinite(g->beta_fast) ||
        !std::isfinite(g->beta_slow) || !(g->beta_fast > g->beta_slow)))
     return DCP_EINVAL;
-  double base = g->base;
-  if (g->scaling == DCP_ROPE_BASE && g->rot_dim > 2) {
-    base *= std::pow(g->factor, (double)g->rot_dim / (g->rot_dim - 2));
+  const int rot = g->rot_dim;
+  if (g->scaling == DCP_ROPE_BASE && rot > 2) {
+    const double base = g->base * std::pow(g->factor, (double)rot / (rot - 2));
     if (!std::isfinite(base) || !(base > 0.0)) return DCP_EINVAL;
   }
+  Two log_base = log_two(g->base);
+  if (g->scaling == DCP_ROPE_BASE && rot > 2)
+    log_base = log_base + log_two(g->factor) * Two{(double)rot, 0.0} / Two{rot - 2.0, 0.0};
+  const Two factor{g->factor, 0.0}, one{1.0, 0.0};
   uint64_t turn_of[DCP_ROPE_MAX_PAIRS] = {};
-  for (int p = 0; p < g->rot_dim / 2; ++p) {
-    double theta = std::pow(base, -2.0 * p / g->rot_dim);
-    if (g->scaling == DCP_ROPE_LINEAR) theta /= g->factor;
+  for (int p = 0; p < rot / 2; ++p) {
+    Two theta = exp_two(log_base * Two{-2.0 * p, 0.0} / Two{(double)rot, 0.0});
+    if (g->scaling == DCP_ROPE_LINEAR) theta = theta / factor;
     if (g->scaling == DCP_ROPE_PARTS) {
-      const double r = (g->orig_len * theta / kTwoPi - g->beta_slow) / (g->beta_fast - g->beta_slow);
-      const double ramp = r < 0.0 ? 0.0 : r > 1.0 ? 1.0 : r;
-      theta *= ramp + (1.0 - ramp) / g->factor;
+      const double rough = (g->orig_len * theta.hi / kTwoPi.hi - g->beta_slow) / (g->beta_fast - g->beta_slow);
+      const Two slow{-g->beta_slow, 0.0};
+      Two ramp = rough > 0.5 ? one : Two{0.0, 0.0};
+      if (rough > -1.0 && rough < 2.0) {
+        const Two r = (theta * Two{g->orig_len, 0.0} / kTwoPi + slow) / (Two{g->beta_fast, 0.0} + slow);
+        if (r.hi >= 0.0 && r.hi < 1.0) ramp = r;
+      }
+      theta = theta * (ramp + (one + -ramp) / factor);
     }
-    const double turns = theta / kTwoPi;
-    if (!std::isfinite(turns)) return DCP_EINVAL;
-    turn_of[p] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+    const Two turns = theta / kTwoPi;
+    if (!std::isfinite(turns.hi) || !std::isfinite(turns.lo)) return DCP_EINVAL;
+    turn_of[p] = fraction(turns);
   }
   for (int p = 0; p < DCP_ROPE_MAX_PAIRS; ++p) plan->turns[p] = turn_of[p];
   plan->rot_dim = g->rot_dim;

@@ -427,7 +427,8 @@ dcp_status dcp_rope_plan_init(const dcp_rope_config* cfg, dcp_rope_plan* plan);
  *         keys are appended).
  * kv_len_per_head must be 0.  Rows of q that belong to no sequence are not written.  A new token whose cache position
  * is negative (kv_len < q_len) is turned into q_out and not stored.
- * Sequences must not share the pages their new tokens enter.  Angles are exact to 2^-30 turns for any int32 position. */
+ * Sequences must not share the pages their new tokens enter.  Phases are exact to 2^-30 turns for any int32 position;
+ * sines and cosines are then held in fp32. */
 dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_plan* plan,
                            const void* q_dev, int64_t q_stride, int32_t Hq, const void* k_dev, const void* v_dev,
                            int64_t kv_stride, const int32_t* positions_dev, void* q_out_dev, void* stream);
