@@ -91,9 +91,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo: hi the upper 11 significant bits, lo the rest, rounded where the products cut it (they read 11 bits).
-// Infinities and NaN stay in hi alone.
+// An infinity or NaN is (0, x): of the three products, only the one with the other factor's large part then sees it.
+// (As (x, 0) it met the other's low part too, which is 0 for a factor of few bits, a weight of 1 among them: 0 times
+// infinity is NaN.)  A NaN has all its bits set, lest the cut make it an infinity.
 __device__ __forceinline__ uint2 halves(uint32_t x) {
-  if ((x & 0x7F800000u) == 0x7F800000u) return make_uint2(x, 0);
+  if ((x & 0x7F800000u) == 0x7F800000u) return make_uint2(0, x & 0x007FFFFFu ? 0x7FFFFFFFu : x);
   const uint32_t hi = x & 0xFFFFE000u;
   return make_uint2(hi, __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u);
 }
