@@ -5,8 +5,9 @@
 
 namespace dcp {
 
-// A split leaves for each of its rows [m, l, -, -, o_0 .. o_{D-1}] in fp32: the running maximum in units of log2, and
-// the sums of weights and weighted values relative to it.  An item's parts are [split][rows][kPartHead + D].
+// A split leaves for each of its rows [m, l, -, -, o_0 .. o_{D-1}] in fp32: the running maximum of the scores before
+// scaling (scaled maxima lose the bits that tell large ones apart), and the sums of weights and weighted values relative
+// to it.  An item's parts are [split][rows][kPartHead + D].
 constexpr int kPartHead = 4;
 
 __device__ __forceinline__ float* part_of(float* parts, int64_t item, int splits, int split, int rows, int D, int r) {
@@ -19,9 +20,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// lse of a row from its maximum (in units of log2) and sum.
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l != 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+// lse of a row from its maximum (before scaling) and sum.
+__device__ __forceinline__ float row_lse(const AttendParams& a, float m, float l) {
+  return l != 0.f ? m * fabsf(a.scale) + __log2f(l) * 0.6931471805599453f : -INFINITY;
 }
 
 // Called by a whole CTA after its part is written; true for the item's last CTA.  The parts are read in the order of
@@ -93,7 +94,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     for (int k = lane; k < splits; k += 32) {
-      const float wk = ls[k] == 0.f ? 0.f : exp2_fast(w[k] - top);
+      const float wk = ls[k] == 0.f ? 0.f : exp2_fast((w[k] - top) * a.scale_log2);
       w[k] = wk;
       if (wk != 0.f) l += wk * ls[k];
     }
@@ -102,7 +103,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
     if (lane == 0) {
       inv[r] = l != 0.f ? 1.f / l : 0.f;
       const int R = row0 + r, tok = R / a.G;
-      if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(top, l);
+      if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(a, top, l);
     }
   }
   __syncthreads();

@@ -29,13 +29,11 @@ constexpr int kMaxSplits = 64;
 constexpr int kEvenItems = 512;  // items whose tiles can be shared evenly
 
 constexpr int kMaxSms = 160;       // the join's scratch holds a part of two CTAs on each
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct RowParams {
   AttendParams a;
   int even;                     // 1: the CTAs share all items' key tiles evenly
   int splits, span, row_tiles;  // else keys of an item are cut into pieces of `span`
-  float scale_log2;             // |scale| log2 e
   uint32_t flip;                // sign bit of a scale below 0, put into q
   float* part;
   uint32_t* done;
@@ -311,16 +309,17 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
         for (int n = 0; n < R::kTiles; ++n) top = fmaxf(top, fmaxf(x[n][2 * e], x[n][2 * e + 1]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        keep[e] = m[e] == top ? 1.f : exp2_fast((m[e] - top) * p.scale_log2);
+        keep[e] = m[e] == top ? 1.f : exp2_fast((m[e] - top) * a.scale_log2);
         m[e] = top;
-        const float off = top == -INFINITY ? 0.f : top * p.scale_log2;
+        // the maximum comes off before the scaling: the scaled one is rounded by more than fp32's exponents from 2^31 on
+        const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
 #pragma unroll
         for (int n = 0; n < R::kTiles; ++n)
 #pragma unroll
           for (int b = 2 * e; b < 2 * e + 2; ++b) {
             const bool hidden = x[n][b] == -INFINITY;
-            x[n][b] = exp2_fast(fmaf(x[n][b], p.scale_log2, -off));
+            x[n][b] = exp2_fast((x[n][b] - base) * a.scale_log2);
             sum += x[n][b];
             if (poison && hidden) x[n][b] = -1.f;
           }
@@ -414,7 +413,6 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
   for (int e = 0; e < 2; ++e) {
     l[e] += __shfl_xor_sync(~0u, l[e], 1);
     l[e] += __shfl_xor_sync(~0u, l[e], 2);
-    if (m[e] != -INFINITY) m[e] *= p.scale_log2;
   }
 
   // ---- results
@@ -433,7 +431,7 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
       *reinterpret_cast<uint32_t*>(a.out + (row * D + d) * 2) = pack_bf16x2(y0 * inv, y1 * inv);
     else
       *reinterpret_cast<float2*>(a.out + (row * D + d) * 4) = make_float2(y0 * inv, y1 * inv);
-    if (a.lse && d == 0) a.lse[row] = row_lse(mr, lr);
+    if (a.lse && d == 0) a.lse[row] = row_lse(a, mr, lr);
   };
   if constexpr (MW > 1) {
 #pragma unroll
@@ -467,7 +465,7 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
       for (int w = 0; w < R::kWarps; ++w) {
         const float* at = join + (w * 16 + r) * (DP + 2);
         if (at[1] == 0.f) continue;
-        const float k = exp2_fast(at[0] - top);
+        const float k = exp2_fast((at[0] - top) * a.scale_log2);
         sum += k * at[1];
         y0 += k * at[2 + d];
         y1 += k * at[3 + d];
@@ -673,10 +671,6 @@ cudaError_t launch_attend_rows(const AttendParams& a, int64_t max_kv, void* ws, 
   p.splits = r.splits;
   p.span = r.span;
   p.row_tiles = r.tiles;
-  // a scale below 0 negates q (the running maximum then is of what is exponentiated); one near 0 is held where masked
-  // scores of -inf still scale to -inf
-  const float mag = a.scale < 0.f ? -a.scale : a.scale;
-  p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
   p.flip = a.scale < 0.f ? 0x80000000u : 0u;
   p.done = done_counters(ws);
   p.part = (float*)((char*)ws + kScratch);

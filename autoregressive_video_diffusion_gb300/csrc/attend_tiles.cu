@@ -13,7 +13,8 @@
 // tile's weights have added up to more than 2^8, which leaves O untouched in almost every step; m has moved or not, the
 // quotient O / l is the same (weights keep their relative precision in bf16, sums are held in 32 bits).  Only a row
 // whose scores rise by more than 2^64 within one tile, or lie beyond 2^8192 (levels travel between a row's threads in
-// bf16), needs more care: its item is then done again with each tile's own maximum, told in two parts.
+// bf16), needs more care: its item is then done again with each tile's own maximum, in fp32, taken off before the
+// scaling.
 //
 // Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warps 16, 17: issue the matrix products of row tile 0 and 1 (one
 // warp for both was busy for 3600 clocks a step of 2048 clocks of products).  Warps 18, 19: copy the pages of the keys
@@ -40,7 +41,6 @@ constexpr int kKeys = 128;             // keys of a tile
 constexpr int kTileThreads = 640;
 constexpr int kSoftWarps = 16;
 constexpr int kMaxSplits = 92;         // of an item: what the join's scratch holds
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
 constexpr float kFar = 64.f;           // and within one tile before the item is done again
 constexpr float kHuge = 8192.f;        // log2 of a weight whose level, heard in bf16, is too coarse for kFar
@@ -88,7 +88,6 @@ struct TileParams {
   Tiling tl;
   int splits, q_tiles;
   int whole;                           // items of one CTA each before those that are split
-  float scale_log2;                    // |scale| log2 e
   uint32_t idesc_qk, idesc_pv;
   float* part;                         // [item][split][256][kPartHead + D] partial results
   uint32_t* done;                      // [item] splits finished, 0 between calls
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const bool mine = r < rows_i;  // rows past the sequence's take part unmasked, and nothing of theirs is kept
     const int seen_end = a.causal && mine ? min(it.kv, c + 1) : it.kv;
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
-    const float sc = p.scale_log2, per_log2 = 1.f / sc;
+    const float sc = a.scale_log2, per_log2 = 1.f / sc;
     const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
     const bool narrow = tl.columns() < kKeys || tl.gaps();
     uint32_t see_open[2];  // columns that stand for keys
@@ -570,20 +569,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int u = 0; u < 32; ++u) top[u & 3] = max3(top[u & 3], x[0][u], x[1][u]);
           const float mine_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           if (careful) {
-            // both threads here, then the maximum in two bf16 parts through both buffers
+            // both threads here, then the maximum as it is, in the place of both buffers
             if (lane == 0) bar_arrive(met);
             ok = warp_wait(met, swaps++ & 1, &sh.dead);
-            const __nv_bfloat16 high = __float2bfloat16_rn(mine_top);
-            const float rest = mine_top - __bfloat162float(high);
-            const __nv_bfloat16 low = __float2bfloat16_rn(rest == rest ? rest : 0.f);
-            sh.swap.top[i][0][hf][r] = high;
-            sh.swap.top[i][1][hf][r] = low;
+            sh.swap.sum[i][hf][r] = mine_top;
             __syncwarp();
             if (lane == 0) bar_arrive(met);
             ok = ok && warp_wait(met, swaps++ & 1, &sh.dead);
-            seen = fmaxf(seen, fmaxf(__bfloat162float(high) + __bfloat162float(low),
-                                     __bfloat162float(sh.swap.top[i][0][hf ^ 1][r]) +
-                                         __bfloat162float(sh.swap.top[i][1][hf ^ 1][r])));
+            seen = fmaxf(seen, fmaxf(mine_top, sh.swap.sum[i][hf ^ 1][r]));
           } else {
             tell(mine_top);
             hear();
@@ -594,7 +587,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         } else if (hide) {
           cover(0);
         }
-        const float off = m == -INFINITY ? 0.f : -m * sc;
+        const float base = m == -INFINITY ? 0.f : m, off = careful ? 0.f : -base * sc;
+        if (careful) {  // scores of any size: their distance from the level is scaled, not the level
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int u = 0; u < 32; ++u) x[e][u] = __float_as_uint(__uint_as_float(x[e][u]) - base);
+        }
         const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -742,10 +741,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (mine && ok && hf == 0) {
       if (splits > 1) {
-        part[0] = m == -INFINITY ? m : m * sc;
+        part[0] = m;
         part[1] = l;
       } else if (a.lse) {
-        a.lse[row] = row_lse(m * sc, l);
+        a.lse[row] = row_lse(a, m, l);
       }
     }
   } else {
@@ -990,10 +989,6 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   p.splits = t.splits;
   p.whole = (int)t.whole;
   p.q_tiles = t.q_tiles;
-  // a scale below 0 negates the products (the running maximum then is of what is exponentiated); one near 0 is held
-  // where masked scores of -inf still scale to -inf
-  const float mag = a.scale < 0.f ? -a.scale : a.scale;
-  p.scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * kLog2e;
   p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
   p.idesc_pv = idesc((a.pool.D + 15) / 16 * 16, true, false);
   p.done = done_counters(ws);

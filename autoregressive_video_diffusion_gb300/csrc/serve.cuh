@@ -52,6 +52,8 @@ struct AttendParams {
   int32_t Hq, G;                // query heads, and those of one KV head
   int32_t causal, window;
   float scale;
+  float scale_log2;             // its size in units of log2 (exponentials are powers of two), in kernels; the sign is the
+                                // products' (a scale below 0 negates them: maxima then are of what is exponentiated)
 };
 
 struct PageParams {

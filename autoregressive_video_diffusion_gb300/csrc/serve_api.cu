@@ -1,5 +1,6 @@
 // Host side of the serving operators: argument checks, the rotary plan and the launches.
 // The entry points and their contracts are documented in include/dcp.h.
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -135,6 +136,9 @@ AttendParams attend_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, cons
   p.causal = cfg->causal;
   p.window = cfg->window < kMaxKv ? cfg->window : kMaxKv;
   p.scale = cfg->scale;
+  // one near 0 is held where masked scores of -inf still scale to -inf
+  const double mag = std::fabs((double)cfg->scale);
+  p.scale_log2 = (float)std::fmin((mag < 1e-30 ? 1e-30 : mag) * 1.4426950408889634, (double)FLT_MAX);
   return p;
 }
 

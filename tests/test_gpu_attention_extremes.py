@@ -75,3 +75,36 @@ def test_attention_nan_that_is_seen(gpu, dtype, nq):
     out, _ = attend(c, q, False)
     nan = torch.isnan(out)
     assert nan[:, :, 3].all() and not nan[:, :, :3].any() and not nan[:, :, 4:].any()
+
+
+# ------------------------------------------------------------------------------------------ scores of any size
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,kv,hq,h", [(1, 600, 2, 2), (1, 9000, 4, 1), (40, 600, 2, 2), (200, 600, 4, 2),
+                                        (200, 5000, 2, 1)])
+@pytest.mark.parametrize("scale", [3e4, 1e6, -1e9, 1e20, 3e35])
+def test_attention_of_a_finite_scale(gpu, dtype, nq, kv, hq, h, scale):
+    """Queries and keys are small whole numbers, so products are exact in 32 bits and the largest scores lie at least
+    `scale` apart: a row is the mean of the values at its largest score, its lse that score (and the log of their
+    number)."""
+    c = Cache(dtype, HND, h, 64, 16, [nq], [kv], seed=24)
+    c.keys[0] = torch.randint(-8, 9, (kv, h, 64), generator=c.g).to(c.dt).cuda()
+    c.fill()
+    q = torch.randint(-8, 9, (nq, hq, 64), generator=c.g).to(c.dt).cuda()
+    out, lse = attend(c, q, True, -1, scale=scale)
+    assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
+    scale = float(torch.tensor(scale))  # as the call holds it
+    step = sv.HALF_STEP[c.dt]
+    hidden = torch.arange(kv, device="cuda")[None] > torch.arange(kv - nq, kv, device="cuda")[:, None]
+    for i in range(hq):
+        k, v = (x[:, i // (hq // h)].double() for x in (c.keys[0], c.values[0]))
+        raw = math.copysign(1.0, scale) * (q[:, i].double() @ k.T)
+        raw[hidden] = -math.inf
+        top = raw.amax(-1, keepdim=True)
+        won = (raw == top).double()
+        n = won.sum(-1, keepdim=True)
+        o, mass, l = won @ v / n, won @ v.abs() / n, (top * abs(scale) + n.log())[:, 0]
+        # equal weights of 1 (exact in bf16 too), summed in 32 bits, one reciprocal, the result's rounding
+        tol = mass * 8 * 2.0 ** -24 + step * o.abs()
+        assert ((out[:, i].double() - o).abs() <= tol).all(), (i, (out[:, i].double() - o).abs().max().item())
+        # the score in 32 bits: the scale in units of log2, the product, back, and the logarithm: a few roundings each
+        assert ((lse[:, i].double() - l).abs() <= 2.0 ** -21 * l.abs() + 2.0 ** -20).all()
