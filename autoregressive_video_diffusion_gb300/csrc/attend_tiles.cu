@@ -13,8 +13,8 @@
 // tile's weights have added up to more than 2^8, which leaves O untouched in almost every step; m has moved or not, the
 // quotient O / l is the same (weights keep their relative precision in bf16, sums are held in 32 bits).  Only a row
 // whose scores rise by more than 2^64 within one tile, or lie beyond 2^8192 (levels travel between a row's threads in
-// bf16), needs more care: its item is then done again with each tile's own maximum, in fp32, taken off before the
-// scaling.
+// bf16), or whose O has passed fp32's range by the weights of a level left behind, needs more care: its item is then done
+// again with each tile's own maximum, in fp32, taken off before the scaling.
 //
 // Warps 0-7 and 8-15: softmax of row tile 0 and 1.  Warps 16, 17: issue the matrix products of row tile 0 and 1 (one
 // warp for both was busy for 3600 clocks a step of 2048 clocks of products).  Warps 18, 19: copy the pages of the keys
@@ -43,6 +43,7 @@ constexpr int kSoftWarps = 16;
 constexpr int kMaxSplits = 92;         // of an item: what the join's scratch holds
 constexpr float kGrow = 8.f;           // log2 of how far a row's maximum may grow before m follows,
 constexpr float kFar = 64.f;           // and within one tile before the item is done again
+constexpr float kSteep = 0x1p15f;      // sum of half a tile's weights that only a rise within the tile brings about
 constexpr float kHuge = 8192.f;        // log2 of a weight whose level, heard in bf16, is too coarse for kFar
 constexpr long long kPatience = 4000000000ll;  // limit of every wait, in SM clocks (two seconds)
 
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float sum[2][2][kRows];
     } swap;
     uint32_t tmem;
-    int dead, poison, last, far;
+    int dead, poison, last, far, steep;
   };
   static_assert(sizeof(Head) <= Sh::kHead, "the head fits before the tiles");
   Head& sh = *reinterpret_cast<Head*>(smem_raw);
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         : own < 14 ? 2 : own < 15 ? 32 * kSoftWarps : 1;
       bar_init(bars + 8 * i, count);
     }
-    if (lane == 0) sh.dead = sh.poison = sh.far = 0;
+    if (lane == 0) sh.dead = sh.poison = sh.far = sh.steep = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
@@ -661,6 +662,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         y0 += y1;
         l += y0;
         if (!exact) {  // the largest weight is between a 64th of the sum and the sum
+          if (y0 > kSteep) sh.steep = 1;
           tell(m + __log2f(y0) * per_log2);
           if ((seen - m) * sc > kFar || (fabsf(seen) * sc > kHuge && seen != -INFINITY)) sh.far = 1;
         }
@@ -674,6 +676,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_before();
       __syncthreads();
       fence_after();
+      if (!careful && sh.steep) {  // weights of a level left far behind, times large values: past fp32 though O / l is not
+        bool over = false;
+        for (int e = 0; e < Sh::kD / 64 && ok && t0 < t1; ++e) {
+          uint32_t o[32];
+          tm_ld32(o, t_o + 32 * e);
+          wait_ld(o);
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            over |= hf * (Sh::kD / 2) + 32 * e + u < D && !(fabsf(__uint_as_float(o[u])) < INFINITY);
+        }
+        if (over) sh.far = 1;
+        fence_before();
+        __syncthreads();
+        fence_after();
+      }
       if (careful || !sh.far) break;
       m = seen = -INFINITY;
       l = 0.f;
@@ -802,6 +819,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           issued = 0;
         }
         __syncthreads();
+        if (!careful && sh.steep) __syncthreads();
         if (careful || !sh.far) break;
       }
     } else {
@@ -880,6 +898,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_before();
         __syncthreads();
         fence_after();
+        if (!careful && sh.steep) __syncthreads();
         if (careful || !sh.far) break;
       }
     }

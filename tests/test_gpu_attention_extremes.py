@@ -108,3 +108,28 @@ def test_attention_of_a_finite_scale(gpu, dtype, nq, kv, hq, h, scale):
         assert ((out[:, i].double() - o).abs() <= tol).all(), (i, (out[:, i].double() - o).abs().max().item())
         # the score in 32 bits: the scale in units of log2, the product, back, and the logarithm: a few roundings each
         assert ((lse[:, i].double() - l).abs() <= 2.0 ** -21 * l.abs() + 2.0 ** -20).all()
+
+
+# ------------------------------------------------------------------------------------------ large values
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 200])
+@pytest.mark.parametrize("rise", [7.0, 14.0, 30.0, 43.0])
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** 90, 2.0 ** 100])
+def test_attention_large_values_where_scores_rise(gpu, dtype, nq, rise, size):
+    """One key late in a tile outweighs all before it by e^rise and its value is large: the quotient is finite, so the
+    result is, however far the row's running level lags behind."""
+    c = Cache(dtype, HND, 1, 64, 16, [nq], [520], seed=25)
+    c.keys[0] = torch.zeros_like(c.keys[0])
+    c.values[0] = torch.ones_like(c.values[0])
+    for j in (178, 430):
+        c.keys[0][j] = rise
+        c.values[0][j] = (size * (1 + torch.arange(64) / 64)).to(c.dt).cuda()
+    c.fill()
+    q = torch.ones(nq, 2, 64, dtype=c.dt, device="cuda")
+    out, lse = attend(c, q, False, -1, scale=1.0 / 64)
+    assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
+    o, l, mass, terms = sv.attention_64(q[:, 0], c.keys[0][:, 0], c.values[0][:, 0], 0, 1.0 / 64, False, -1)
+    tol, tol_l = sv.attention_bounds(c.dt, 64, 520, o, mass, l, terms)
+    for i in range(2):
+        assert ((out[:, i].double() - o).abs() <= tol).all()
+        assert ((lse[:, i].double() - l).abs() <= tol_l).all()
