@@ -673,6 +673,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_after();
       }
       if (ok && pending) hear();
+      if (!ok) wait_st();  // weights on their way
       fence_before();
       __syncthreads();
       fence_after();
@@ -786,6 +787,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       Ring<Sh::kSlots> at{values, 0};
       int issued = 0;
+      auto in_flight = [&] {  // copies in flight end by themselves: leave when they have (or have been used)
+        const long long start = clock64();
+        for (int k = 0; k < (Sh::kSlots + 1) / 2 && k < issued; ++k) {
+          at.back();
+          at.back();
+          while (!bar_try(full(at.slot), at.phase) && !bar_try(empty(at.slot), at.phase) &&
+                 clock64() - start < kPatience) {
+          }
+        }
+        issued = 0;
+      };
       for (bool careful = false;; careful = true) {
         int next = entry(tb);
         for (int t = tb; t < te && ok; ++t) {
@@ -808,20 +820,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           at.step();
           ++issued;
         }
-        if (!ok) {  // copies in flight end by themselves: leave when they have
-          const long long start = clock64();
-          for (int k = 0; k < (Sh::kSlots + 1) / 2 && k < issued; ++k) {
-            at.back();
-            at.back();
-            while (!bar_try(full(at.slot), at.phase) && clock64() - start < kPatience) {
-            }
-          }
-          issued = 0;
-        }
+        if (!ok) in_flight();
         __syncthreads();
         if (!careful && sh.steep) __syncthreads();
         if (careful || !sh.far) break;
       }
+      if (sh.dead) in_flight();  // another warp gave up
     } else {
       // ---------------------------------------------------------------------------------- matrix products
       const int i = warp - kSoftWarps;
@@ -831,6 +835,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t lead = elected();
       const bool every_dim = a.pool.D > Sh::kD - 16;
       uint32_t weighed = 0, turns = 0;
+      bool waited = false;
+      auto in_flight = [&] {  // products in flight end by themselves: leave when they have
+        if (waited) return;
+        waited = true;
+        mma_commit(finished(i), lead);
+        const long long start = clock64();
+        while (!bar_try(finished(i), 0) && clock64() - start < kPatience) {
+        }
+      };
       Ring<Sh::kSlots> at{0, 0};  // the next fill to be used: the keys of a tile, then its values
       auto scores = [&](int t) {
         if (t < t0 || t >= t1) return;
@@ -888,11 +901,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             at.step();
           }
         }
-        if (!ok) {  // products in flight end by themselves: leave when they have
-          mma_commit(finished(i), lead);
-          const long long start = clock64();
-          while (!bar_try(finished(i), 0) && clock64() - start < kPatience) {
-          }
+        if (!ok) {
+          in_flight();
           set_status(a.b.status, DCP_ETIMEOUT);
         }
         fence_before();
@@ -901,6 +911,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!careful && sh.steep) __syncthreads();
         if (careful || !sh.far) break;
       }
+      if (sh.dead) in_flight();  // another warp gave up
     }
     __syncwarp();
   }
