@@ -452,7 +452,7 @@ def dcp_paged_prune_step(cache: PagedKVCache, cfg: Config, x0hat: torch.Tensor, 
     if ref is None:
         _check(lib.dcp_paged_prune_step(ctypes.byref(cc), ctypes.byref(gc), *args), "dcp_paged_prune_step")
         return
-    if ref.dtype != torch.int32 or not ref.is_contiguous() or ref.numel() != cache.n_blocks:
+    if ref.dtype != torch.int32 or not ref.is_contiguous() or not ref.is_cuda or ref.numel() != cache.n_blocks:
         raise DcpError("dcp_paged_prune_step", DCP_EINVAL)
     _check(lib.dcp_paged_prune_step_shared(ctypes.byref(cc), ctypes.byref(gc), _ptr(ref), *args),
            "dcp_paged_prune_step_shared")
@@ -522,7 +522,7 @@ class KVPool:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, layout: int):
         if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or \
-                k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float32):
+                k.stride(3) != 1 or k.dtype not in (torch.bfloat16, torch.float32) or not (k.is_cuda and v.is_cuda):
             raise DcpError("KVPool", DCP_EINVAL)
         h, r = (1, 2) if layout == DCP_PAGED_HND else (2, 1)
         self.k, self.v, self.D, self.H, self.dtype = k, v, k.shape[3], k.shape[h], k.dtype
@@ -553,9 +553,10 @@ class SeqBatch:
 
     def __init__(self, q_start: torch.Tensor, tables: torch.Tensor, kv_len: torch.Tensor, status: torch.Tensor,
                  total_q: int, max_q: int, max_kv: int, kv_len_add: int = 0):
-        n = tables.shape[0]
-        if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (q_start, tables, kv_len, status)) or \
-                tables.dim() != 2 or q_start.numel() != n + 1 or kv_len.dim() not in (1, 2) or kv_len.shape[0] != n:
+        n = tables.shape[0] if tables.dim() == 2 else -1
+        if any(t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda
+               for t in (q_start, tables, kv_len, status)) or q_start.numel() != n + 1 or \
+                kv_len.dim() not in (1, 2) or kv_len.shape[0] != n:
             raise DcpError("SeqBatch", DCP_EINVAL)
         self.tensors = (q_start, tables, kv_len, status)
         self.n_seqs, self.total_q, self.kv_heads = n, total_q, kv_len.shape[1] if kv_len.dim() == 2 else 0
@@ -595,7 +596,7 @@ def dcp_rope_plan(cfg: RopeConfig) -> DcpRopePlanC:
 def _rows_of(t: torch.Tensor, pool: KVPool, batch: SeqBatch, heads: int, what: str) -> int:
     """Token stride of a [total_q][heads][D] tensor of the pool's type whose heads are dense."""
     n, D = batch.total_q, pool.D
-    if t.dtype is not pool.dtype or t.shape != (n, heads, D):
+    if t.dtype is not pool.dtype or t.shape != (n, heads, D) or not t.is_cuda:
         raise DcpError(what, DCP_EINVAL)
     token, head, dim = t.stride()
     if dim != 1 or (head != D and heads > 1):
@@ -610,7 +611,7 @@ def dcp_rope_append(pool: KVPool, batch: SeqBatch, plan: DcpRopePlanC, q, k: tor
     kv_stride = _rows_of(k, pool, batch, pool.H, "dcp_rope_append")
     if _rows_of(v, pool, batch, pool.H, "dcp_rope_append") != kv_stride or \
             (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
-                                        positions.numel() != batch.total_q)):
+                                        not positions.is_cuda or positions.numel() != batch.total_q)):
         raise DcpError("dcp_rope_append", DCP_EINVAL)
     hq, q_stride = 0, 0
     if q is not None:
@@ -646,8 +647,8 @@ def dcp_paged_attention(pool: KVPool, batch: SeqBatch, cfg: AttnConfig, q: torch
     hq = q.shape[1]
     q_stride = _rows_of(q, pool, batch, hq, "dcp_paged_attention")
     if _rows_of(out, pool, batch, hq, "dcp_paged_attention") != hq * pool.D or batch.kv_heads not in (0, pool.H) or \
-            (lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
-                                  lse.numel() != batch.total_q * hq)):
+            (lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or
+                                  lse.numel() != batch.total_q * hq)) or not ws.is_cuda:
         raise DcpError("dcp_paged_attention", DCP_EINVAL)
     _check(lib.dcp_paged_attention(pool.ref, batch.ref, cfg.c(pool.D), _ptr(q), q_stride, hq, _ptr(out), _ptr(lse),
                                    _ptr(ws), ws.numel(), _stream(stream)), "dcp_paged_attention")
@@ -658,11 +659,12 @@ class PagePool:
     the trailing dims (either layout of PagedKVCache)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_size: int, status: torch.Tensor):
-        if k.shape != v.shape or k.dtype != v.dtype or k.dim() < 3 or not k.is_contiguous() or not v.is_contiguous():
+        if k.shape != v.shape or k.dtype != v.dtype or k.dim() < 3 or not k.is_contiguous() or \
+                not v.is_contiguous() or status.dtype != torch.int32 or not (k.is_cuda and v.is_cuda and status.is_cuda):
             raise DcpError("PagePool", DCP_EINVAL)
         self.tensors, self.n_blocks = (k, v, status), k.shape[1]
         self._c = DcpPagePoolC(_ptr(k), _ptr(v), k.shape[0], block_size, k.shape[1],
-                               k[0, 0].numel() * k.element_size(), _ptr(status))
+                               k.stride(1) * k.element_size(), _ptr(status))
         self.ref = ctypes.byref(self._c)
 
     @classmethod
@@ -675,7 +677,7 @@ class PagePool:
 
 def _ints(what: str, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda):
             raise DcpError(what, DCP_EINVAL)
 
 
@@ -701,6 +703,8 @@ def dcp_pages_fork(pool: PagePool, tables: torch.Tensor, lens: torch.Tensor, par
     that will be written must not be shared: of a cache whose prune steps turn the history's keys (reindex_mode 0, q0 - T_s
     past the span) only those before the history are.  Set PagedKVCache.block_ref to `ref` to have this checked."""
     _ints("dcp_pages_fork", tables, lens, parent, shared, reserve, ref, child_tables, ref_out)
+    if tables.dim() != 2 or not ws.is_cuda:
+        raise DcpError("dcp_pages_fork", DCP_EINVAL)
     (rows, stride), n = tables.shape, parent.numel()
     if child_tables.shape != (n, stride) or lens.numel() != rows or ref.numel() != pool.n_blocks or \
             ref_out.numel() != pool.n_blocks or any(t is not None and t.numel() != n for t in (shared, reserve)):
@@ -712,7 +716,8 @@ def dcp_pages_fork(pool: PagePool, tables: torch.Tensor, lens: torch.Tensor, par
 
 def _tables_and_counts(what: str, pool: PagePool, tables, ref, tables_out, ref_out) -> None:
     _ints(what, tables, ref, tables_out, ref_out)
-    if tables_out.shape != tables.shape or ref.numel() != pool.n_blocks or ref_out.numel() != pool.n_blocks:
+    if tables.dim() != 2 or tables_out.shape != tables.shape or ref.numel() != pool.n_blocks or \
+            ref_out.numel() != pool.n_blocks:
         raise DcpError(what, DCP_EINVAL)
 
 
@@ -729,6 +734,8 @@ def dcp_pages_compact(pool: PagePool, tables: torch.Tensor, ref: torch.Tensor, t
     """Pack the live blocks to the front of the pool; tables and counts follow, n_live (int32 [1] or None)."""
     _tables_and_counts("dcp_pages_compact", pool, tables, ref, tables_out, ref_out)
     _ints("dcp_pages_compact", n_live)
+    if not ws.is_cuda or (n_live is not None and n_live.numel() < 1):
+        raise DcpError("dcp_pages_compact", DCP_EINVAL)
     _check(lib.dcp_pages_compact(pool.ref, _ptr(tables), tables.shape[0], tables.shape[1], _ptr(ref),
                                  _ptr(tables_out), _ptr(ref_out), _ptr(n_live), _ptr(ws), ws.numel(),
                                  _stream(stream)), "dcp_pages_compact")
