@@ -14,9 +14,9 @@
 // tensor cores' accumulation (which may truncate) never runs over more than a tile.
 //
 // Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-325 us,
-// 6.2-6.5 TB/s; one token over 1531 keys 12.0-13.1 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
-// fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 192-201 us, bound by the tf32 products
-// (40 % of their rate while a CTA runs).
+// 6.2-6.5 TB/s; one token over 1531 keys 13.2 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
+// fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 195 us, bound by the tf32 products (40 % of
+// their rate while a CTA runs).
 #include <type_traits>
 
 #include "attend_join.cuh"
@@ -645,11 +645,14 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
     r.bytes = (size_t)r.splits * 2 * 16 * (kPartHead + a.pool.D) * 4;
     return r;
   }
-  // Two CTAs of an SM at a time: one round of pieces for a few sequences; several rounds of shorter ones where their
-  // lengths may differ or a causal mask makes tiles of rows differ (fp32, 3 sequences of 100 .. 513 new tokens: 197 us
-  // with 4 rounds, 270 with 1, 198 with 8).  No piece under two tiles (or four, in several rounds), at most kMaxSplits
-  // of an item.
-  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 ? 6 : per == 128 ? 4 : 1;
+  // Two CTAs of an SM at a time: one round of pieces for a few sequences, four rounds of shorter ones where their lengths
+  // may differ (8 sequences on) or a causal mask makes tiles of rows differ (128 rows a CTA).  Measured, us with 1 / 2 /
+  // 4 / 6 / 8 rounds: fp32, heads of 64, 100 .. 513 new tokens, 3 sequences 262 / 210 / 183 / 187 / 195, 8 sequences 529 /
+  // 453 / 373 / 369 / 350, one alone 111 / 128 / 136 / 137 / 137; drafts of 40 rows over 200 .. 16000 keys, 4 sequences
+  // 109 / 115 / 134 / 148 / 180, 8 sequences 167 / 160 / 158 / 183 / 195, 48 sequences 574 / 605 / 565 / 586 / 610, 100
+  // sequences 1055 / 1055 / 1033 / 982 / 980; 16 sequences alike 122 / 140 / 142 / 165 / 164.  No piece under two tiles (or
+  // four, in several rounds), at most kMaxSplits of an item.
+  const int64_t slots = 2 * sm_count(), rounds = a.b.n_seqs >= 8 || per == 128 ? 4 : 1;
   int64_t span = (max_kv * items + slots * rounds - 1) / (slots * rounds);
   const int64_t least = (rounds > 1 ? 4 : 2) * keys;
   if (span < least) span = least;

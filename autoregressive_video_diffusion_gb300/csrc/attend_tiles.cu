@@ -24,8 +24,8 @@
 // softmax warps put zeros for rows past the sequence (page rows never written hold anything) and for infinities and
 // NaN before they hand over their weights; rows that do see those get them back in the epilogue, from the cache.
 //
-// Measured: 6240 tokens, 40 query heads over 8 KV heads of 128, 25907 keys: 2133-2193 us, 1510-1550 TFLOP/s.  Causal
-// chunks of 130 .. 2048 tokens behind up to 12000 keys: 672-716 us, 1340-1430 TFLOP/s.  What bounds it is the chain of
+// Measured: 6240 tokens, 40 query heads over 8 KV heads of 128, 25907 keys: 2155-2180 us, 1520-1540 TFLOP/s.  Causal
+// chunks of 130 .. 2048 tokens behind up to 12000 keys: 700-721 us, 1330-1370 TFLOP/s.  What bounds it is the chain of
 // a row tile (products 1100 clocks, scores ready 300, weights 1150, products awake 300), of which the other row tile's
 // products cover 1100.
 #include <cuda.h>
@@ -999,7 +999,9 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
   // Fewer items than SMs: their keys are split so that the SMs have one part each.  Items of equal work (one sequence
   // without a causal mask) in a few rounds: those of the last, incomplete round are split over the SMs it has.  At least
-  // 2 key tiles a part.
+  // 2 key tiles a part.  (us without / with that split: 976 items of 203 key tiles 2114 / 2008, 200 of 203 tiles 615 /
+  // 466, 640 of 47 tiles 412 / 402; it loses where the parts are short beside their join: 200 of 13 tiles 58 / 70, 160 of
+  // 47 tiles 165 / 179.  From 16 rounds on a round is too little of the whole.)
   const int64_t sms = sm_count(), rounds = items / sms, left = items % sms;
   const bool tail = rounds > 0 && rounds < 16 && left && a.b.n_seqs == 1 && !a.causal;
   int64_t splits = items < sms ? sms / items : tail ? sms / left : 1;

@@ -11,7 +11,7 @@
 
 namespace dcp {
 
-constexpr int kThreads = 256;          // every kernel of the library runs 256-thread CTAs
+constexpr int kThreads = 256;          // threads of a CTA of the prune step's kernels (and of the page copies)
 constexpr int kMaxTile = 256;          // tokens per scan tile (one token per thread in the mask phase)
 
 // Control block at the start of the workspace.  The scan kernel's final CTA writes the verdict fields, which the

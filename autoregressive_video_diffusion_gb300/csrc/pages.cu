@@ -259,6 +259,8 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(PageParams p, const int3
   }
 }
 
+// Five CTAs an SM are what fits.  (Copying 682 pages of 32 KB in 40 layers with 3 / 4 / 5 / 6 / 8 / 10 an SM: 558 / 564 /
+// 568 / 625 / 548 / 562 us; 5461 pages of 2 KB in 2 layers 54 / 48 / 47 / 54 / 46 / 46.)
 cudaError_t move(const PageParams& p, const int32_t* src, const int32_t* dst, int step, const int32_t* count, int32_t n,
                  cudaStream_t s) {
   const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, most = (int64_t)sm_count() * 5;
