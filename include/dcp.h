@@ -438,6 +438,9 @@ dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
  *   0 <= j < kv_len,  j <= c where causal = 1,  j >= c - window where window >= 0 (needs causal = 1).
  *   out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j),   lse = log sum_j w_j.
  * A row that sees nothing (kv_len 0, or c < 0 under the causal mask) gives out = 0, lse = -inf.
+ * Scores, maxima and sums are held in fp32, for any finite scale and values up to 2^100.  Of a bf16 cache the weights are
+ * rounded to bf16 before they meet the values (relative error 2^-8 at most each; lse comes from the unrounded ones); of an
+ * fp32 cache the products are good to 2^-22.  An infinity or NaN that a row sees has its usual effect on that row.
  * What stands in positions a row does not see never reaches that row: unwritten page rows, infinities and NaN past
  * kv_len and behind the masks, and table entries of pages no new token sees (they need not name a block). */
 typedef struct dcp_attn_config {
