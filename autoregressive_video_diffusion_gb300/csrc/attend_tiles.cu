@@ -650,8 +650,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 sh.poison = 1;
               }
             }
-            fence_proxy_async_smem();
           }
+          // also where nothing was left to replace: the other row tile's warps may have done it a moment ago, and this row
+          // tile's product must not read what stood there before
+          fence_proxy_async_smem();
         }
         wait_st();
         fence_before();
