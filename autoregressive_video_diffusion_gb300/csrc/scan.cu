@@ -352,7 +352,7 @@ __device__ void finalize(const ScanParams& p, int* s_warp, int* s_pick) {
       const int64_t shared_lo = (int64_t)(INT32_MAX - shared_first_inv) * p.block_size;
       const int64_t shared_hi = (int64_t)shared_end * p.block_size;
       if ((p.history_turns && longest > shared_lo) ||
-          (has_dyn && common < shared_hi && (int64_t)common + k > shared_lo)) {
+          (has_dyn && k && common < shared_hi && (int64_t)common + k > shared_lo)) {
         abort = 1;
         set_status(p.status, DCP_EDEVICE);
       }

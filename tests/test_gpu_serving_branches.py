@@ -108,6 +108,9 @@ def test_branches_share_full_history_where_no_key_turns(gpu):
     Family(TINY, HND, full).all_go_on()
     Family(TINY, HND, full + 1).all_refused()  # the page that the kept rows enter
     Family(TINY, HND, None).all_refused()
+    f = Family(TINY, HND, full + 1)
+    f.cfg.gamma = 1e9  # no row is kept: nothing is written
+    assert [f.step(m) for m in f.members] == [dcp.DCP_OK] * 3
 
 
 def test_prune_step_without_counts_and_with_bad_ones(gpu):
