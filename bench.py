@@ -36,11 +36,11 @@ FALLBACK_HBM_GBS = 6800.0
 
 # DRAM bytes (read + write) of one full-depth gather launch (gather_staged_kernel<false>), scaled from ncu captures of
 # dram__bytes_read.sum and dram__bytes_write.sum on two reduced cases of the same workload (156 and 312 tokens per
-# frame): reads scale with the algorithmic reads (1.0005x), writes are the algorithmic writes less the ~50 MB still
+# frame): reads scale with the algorithmic reads (1.0006x), writes are the algorithmic writes less the ~50 MB still
 # dirty in L2 when the launch ends.  They describe the kernel code they were taken on (gather.cu and the shared
 # header, `//` comments and blank lines aside): when that code differs, the bench reports no traffic figure.
-GATHER_TRAFFIC_BYTES = 1_501_515_005
-GATHER_TRAFFIC_CODE_SHA256 = "ee4f66eb6fef98f507fc0ed766e666329eb2664c565babdde24abc59bae80072"
+GATHER_TRAFFIC_BYTES = 1_501_957_865
+GATHER_TRAFFIC_CODE_SHA256 = "3f8d90fc091410e08e107e74133167ce8eb79334ef33369ca95a2464d2d22585"
 
 
 def _code_only(text: str) -> str:
