@@ -90,6 +90,20 @@ class DcpRopePlanC(ctypes.Structure):
                 ("ready", ctypes.c_int32), ("turns", ctypes.c_uint64 * DCP_ROPE_MAX_PAIRS)]
 
 
+DCP_ROPE_MAX_AXES = 3
+
+
+class DcpRopeAxesC(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("pair_layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("ready", ctypes.c_int32), ("first", ctypes.c_int32 * DCP_ROPE_MAX_AXES),
+                ("amplitude", ctypes.c_float * DCP_ROPE_MAX_AXES), ("turns", ctypes.c_uint64 * DCP_ROPE_MAX_PAIRS)]
+
+
+class DcpNormConfigC(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32),
+                ("weight_per_head", ctypes.c_int32), ("span", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 class DcpAttnConfigC(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
@@ -143,6 +157,9 @@ _SIGS = {
     "dcp_rope_plan_init": ([ctypes.POINTER(DcpRopeConfigC), ctypes.POINTER(DcpRopePlanC)], _i32),
     "dcp_rope_append": ([_pk, _pb, ctypes.POINTER(DcpRopePlanC), _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp],
                         _i32),
+    "dcp_rope_axes_init": ([ctypes.POINTER(DcpRopeConfigC), _i32, ctypes.POINTER(DcpRopeAxesC)], _i32),
+    "dcp_norm_rope_append": ([_pk, _pb, ctypes.POINTER(DcpRopeAxesC), ctypes.POINTER(DcpNormConfigC), _vp, _i64, _i32,
+                              _vp, _vp, _i64, _vp, _vp, _vp], _i32),
     "dcp_attention_workspace_size": ([_pk, _pb, _pa, _i32], _sz),
     "dcp_paged_attention": ([_pk, _pb, _pa, _vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
     "dcp_pages_workspace_size": ([_pp, _i32, _i32], _sz),
@@ -151,6 +168,7 @@ _SIGS = {
     "dcp_pages_free": ([_pp, _vp, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
     "dcp_pages_compact": ([_pp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "dcp_abi_serving_struct_size": ([_i32], ctypes.c_uint32),
+    "dcp_abi_norm_struct_size": ([_i32], ctypes.c_uint32),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -163,6 +181,9 @@ if (_sizes >> 16) != ctypes.sizeof(DcpCacheC) or (_sizes & 0xFFFF) != ctypes.siz
     raise ImportError("libdcp struct layout does not match the binding")
 for _i, _t in enumerate((DcpKvPoolC, DcpSeqBatchC, DcpRopeConfigC, DcpRopePlanC, DcpAttnConfigC, DcpPagePoolC)):
     if lib.dcp_abi_serving_struct_size(_i) != ctypes.sizeof(_t):
+        raise ImportError(f"libdcp struct layout does not match the binding: {_t.__name__}")
+for _i, _t in enumerate((DcpRopeAxesC, DcpNormConfigC)):
+    if lib.dcp_abi_norm_struct_size(_i) != ctypes.sizeof(_t):
         raise ImportError(f"libdcp struct layout does not match the binding: {_t.__name__}")
 
 
@@ -604,23 +625,70 @@ def _rows_of(t: torch.Tensor, pool: KVPool, batch: SeqBatch, heads: int, what: s
     return token if n > 1 else heads * D
 
 
+def _append_args(what: str, pool: KVPool, batch: SeqBatch, q, k, v, positions, n_axes: int, q_out):
+    """(q, its token stride, query heads, k, v, their token stride, positions, q_out) of an append, checked."""
+    kv_stride = _rows_of(k, pool, batch, pool.H, what)
+    if _rows_of(v, pool, batch, pool.H, what) != kv_stride or \
+            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
+                                        not positions.is_cuda or positions.numel() != n_axes * batch.total_q)):
+        raise DcpError(what, DCP_EINVAL)
+    hq, q_stride = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        q_stride = _rows_of(q, pool, batch, hq, what)
+        if q_out is None or _rows_of(q_out, pool, batch, hq, what) != hq * pool.D:
+            raise DcpError(what, DCP_EINVAL)
+    return _ptr(q), q_stride, hq, _ptr(k), _ptr(v), kv_stride, _ptr(positions), _ptr(q_out)
+
+
 def dcp_rope_append(pool: KVPool, batch: SeqBatch, plan: DcpRopePlanC, q, k: torch.Tensor, v: torch.Tensor,
                     positions, q_out, stream=None) -> None:
     """Turn q and k of the new tokens, put k and v into the pool's pages; q_out gets the turned q.  q, k, v are
     [total_q][heads][D] (views of one fused projection are fine), positions int32 [total_q] or None."""
-    kv_stride = _rows_of(k, pool, batch, pool.H, "dcp_rope_append")
-    if _rows_of(v, pool, batch, pool.H, "dcp_rope_append") != kv_stride or \
-            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
-                                        not positions.is_cuda or positions.numel() != batch.total_q)):
-        raise DcpError("dcp_rope_append", DCP_EINVAL)
-    hq, q_stride = 0, 0
-    if q is not None:
-        hq = q.shape[1]
-        q_stride = _rows_of(q, pool, batch, hq, "dcp_rope_append")
-        if q_out is None or _rows_of(q_out, pool, batch, hq, "dcp_rope_append") != hq * pool.D:
-            raise DcpError("dcp_rope_append", DCP_EINVAL)
-    _check(lib.dcp_rope_append(pool.ref, batch.ref, plan, _ptr(q), q_stride, hq, _ptr(k), _ptr(v), kv_stride,
-                               _ptr(positions), _ptr(q_out), _stream(stream)), "dcp_rope_append")
+    args = _append_args("dcp_rope_append", pool, batch, q, k, v, positions, 1, q_out)
+    _check(lib.dcp_rope_append(pool.ref, batch.ref, plan, *args, _stream(stream)), "dcp_rope_append")
+
+
+def dcp_rope_axes(cfgs) -> DcpRopeAxesC:
+    """The rotary plan of one to three position axes (a RopeConfig each, of one pair layout): made once, kept by the
+    caller, passed to every dcp_norm_rope_append."""
+    axes, c = DcpRopeAxesC(), (DcpRopeConfigC * len(cfgs))(*(cfg.c() for cfg in cfgs))
+    _check(lib.dcp_rope_axes_init(c, len(cfgs), ctypes.byref(axes)), "dcp_rope_axes_init")
+    return axes
+
+
+DCP_NORM_HEAD, DCP_NORM_TOKEN = 0, 1
+
+
+class NormConfig:
+    """Root-mean-square norms of q and k (dcp_norm_config): over each head (DCP_NORM_HEAD) or all heads of a token
+    (DCP_NORM_TOKEN).  Weights, bf16 or fp32 device tensors of one type: [D] for every head or [heads][D]; None: ones."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, span: int = DCP_NORM_HEAD):
+        given = [w for w in (q_weight, k_weight) if w is not None]
+        if any(w.dtype not in (torch.bfloat16, torch.float32) or not w.is_contiguous() or not w.is_cuda or
+               w.dim() not in (1, 2) or w.dim() != given[0].dim() or w.dtype != given[0].dtype for w in given):
+            raise DcpError("NormConfig", DCP_EINVAL)
+        self.weights = (q_weight, k_weight)
+        self._c = DcpNormConfigC(_ptr(q_weight), _ptr(k_weight),
+                                 DCP_BF16 if given and given[0].dtype == torch.bfloat16 else DCP_F32,
+                                 int(bool(given) and given[0].dim() == 2), span, eps)
+        self.ref = ctypes.byref(self._c)
+
+    def c(self) -> DcpNormConfigC:
+        return self._c
+
+
+def dcp_norm_rope_append(pool: KVPool, batch: SeqBatch, axes: DcpRopeAxesC, norm: NormConfig, q, k: torch.Tensor,
+                         v: torch.Tensor, positions, q_out, stream=None) -> None:
+    """dcp_rope_append with q and k normalised before they turn; positions int32 [n_axes][total_q] (an axis behind the
+    other), or None where there is one axis and it is the cache position."""
+    args = _append_args("dcp_norm_rope_append", pool, batch, q, k, v, positions, axes.n_axes, q_out)
+    for w, heads in zip(norm.weights, (args[2], pool.H)):
+        if w is not None and w.shape != ((pool.D,) if w.dim() == 1 else (heads, pool.D)) and (heads or w.dim() == 1):
+            raise DcpError("dcp_norm_rope_append", DCP_EINVAL)
+    _check(lib.dcp_norm_rope_append(pool.ref, batch.ref, axes, norm.ref, *args, _stream(stream)),
+           "dcp_norm_rope_append")
 
 
 @dataclass

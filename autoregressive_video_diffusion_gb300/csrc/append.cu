@@ -9,61 +9,13 @@
 // The bound is HBM (each of q, k, v read and written once); a few tokens are bound by the chain launch -> q_start,
 // kv_len -> table -> store.  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in bf16 68 us (5.7 TB/s), 3375 tokens
 // of 32 + 8 + 8 fp32 heads of 96 25 us (5.0 TB/s), 32 tokens 4.0 us in a graph.
-#include "serve.cuh"
+#include "append.cuh"
 
 namespace dcp {
 
 namespace {
 
 constexpr int kTurners = 128;  // threads of a CTA
-
-struct Where {
-  int64_t off;   // element offset of the token's row in head 0 of the pool, -1: not stored
-  int32_t phase;
-  int32_t seq;   // -1: no sequence owns the row
-};
-
-// Elements of a 16-byte vector in fp32 and back (bf16: round to nearest even, once).
-template <typename T>
-struct Elems;
-template <>
-struct Elems<__nv_bfloat16> {
-  static constexpr int kN = 8;
-  static __device__ __forceinline__ void get(const uint4& x, float (&y)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = bf16lo(w[i]);
-      y[2 * i + 1] = bf16hi(w[i]);
-    }
-  }
-  static __device__ __forceinline__ uint4 put(const float (&y)[8]) {
-    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
-  }
-  static __device__ __forceinline__ float one(const uint4* row, int d) {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
-  }
-};
-template <>
-struct Elems<float> {
-  static constexpr int kN = 4;
-  static __device__ __forceinline__ void get(const uint4& x, float (&y)[4]) {
-    y[0] = __uint_as_float(x.x), y[1] = __uint_as_float(x.y), y[2] = __uint_as_float(x.z), y[3] = __uint_as_float(x.w);
-  }
-  static __device__ __forceinline__ uint4 put(const float (&y)[4]) {
-    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-  }
-  static __device__ __forceinline__ float one(const uint4* row, int d) {
-    return reinterpret_cast<const float*>(row)[d];
-  }
-};
-
-enum Pairs {
-  kInterleaved,  // pair (2p, 2p + 1): inside a vector
-  kHalfVec,      // pair (p, p + half), half a whole number of vectors: a unit is the two vectors of its pairs
-  kHalfAny,      // any other half: partners are read from a copy of the rows in shared memory
-};
 
 template <typename T, int PAIRS>
 __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant__ AppendParams p) {
@@ -119,35 +71,10 @@ __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant_
   load(first(0), x[0], y[0]);
   if (threadIdx.x == 0) where.seq = -1;
   __syncthreads();
-  for (int s = threadIdx.x; s < p.b.n_seqs; s += kTurners) {
-    int lo, len;
-    int64_t kv;
-    const bool sound = seq_rows(p.b, s, lo, len) & seq_kv(p.b, p.pool.bs, p.pool.H, s, 0, kv);
-    if (!sound || tok < lo || tok >= lo + len) continue;
-    const int64_t c = kv - len + (tok - lo);
-    Where w{-1, (int32_t)c, s};
-    if (c >= 0) {
-      const int64_t page = c / p.pool.bs;
-      const int64_t blk = p.b.tables[s * p.b.table_stride + page];
-      if (blk >= 0 && blk < p.pool.n_blocks)
-        w.off = blk * p.pool.s_block + (c - page * p.pool.bs) * p.pool.s_row;
-      else
-        set_status(p.b.status, DCP_EDEVICE);
-    }
-    where = w;
-  }
+  find_token<kTurners>(p.b, p.pool, tok, where);
   __syncthreads();
-  for (int i = threadIdx.x; i < half; i += kTurners) {
-    const int32_t phase = p.positions ? p.positions[tok] : where.phase;
-    const uint64_t turn = (uint64_t)(int64_t)phase * p.turns[i];
-    // the fraction of a turn, 32 bits: what fp32 holds of it, and the rest as a first-order correction
-    const int32_t fraction = (int32_t)(turn >> 32);
-    const float most = (float)fraction;
-    const float rest = (float)((int64_t)fraction - (int64_t)most) * (float)(3.14159265358979323846 * 0x1p-31);
-    float s, c;
-    sincospif(most * 0x1p-31f, &s, &c);
-    cs[i] = make_float2(fmaf(-s, rest, c) * p.amplitude, fmaf(c, rest, s) * p.amplitude);
-  }
+  for (int i = threadIdx.x; i < half; i += kTurners)
+    cs[i] = turn_at(p.positions ? p.positions[tok] : where.phase, p.turns[i], p.amplitude);
   __syncthreads();
 
   const int batches = (per_token + batch - 1) / batch;

@@ -42,6 +42,18 @@ struct AppendParams {
   uint64_t turns[DCP_ROPE_MAX_PAIRS];
 };
 
+struct NormParams {
+  AppendParams a;               // its amplitude is not used
+  const char* q_weight;         // nullable: ones
+  const char* k_weight;
+  int32_t weight_bf16, weight_heads;  // their type; weights of each head, or one row for all
+  int32_t token_span;           // the mean goes over all heads of a token
+  int32_t lanes_log2;           // lanes that hold a head
+  float eps;
+  int32_t first[3];             // first pair of each axis, the number of pairs for those that are not there
+  float amplitude[3];
+};
+
 struct AttendParams {
   Pool pool;
   Batch b;
@@ -65,6 +77,7 @@ struct PageParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_norm_append(const NormParams& p, cudaStream_t s);
 // The attention's workspace: the counters at its start (kDoneItems of them), from kScratch on the parts.
 inline uint32_t* done_counters(void* ws) { return (uint32_t*)((char*)ws + sizeof(Ctrl)); }
 

@@ -117,6 +117,33 @@ bool token_stride_ok(int64_t stride, int64_t heads, int64_t D, int es) {
 
 dcp_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ECUDA; }
 
+// What both appends take: the checks, and everything but the turn.
+dcp_status append_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const void* q, int64_t q_stride, int32_t Hq,
+                     const void* k, const void* v, int64_t kv_stride, const int32_t* positions, void* q_out,
+                     AppendParams& p) {
+  if (check_pool(pool) != DCP_OK || check_batch(batch) != DCP_OK || batch->kv_len_per_head) return DCP_EINVAL;
+  const int es = elem_size(pool->dtype);
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !token_stride_ok(kv_stride, pool->H, pool->D, es))
+    return DCP_EINVAL;
+  if (!q != !q_out || !aligned(positions, 4)) return DCP_EINVAL;
+  if (q) {
+    if (Hq < 1 || Hq > 65535 || !aligned(q, 16) || !aligned(q_out, 16) || !token_stride_ok(q_stride, Hq, pool->D, es))
+      return DCP_EINVAL;
+    if (q == q_out && q_stride != (int64_t)Hq * pool->D) return DCP_EINVAL;
+  }
+  p.pool = pool_of(pool);
+  p.b = batch_of(batch);
+  p.q = (const char*)q;
+  p.k = (const char*)k;
+  p.v = (const char*)v;
+  p.q_out = (char*)q_out;
+  p.q_stride = q_stride;
+  p.kv_stride = kv_stride;
+  p.Hq = q ? Hq : 0;
+  p.positions = positions;
+  return DCP_OK;
+}
+
 dcp_status check_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
                            int32_t Hq) {
   if (check_pool(pool) != DCP_OK || check_batch(batch) != DCP_OK || !cfg) return DCP_EINVAL;
@@ -219,37 +246,70 @@ dcp_status dcp_rope_plan_init(const dcp_rope_config* g, dcp_rope_plan* plan) {
   return DCP_OK;
 }
 
+dcp_status dcp_rope_axes_init(const dcp_rope_config* cfg, int32_t n_axes, dcp_rope_axes* axes) {
+  if (!cfg || !axes || n_axes < 1 || n_axes > DCP_ROPE_MAX_AXES) return DCP_EINVAL;
+  dcp_rope_axes out{};
+  out.n_axes = n_axes;
+  out.pair_layout = cfg[0].pair_layout;
+  for (int a = 0; a < n_axes; ++a) {
+    dcp_rope_plan plan;
+    if (cfg[a].pair_layout != out.pair_layout || dcp_rope_plan_init(&cfg[a], &plan) != DCP_OK) return DCP_EINVAL;
+    if (out.rot_dim + plan.rot_dim > 2 * DCP_ROPE_MAX_PAIRS) return DCP_EINVAL;
+    out.first[a] = out.rot_dim / 2;
+    out.amplitude[a] = plan.amplitude;
+    for (int i = 0; i < plan.rot_dim / 2; ++i) out.turns[out.rot_dim / 2 + i] = plan.turns[i];
+    out.rot_dim += plan.rot_dim;
+  }
+  for (int a = n_axes; a < DCP_ROPE_MAX_AXES; ++a) out.first[a] = out.rot_dim / 2;
+  out.ready = 1;
+  *axes = out;
+  return DCP_OK;
+}
+
 dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_plan* plan,
                            const void* q, int64_t q_stride, int32_t Hq, const void* k, const void* v,
                            int64_t kv_stride, const int32_t* positions, void* q_out, void* stream) {
-  if (check_pool(pool) != DCP_OK || check_batch(batch) != DCP_OK || batch->kv_len_per_head) return DCP_EINVAL;
+  AppendParams p{};
+  if (append_of(pool, batch, q, q_stride, Hq, k, v, kv_stride, positions, q_out, p) != DCP_OK) return DCP_EINVAL;
   if (!plan || plan->ready != 1 || plan->rot_dim < 0 || plan->rot_dim > pool->D || (plan->rot_dim & 1))
     return DCP_EINVAL;
-  const int es = elem_size(pool->dtype);
-  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !token_stride_ok(kv_stride, pool->H, pool->D, es))
-    return DCP_EINVAL;
-  if (!q != !q_out || !aligned(positions, 4)) return DCP_EINVAL;
-  if (q) {
-    if (Hq < 1 || Hq > 65535 || !aligned(q, 16) || !aligned(q_out, 16) || !token_stride_ok(q_stride, Hq, pool->D, es))
-      return DCP_EINVAL;
-    if (q == q_out && q_stride != (int64_t)Hq * pool->D) return DCP_EINVAL;
-  }
-  AppendParams p{};
-  p.pool = pool_of(pool);
-  p.b = batch_of(batch);
-  p.q = (const char*)q;
-  p.k = (const char*)k;
-  p.v = (const char*)v;
-  p.q_out = (char*)q_out;
-  p.q_stride = q_stride;
-  p.kv_stride = kv_stride;
-  p.Hq = q ? Hq : 0;
-  p.positions = positions;
   p.half_layout = plan->pair_layout == DCP_ROPE_HALF;
   p.half = plan->rot_dim / 2;
   p.amplitude = plan->amplitude;
   for (int i = 0; i < DCP_ROPE_MAX_PAIRS; ++i) p.turns[i] = plan->turns[i];
   return cuda_ok(launch_append(p, (cudaStream_t)stream));
+}
+
+dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_axes* axes,
+                                const dcp_norm_config* norm, const void* q, int64_t q_stride, int32_t Hq, const void* k,
+                                const void* v, int64_t kv_stride, const int32_t* positions, void* q_out, void* stream) {
+  NormParams n{};
+  AppendParams& p = n.a;
+  if (append_of(pool, batch, q, q_stride, Hq, k, v, kv_stride, positions, q_out, p) != DCP_OK) return DCP_EINVAL;
+  if (!axes || axes->ready != 1 || axes->n_axes < 1 || axes->n_axes > DCP_ROPE_MAX_AXES || axes->rot_dim < 0 ||
+      axes->rot_dim > pool->D || (axes->rot_dim & 1))
+    return DCP_EINVAL;
+  if (axes->n_axes > 1 && !positions) return DCP_EINVAL;
+  if (!norm || (norm->span != DCP_NORM_HEAD && norm->span != DCP_NORM_TOKEN) || !std::isfinite(norm->eps) ||
+      norm->eps < 0.f)
+    return DCP_EINVAL;
+  if (norm->weight_dtype != DCP_BF16 && norm->weight_dtype != DCP_F32) return DCP_EINVAL;
+  if (norm->weight_per_head != 0 && norm->weight_per_head != 1) return DCP_EINVAL;
+  if (!aligned(norm->q_weight, 16) || !aligned(norm->k_weight, 16)) return DCP_EINVAL;
+  p.half_layout = axes->pair_layout == DCP_ROPE_HALF;
+  p.half = axes->rot_dim / 2;
+  for (int i = 0; i < DCP_ROPE_MAX_PAIRS; ++i) p.turns[i] = axes->turns[i];
+  n.q_weight = (const char*)norm->q_weight;
+  n.k_weight = (const char*)norm->k_weight;
+  n.weight_bf16 = norm->weight_dtype == DCP_BF16;
+  n.weight_heads = norm->weight_per_head;
+  n.token_span = norm->span == DCP_NORM_TOKEN;
+  n.eps = norm->eps;
+  for (int a = 0; a < DCP_ROPE_MAX_AXES; ++a) {
+    n.first[a] = axes->first[a];
+    n.amplitude[a] = axes->amplitude[a];
+  }
+  return cuda_ok(launch_norm_append(n, (cudaStream_t)stream));
 }
 
 size_t dcp_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_attn_config* cfg,
@@ -316,6 +376,14 @@ dcp_status dcp_pages_compact(const dcp_page_pool* pool, const int32_t* tables, i
   if (!ws_ok(ws, ws_bytes, dcp_pages_workspace_size(pool, n_rows, stride))) return DCP_EINVAL;
   return cuda_ok(launch_pages_compact(pages_of(pool), tables, n_rows, stride, ref_in, tables_out, ref_out, n_live,
                                       (int32_t*)ws, (cudaStream_t)stream));
+}
+
+uint32_t dcp_abi_norm_struct_size(int32_t which) {
+  switch (which) {
+    case 0: return sizeof(dcp_rope_axes);
+    case 1: return sizeof(dcp_norm_config);
+    default: return 0;
+  }
 }
 
 uint32_t dcp_abi_serving_struct_size(int32_t which) {

@@ -433,6 +433,50 @@ dcp_status dcp_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
                            const void* q_dev, int64_t q_stride, int32_t Hq, const void* k_dev, const void* v_dev,
                            int64_t kv_stride, const int32_t* positions_dev, void* q_out_dev, void* stream);
 
+/* Positions of several axes (a latent frame, a row and a column of a video token): axis a turns the pairs that follow
+ * those of the axes before it, with the frequencies of its own config over its own rot_dim.  All have one pair layout; with
+ * DCP_ROPE_HALF the halves are those of the rot_dims together. */
+#define DCP_ROPE_MAX_AXES 3
+
+/* Made once by dcp_rope_axes_init and kept by the caller. */
+typedef struct dcp_rope_axes {
+  int32_t n_axes, pair_layout;
+  int32_t rot_dim;                       /* of all axes together */
+  int32_t ready;
+  int32_t first[DCP_ROPE_MAX_AXES];      /* first pair of each axis */
+  float amplitude[DCP_ROPE_MAX_AXES];
+  uint64_t turns[DCP_ROPE_MAX_PAIRS];
+} dcp_rope_axes;
+
+/* Host only; cfg[n_axes].  DCP_EINVAL: null pointers, n_axes outside 1 .. 3, a config that dcp_rope_plan_init refuses, pair
+ * layouts that differ, more than 64 pairs together. */
+dcp_status dcp_rope_axes_init(const dcp_rope_config* cfg, int32_t n_axes, dcp_rope_axes* axes);
+
+/* Root-mean-square norms of q and k: y = x / sqrt(mean x^2 + eps) * w.  The mean goes over a head's D dims, or over all
+ * heads of a token together (q and k apart). */
+#define DCP_NORM_HEAD 0
+#define DCP_NORM_TOKEN 1
+
+typedef struct dcp_norm_config {
+  const void* q_weight;        /* device, [D] or [Hq][D], 16-byte aligned; null: ones */
+  const void* k_weight;        /* device, [D] or [H][D] */
+  int32_t weight_dtype;        /* DCP_BF16 or DCP_F32, whatever the pool's */
+  int32_t weight_per_head;     /* 0: one [D] for every head, 1: [heads][D] */
+  int32_t span;                /* DCP_NORM_HEAD or DCP_NORM_TOKEN */
+  float eps;                   /* finite, >= 0 */
+} dcp_norm_config;
+
+/* dcp_rope_append whose q and k are normalised before they turn, one launch and one pass over the data.  Same arguments,
+ * layouts and errors, but
+ *   positions_dev: int32 [n_axes][total_q], an axis behind the other; null (the cache position) for one axis only.
+ * Everything between reading and the one rounding to the pool's type is held in fp32.  Any finite values are normalised as
+ * the formula says (squares that would leave fp32 are taken of scaled values); a row of zeros with eps 0 gives NaN, and an
+ * infinity or NaN has its usual effect on what shares its mean. */
+dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_axes* axes,
+                                const dcp_norm_config* norm, const void* q_dev, int64_t q_stride, int32_t Hq,
+                                const void* k_dev, const void* v_dev, int64_t kv_stride, const int32_t* positions_dev,
+                                void* q_out_dev, void* stream);
+
 /* Attention of the new tokens over the cache (which already holds their keys and values).
  * Query head h reads KV head h / (Hq / H).  Token i at cache position c = kv_len - q_len + i sees position j if
  *   0 <= j < kv_len,  j <= c where causal = 1,  j >= c - window where window >= 0 (needs causal = 1).
@@ -524,6 +568,9 @@ dcp_status dcp_pages_compact(const dcp_page_pool* pool, const int32_t* tables_de
 /* ABI check for bindings: sizes of the structs above, in the order dcp_kv_pool, dcp_seq_batch, dcp_rope_config,
  * dcp_rope_plan, dcp_attn_config, dcp_page_pool (0 past the last). */
 uint32_t dcp_abi_serving_struct_size(int32_t which);
+
+/* The same for dcp_rope_axes, dcp_norm_config (0 past the last). */
+uint32_t dcp_abi_norm_struct_size(int32_t which);
 
 /* Device addresses inside a prune-step workspace: l (fp32 [C]), the mask (uint8 [C]) and the index list
  * (int32 [C], first `kept` entries valid) of the last dcp_prune_step / dcp_compact_layers call. */

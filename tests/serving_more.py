@@ -1,0 +1,51 @@
+"""Plain 64-bit statements of the norms in front of the rotary turn, of windows with first positions, and of branches
+that share a prefix, and the inputs their tests share.  Test infrastructure, as tests/serving.py."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+import autoregressive_video_diffusion_gb300 as dcp
+from tests.serving import HALF_STEP, HND, Cache, attention_bounds, ints, thetas_64
+
+
+# ------------------------------------------------------------------------------------------ norms
+def normed_64(x, w, eps, span):
+    """x [n][heads][d] normalised in 64 bits."""
+    y = x.double()
+    over = (2,) if span == dcp.DCP_NORM_HEAD else (1, 2)
+    y = y / torch.sqrt(y.square().mean(over, keepdim=True) + eps)
+    return y if w is None else y * w.double()
+
+
+def norm_turned_64(x, w, eps, span, positions, cfgs):
+    """x normalised and turned by positions [n_axes][n] in 64 bits, and |a| + |b| of each dim's (normalised) pair."""
+    y = normed_64(x, w, eps, span)
+    z, size, done = y.clone(), torch.zeros_like(y), 0
+    pairs = sum(cfg.rot_dim for cfg in cfgs) // 2
+    for cfg, at in zip(cfgs, positions):
+        pos = torch.as_tensor(np.asarray(at), dtype=torch.float64)
+        for t in thetas_64(cfg):
+            i, j = (2 * done, 2 * done + 1) if cfg.pair_layout == dcp.DCP_ROPE_INTERLEAVED else (done, done + pairs)
+            a, b = y[..., i], y[..., j]
+            c = (torch.cos(pos * t) * cfg.amplitude).to(x.device)[:, None]
+            s = (torch.sin(pos * t) * cfg.amplitude).to(x.device)[:, None]
+            z[..., i], z[..., j] = a * c - b * s, a * s + b * c
+            size[..., i] = size[..., j] = (a.abs() + b.abs()) * abs(cfg.amplitude)
+            done += 1
+    return z, size
+
+
+def check_norm_turned(got, x, w, eps, span, positions, cfgs):
+    want, size = norm_turned_64(x, w, eps, span, positions, cfgs)
+    # a sum of squares (all positive): at most 16 terms of a head behind one another in a lane and 5 sums of lanes; of a
+    # token at most 2 terms a head and 16 more, 5 sums of lanes and 8 of warps.  Half of it in the root; the mean, the root
+    # and four products are a rounding each.
+    chain = 24 if span == dcp.DCP_NORM_HEAD else 2 * x.shape[1] + 32
+    norm = (0.5 * chain + 7) * 2.0 ** -24
+    # the turn as in tests/serving.py: phase off by 2^-30 turns and its rounding, sine and cosine by 2 ulp, three roundings
+    plain = torch.where(size > 0, size, want.abs())
+    tol = plain * norm + size * 2.0 ** -21 + HALF_STEP[x.dtype] * want.abs() + 1e-37
+    assert ((got.double() - want).abs() <= tol).all(), ((got.double() - want).abs() / tol.clamp(min=1e-300)).max().item()
