@@ -17,6 +17,28 @@ namespace {
 
 constexpr int kTurners = 128;  // threads of a CTA
 
+// Called by a whole CTA of kTurners threads: the thread that meets the sequence of token `tok` notes its place in
+// `where`, which holds seq = -1 before (and is read after the next barrier).
+__device__ __forceinline__ void find_token(const Batch& b, const Pool& pool, int64_t tok, Where& where) {
+  for (int s = threadIdx.x; s < b.n_seqs; s += kTurners) {
+    int lo, len;
+    int64_t kv;
+    const bool sound = seq_rows(b, s, lo, len) & seq_kv(b, pool.bs, pool.H, s, 0, kv);
+    if (!sound || tok < lo || tok >= lo + len) continue;
+    const int64_t c = kv - len + (tok - lo);
+    Where w{-1, (int32_t)c, s};
+    if (c >= 0) {
+      const int64_t page = c / pool.bs;
+      const int64_t blk = b.tables[s * b.table_stride + page];
+      if (blk >= 0 && blk < pool.n_blocks)
+        w.off = blk * pool.s_block + (c - page * pool.bs) * pool.s_row;
+      else
+        set_status(b.status, DCP_EDEVICE);
+    }
+    where = w;
+  }
+}
+
 template <typename T, int PAIRS>
 __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant__ AppendParams p) {
   using E = Elems<T>;
@@ -71,7 +93,7 @@ __global__ void __launch_bounds__(kTurners) append_kernel(const __grid_constant_
   load(first(0), x[0], y[0]);
   if (threadIdx.x == 0) where.seq = -1;
   __syncthreads();
-  find_token<kTurners>(p.b, p.pool, tok, where);
+  find_token(p.b, p.pool, tok, where);
   __syncthreads();
   for (int i = threadIdx.x; i < half; i += kTurners)
     cs[i] = turn_at(p.positions ? p.positions[tok] : where.phase, p.turns[i], p.amplitude);

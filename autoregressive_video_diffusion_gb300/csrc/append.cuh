@@ -56,29 +56,6 @@ enum Pairs {
 
 #ifdef __CUDACC__
 
-// Called by a whole CTA of THREADS threads: the thread that meets the sequence of token `tok` notes its place in
-// `where`, which holds seq = -1 before (and is read after the next barrier).
-template <int THREADS>
-__device__ __forceinline__ void find_token(const Batch& b, const Pool& pool, int64_t tok, Where& where) {
-  for (int s = threadIdx.x; s < b.n_seqs; s += THREADS) {
-    int lo, len;
-    int64_t kv;
-    const bool sound = seq_rows(b, s, lo, len) & seq_kv(b, pool.bs, pool.H, s, 0, kv);
-    if (!sound || tok < lo || tok >= lo + len) continue;
-    const int64_t c = kv - len + (tok - lo);
-    Where w{-1, (int32_t)c, s};
-    if (c >= 0) {
-      const int64_t page = c / pool.bs;
-      const int64_t blk = b.tables[s * b.table_stride + page];
-      if (blk >= 0 && blk < pool.n_blocks)
-        w.off = blk * pool.s_block + (c - page * pool.bs) * pool.s_row;
-      else
-        set_status(b.status, DCP_EDEVICE);
-    }
-    where = w;
-  }
-}
-
 // (cos, sin) of the phase in turns, an integer product modulo 2^64, times the amplitude.
 __device__ __forceinline__ float2 turn_at(int32_t phase, uint64_t turns, float amplitude) {
   const uint64_t turn = (uint64_t)(int64_t)phase * turns;

@@ -220,25 +220,6 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
-// Two fp32 in a register pair.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t z;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
-  return z;
-}
-__device__ __forceinline__ void unpair(uint64_t z, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t w;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
-  return w;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t w;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
-  return w;
-}
 __device__ __forceinline__ float max3(float x, uint32_t y, uint32_t z) {
   float w;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(w) : "f"(x), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));

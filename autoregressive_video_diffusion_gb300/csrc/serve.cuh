@@ -50,6 +50,7 @@ struct NormParams {
   int32_t token_span;           // the mean goes over all heads of a token
   int32_t lanes_log2;           // lanes that hold a head
   float eps;
+  float inv_head, inv_q, inv_k; // 1 / the dims of a head, of all query heads, of all KV heads
   int32_t first[3];             // first pair of each axis, the number of pairs for those that are not there
   float amplitude[3];
 };
@@ -128,6 +129,31 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// Two fp32 in a register pair.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ void unpair(uint64_t z, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t w;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  return w;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t w;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  return w;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t w;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  return w;
 }
 
 // Sequence s of the batch: its first row of q and its length, checked.  False (and the status word) where they are

@@ -305,6 +305,9 @@ dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* ba
   n.weight_heads = norm->weight_per_head;
   n.token_span = norm->span == DCP_NORM_TOKEN;
   n.eps = norm->eps;
+  n.inv_head = (float)(1.0 / pool->D);
+  n.inv_q = p.Hq ? (float)(1.0 / ((double)p.Hq * pool->D)) : 1.f;
+  n.inv_k = (float)(1.0 / ((double)pool->H * pool->D));
   for (int a = 0; a < DCP_ROPE_MAX_AXES; ++a) {
     n.first[a] = axes->first[a];
     n.amplitude[a] = axes->amplitude[a];
