@@ -106,7 +106,7 @@ class DcpNormConfigC(ctypes.Structure):
 
 class DcpAttnConfigC(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("sink", ctypes.c_int32)]
 
 
 class DcpPagePoolC(ctypes.Structure):
@@ -693,13 +693,15 @@ def dcp_norm_rope_append(pool: KVPool, batch: SeqBatch, axes: DcpRopeAxesC, norm
 
 @dataclass
 class AttnConfig:
-    """Attention over the paged cache (dcp_attn_config); scale None: D ** -0.5."""
+    """Attention over the paged cache (dcp_attn_config); scale None: D ** -0.5.  Under a window (>= 0) the first `sink`
+    positions stay visible."""
     scale: float | None = None
     causal: bool = True
     window: int = -1
+    sink: int = 0
 
     def c(self, D: int) -> DcpAttnConfigC:
-        return DcpAttnConfigC(D ** -0.5 if self.scale is None else self.scale, int(self.causal), self.window, 0)
+        return DcpAttnConfigC(D ** -0.5 if self.scale is None else self.scale, int(self.causal), self.window, self.sink)
 
 
 def dcp_attention_workspace_size(pool: KVPool, batch: SeqBatch, cfg: AttnConfig, Hq: int) -> int:

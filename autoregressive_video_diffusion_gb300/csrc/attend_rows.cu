@@ -104,24 +104,32 @@ __device__ __forceinline__ void store_halves(uint8_t* to, const uint4& x) {
   *reinterpret_cast<uint4*>(to + 16) = make_uint4(c.x, c.y, d.x, d.y);
 }
 
+// The keys some of an item's rows see, by place: place x stands for position x from `seam` on, and for position x - gap
+// before it (the first positions, which stay visible behind a window that has left them).
+struct Seen {
+  int begin, end, seam, gap;
+  __device__ __forceinline__ int pos(int x) const { return x < seam ? x - gap : x; }
+};
+
 // Rows [row0, row0 + rows) of (token, head of the KV head) of sequence s, which has `len` new tokens from row lo of q
-// on and `kv` cached positions, against the keys [begin, end).  The result goes to out and lse, or to `part`.
+// on and `kv` cached positions, against the keys at the places of `keys`.  The result goes to out and lse, or to `part`.
 template <typename T, int DP, int MW>
 __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
                                              int64_t (*s_off)[Rows<T, DP, MW>::kKeys], int s, int kh, int lo,
-                                             int len, int kv, int row0, int rows, int begin, int end, float* part) {
+                                             int len, int kv, int row0, int rows, const Seen& keys, float* part) {
   using R = Rows<T, DP, MW>;
   const AttendParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int D = a.pool.D, bs = a.pool.bs;
   const int c_lo = kv - len + row0 / a.G, c_hi = kv - len + (row0 + rows - 1) / a.G;  // first and last row's position
+  const int begin = keys.begin, end = keys.end;
   const int n_tiles = (end - begin + R::kKeys - 1) / R::kKeys;
   const int32_t* table = a.b.tables + (int64_t)s * a.b.table_stride;
 
   auto find = [&](int t) -> int64_t {
-    const int pos = begin + t * R::kKeys + threadIdx.x;
-    if (threadIdx.x >= R::kKeys || pos >= end) return -1;
-    const int page = pos / bs, blk = table[page];
+    const int x = begin + t * R::kKeys + threadIdx.x;
+    if (threadIdx.x >= R::kKeys || x >= end) return -1;
+    const int pos = keys.pos(x), page = pos / bs, blk = table[page];
     if (blk < 0 || blk >= a.pool.n_blocks) {
       set_status(a.b.status, DCP_EDEVICE);
       return -1;
@@ -212,8 +220,10 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
     const uint8_t* kp = smem + (t % R::kStages) * R::kStage;
     const uint8_t* vp = kp + R::kKeys * R::kRow;
     const int p0 = begin + t * R::kKeys;
-    const bool all = p0 + R::kKeys <= end && (!a.causal || p0 + R::kKeys - 1 <= c_lo) &&
-                     (a.window < 0 || p0 >= c_hi - a.window);
+    // no row's mask hides a key: first positions lie before every row, the window's own masks where it begins and ends
+    const bool all = p0 + R::kKeys <= keys.seam ||
+                     (p0 + R::kKeys <= end && p0 >= keys.seam && (!a.causal || p0 + R::kKeys - 1 <= c_lo) &&
+                      (a.window < 0 || p0 >= c_hi - a.window));
     // a masked tile whose values hold infinities or NaN: 0 times those must not reach a row that does not see them
     bool poison = false;
     uint8_t* const pk = smem + R::kBuffers + R::kQ;
@@ -298,8 +308,8 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
         for (int n = 0; n < R::kTiles; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int pos = p0 + k0 + 8 * n + 2 * c + (e & 1), at = pos_of[e >> 1];
-            if (pos >= end || (a.causal && pos > at) || (a.window >= 0 && pos < at - a.window)) x[n][e] = -INFINITY;
+            const int place = p0 + k0 + 8 * n + 2 * c + (e & 1);
+            if (place >= end || !sees(a, pos_of[e >> 1], keys.pos(place))) x[n][e] = -INFINITY;
           }
       }
 #pragma unroll
@@ -476,11 +486,14 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
 }
 
 // The keys some of the rows see.
-__device__ __forceinline__ void seen_range(const AttendParams& a, int kv, int len, int row0, int rows, int& begin,
-                                           int& end) {
+__device__ __forceinline__ Seen seen_range(const AttendParams& a, int kv, int len, int row0, int rows) {
   const int c_lo = kv - len + row0 / a.G, c_hi = kv - len + (row0 + rows - 1) / a.G;
-  begin = a.window >= 0 ? max(0, c_lo - a.window) : 0;
-  end = max(a.causal ? min(kv, c_hi + 1) : kv, begin);
+  Seen k;
+  k.seam = a.window >= 0 ? max(0, c_lo - a.window) : 0;
+  k.begin = k.seam - (a.window >= 0 ? min(a.sink, k.seam) : 0);
+  k.gap = k.begin;
+  k.end = max(a.causal ? min(kv, c_hi + 1) : kv, k.begin);
+  return k;
 }
 
 // An item is a tile of rows of one sequence and KV head.
@@ -504,20 +517,21 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       __shared__ int64_t s_warp[R::kWarps];
       const int items = a.b.n_seqs * a.pool.H, each = (items + R::kThreads - 1) / R::kThreads;
       const int i0 = min(items, (int)threadIdx.x * each), i1 = min(items, i0 + each);
-      auto look = [&](int i, int& lo, int& len, int& kv, int& begin, int& end) -> int64_t {
+      auto look = [&](int i, int& lo, int& len, int& kv, Seen& seen) -> int64_t {
         int64_t kv64;
         const bool sound = seq_rows(a.b, i / a.pool.H, lo, len) &
                            seq_kv(a.b, a.pool.bs, a.pool.H, i / a.pool.H, i % a.pool.H, kv64);
         if (!sound || len == 0) return 0;
         kv = (int)kv64;
-        seen_range(a, kv, len, 0, len * a.G, begin, end);
-        return max(1, (end - begin + R::kKeys - 1) / R::kKeys);  // rows that see nothing have their result too
+        seen = seen_range(a, kv, len, 0, len * a.G);
+        return max(1, (seen.end - seen.begin + R::kKeys - 1) / R::kKeys);  // rows that see nothing have their result too
       };
-      int lo, len, kv, begin, end;
+      int lo, len, kv;
+      Seen seen;
       int64_t mine = 0;
       for (int i = i0; i < i1; ++i) {
         s_first[i] = mine;
-        mine += look(i, lo, len, kv, begin, end);
+        mine += look(i, lo, len, kv, seen);
       }
       int64_t before = mine;
 #pragma unroll
@@ -547,14 +561,16 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       for (; at < to; ++item) {
         const int64_t f0 = s_first[item], f1 = s_first[item + 1];
         if (f1 <= at) continue;
-        look(item, lo, len, kv, begin, end);
+        look(item, lo, len, kv, seen);
         const int64_t stop = min(to, f1);
         const bool opens = at == f0, closes = stop == f1;
         const int s = item / a.pool.H, kh = item % a.pool.H, rows = len * a.G;
-        const int from = begin + (int)(at - f0) * R::kKeys, upto = min(end, begin + (int)(stop - f0) * R::kKeys);
+        Seen piece = seen;
+        piece.begin += (int)(at - f0) * R::kKeys;
+        piece.end = min(seen.end, seen.begin + (int)(stop - f0) * R::kKeys);
         const int64_t slot = (int64_t)16 * width;  // parts of a CTA: of an item it goes on with, of one it begins
         float* const part = opens && closes ? nullptr : p.part + (2 * (int64_t)blockIdx.x + opens) * slot;
-        attend_piece<T, DP, 1>(p, smem, s_off, s, kh, lo, len, kv, 0, rows, from, upto, part);
+        attend_piece<T, DP, 1>(p, smem, s_off, s, kh, lo, len, kv, 0, rows, piece, part);
         if (part) {
           const int64_t c0 = ((f0 + 1) * ctas - 1) / total, c1 = (f1 * ctas - 1) / total;
           const int n = (int)(c1 - c0 + 1);
@@ -578,19 +594,18 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
   const int kv = (int)kv64, n_rows = len * a.G, row0 = tile * 16 * MW;
   if (row0 >= n_rows) return;
   const int rows = min(16 * MW, n_rows - row0);
-  int begin, end;
-  seen_range(a, kv, len, row0, rows, begin, end);
+  Seen seen = seen_range(a, kv, len, row0, rows);
   if (p.splits > 1) {
     // as even pieces of whole tiles as the splits allow (a longer sequence than max_kv has longer pieces)
-    const int span = max((int64_t)p.span, ((int64_t)(end - begin) + p.splits - 1) / p.splits);
+    const int span = max((int64_t)p.span, ((int64_t)(seen.end - seen.begin) + p.splits - 1) / p.splits);
     const int whole = (span + R::kKeys - 1) / R::kKeys * R::kKeys;
-    begin = (int)min((int64_t)end, begin + (int64_t)split * whole);
-    end = (int)min((int64_t)end, (int64_t)begin + whole);
+    seen.begin = (int)min((int64_t)seen.end, seen.begin + (int64_t)split * whole);
+    seen.end = (int)min((int64_t)seen.end, (int64_t)seen.begin + whole);
   }
   const int64_t item = ((int64_t)s * a.pool.H + kh) * p.row_tiles + tile;
   float* const parts = p.splits > 1 ? part_of(p.part, item, p.splits, 0, 16 * MW, D, 0) : nullptr;
   const int64_t step = (int64_t)16 * MW * width;
-  attend_piece<T, DP, MW>(p, smem, s_off, s, kh, lo, len, kv, row0, rows, begin, end,
+  attend_piece<T, DP, MW>(p, smem, s_off, s, kh, lo, len, kv, row0, rows, seen,
                           parts ? parts + split * step : nullptr);
   if (parts && last_of(p.done + item, p.splits, &s_last))
     join_parts<T>(a, parts, parts + step, step, p.splits, rows, row0, lo, kh, smem, R::kSmem);
@@ -627,7 +642,7 @@ bool attend_by_rows(const AttendParams& a) {
 RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   RowPlan r;
   const int keys = a.pool.dtype == DCP_BF16 ? 64 : 32;
-  const int64_t seen = (int64_t)a.window + 128 / a.G + 2;  // of a tile's rows under a window
+  const int64_t seen = (int64_t)a.window + a.sink + 128 / a.G + 2;  // of a tile's rows under a window
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
   // So few keys that an item in one go is over before parts of it would be joined (11 sequences' tokens over 10 keys in
   // a graph: 6.3 us, against 12.4 in shares of two tiles).

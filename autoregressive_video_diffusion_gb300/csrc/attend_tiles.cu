@@ -52,7 +52,8 @@ struct Item {                          // what a CTA works on
   int row0;                            // first (token, head) row
   int kv;                              // cached positions
   int rows[2];                         // rows of each tile
-  int t0[2], t1[2];                    // key tiles each row tile sees
+  int t0[2], t1[2];                    // key tiles each row tile sees,
+  int seam, gap;                       // of which those before `seam` stand for the tile `gap` before their number
   int c0[2], c1[2];                    // cache positions of its first and last row
 };
 
@@ -260,16 +261,16 @@ __device__ __forceinline__ uint32_t no_special(uint32_t w) {
 }
 
 __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, int pos) {
-  return pos < kv && (!a.causal || pos <= c) && (a.window < 0 || pos >= c - a.window);
+  return pos < kv && sees(a, c, pos);
 }
 
-// The key tiles [x, y) of which every row at cache positions c_lo .. c_hi sees every key.
-__device__ __forceinline__ int2 open_tiles(const AttendParams& a, const Tiling& tl, int kv, int c_lo, int c_hi) {
-  if (!tl.span) return make_int2(0, 0);
+// The key tiles [x, y) and [0, min(y, z)) of which every row at cache positions c_lo .. c_hi sees every key.
+__device__ __forceinline__ int3 open_tiles(const AttendParams& a, const Tiling& tl, int kv, int c_lo, int c_hi) {
+  if (!tl.span) return make_int3(0, 0, 0);
   const int end = a.causal ? min(kv, c_lo + 1) : kv, begin = a.window >= 0 ? max(0, c_hi - a.window) : 0;
-  return make_int2((begin + tl.span - 1) / tl.span, max(end, 0) / tl.span);
+  return make_int3((begin + tl.span - 1) / tl.span, max(end, 0) / tl.span, a.sink / tl.span);
 }
-__device__ __forceinline__ bool within(int2 range, int t) { return t >= range.x && t < range.y; }
+__device__ __forceinline__ bool within(int3 range, int t) { return (t >= range.x || t < range.z) && t < range.y; }
 
 // A place in the ring and the parity of its fill.
 template <int SLOTS>
@@ -369,6 +370,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       it.t1[i] = tl.tile_of(end - 1) + 1;
     }
   }
+  it.seam = it.gap = 0;
+  if (a.sink > 0) {  // the first positions' tiles come before the window's; both row tiles begin with them
+    const int first = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], some = min(a.sink, it.kv);
+    const int take = some > 0 ? min(first, tl.tile_of(some - 1) + 1) : 0;
+    it.seam = first;
+    it.gap = first - take;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (it.t0[i] < it.t1[i]) it.t0[i] = it.gap;
+  }
+  auto real = [&](int t) { return t < it.seam ? t - it.gap : t; };
   if (splits > 1) {  // this split's share of the tiles the item's rows see
     const bool one = it.t1[1] <= it.t0[1];
     const int lo = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], hi = one ? it.t1[0] : it.t1[1];
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : act0 ? it.t1[0] : tb;
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
 
-  const int2 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
+  const int3 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
 
   // ---- the rest of the set-up
   // rows of the ring no page ever fills: a weight of 0 must meet a value of 0 there
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int seen_end = a.causal && mine ? min(it.kv, c + 1) : it.kv;
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
     const float sc = a.scale_log2, per_log2 = 1.f / sc;
-    const int2 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
+    const int3 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
     const bool narrow = tl.columns() < kKeys || tl.gaps();
     uint32_t see_open[2];  // columns that stand for keys
 #pragma unroll
@@ -487,15 +499,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     for (bool careful = false;; careful = true) {
       for (int t = t0; t < t1 && ok; ++t) {
+        const int kt = real(t);
         // columns the row sees: in a masked tile those it may see, else those that stand for keys
         uint32_t see[2] = {see_open[0], see_open[1]};
-        const bool masked = !within(mine_open, t), hide = masked || narrow;
+        const bool masked = !within(mine_open, kt), hide = masked || narrow;
         if (masked) {
-          const int p0 = tl.first(t);
+          const int p0 = tl.first(kt);
           if (!tl.gaps()) {
-            const int hi = min(seen_end - p0, tl.count(t)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
+            const int hi = min(seen_end - p0, tl.count(kt)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
+            const int firsts = a.sink - p0 - 64 * hf;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) see[e] = low_bits(hi - 32 * e) & ~low_bits(lo - 32 * e);
+            for (int e = 0; e < 2; ++e)
+              see[e] = low_bits(hi - 32 * e) & (~low_bits(lo - 32 * e) | low_bits(firsts - 32 * e));
           } else {
             int page = 64 * hf / tl.box, row = 64 * hf - page * tl.box;
 #pragma unroll
@@ -504,7 +519,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 4
               for (int b = 0; b < 32; ++b) {
                 const int pos = p0 + page * tl.bs + row;
-                bits |= (uint32_t)(pos >= seen_begin && pos < seen_end) << b;
+                bits |= (uint32_t)((pos >= seen_begin || pos < a.sink) && pos < seen_end) << b;
                 if (++row == tl.box) {
                   row = 0;
                   ++page;
@@ -605,7 +620,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = warp_wait(full(slot), (n / Sh::kSlots) & 1, &sh.dead);
           if (!ok) break;
           uint8_t* const v = gbase + (2 + slot) * Sh::kTile + (threadIdx.x & 255) * 16;
-          const int p0 = tl.first(t), row_a = (threadIdx.x & 255) >> 3, filled = min(tl.count(t), it.kv - p0);
+          const int p0 = tl.first(kt), row_a = (threadIdx.x & 255) >> 3, filled = min(tl.count(kt), it.kv - p0);
           uint4 y[4 * HALVES];
           uint32_t special = 0;
 #pragma unroll
@@ -620,7 +635,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               const int row = row_a + 32 * (k & 3);  // of 128 rows of 64 dims, twice
               bool stands = row < filled;
               if (tl.gaps()) {
-                const int place = tl.place(t, row);
+                const int place = tl.place(kt, row);
                 stands = place >= 0 && p0 + place < it.kv;
               }
               if (!stands)
@@ -704,9 +719,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (sh.poison && mine) {  // infinities and NaN this row sees in the guarded tiles
         for (int t = t0; t < t1; ++t) {
-          if (within(open, t)) continue;
+          const int kt = real(t);
+          if (within(open, kt)) continue;
           for (int col = 0; col < kKeys; ++col) {
-            const int at = tl.place(t, col), pos = tl.first(t) + at;
+            const int at = tl.place(kt, col), pos = tl.first(kt) + at;
             if (at < 0 || !visible(a, it.kv, c, pos)) continue;
             const int blk = table[pos / tl.bs];
             if (blk < 0 || blk >= a.pool.n_blocks) continue;
@@ -760,11 +776,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // pages some row of the item sees: these must name a block
       const int see_lo = a.window >= 0 ? max(0, c_lo - a.window) : 0, see_hi = a.causal ? min(it.kv, c_hi + 1) : it.kv;
       auto entry = [&](int t) {  // this lane's page of tile t
-        const int pg = (tl.subs == 1 ? t * tl.pages : t / tl.subs) + lane;
+        const int pg = (tl.subs == 1 ? real(t) * tl.pages : real(t) / tl.subs) + lane;
         if (t >= te || lane >= n_pages || pg > last_page) return 0;
         const int blk = table[pg];
         if (blk >= 0 && blk < a.pool.n_blocks) return blk;
-        if (pg * tl.bs < see_hi && (pg + 1) * tl.bs > see_lo) set_status(a.b.status, DCP_EDEVICE);
+        if (pg * tl.bs < see_hi && ((pg + 1) * tl.bs > see_lo || pg * tl.bs < a.sink)) set_status(a.b.status, DCP_EDEVICE);
         return (int)a.pool.n_blocks;  // outside the tensor map: zeros
       };
       bool ok = true;
@@ -786,8 +802,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int t = tb; t < te && ok; ++t) {
           const int blk = next;
           next = entry(t + 1);
-          const int row = tl.subs == 1 ? 0 : t % tl.subs * kKeys;
-          const int here = min(n_pages, last_page + 1 - (tl.subs == 1 ? t * tl.pages : t / tl.subs));
+          const int kt = real(t), row = tl.subs == 1 ? 0 : kt % tl.subs * kKeys;
+          const int here = min(n_pages, last_page + 1 - (tl.subs == 1 ? kt * tl.pages : kt / tl.subs));
           ok = warp_wait(empty(at.slot), at.phase ^ 1, &sh.dead);  // at once in the first round
           if (!ok) break;
           const uint32_t dst = ring + at.slot * Sh::kTile, bar = full(at.slot);
@@ -977,7 +993,7 @@ TilePlan plan_tiles(const AttendParams& a, int64_t max_kv) {
   TilePlan t;
   t.q_tiles = (int)(((int64_t)a.b.max_q * a.G + 2 * kRows - 1) / (2 * kRows));
   const int64_t items = (int64_t)t.q_tiles * a.pool.H * a.b.n_seqs;
-  const int64_t seen = (int64_t)a.window + 2 * kRows / a.G + 2;  // of an item's rows under a window
+  const int64_t seen = (int64_t)a.window + a.sink + 2 * kRows / a.G + 2;  // of an item's rows under a window
   if (a.window >= 0 && max_kv > seen) max_kv = seen;
   const int64_t key_tiles = (max_kv + kKeys - 1) / kKeys;
   // Fewer items than SMs: their keys are split so that the SMs have one part each.  Items of equal work (one sequence

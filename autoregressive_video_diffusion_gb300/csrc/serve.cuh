@@ -64,6 +64,7 @@ struct AttendParams {
   int64_t q_stride;
   int32_t Hq, G;                // query heads, and those of one KV head
   int32_t causal, window;
+  int32_t sink;                 // under a window: positions below it are seen by every row behind them
   float scale;
   float scale_log2;             // its size in units of log2 (exponentials are powers of two), in kernels; the sign is the
                                 // products' (a scale below 0 negates them: maxima then are of what is exponentiated)
@@ -76,6 +77,13 @@ struct PageParams {
   int64_t n_blocks, page_bytes;
   int32_t* status;
 };
+
+#ifdef __CUDACC__
+// Whether a row at cache position c sees position pos < kv.
+__device__ __forceinline__ bool sees(const AttendParams& a, int c, int pos) {
+  return (!a.causal || pos <= c) && (a.window < 0 || pos >= c - a.window || pos < a.sink);
+}
+#endif
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_norm_append(const NormParams& p, cudaStream_t s);

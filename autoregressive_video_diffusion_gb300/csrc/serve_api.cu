@@ -148,8 +148,9 @@ dcp_status check_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, 
                            int32_t Hq) {
   if (check_pool(pool) != DCP_OK || check_batch(batch) != DCP_OK || !cfg) return DCP_EINVAL;
   if (Hq < 1 || Hq > 65535 || Hq % pool->H) return DCP_EINVAL;
-  if (!std::isfinite(cfg->scale) || (cfg->causal != 0 && cfg->causal != 1) || cfg->reserved != 0) return DCP_EINVAL;
+  if (!std::isfinite(cfg->scale) || (cfg->causal != 0 && cfg->causal != 1)) return DCP_EINVAL;
   if (cfg->window < -1 || (cfg->window >= 0 && !cfg->causal)) return DCP_EINVAL;
+  if (cfg->sink < 0 || (cfg->sink && cfg->window < 0)) return DCP_EINVAL;
   if ((int64_t)batch->max_q * Hq > kMaxKv) return DCP_EINVAL;
   return DCP_OK;
 }
@@ -162,6 +163,7 @@ AttendParams attend_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, cons
   p.G = Hq / pool->H;
   p.causal = cfg->causal;
   p.window = cfg->window < kMaxKv ? cfg->window : kMaxKv;
+  p.sink = cfg->sink < kMaxKv ? cfg->sink : kMaxKv;
   p.scale = cfg->scale;
   // one near 0 is held where masked scores of -inf still scale to -inf
   const double mag = std::fabs((double)cfg->scale);

@@ -479,7 +479,9 @@ dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* ba
 
 /* Attention of the new tokens over the cache (which already holds their keys and values).
  * Query head h reads KV head h / (Hq / H).  Token i at cache position c = kv_len - q_len + i sees position j if
- *   0 <= j < kv_len,  j <= c where causal = 1,  j >= c - window where window >= 0 (needs causal = 1).
+ *   0 <= j < kv_len,  j <= c where causal = 1,  j >= c - window or j < sink where window >= 0 (needs causal = 1).
+ * (A sink of the first chunks and a window of the last ones are the Streaming policy [differs] as a mask: the pages between
+ * them are not read, and need not name a block.)
  *   out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale * q.k_j),   lse = log sum_j w_j.
  * A row that sees nothing (kv_len 0, or c < 0 under the causal mask) gives out = 0, lse = -inf.
  * Scores, maxima and sums are held in fp32, for any finite scale and values up to 2^100.  Of a bf16 cache the weights are
@@ -491,7 +493,7 @@ typedef struct dcp_attn_config {
   float scale;                 /* finite */
   int32_t causal;              /* 0 or 1 */
   int32_t window;              /* -1: none */
-  int32_t reserved;            /* 0 */
+  int32_t sink;                /* first positions that stay visible under a window: >= 0, 0 without one */
 } dcp_attn_config;
 
 /* Workspace bytes dcp_paged_attention needs (256-byte aligned, zeroed once with dcp_workspace_init); 0 for invalid

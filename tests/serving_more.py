@@ -49,3 +49,45 @@ def check_norm_turned(got, x, w, eps, span, positions, cfgs):
     plain = torch.where(size > 0, size, want.abs())
     tol = plain * norm + size * 2.0 ** -21 + HALF_STEP[x.dtype] * want.abs() + 1e-37
     assert ((got.double() - want).abs() <= tol).all(), ((got.double() - want).abs() / tol.clamp(min=1e-300)).max().item()
+
+
+# ------------------------------------------------------------------------------------------ windows with first positions
+def attention_sink_64(q, k, v, c0, scale, causal, window, sink):
+    """out, lse, sum w|v| and the largest sum |scale q k| of one sequence and head in 64 bits (tests/serving.py's
+    attention_64 with first positions that stay visible).  Only the visible positions of a row are touched."""
+    q, k, v = q.double(), k.double(), v.double()
+    nq, nk = q.shape[0], k.shape[0]
+    c = c0 + torch.arange(nq, device=q.device)[:, None]
+    j = torch.arange(nk, device=q.device)[None]
+    seen = torch.ones(nq, nk, dtype=torch.bool, device=q.device)
+    if causal:
+        seen &= j <= c
+    if window >= 0:
+        seen &= (j >= c - window) | (j < sink)
+    used = seen.any(0)
+    k, v = torch.where(used[:, None], k, 0.0), torch.where(used[:, None], v, 0.0)
+    s = (q @ k.T * scale).masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(s, -1) if nk else torch.full((nq,), -math.inf, dtype=torch.float64, device=q.device)
+    w = torch.where(seen, torch.exp(s - torch.where(lse == -math.inf, 0.0, lse)[:, None]), 0.0)
+    terms = (q.abs() @ k.abs().T * abs(scale)).max().item() if nk and nq else 0.0
+    return w @ v, lse, w @ v.abs(), terms
+
+
+def check_attention_sink(cache, q, out, lse, scale, causal, window, sink, kv_of=None):
+    """Every row of out and lse against 64 bits."""
+    hq = q.shape[1]
+    for i, nq in enumerate(cache.q_lens):
+        r = slice(cache.start[i], cache.start[i + 1])
+        for h in range(hq):
+            kh = h // (hq // cache.h)
+            nk = cache.kv_lens[i] if kv_of is None else kv_of[i][kh]
+            o, l, mass, terms = attention_sink_64(q[r, h], cache.keys[i][:nk, kh], cache.values[i][:nk, kh], nk - nq,
+                                                  scale, causal, window, sink)
+            tol, tol_l = attention_bounds(cache.dt, cache.d, max(nk, 1), o, mass, l, terms)
+            got = out[r, h].double()
+            assert torch.isfinite(got).all(), (i, h)
+            assert ((got - o).abs() <= tol).all(), (i, h, (got - o).abs().max().item())
+            if lse is not None:
+                empty = l == -math.inf
+                assert torch.equal(lse[r, h] == -math.inf, empty), (i, h)
+                assert ((lse[r, h].double() - l).abs()[~empty] <= tol_l[~empty]).all(), (i, h)
