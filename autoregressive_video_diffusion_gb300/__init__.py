@@ -109,6 +109,11 @@ class DcpAttnConfigC(ctypes.Structure):
                 ("sink", ctypes.c_int32)]
 
 
+class DcpPrefixGroupsC(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_prefix", ctypes.c_int64),
+                ("start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
 class DcpPagePoolC(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("L", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("n_blocks", ctypes.c_int64), ("page_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)]
@@ -162,6 +167,9 @@ _SIGS = {
                               _vp, _vp, _i64, _vp, _vp, _vp], _i32),
     "dcp_attention_workspace_size": ([_pk, _pb, _pa, _i32], _sz),
     "dcp_paged_attention": ([_pk, _pb, _pa, _vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "dcp_shared_attention_workspace_size": ([_pk, _pb, ctypes.POINTER(DcpPrefixGroupsC), _pa, _i32], _sz),
+    "dcp_shared_attention": ([_pk, _pb, ctypes.POINTER(DcpPrefixGroupsC), _pa, _vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp],
+                             _i32),
     "dcp_pages_workspace_size": ([_pp, _i32, _i32], _sz),
     "dcp_pages_copy": ([_pp, _vp, _vp, _i32, _vp], _i32),
     "dcp_pages_fork": ([_pp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
@@ -182,7 +190,7 @@ if (_sizes >> 16) != ctypes.sizeof(DcpCacheC) or (_sizes & 0xFFFF) != ctypes.siz
 for _i, _t in enumerate((DcpKvPoolC, DcpSeqBatchC, DcpRopeConfigC, DcpRopePlanC, DcpAttnConfigC, DcpPagePoolC)):
     if lib.dcp_abi_serving_struct_size(_i) != ctypes.sizeof(_t):
         raise ImportError(f"libdcp struct layout does not match the binding: {_t.__name__}")
-for _i, _t in enumerate((DcpRopeAxesC, DcpNormConfigC)):
+for _i, _t in enumerate((DcpRopeAxesC, DcpNormConfigC, DcpPrefixGroupsC)):
     if lib.dcp_abi_norm_struct_size(_i) != ctypes.sizeof(_t):
         raise ImportError(f"libdcp struct layout does not match the binding: {_t.__name__}")
 
@@ -711,17 +719,56 @@ def dcp_attention_workspace_size(pool: KVPool, batch: SeqBatch, cfg: AttnConfig,
     return n
 
 
+def _attention_args(what: str, pool: KVPool, batch: SeqBatch, q, out, lse, ws):
+    """(q, its token stride, query heads, out, lse, workspace, its bytes) of an attention, checked."""
+    hq = q.shape[1]
+    q_stride = _rows_of(q, pool, batch, hq, what)
+    if _rows_of(out, pool, batch, hq, what) != hq * pool.D or batch.kv_heads not in (0, pool.H) or \
+            (lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or
+                                  lse.numel() != batch.total_q * hq)) or not ws.is_cuda:
+        raise DcpError(what, DCP_EINVAL)
+    return _ptr(q), q_stride, hq, _ptr(out), _ptr(lse), _ptr(ws), ws.numel()
+
+
 def dcp_paged_attention(pool: KVPool, batch: SeqBatch, cfg: AttnConfig, q: torch.Tensor, out: torch.Tensor, lse,
                         ws: torch.Tensor, stream=None) -> None:
     """out [total_q][Hq][D] = attention of the new tokens q over the cache; lse (or None): fp32 [total_q][Hq]."""
-    hq = q.shape[1]
-    q_stride = _rows_of(q, pool, batch, hq, "dcp_paged_attention")
-    if _rows_of(out, pool, batch, hq, "dcp_paged_attention") != hq * pool.D or batch.kv_heads not in (0, pool.H) or \
-            (lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or not lse.is_cuda or
-                                  lse.numel() != batch.total_q * hq)) or not ws.is_cuda:
-        raise DcpError("dcp_paged_attention", DCP_EINVAL)
-    _check(lib.dcp_paged_attention(pool.ref, batch.ref, cfg.c(pool.D), _ptr(q), q_stride, hq, _ptr(out), _ptr(lse),
-                                   _ptr(ws), ws.numel(), _stream(stream)), "dcp_paged_attention")
+    args = _attention_args("dcp_paged_attention", pool, batch, q, out, lse, ws)
+    _check(lib.dcp_paged_attention(pool.ref, batch.ref, cfg.c(pool.D), *args, _stream(stream)), "dcp_paged_attention")
+
+
+class PrefixGroups:
+    """Groups of consecutive sequences that share their first positions (dcp_prefix_groups).  Device int32 tensors: start
+    [n + 1] (sequences of a batch), prefix_len [n].  max_q (new tokens of a group) and max_prefix are bounds the host
+    knows."""
+
+    def __init__(self, start: torch.Tensor, prefix_len: torch.Tensor, max_prefix: int, max_q: int):
+        n = prefix_len.numel()
+        if any(t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda for t in (start, prefix_len)) or \
+                start.numel() != n + 1:
+            raise DcpError("PrefixGroups", DCP_EINVAL)
+        self.tensors = (start, prefix_len)
+        self._c = DcpPrefixGroupsC(n, max_q, max_prefix, _ptr(start), _ptr(prefix_len))
+        self.ref = ctypes.byref(self._c)
+
+    def c(self) -> DcpPrefixGroupsC:
+        return self._c
+
+
+def dcp_shared_attention_workspace_size(pool: KVPool, batch: SeqBatch, groups: PrefixGroups, cfg: AttnConfig,
+                                        Hq: int) -> int:
+    n = lib.dcp_shared_attention_workspace_size(pool.ref, batch.ref, groups.ref, cfg.c(pool.D), Hq)
+    if n == 0:
+        raise DcpError("dcp_shared_attention_workspace_size", DCP_EINVAL)
+    return n
+
+
+def dcp_shared_attention(pool: KVPool, batch: SeqBatch, groups: PrefixGroups, cfg: AttnConfig, q: torch.Tensor,
+                         out: torch.Tensor, lse, ws: torch.Tensor, stream=None) -> None:
+    """dcp_paged_attention of sequences that share prefixes, each read once for its group."""
+    args = _attention_args("dcp_shared_attention", pool, batch, q, out, lse, ws)
+    _check(lib.dcp_shared_attention(pool.ref, batch.ref, groups.ref, cfg.c(pool.D), *args, _stream(stream)),
+           "dcp_shared_attention")
 
 
 class PagePool:

@@ -11,13 +11,15 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdcp.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 SOURCES = ["scan.cu", "gather.cu", "rephase.cu", "read.cu", "snapshot.cu", "api.cu", "noalloc.cu",
-           "append.cu", "norm_append.cu", "attend_rows.cu", "attend_tiles.cu", "pages.cu", "serve_api.cu"]
+           "append.cu", "norm_append.cu", "attend_rows.cu", "attend_rows_sink.cu", "attend_rows_prefix.cu",
+           "attend_rows_rest.cu", "attend_tiles.cu", "shared.cu", "pages.cu", "serve_api.cu"]
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 
 
 def _deps():
     out = [os.path.join(CSRC, s) for s in SOURCES]
-    out += [os.path.join(CSRC, h) for h in ("dcp_internal.cuh", "rephase_body.cuh", "serve.cuh", "append.cuh", "attend_join.cuh")]
+    out += [os.path.join(CSRC, h) for h in ("dcp_internal.cuh", "rephase_body.cuh", "serve.cuh", "append.cuh", "attend_join.cuh",
+                                             "attend_rows.cuh")]
     out += [os.path.join(HERE, "..", "include", "dcp.h")]
     return out
 

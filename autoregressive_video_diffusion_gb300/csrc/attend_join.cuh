@@ -39,51 +39,101 @@ __device__ __forceinline__ bool last_of(uint32_t* done, int splits, int* s_last)
   return *s_last;
 }
 
+// A piece of a group's prefix, and the rows that see it.
+struct PrefixPiece {
+  GroupRows of;
+  int split, splits;            // the piece's number among the group's
+};
+__device__ __forceinline__ float* prefix_part(const PrefixPlan& pre, int D, int slot, int kh, int tile, int r) {
+  return pre.part + ((((int64_t)slot * pre.heads + kh) * pre.tiles + tile) * pre.rows + r) * (kPartHead + D);
+}
+
+// The piece of slot `slot`, by a whole warp: each group with rows and a prefix has a slot, and of those left over as many
+// as its share of all prefixes, rounded down.  (Without rows: len = 0.)  With `note` the groups' slots go to the table.
+__device__ __forceinline__ PrefixPiece prefix_piece(const AttendParams& a, const PrefixPlan& pre, int slot, bool note) {
+  const int lane = threadIdx.x & 31;
+  auto units = [&](int g, GroupRows& of) -> int64_t {
+    if (g >= a.groups.n || !group_at(a, g, of) || of.len == 0) return 0;
+    return ((int64_t)of.prefix + pre.unit - 1) / pre.unit;
+  };
+  GroupRows of{};
+  int64_t total = 0;
+  for (int g = lane; g < a.groups.n; g += 32) total += units(g, of);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  PrefixPiece found{};
+  int first = 0;  // slots of the groups before
+  for (int g0 = 0; g0 < a.groups.n; g0 += 32) {
+    const int64_t w = units(g0 + lane, of);
+    const int n = w ? (int)min((int64_t)pre.cap, min(w, 1 + (pre.slots - a.groups.n) * w / total)) : 0;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, end, o);
+      if (lane >= o) end += y;
+    }
+    const int at = first + end - n;
+    if (note && g0 + lane < a.groups.n) pre.table[g0 + lane] = make_int2(at, n);
+    const uint32_t hit = __ballot_sync(~0u, slot >= at && slot < at + n);
+    if (hit) {
+      const int who = __ffs(hit) - 1;
+      found.of.g = __shfl_sync(~0u, of.g, who);
+      found.of.s = __shfl_sync(~0u, of.s, who);
+      found.of.lo = __shfl_sync(~0u, of.lo, who);
+      found.of.len = __shfl_sync(~0u, of.len, who);
+      found.of.prefix = __shfl_sync(~0u, of.prefix, who);
+      found.split = slot - __shfl_sync(~0u, at, who);
+      found.splits = __shfl_sync(~0u, n, who);
+      if (!note) break;
+    }
+    first += __shfl_sync(~0u, end, 31);
+  }
+  return found;
+}
+
 // Joins `splits` parts of `rows` rows whose first is row `row0` of (token, head of the KV
 // head) rows, sequence start lo.  Called by a whole CTA; scratch: `room` bytes of shared memory, at least
 // join_scratch(rows, splits).  Everything is fetched at once where it fits the scratch (a loop over the parts in global
 // memory pays a memory latency every few of them: 5 us for 12 parts of 5 rows, 1 us this way), else the maxima and sums
 // first and the values with several loads in flight.
+// parts.row(k, r): part k's row r; parts.chunk(k, c): its 16-byte chunk c, counted from row 0 on.
 __host__ __device__ constexpr int64_t join_scratch(int rows, int splits) {
   return (int64_t)rows * (2 * splits + 1) * 4;
 }
 
-// The first part is at `part0`, the others from `part1` on, `step` floats apart.
-template <typename T>
-__device__ __forceinline__ void join_parts(const AttendParams& a, const float* part0, const float* part1, int64_t step,
-                                           int splits, int rows, int row0, int lo, int kh, uint8_t* scratch,
-                                           int64_t room) {
+template <typename T, typename Parts>
+__device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& parts, int splits, int rows, int row0,
+                                          int lo, int kh, uint8_t* scratch, int64_t room) {
   const int D = a.pool.D, quads = D / 4, width = kPartHead + D;
-  auto part = [&](int k) { return k ? part1 + (k - 1) * step : part0; };
   float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]: the maximum, then the part's weight
   float* const sum = weight + rows * splits;                // [rows][splits]
   float* const inv = sum + rows * splits;                   // [rows]
   const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
   __syncthreads();
   const bool local = used + (int64_t)rows * splits * width * 4 <= room;
+  const float* const here = reinterpret_cast<const float*>(scratch + used);  // [split][row][width]
   if (local) {
     const int chunks = rows * width / 4;
     const uint32_t to = smem_u32(scratch + used);
     for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
       const int k = u / chunks;
-      cp_async16(to + u * 16, part(k) + (u - k * chunks) * 4);
+      cp_async16(to + u * 16, parts.chunk(k, u - k * chunks));
     }
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
-    step = (int64_t)rows * width;
-    part0 = reinterpret_cast<const float*>(scratch + used);
-    part1 = part0 + step;
   }
+  auto row_of = [&](int k, int r) { return local ? here + ((int64_t)k * rows + r) * width : parts.row(k, r); };
   for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
     const int r = u / splits;
-    const float2* at = reinterpret_cast<const float2*>(part(u - r * splits) + (int64_t)r * width);
+    const float2* at = reinterpret_cast<const float2*>(row_of(u - r * splits, r));
     const float2 ml = local ? *at : __ldcg(at);
     weight[u] = ml.x;
     sum[u] = ml.y;
   }
   __syncthreads();
-  // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
+  // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0).  -1 marks one whose weight is too
+  // small for fp32 though it saw keys: an infinity or NaN in it is the row's all the same.
   for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
     const int lane = threadIdx.x & 31;
     float* const w = weight + r * splits;
@@ -95,7 +145,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     for (int k = lane; k < splits; k += 32) {
       const float wk = ls[k] == 0.f ? 0.f : exp2_fast((w[k] - top) * a.scale_log2);
-      w[k] = wk;
+      w[k] = wk == 0.f && ls[k] != 0.f ? -1.f : wk;
       if (wk != 0.f) l += wk * ls[k];
     }
 #pragma unroll
@@ -109,15 +159,21 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
   __syncthreads();
   for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
     const int r = u / quads, d = (u - r * quads) * 4;
-    const int64_t at = (int64_t)r * width + kPartHead + d;
     const float* w = weight + r * splits;
     float o[4] = {};
 #pragma unroll 8
     for (int k = 0; k < splits; ++k) {
-      const float4* from = reinterpret_cast<const float4*>(part(k) + at);
+      const float4* from = reinterpret_cast<const float4*>(row_of(k, r) + kPartHead + d);
       const float4 x = local ? *from : __ldcg(from);
       const float wk = w[k];
-      if (wk != 0.f) o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;
+      if (wk < 0.f) {
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!isfinite(y[e])) o[e] += y[e];
+      } else if (wk != 0.f) {
+        o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;
+      }
     }
     const int R = row0 + r, tok = R / a.G;
     const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G);
@@ -128,6 +184,49 @@ __device__ __forceinline__ void join_parts(const AttendParams& a, const float* p
     else
       *reinterpret_cast<float4*>(a.out + (row * D + d) * 4) = make_float4(o[0] * n, o[1] * n, o[2] * n, o[3] * n);
   }
+}
+
+// The parts of a row's own keys: the first is at `part0`, the others from `part1` on, `step` floats apart.
+struct OwnParts {
+  const float* part0;
+  const float* part1;
+  int64_t step;
+  int width;
+  __device__ __forceinline__ const float* part(int k) const { return k ? part1 + (k - 1) * step : part0; }
+  __device__ __forceinline__ const float* row(int k, int r) const { return part(k) + (int64_t)r * width; }
+  __device__ __forceinline__ const float* chunk(int k, int c) const { return part(k) + c * 4; }
+};
+template <typename T>
+__device__ __forceinline__ void join_parts(const AttendParams& a, const float* part0, const float* part1, int64_t step,
+                                           int splits, int rows, int row0, int lo, int kh, uint8_t* scratch,
+                                           int64_t room) {
+  join_rows<T>(a, OwnParts{part0, part1, step, kPartHead + a.pool.D}, splits, rows, row0, lo, kh, scratch, room);
+}
+
+// The same and, behind them, those of the group's prefix, whose rows are counted from the group's first one on.
+struct AllParts {
+  OwnParts own;
+  PrefixPlan pre;
+  int n, first, kh, row0;       // own parts; the prefix's first slot; the item's first row among the group's
+  __device__ __forceinline__ const float* row(int k, int r) const {
+    if (k < n) return own.row(k, r);
+    const int R = row0 + r, tile = R / pre.rows;
+    return prefix_part(pre, own.width - kPartHead, first + k - n, kh, tile, R - tile * pre.rows);
+  }
+  __device__ __forceinline__ const float* chunk(int k, int c) const {
+    if (k < n) return own.chunk(k, c);
+    const int quads = own.width / 4, r = c / quads;
+    return row(k, r) + (c - r * quads) * 4;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void join_with_prefix(const AttendParams& a, const PrefixPlan& pre, const GroupRows& of,
+                                                 const float* part0, const float* part1, int64_t step, int splits,
+                                                 int rows, int row0, int lo, int kh, uint8_t* scratch, int64_t room) {
+  const int2 slots = of.g < 0 ? make_int2(0, 0) : pre.table[of.g];
+  const AllParts all{OwnParts{part0, part1, step, kPartHead + a.pool.D}, pre, splits, slots.x, kh,
+                     (lo - of.lo) * a.G + row0};
+  join_rows<T>(a, all, splits + slots.y, rows, row0, lo, kh, scratch, room);
 }
 
 }  // namespace dcp

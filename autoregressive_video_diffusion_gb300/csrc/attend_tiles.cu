@@ -85,8 +85,16 @@ struct Tiling {
   }
 };
 
+// What the kernel is built for, so that none pays for another's tests.
+enum Form {
+  kPlain,   // a causal mask, a window
+  kSink,    // a window whose first positions stay visible
+  kPrefix,  // the rows of all sequences of a group against the prefix they share; leaves parts
+};
+
 struct TileParams {
   AttendParams a;
+  PrefixPlan pre;                      // kPrefix
   Tiling tl;
   int splits, q_tiles;
   int whole;                           // items of one CTA each before those that are split
@@ -265,12 +273,16 @@ __device__ __forceinline__ bool visible(const AttendParams& a, int kv, int c, in
 }
 
 // The key tiles [x, y) and [0, min(y, z)) of which every row at cache positions c_lo .. c_hi sees every key.
+template <int FORM>
 __device__ __forceinline__ int3 open_tiles(const AttendParams& a, const Tiling& tl, int kv, int c_lo, int c_hi) {
   if (!tl.span) return make_int3(0, 0, 0);
   const int end = a.causal ? min(kv, c_lo + 1) : kv, begin = a.window >= 0 ? max(0, c_hi - a.window) : 0;
-  return make_int3((begin + tl.span - 1) / tl.span, max(end, 0) / tl.span, a.sink / tl.span);
+  return make_int3((begin + tl.span - 1) / tl.span, max(end, 0) / tl.span, FORM == kSink ? a.sink / tl.span : 0);
 }
-__device__ __forceinline__ bool within(int3 range, int t) { return (t >= range.x || t < range.z) && t < range.y; }
+template <int FORM>
+__device__ __forceinline__ bool within(int3 range, int t) {
+  return (t >= range.x || (FORM == kSink && t < range.z)) && t < range.y;
+}
 
 // A place in the ring and the parity of its fill.
 template <int SLOTS>
@@ -291,7 +303,7 @@ struct Ring {
   }
 };
 
-template <int HALVES>
+template <int HALVES, int FORM>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ TileParams p, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
@@ -305,6 +317,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } swap;
     uint32_t tmem;
     int dead, poison, last, far, steep;
+    PrefixPiece piece;
   };
   static_assert(sizeof(Head) <= Sh::kHead, "the head fits before the tiles");
   Head& sh = *reinterpret_cast<Head*>(smem_raw);
@@ -339,21 +352,45 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   // ---- the item
   Item it;
-  // blocks in the order: row tile, KV head, sequence; the first `whole` items are one CTA's, the others are split
-  const int cut = max(0, (int)blockIdx.x - p.whole), item = cut ? p.whole + cut / p.splits : min(blockIdx.x, p.whole);
-  const int splits = item < p.whole ? 1 : p.splits, split = item < p.whole ? 0 : cut % p.splits;
-  const int qt = p.q_tiles - 1 - item % p.q_tiles;  // the rows that see most keys first
-  it.kh = item / p.q_tiles % a.pool.H;
-  it.s = item / p.q_tiles / a.pool.H;
-  allow_dependents();
-  wait_for_predecessor();
-  int64_t kv64;
-  const bool sound = seq_rows(a.b, it.s, it.lo, it.len) & seq_kv(a.b, tl.bs, a.pool.H, it.s, it.kh, kv64);
-  if (!sound) return;
+  int item = 0, splits, split, qt;
+  if constexpr (FORM == kPrefix) {
+    // blocks in the order: row tile, KV head, slot
+    const int at = blockIdx.x / p.q_tiles, slot = at / a.pool.H;
+    qt = blockIdx.x % p.q_tiles;
+    it.kh = at % a.pool.H;
+    allow_dependents();
+    wait_for_predecessor();
+    if (warp == 1) {
+      const PrefixPiece piece = prefix_piece(a, p.pre, slot, blockIdx.x == 0);
+      if (lane == 0) sh.piece = piece;
+    }
+    __syncthreads();
+    const PrefixPiece piece = sh.piece;
+    splits = piece.splits;
+    split = piece.split;
+    it.s = piece.of.s;
+    it.lo = piece.of.lo;
+    it.len = piece.of.len;
+    it.kv = piece.of.prefix;
+  } else {
+    // blocks in the order: row tile, KV head, sequence; the first `whole` items are one CTA's, the others are split
+    const int cut = max(0, (int)blockIdx.x - p.whole);
+    item = cut ? p.whole + cut / p.splits : min(blockIdx.x, p.whole);
+    splits = item < p.whole ? 1 : p.splits;
+    split = item < p.whole ? 0 : cut % p.splits;
+    qt = p.q_tiles - 1 - item % p.q_tiles;  // the rows that see most keys first
+    it.kh = item / p.q_tiles % a.pool.H;
+    it.s = item / p.q_tiles / a.pool.H;
+    allow_dependents();
+    wait_for_predecessor();
+    int64_t kv64;
+    const bool sound = seq_rows(a.b, it.s, it.lo, it.len) & seq_kv(a.b, tl.bs, a.pool.H, it.s, it.kh, kv64);
+    if (!sound) return;
+    it.kv = (int)kv64;
+  }
   const int n_rows = it.len * a.G;
   it.row0 = qt * 2 * kRows;
   if (it.row0 >= n_rows) return;
-  it.kv = (int)kv64;
   const int32_t* table = a.b.tables + (int64_t)it.s * a.b.table_stride;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -371,7 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   }
   it.seam = it.gap = 0;
-  if (a.sink > 0) {  // the first positions' tiles come before the window's; both row tiles begin with them
+  if constexpr (FORM == kSink) {  // the first positions' tiles come before the window's; both row tiles begin with them
     const int first = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], some = min(a.sink, it.kv);
     const int take = some > 0 ? min(first, tl.tile_of(some - 1) + 1) : 0;
     it.seam = first;
@@ -380,7 +417,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < 2; ++i)
       if (it.t0[i] < it.t1[i]) it.t0[i] = it.gap;
   }
-  auto real = [&](int t) { return t < it.seam ? t - it.gap : t; };
+  auto real = [&](int t) { return FORM == kSink && t < it.seam ? t - it.gap : t; };
   if (splits > 1) {  // this split's share of the tiles the item's rows see
     const bool one = it.t1[1] <= it.t0[1];
     const int lo = it.t0[0] < it.t1[0] ? it.t0[0] : it.t0[1], hi = one ? it.t1[0] : it.t1[1];
@@ -396,7 +433,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int te = act1 ? max(it.t1[1], act0 ? it.t1[0] : 0) : act0 ? it.t1[0] : tb;
   const int c_lo = it.c0[0], c_hi = it.rows[1] ? it.c1[1] : it.c1[0];
 
-  const int3 open = open_tiles(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
+  const int3 open = open_tiles<FORM>(a, tl, it.kv, c_lo, c_hi);  // tiles without a mask
 
   // ---- the rest of the set-up
   // rows of the ring no page ever fills: a weight of 0 must meet a value of 0 there
@@ -466,7 +503,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int seen_end = a.causal && mine ? min(it.kv, c + 1) : it.kv;
     const int seen_begin = a.window >= 0 && mine ? c - a.window : 0;
     const float sc = a.scale_log2, per_log2 = 1.f / sc;
-    const int3 mine_open = open_tiles(a, tl, it.kv, cmin, cmax);
+    const int3 mine_open = open_tiles<FORM>(a, tl, it.kv, cmin, cmax);
     const bool narrow = tl.columns() < kKeys || tl.gaps();
     uint32_t see_open[2];  // columns that stand for keys
 #pragma unroll
@@ -502,15 +539,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int kt = real(t);
         // columns the row sees: in a masked tile those it may see, else those that stand for keys
         uint32_t see[2] = {see_open[0], see_open[1]};
-        const bool masked = !within(mine_open, kt), hide = masked || narrow;
+        const bool masked = !within<FORM>(mine_open, kt), hide = masked || narrow;
         if (masked) {
           const int p0 = tl.first(kt);
           if (!tl.gaps()) {
             const int hi = min(seen_end - p0, tl.count(kt)) - 64 * hf, lo = seen_begin - p0 - 64 * hf;
-            const int firsts = a.sink - p0 - 64 * hf;
+            const int firsts = FORM == kSink ? a.sink - p0 - 64 * hf : 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              see[e] = low_bits(hi - 32 * e) & (~low_bits(lo - 32 * e) | low_bits(firsts - 32 * e));
+              see[e] = low_bits(hi - 32 * e) &
+                       (FORM == kSink ? ~low_bits(lo - 32 * e) | low_bits(firsts - 32 * e) : ~low_bits(lo - 32 * e));
           } else {
             int page = 64 * hf / tl.box, row = 64 * hf - page * tl.box;
 #pragma unroll
@@ -519,7 +557,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 4
               for (int b = 0; b < 32; ++b) {
                 const int pos = p0 + page * tl.bs + row;
-                bits |= (uint32_t)((pos >= seen_begin || pos < a.sink) && pos < seen_end) << b;
+                bits |= (uint32_t)((pos >= seen_begin || (FORM == kSink && pos < a.sink)) && pos < seen_end) << b;
                 if (++row == tl.box) {
                   row = 0;
                   ++page;
@@ -705,7 +743,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (!ok) set_status(a.b.status, DCP_ETIMEOUT);
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(it.lo + tok) * a.Hq + it.kh * a.G + g;
-    float* part = part_of(p.part, item - p.whole, p.splits, split, 2 * kRows, D, i * kRows + r);
+    const bool parted = FORM == kPrefix || splits > 1;
+    float* part;
+    if constexpr (FORM == kPrefix)
+      part = prefix_part(p.pre, D, blockIdx.x / (p.q_tiles * a.pool.H), it.kh, qt, i * kRows + r);
+    else
+      part = part_of(p.part, item - p.whole, p.splits, split, 2 * kRows, D, i * kRows + r);
 #pragma unroll 1
     for (int e = 0; e < Sh::kD / 64 && ok; ++e) {
       const int d0 = hf * (Sh::kD / 2) + 32 * e;
@@ -720,7 +763,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (sh.poison && mine) {  // infinities and NaN this row sees in the guarded tiles
         for (int t = t0; t < t1; ++t) {
           const int kt = real(t);
-          if (within(open, kt)) continue;
+          if (within<FORM>(open, kt)) continue;
           for (int col = 0; col < kKeys; ++col) {
             const int at = tl.place(kt, col), pos = tl.first(kt) + at;
             if (at < 0 || !visible(a, it.kv, c, pos)) continue;
@@ -737,7 +780,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!mine) continue;
-      if (splits > 1) {
+      if (parted) {
 #pragma unroll
         for (int u = 0; u < 32; u += 2)
           if (d0 + u < D)
@@ -757,7 +800,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     if (mine && ok && hf == 0) {
-      if (splits > 1) {
+      if (parted) {
         part[0] = m;
         part[1] = l;
       } else if (a.lse) {
@@ -780,7 +823,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (t >= te || lane >= n_pages || pg > last_page) return 0;
         const int blk = table[pg];
         if (blk >= 0 && blk < a.pool.n_blocks) return blk;
-        if (pg * tl.bs < see_hi && ((pg + 1) * tl.bs > see_lo || pg * tl.bs < a.sink)) set_status(a.b.status, DCP_EDEVICE);
+        if (pg * tl.bs < see_hi && ((pg + 1) * tl.bs > see_lo || (FORM == kSink && pg * tl.bs < a.sink)))
+          set_status(a.b.status, DCP_EDEVICE);
         return (int)a.pool.n_blocks;  // outside the tensor map: zeros
       };
       bool ok = true;
@@ -926,7 +970,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 
   // ---- the item's last split joins the parts
-  if (splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
+  if (FORM != kPrefix && splits > 1 && last_of(p.done + item - p.whole, splits, &sh.last))
     join_parts<__nv_bfloat16>(a, part_of(p.part, item - p.whole, p.splits, 0, 2 * kRows, a.pool.D, 0),
                               part_of(p.part, item - p.whole, p.splits, 1, 2 * kRows, a.pool.D, 0),
                               (int64_t)2 * kRows * (kPartHead + a.pool.D), splits, it.rows[0] + it.rows[1], it.row0,
@@ -973,18 +1017,31 @@ uint32_t idesc(int n, bool b_by_rows, bool negate) {
          ((uint32_t)(n / 8) << 17) | ((uint32_t)(kRows / 16) << 24);
 }
 
-LaunchCache g_tile_launch[2];
-
-template <int HALVES>
-cudaError_t launch(const TileParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+template <int HALVES, int FORM>
+cudaError_t launch(const TileParams& p, int64_t grid, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  static LaunchCache lc;
   int blocks;
-  const cudaError_t e = launch_setup(g_tile_launch[HALVES - 1], tile_kernel<HALVES>, kTileThreads,
-                                     Shape<HALVES>::kSmem, &blocks);
+  const cudaError_t e = launch_setup(lc, tile_kernel<HALVES, FORM>, kTileThreads, Shape<HALVES>::kSmem, &blocks);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)p.q_tiles * p.a.pool.H * p.a.b.n_seqs;
-  const int64_t grid = p.whole + (items - p.whole) * p.splits;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_behind(tile_kernel<HALVES>, dim3((unsigned)grid), kTileThreads, Shape<HALVES>::kSmem, s, p, k, v);
+  return launch_behind(tile_kernel<HALVES, FORM>, dim3((unsigned)grid), kTileThreads, Shape<HALVES>::kSmem, s, p, k, v);
+}
+
+template <int FORM>
+cudaError_t launch_form(TileParams& p, int64_t grid, cudaStream_t s) {
+  const AttendParams& a = p.a;
+  const int bs = a.pool.bs;
+  p.tl.bs = bs;
+  p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
+  p.tl.pages = kKeys / p.tl.box;
+  p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
+  p.tl.span = bs % kKeys == 0 ? kKeys : bs < kKeys ? p.tl.pages * bs : 0;
+  p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
+  p.idesc_pv = idesc((a.pool.D + 15) / 16 * 16, true, false);
+  CUtensorMap mk, mv;
+  if (!encode(&mk, a.pool, a.pool.k, p.tl.box) || !encode(&mv, a.pool, a.pool.v, p.tl.box))
+    return cudaErrorInvalidValue;
+  return a.pool.D <= 64 ? launch<1, FORM>(p, grid, mk, mv, s) : launch<2, FORM>(p, grid, mk, mv, s);
 }
 
 }  // namespace
@@ -1018,23 +1075,22 @@ cudaError_t launch_attend_tiles(const AttendParams& a, int64_t max_kv, void* ws,
   if (t.whole > INT32_MAX) return cudaErrorInvalidValue;
   TileParams p{};
   p.a = a;
-  const int bs = a.pool.bs;
-  p.tl.bs = bs;
-  p.tl.box = bs >= kKeys ? kKeys : (bs + 7) / 8 * 8;
-  p.tl.pages = kKeys / p.tl.box;
-  p.tl.subs = bs > kKeys ? (bs + kKeys - 1) / kKeys : 1;
-  p.tl.span = bs % kKeys == 0 ? kKeys : bs < kKeys ? p.tl.pages * bs : 0;
   p.splits = t.splits;
   p.whole = (int)t.whole;
   p.q_tiles = t.q_tiles;
-  p.idesc_qk = idesc(kKeys, false, a.scale < 0.f);
-  p.idesc_pv = idesc((a.pool.D + 15) / 16 * 16, true, false);
   p.done = done_counters(ws);
   p.part = (float*)((char*)ws + kScratch);
-  CUtensorMap mk, mv;
-  if (!encode(&mk, a.pool, a.pool.k, p.tl.box) || !encode(&mv, a.pool, a.pool.v, p.tl.box))
-    return cudaErrorInvalidValue;
-  return a.pool.D <= 64 ? launch<1>(p, mk, mv, s) : launch<2>(p, mk, mv, s);
+  const int64_t items = (int64_t)p.q_tiles * a.pool.H * a.b.n_seqs, grid = p.whole + (items - p.whole) * p.splits;
+  return a.sink ? launch_form<kSink>(p, grid, s) : launch_form<kPlain>(p, grid, s);
+}
+
+cudaError_t launch_prefix_tiles(const AttendParams& a, const PrefixPlan& pre, cudaStream_t s) {
+  TileParams p{};
+  p.a = a;
+  p.pre = pre;
+  p.splits = 1;
+  p.q_tiles = pre.tiles;
+  return launch_form<kPrefix>(p, (int64_t)pre.slots * pre.heads * pre.tiles, s);
 }
 
 }  // namespace dcp

@@ -55,9 +55,26 @@ struct NormParams {
   float amplitude[3];
 };
 
+// Groups of consecutive sequences that share their first positions (dcp_prefix_groups).
+struct Groups {
+  int32_t n, max_q;             // 0: none; new tokens of a group at most
+  const int32_t* start;
+  const int32_t* prefix;
+};
+
+// How the groups' prefixes are divided: a slot is a piece of one group's prefix, worked on by a CTA for each tile of the
+// group's rows and each KV head, which leaves a part for each of its rows.  The slots go to the groups by their lengths.
+struct PrefixPlan {
+  float* part;                  // [slot][KV head][tile][row][kPartHead + D]
+  int2* table;                  // [group] first slot, number of slots
+  int32_t slots, tiles, rows, heads;
+  int32_t unit, cap;            // keys of the smallest piece worth a slot; slots of a group at most
+};
+
 struct AttendParams {
   Pool pool;
   Batch b;
+  Groups groups;
   const char* q;
   char* out;
   float* lse;
@@ -98,6 +115,9 @@ struct RowPlan {
 bool attend_by_rows(const AttendParams& p);
 RowPlan plan_rows(const AttendParams& p, int64_t max_kv);
 cudaError_t launch_attend_rows(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);
+cudaError_t launch_prefix_rows(const AttendParams& p, const PrefixPlan& pre, cudaStream_t s);
+cudaError_t launch_rest_rows(const AttendParams& p, const RowPlan& r, const PrefixPlan& pre, void* ws, cudaStream_t s);
+int join_parts_room(const AttendParams& p, const RowPlan& r);  // parts of a row that the join's scratch holds
 
 // The same for the tiled attention.
 struct TilePlan {
@@ -105,8 +125,13 @@ struct TilePlan {
   int64_t whole;  // items that are not split, the first ones
   size_t bytes;
 };
+cudaError_t launch_prefix_tiles(const AttendParams& p, const PrefixPlan& pre, cudaStream_t s);
 TilePlan plan_tiles(const AttendParams& p, int64_t max_kv);
 cudaError_t launch_attend_tiles(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);
+
+// Attention of groups that share a prefix: the bytes of parts it needs, and its launches.
+size_t shared_bytes(const AttendParams& p, int64_t max_kv, int64_t max_prefix);
+cudaError_t launch_shared(const AttendParams& p, int64_t max_kv, int64_t max_prefix, void* ws, cudaStream_t s);
 
 cudaError_t launch_pages_copy(const PageParams& p, const int32_t* src, const int32_t* dst, int32_t n, cudaStream_t s);
 cudaError_t launch_pages_fork(const PageParams& p, const int32_t* tables, const int32_t* len, int32_t n_rows,
@@ -185,6 +210,51 @@ __device__ __forceinline__ bool seq_kv(const Batch& b, int bs, int H, int s, int
     return false;
   }
   return true;
+}
+
+// Group g of the batch: its first sequence, rows of q and shared positions, checked.
+struct GroupRows {
+  int g, s, lo, len, prefix;    // g = -1: no group
+};
+__device__ __forceinline__ bool group_at(const AttendParams& a, int g, GroupRows& of) {
+  of.g = g;
+  of.s = a.groups.start[g];
+  const int end = a.groups.start[g + 1];
+  bool sound = of.s >= 0 && end >= of.s && end <= a.b.n_seqs;
+  if (sound) {
+    of.lo = a.b.q_start[of.s];
+    const int hi = a.b.q_start[end];
+    of.len = hi - of.lo;
+    of.prefix = a.groups.prefix[g];
+    sound = of.lo >= 0 && hi >= of.lo && hi <= a.b.total_q && of.len <= a.groups.max_q && of.prefix >= 0 &&
+            of.prefix <= a.b.table_stride * a.pool.bs && of.prefix <= kMaxKv;
+  }
+  if (!sound) set_status(a.b.status, DCP_EDEVICE);
+  return sound;
+}
+
+// The group of sequence s, whose `len` new tokens begin at row lo of q and end its `kv` positions; `from` is the first
+// position that it holds for itself.  False (and the status word) where the group or its prefix is unsound.
+__device__ __forceinline__ bool group_of(const AttendParams& a, int s, int lo, int len, int kv, GroupRows& of,
+                                         int& from) {
+  int g = 0;  // the first group that begins behind s
+  for (int n = a.groups.n; n > 0;) {
+    const int half = n / 2;
+    if (a.groups.start[g + half] <= s) {
+      g += half + 1;
+      n -= half + 1;
+    } else {
+      n = half;
+    }
+  }
+  of = GroupRows{-1, 0, 0, 0, 0};
+  from = 0;
+  if (g == 0 || s >= a.groups.start[g]) return true;  // start[n] ends the last group
+  if (!group_at(a, g - 1, of)) return false;
+  from = of.prefix;
+  if (of.prefix <= kv - len && lo >= of.lo && lo + len <= of.lo + of.len) return true;
+  set_status(a.b.status, DCP_EDEVICE);
+  return false;
 }
 
 #endif

@@ -171,6 +171,18 @@ AttendParams attend_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, cons
   return p;
 }
 
+bool shared_of(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_prefix_groups* g,
+               const dcp_attn_config* cfg, int32_t Hq, AttendParams& p) {
+  if (check_attention(pool, batch, cfg, Hq) != DCP_OK || !g) return false;
+  if (!g->start || !g->prefix_len || !aligned(g->start, 4) || !aligned(g->prefix_len, 4)) return false;
+  if (g->n_groups < 1 || g->n_groups > batch->n_seqs || g->max_q < 1 || g->max_q > batch->total_q || g->max_prefix < 0)
+    return false;
+  if ((int64_t)g->max_q * Hq > kMaxKv) return false;
+  p = attend_of(pool, batch, cfg, Hq);
+  p.groups = Groups{g->n_groups, g->max_q, g->start, g->prefix_len};
+  return true;
+}
+
 dcp_status check_pages(const dcp_page_pool* p) {
   if (!p || !p->k || !p->v || !p->status || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->status, 4))
     return DCP_EINVAL;
@@ -340,6 +352,28 @@ dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* bat
                                    : launch_attend_tiles(p, batch->max_kv, ws, (cudaStream_t)stream));
 }
 
+size_t dcp_shared_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch,
+                                           const dcp_prefix_groups* groups, const dcp_attn_config* cfg, int32_t Hq) {
+  AttendParams p;
+  if (!shared_of(pool, batch, groups, cfg, Hq, p)) return 0;
+  return kScratch + (shared_bytes(p, batch->max_kv, groups->max_prefix) + 255) / 256 * 256;
+}
+
+dcp_status dcp_shared_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_prefix_groups* groups,
+                                const dcp_attn_config* cfg, const void* q, int64_t q_stride, int32_t Hq, void* out,
+                                float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!ws_ok(ws, ws_bytes, dcp_shared_attention_workspace_size(pool, batch, groups, cfg, Hq))) return DCP_EINVAL;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DCP_EINVAL;
+  if (!token_stride_ok(q_stride, Hq, pool->D, elem_size(pool->dtype))) return DCP_EINVAL;
+  AttendParams p;
+  shared_of(pool, batch, groups, cfg, Hq, p);
+  p.q = (const char*)q;
+  p.out = (char*)out;
+  p.lse = lse;
+  p.q_stride = q_stride;
+  return cuda_ok(launch_shared(p, batch->max_kv, groups->max_prefix, ws, (cudaStream_t)stream));
+}
+
 size_t dcp_pages_workspace_size(const dcp_page_pool* pool, int32_t n_rows, int32_t stride) {
   if (check_pages(pool) != DCP_OK || !rows_ok(n_rows, stride)) return 0;
   // the list of moves and the fresh blocks of a fork, or the list of moves and the map of a packing
@@ -387,6 +421,7 @@ uint32_t dcp_abi_norm_struct_size(int32_t which) {
   switch (which) {
     case 0: return sizeof(dcp_rope_axes);
     case 1: return sizeof(dcp_norm_config);
+    case 2: return sizeof(dcp_prefix_groups);
     default: return 0;
   }
 }

@@ -510,6 +510,32 @@ dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* bat
                                const void* q_dev, int64_t q_stride, int32_t Hq, void* out_dev, float* lse_dev,
                                void* workspace_dev, size_t ws_bytes, void* stream);
 
+/* Attention of sequences that share their first positions (branches that dcp_pages_fork made of one session): group g is
+ * the sequences start[g] .. start[g+1] - 1, which hold the same keys and values in their first prefix_len[g] positions.
+ * Results are those of dcp_paged_attention; a prefix is read once for all of its group, through the table row of any of
+ * them (so it is enough that their pages hold the same).  A prefix lies before the new tokens: prefix_len <= kv_len - q_len of each sequence with new tokens.  Sequences
+ * before start[0] or from start[n_groups] on share nothing.
+ * Groups are worked on together where that pays: not under a window, nor where a sequence has many rows of its own (more
+ * than 64 of a KV head, 128 in fp32). */
+typedef struct dcp_prefix_groups {
+  int32_t n_groups;            /* 1 .. n_seqs */
+  int32_t max_q;               /* no group has more new tokens, its sequences together */
+  int64_t max_prefix;          /* a bound of the longest prefix, for dividing the work: larger ones still work */
+  const int32_t* start;        /* device [n_groups + 1] */
+  const int32_t* prefix_len;   /* device [n_groups] */
+} dcp_prefix_groups;
+
+/* As dcp_attention_workspace_size; also by the sizes in groups. */
+size_t dcp_shared_attention_workspace_size(const dcp_kv_pool* pool, const dcp_seq_batch* batch,
+                                           const dcp_prefix_groups* groups, const dcp_attn_config* cfg, int32_t Hq);
+
+/* Arguments and errors as dcp_paged_attention's; DCP_EDEVICE also for a group whose start decreases or leaves
+ * [0, n_seqs], that has more than max_q new tokens or whose prefix leaves its sequences' table rows or reaches past their
+ * kv_len - q_len.  One or two launches. */
+dcp_status dcp_shared_attention(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_prefix_groups* groups,
+                                const dcp_attn_config* cfg, const void* q_dev, int64_t q_stride, int32_t Hq,
+                                void* out_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes, void* stream);
+
 /* Pages of every layer's pool, handled whole: k and v are [L][n_blocks][page], page_bytes = H * block_size * D *
  * element size (either layout of dcp_paged_cache).  ref[b] counts the table entries that name block b (and any other
  * holder); a block with ref 0 is free.  Entries < 0 of a table row are empty.  Table rows hold `stride` entries. */
@@ -571,7 +597,7 @@ dcp_status dcp_pages_compact(const dcp_page_pool* pool, const int32_t* tables_de
  * dcp_rope_plan, dcp_attn_config, dcp_page_pool (0 past the last). */
 uint32_t dcp_abi_serving_struct_size(int32_t which);
 
-/* The same for dcp_rope_axes, dcp_norm_config (0 past the last). */
+/* The same for dcp_rope_axes, dcp_norm_config, dcp_prefix_groups (0 past the last). */
 uint32_t dcp_abi_norm_struct_size(int32_t which);
 
 /* Device addresses inside a prune-step workspace: l (fp32 [C]), the mask (uint8 [C]) and the index list

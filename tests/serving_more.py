@@ -91,3 +91,43 @@ def check_attention_sink(cache, q, out, lse, scale, causal, window, sink, kv_of=
                 empty = l == -math.inf
                 assert torch.equal(lse[r, h] == -math.inf, empty), (i, h)
                 assert ((lse[r, h].double() - l).abs()[~empty] <= tol_l[~empty]).all(), (i, h)
+
+
+# ------------------------------------------------------------------------------------------ shared prefixes
+class Branches(Cache):
+    """Pages of sequences in groups: [(prefix, [(new tokens, positions behind the prefix, new tokens among them), ...]),
+    ...]; `before` and `after` further sequences that belong to no group.  A branch names its group's full pages and holds
+    a copy of the prefix's last, partial one."""
+
+    def __init__(self, dtype, layout, h, d, bs, groups, before=(), after=(), seed=0):
+        self.prefix = [p for p, _ in groups]
+        seqs = [(q, n) for q, n in before]
+        self.group_at = [len(seqs)]
+        for p, members in groups:
+            seqs += [(q, p + n) for q, n in members]
+            self.group_at.append(len(seqs))
+        seqs += list(after)
+        super().__init__(dtype, layout, h, d, bs, [q for q, _ in seqs], [n for _, n in seqs], seed)
+        for g, p in enumerate(self.prefix):
+            for s in range(self.group_at[g] + 1, self.group_at[g + 1]):
+                first = self.group_at[g]
+                self.keys[s][:p], self.values[s][:p] = self.keys[first][:p], self.values[first][:p]
+                self.table[s, :p // bs] = self.table[first, :p // bs]
+        self.tables = torch.from_numpy(self.table).cuda()
+        self.start_dev, self.prefix_dev = ints(self.group_at), ints(self.prefix)
+
+    def groups(self, **over):
+        kw = dict(max_prefix=max(self.prefix), max_q=max(
+            1, *(self.start[b] - self.start[a] for a, b in zip(self.group_at, self.group_at[1:]))))
+        kw.update(over)
+        return dcp.PrefixGroups(self.start_dev, self.prefix_dev, **kw)
+
+    def attend(self, q, causal=True, window=-1, sink=0, scale=None, batch=None, groups=None):
+        out = torch.full_like(q, math.nan, memory_format=torch.contiguous_format)
+        lse = torch.full(q.shape[:2], math.nan, device="cuda")
+        cfg, pool = dcp.AttnConfig(scale, causal, window, sink), self.pool()
+        batch, groups = batch or self.batch(), groups or self.groups()
+        ws = dcp.new_workspace(dcp.dcp_shared_attention_workspace_size(pool, batch, groups, cfg, q.shape[1]))
+        for _ in range(2):  # the workspace is left ready for the next call
+            dcp.dcp_shared_attention(pool, batch, groups, cfg, q, out, lse, ws)
+        return out, lse
