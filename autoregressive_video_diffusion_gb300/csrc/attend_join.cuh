@@ -101,13 +101,95 @@ __host__ __device__ constexpr int64_t join_scratch(int rows, int splits) {
   return (int64_t)rows * (2 * splits + 1) * 4;
 }
 
+// The parts of a row's own keys: the first is at `part0`, the others from `part1` on, `step` floats apart.
+struct OwnParts {
+  const float* part0;
+  const float* part1;
+  int64_t step;
+  int width;
+  __device__ __forceinline__ const float* part(int k) const { return k ? part1 + (k - 1) * step : part0; }
+  __device__ __forceinline__ const float* row(int k, int r) const { return part(k) + (int64_t)r * width; }
+  __device__ __forceinline__ const float* chunk(int k, int c) const { return part(k) + c * 4; }
+};
+
+// join_rows once the parts are where `get` reads them; `weight` is its scratch.
+template <typename T, typename Parts, typename Get>
+__device__ __forceinline__ void join_fetched(const AttendParams& a, const Parts& parts, int splits, int rows, int row0,
+                                             int lo, int kh, float* weight, Get get) {
+  const int D = a.pool.D, quads = D / 4;
+  float* const sum = weight + rows * splits;
+  float* const inv = sum + rows * splits;
+  for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
+    const int r = u / splits;
+    const float2 ml = get(reinterpret_cast<const float2*>(parts.row(u - r * splits, r)));
+    weight[u] = ml.x;
+    sum[u] = ml.y;
+  }
+  __syncthreads();
+  // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
+  for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+    const int lane = threadIdx.x & 31;
+    float* const w = weight + r * splits;
+    const float* const ls = sum + r * splits;
+    float top = -INFINITY, l = 0.f;
+    bool tiny = false;
+    for (int k = lane; k < splits; k += 32)
+      if (ls[k] != 0.f) top = fmaxf(top, w[k]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    for (int k = lane; k < splits; k += 32) {
+      const float wk = ls[k] == 0.f ? 0.f : exp2_fast((w[k] - top) * a.scale_log2);
+      w[k] = wk;
+      if (wk != 0.f) l += wk * ls[k];
+      tiny |= wk == 0.f && ls[k] != 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    tiny = __any_sync(~0u, tiny);
+    if (lane == 0) {
+      inv[r] = l != 0.f ? (tiny ? -1.f / l : 1.f / l) : 0.f;  // below 0: see below
+      const int R = row0 + r, tok = R / a.G;
+      if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(a, top, l);
+    }
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
+    const int r = u / quads, d = (u - r * quads) * 4;
+    const float* w = weight + r * splits;
+    float o[4] = {};
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) {
+      const float4 x = get(reinterpret_cast<const float4*>(parts.row(k, r) + kPartHead + d));
+      const float wk = w[k];
+      if (wk != 0.f) o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;
+    }
+    if (inv[r] < 0.f) {  // a part whose weight is too small for fp32: an infinity or NaN in it is the row's all the same
+      for (int k = 0; k < splits; ++k) {
+        if (w[k] != 0.f || sum[r * splits + k] == 0.f) continue;
+        const float4 x = get(reinterpret_cast<const float4*>(parts.row(k, r) + kPartHead + d));
+        if (!isfinite(x.x)) o[0] += x.x;
+        if (!isfinite(x.y)) o[1] += x.y;
+        if (!isfinite(x.z)) o[2] += x.z;
+        if (!isfinite(x.w)) o[3] += x.w;
+      }
+    }
+    const int R = row0 + r, tok = R / a.G;
+    const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G);
+    const float n = fabsf(inv[r]);
+    if (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) =
+          make_uint2(pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n));
+    else
+      *reinterpret_cast<float4*>(a.out + (row * D + d) * 4) = make_float4(o[0] * n, o[1] * n, o[2] * n, o[3] * n);
+  }
+}
+
 template <typename T, typename Parts>
 __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& parts, int splits, int rows, int row0,
                                           int lo, int kh, uint8_t* scratch, int64_t room) {
-  const int D = a.pool.D, quads = D / 4, width = kPartHead + D;
-  float* const weight = reinterpret_cast<float*>(scratch);  // [rows][splits]: the maximum, then the part's weight
-  float* const sum = weight + rows * splits;                // [rows][splits]
-  float* const inv = sum + rows * splits;                   // [rows]
+  const int width = kPartHead + a.pool.D;
+  // [rows][splits] the parts' maxima, then their weights, [rows][splits] their sums, [rows] the row's factor
+  float* const weight = reinterpret_cast<float*>(scratch);
   const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
   __syncthreads();
   const bool local = used + (int64_t)rows * splits * width * 4 <= room;
@@ -123,79 +205,13 @@ __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& pa
     cp_async_wait<0>();
     __syncthreads();
   }
-  auto row_of = [&](int k, int r) { return local ? here + ((int64_t)k * rows + r) * width : parts.row(k, r); };
-  for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
-    const int r = u / splits;
-    const float2* at = reinterpret_cast<const float2*>(row_of(u - r * splits, r));
-    const float2 ml = local ? *at : __ldcg(at);
-    weight[u] = ml.x;
-    sum[u] = ml.y;
-  }
-  __syncthreads();
-  // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0).  -1 marks one whose weight is too
-  // small for fp32 though it saw keys: an infinity or NaN in it is the row's all the same.
-  for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
-    const int lane = threadIdx.x & 31;
-    float* const w = weight + r * splits;
-    const float* const ls = sum + r * splits;
-    float top = -INFINITY, l = 0.f;
-    for (int k = lane; k < splits; k += 32)
-      if (ls[k] != 0.f) top = fmaxf(top, w[k]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    for (int k = lane; k < splits; k += 32) {
-      const float wk = ls[k] == 0.f ? 0.f : exp2_fast((w[k] - top) * a.scale_log2);
-      w[k] = wk == 0.f && ls[k] != 0.f ? -1.f : wk;
-      if (wk != 0.f) l += wk * ls[k];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) {
-      inv[r] = l != 0.f ? 1.f / l : 0.f;
-      const int R = row0 + r, tok = R / a.G;
-      if (a.lse) a.lse[(int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G)] = row_lse(a, top, l);
-    }
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < rows * quads; u += blockDim.x) {
-    const int r = u / quads, d = (u - r * quads) * 4;
-    const float* w = weight + r * splits;
-    float o[4] = {};
-#pragma unroll 8
-    for (int k = 0; k < splits; ++k) {
-      const float4* from = reinterpret_cast<const float4*>(row_of(k, r) + kPartHead + d);
-      const float4 x = local ? *from : __ldcg(from);
-      const float wk = w[k];
-      if (wk < 0.f) {
-        const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!isfinite(y[e])) o[e] += y[e];
-      } else if (wk != 0.f) {
-        o[0] += wk * x.x, o[1] += wk * x.y, o[2] += wk * x.z, o[3] += wk * x.w;
-      }
-    }
-    const int R = row0 + r, tok = R / a.G;
-    const int64_t row = (int64_t)(lo + tok) * a.Hq + kh * a.G + (R - tok * a.G);
-    const float n = inv[r];
-    if (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) =
-          make_uint2(pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n));
-    else
-      *reinterpret_cast<float4*>(a.out + (row * D + d) * 4) = make_float4(o[0] * n, o[1] * n, o[2] * n, o[3] * n);
-  }
+  if (local)
+    join_fetched<T>(a, OwnParts{here, here + rows * width, (int64_t)rows * width, width}, splits, rows, row0, lo, kh, weight,
+                    [](const auto* x) { return *x; });
+  else
+    join_fetched<T>(a, parts, splits, rows, row0, lo, kh, weight, [](const auto* x) { return __ldcg(x); });
 }
 
-// The parts of a row's own keys: the first is at `part0`, the others from `part1` on, `step` floats apart.
-struct OwnParts {
-  const float* part0;
-  const float* part1;
-  int64_t step;
-  int width;
-  __device__ __forceinline__ const float* part(int k) const { return k ? part1 + (k - 1) * step : part0; }
-  __device__ __forceinline__ const float* row(int k, int r) const { return part(k) + (int64_t)r * width; }
-  __device__ __forceinline__ const float* chunk(int k, int c) const { return part(k) + c * 4; }
-};
 template <typename T>
 __device__ __forceinline__ void join_parts(const AttendParams& a, const float* part0, const float* part1, int64_t step,
                                            int splits, int rows, int row0, int lo, int kh, uint8_t* scratch,

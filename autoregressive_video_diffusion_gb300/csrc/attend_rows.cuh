@@ -33,12 +33,12 @@ constexpr int kLeastSlots = 32;    // and at least so many of a shared prefix
 
 struct RowParams {
   AttendParams a;
-  PrefixPlan pre;               // kPrefix, kRest
   int even;                     // 1: the CTAs share all items' key tiles evenly
   int splits, span, row_tiles;  // else keys of an item are cut into pieces of `span`
   uint32_t flip;                // sign bit of a scale below 0, put into q
   float* part;
   uint32_t* done;
+  PrefixPlan pre;               // kPrefix, kRest
 };
 
 namespace {

@@ -74,7 +74,7 @@ struct PrefixPlan {
 struct AttendParams {
   Pool pool;
   Batch b;
-  Groups groups;
+
   const char* q;
   char* out;
   float* lse;
@@ -83,6 +83,7 @@ struct AttendParams {
   int32_t causal, window;
   int32_t sink;                 // under a window: positions below it are seen by every row behind them
   float scale;
+  Groups groups;                // where sequences share prefixes
   float scale_log2;             // its size in units of log2 (exponentials are powers of two), in kernels; the sign is the
                                 // products' (a scale below 0 negates them: maxima then are of what is exponentiated)
 };
