@@ -96,7 +96,7 @@ __device__ __forceinline__ PrefixPiece prefix_piece(const AttendParams& a, const
 // join_scratch(rows, splits).  Everything is fetched at once where it fits the scratch (a loop over the parts in global
 // memory pays a memory latency every few of them: 5 us for 12 parts of 5 rows, 1 us this way), else the maxima and sums
 // first and the values with several loads in flight.
-// parts.row(k, r): part k's row r; parts.chunk(k, c): its 16-byte chunk c, counted from row 0 on.
+// parts.row(k, r): part k's row r.
 __host__ __device__ constexpr int64_t join_scratch(int rows, int splits) {
   return (int64_t)rows * (2 * splits + 1) * 4;
 }
@@ -109,7 +109,7 @@ struct OwnParts {
   int width;
   __device__ __forceinline__ const float* part(int k) const { return k ? part1 + (k - 1) * step : part0; }
   __device__ __forceinline__ const float* row(int k, int r) const { return part(k) + (int64_t)r * width; }
-  __device__ __forceinline__ const float* chunk(int k, int c) const { return part(k) + c * 4; }
+  static constexpr bool kByRow = false;  // a part's rows lie one behind the other
 };
 
 // join_rows once the parts are where `get` reads them; `weight` is its scratch.
@@ -195,11 +195,19 @@ __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& pa
   const bool local = used + (int64_t)rows * splits * width * 4 <= room;
   const float* const here = reinterpret_cast<const float*>(scratch + used);  // [split][row][width]
   if (local) {
-    const int chunks = rows * width / 4;
     const uint32_t to = smem_u32(scratch + used);
-    for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
-      const int k = u / chunks;
-      cp_async16(to + u * 16, parts.chunk(k, u - k * chunks));
+    if constexpr (Parts::kByRow) {  // a warp a row
+      for (int u = threadIdx.x >> 5; u < splits * rows; u += blockDim.x >> 5) {
+        const int k = u / rows;
+        const float* from = parts.row(k, u - k * rows);
+        for (int c = threadIdx.x & 31; c < width / 4; c += 32) cp_async16(to + (u * (width / 4) + c) * 16, from + c * 4);
+      }
+    } else {
+      const int chunks = rows * width / 4;
+      for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
+        const int k = u / chunks;
+        cp_async16(to + u * 16, parts.part(k) + (u - k * chunks) * 4);
+      }
     }
     cp_async_commit();
     cp_async_wait<0>();
@@ -229,11 +237,7 @@ struct AllParts {
     const int R = row0 + r, tile = R / pre.rows;
     return prefix_part(pre, own.width - kPartHead, first + k - n, kh, tile, R - tile * pre.rows);
   }
-  __device__ __forceinline__ const float* chunk(int k, int c) const {
-    if (k < n) return own.chunk(k, c);
-    const int quads = own.width / 4, r = c / quads;
-    return row(k, r) + (c - r * quads) * 4;
-  }
+  static constexpr bool kByRow = true;
 };
 template <typename T>
 __device__ __forceinline__ void join_with_prefix(const AttendParams& a, const PrefixPlan& pre, const GroupRows& of,

@@ -522,6 +522,16 @@ __device__ __forceinline__ Seen seen_range(const AttendParams& a, int from, int 
   return k;
 }
 
+// What a sequence holds behind its group's prefix (kRest); without slots it is worked on alone, its group only checked.
+__device__ __forceinline__ bool rest_of(const RowParams& p, int s, int lo, int len, int kv, GroupRows& of, int& from) {
+  const bool sound = group_of(p.a, s, lo, len, kv, of, from);
+  if (p.pre.slots == 0) {
+    from = 0;
+    of.g = -1;
+  }
+  return sound;
+}
+
 // An item is a tile of rows of one sequence and KV head.
 template <typename T, int DP, int MW, int FORM>
 __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kCtas)
@@ -539,6 +549,10 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
     if (p.even) {
       // Every CTA takes the same number of consecutive key tiles of all items together: the sums of the items' tiles,
       // then the pieces of the items that lie in the CTA's share.  At most its first and its last piece are parts.
+      // Where items are joined with a prefix's parts, an item counts kBegin tiles more, for its look-ups and its join (of
+      // single tiles a CTA had up to 13 items, and 32 branches of 20 .. 700 positions behind their prefix took 103 us);
+      // a share that would end among these leaves the item to the next CTA.
+      constexpr int kBegin = FORM == kRest ? 10 : 0;
       __shared__ int64_t s_first[kEvenItems + 1];  // tiles before an item
       __shared__ int64_t s_warp[R::kWarps];
       const int items = a.b.n_seqs * a.pool.H, each = (items + R::kThreads - 1) / R::kThreads;
@@ -551,9 +565,10 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
         kv = (int)kv64;
         int from = 0;
         if constexpr (FORM == kRest)
-          if (!group_of(a, i / a.pool.H, lo, len, kv, of, from)) return 0;
+          if (!rest_of(p, i / a.pool.H, lo, len, kv, of, from)) return 0;
         seen = seen_range<FORM>(a, from, kv, len, 0, len * a.G);
-        return max(1, (seen.end - seen.begin + R::kKeys - 1) / R::kKeys);  // rows that see nothing have their result too
+        // rows that see nothing have their result too
+        return max(1, (seen.end - seen.begin + R::kKeys - 1) / R::kKeys) + kBegin;
       };
       int lo, len, kv;
       Seen seen;
@@ -583,11 +598,22 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       // Two tiles a CTA at least, and no fewer CTAs than items (a piece costs as much to begin as several tiles).
       const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, max((total + 1) / 2, min((int64_t)items, total))));
       if (blockIdx.x >= ctas) return;
-      int64_t at = blockIdx.x * total / ctas;
-      const int64_t to = (blockIdx.x + 1) * total / ctas;
-      int item = 0;
-      for (int step = kEvenItems; step; step >>= 1)  // the last item that begins at or before `at`
-        if (item + step < items && s_first[item + step] <= at) item += step;
+      auto item_at = [&](int64_t x) {  // the last item that begins at or before x
+        int item = 0;
+        for (int step = kEvenItems; step; step >>= 1)
+          if (item + step < items && s_first[item + step] <= x) item += step;
+        return item;
+      };
+      auto share = [&](int64_t c) {  // where CTA c's share begins
+        const int64_t x = c * total / ctas;
+        if constexpr (kBegin == 0) return x;
+        if (c == ctas) return total;
+        const int64_t f0 = s_first[item_at(x)];
+        return x - f0 <= kBegin ? f0 : x;
+      };
+      int64_t at = share(blockIdx.x);
+      const int64_t to = share(blockIdx.x + 1);
+      int item = item_at(at);
       for (; at < to; ++item) {
         const int64_t f0 = s_first[item], f1 = s_first[item + 1];
         if (f1 <= at) continue;
@@ -596,13 +622,13 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
         const bool opens = at == f0, closes = stop == f1;
         const int s = item / a.pool.H, kh = item % a.pool.H, rows = len * a.G;
         Seen piece = seen;
-        piece.begin += (int)(at - f0) * R::kKeys;
-        piece.end = min(seen.end, seen.begin + (int)(stop - f0) * R::kKeys);
+        if (!opens) piece.begin += (int)(at - f0 - kBegin) * R::kKeys;
+        if (!closes) piece.end = seen.begin + (int)(stop - f0 - kBegin) * R::kKeys;
         const int64_t slot = (int64_t)16 * width;  // parts of a CTA: of an item it goes on with, of one it begins
-        float* const part = FORM != kRest && opens && closes ? nullptr : p.part + (2 * (int64_t)blockIdx.x + opens) * slot;
+        float* const part = opens && closes && !(FORM == kRest && p.pre.slots) ? nullptr : p.part + (2 * (int64_t)blockIdx.x + opens) * slot;
         attend_piece<T, DP, 1, FORM>(p, smem, s_off, s, kh, lo, len, kv, 0, rows, piece, part);
         if (part) {
-          const int64_t c0 = ((f0 + 1) * ctas - 1) / total, c1 = (f1 * ctas - 1) / total;
+          const int64_t c0 = ((f0 + kBegin + 1) * ctas - 1) / total, c1 = (f1 * ctas - 1) / total;
           const int n = (int)(c1 - c0 + 1);
           float* const part0 = opens ? part : p.part + (2 * c0 + 1) * slot;
           if (FORM == kRest && n == 1)
@@ -656,7 +682,7 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
   GroupRows of{};
   int from = 0;
   if constexpr (FORM == kRest)
-    if (!group_of(a, s, lo, len, kv, of, from)) return;
+    if (!rest_of(p, s, lo, len, kv, of, from)) return;
   Seen seen = seen_range<FORM>(a, from, kv, len, row0, rows);
   if (p.splits > 1) {
     // as even pieces of whole tiles as the splits allow (a longer sequence than max_kv has longer pieces)
@@ -667,7 +693,7 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
   }
   const int64_t item = ((int64_t)s * a.pool.H + kh) * p.row_tiles + tile;
   float* const parts =
-      FORM == kRest || p.splits > 1 ? part_of(p.part, item, p.splits, 0, 16 * MW, D, 0) : nullptr;
+      p.splits > 1 || (FORM == kRest && p.pre.slots) ? part_of(p.part, item, p.splits, 0, 16 * MW, D, 0) : nullptr;
   const int64_t step = (int64_t)16 * MW * width;
   attend_piece<T, DP, MW, FORM>(p, smem, s_off, s, kh, lo, len, kv, row0, rows, seen,
                                 parts ? parts + split * step : nullptr);

@@ -782,10 +782,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!mine) continue;
       if (parted) {
 #pragma unroll
-        for (int u = 0; u < 32; u += 2)
+        for (int u = 0; u < 32; u += 4)
           if (d0 + u < D)
-            *reinterpret_cast<float2*>(part + kPartHead + d0 + u) =
-                make_float2(__uint_as_float(o[u]), __uint_as_float(o[u + 1]));
+            *reinterpret_cast<float4*>(part + kPartHead + d0 + u) =
+                make_float4(__uint_as_float(o[u]), __uint_as_float(o[u + 1]), __uint_as_float(o[u + 2]),
+                            __uint_as_float(o[u + 3]));
       } else {
 #pragma unroll
         for (int u = 0; u < 32; u += 8) {

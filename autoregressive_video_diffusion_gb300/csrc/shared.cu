@@ -19,8 +19,15 @@ namespace {
 
 // Sequences of many rows fill the products by themselves: reading the prefix again from the L2 costs them nothing.  Under a
 // window the rows see little of it.
-bool pays(const AttendParams& a) {
+bool few_rows(const AttendParams& a) {
   return a.window < 0 && (int64_t)a.b.max_q * a.G <= (a.pool.dtype == DCP_BF16 ? 64 : 128);
+}
+
+// What is not read again has to be worth a second launch and the exchange of parts.
+constexpr double kWorth = 60e6;  // bytes
+bool pays(const AttendParams& a, int64_t max_prefix) {
+  const double row = 2.0 * a.pool.H * a.pool.D * (a.pool.dtype == DCP_BF16 ? 2 : 4);
+  return few_rows(a) && (double)(a.b.n_seqs - a.groups.n) * max_prefix * row >= kWorth;
 }
 
 struct SharedPlan {
@@ -80,13 +87,14 @@ __global__ void check_kernel(const __grid_constant__ AttendParams a) {
 }  // namespace
 
 size_t shared_bytes(const AttendParams& a, int64_t max_kv, int64_t max_prefix) {
-  if (!pays(a)) return attend_by_rows(a) ? plan_rows(a, max_kv).bytes : plan_tiles(a, max_kv).bytes;
+  if (!pays(a, max_prefix)) return attend_by_rows(a) ? plan_rows(a, max_kv).bytes : plan_tiles(a, max_kv).bytes;
   const SharedPlan t = plan_shared(a, max_kv, max_prefix);
   return up(t.rest_bytes) + up(t.part_bytes) + up((size_t)a.groups.n * sizeof(int2));
 }
 
 cudaError_t launch_shared(const AttendParams& a, int64_t max_kv, int64_t max_prefix, void* ws, cudaStream_t s) {
-  if (!pays(a)) {
+  if (!pays(a, max_prefix)) {
+    if (few_rows(a)) return launch_rest_rows(a, plan_rows(a, max_kv), PrefixPlan{}, ws, s);
     const cudaError_t e = launch_behind(check_kernel, dim3(8), 256, 0, s, a);
     if (e != cudaSuccess) return e;
     return attend_by_rows(a) ? launch_attend_rows(a, max_kv, ws, s) : launch_attend_tiles(a, max_kv, ws, s);
