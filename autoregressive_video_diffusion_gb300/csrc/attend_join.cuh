@@ -112,13 +112,10 @@ struct OwnParts {
   static constexpr bool kByRow = false;  // a part's rows lie one behind the other
 };
 
-// join_rows once the parts are where `get` reads them; `weight` is its scratch.
-template <typename T, typename Parts, typename Get>
-__device__ __forceinline__ void join_fetched(const AttendParams& a, const Parts& parts, int splits, int rows, int row0,
-                                             int lo, int kh, float* weight, Get get) {
-  const int D = a.pool.D, quads = D / 4;
+// The parts' maxima and sums into join_rows' scratch.
+template <typename Parts, typename Get>
+__device__ __forceinline__ void join_heads(const Parts& parts, int splits, int rows, float* weight, Get get) {
   float* const sum = weight + rows * splits;
-  float* const inv = sum + rows * splits;
   for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
     const int r = u / splits;
     const float2 ml = get(reinterpret_cast<const float2*>(parts.row(u - r * splits, r)));
@@ -126,6 +123,15 @@ __device__ __forceinline__ void join_fetched(const AttendParams& a, const Parts&
     sum[u] = ml.y;
   }
   __syncthreads();
+}
+
+// join_rows once the parts' values are where `get` reads them; `weight` is its scratch, with their maxima and sums.
+template <typename T, typename Parts, typename Get>
+__device__ __forceinline__ void join_values(const AttendParams& a, const Parts& parts, int splits, int rows, int row0,
+                                            int lo, int kh, float* weight, Get get) {
+  const int D = a.pool.D, quads = D / 4;
+  float* const sum = weight + rows * splits;
+  float* const inv = sum + rows * splits;
   // a warp a row: the parts' weights (a split that saw no key of the row has the sum 0)
   for (int r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
     const int lane = threadIdx.x & 31;
@@ -192,32 +198,52 @@ __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& pa
   float* const weight = reinterpret_cast<float*>(scratch);
   const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
   __syncthreads();
-  const bool local = used + (int64_t)rows * splits * width * 4 <= room;
-  const float* const here = reinterpret_cast<const float*>(scratch + used);  // [split][row][width]
-  if (local) {
-    const uint32_t to = smem_u32(scratch + used);
-    if constexpr (Parts::kByRow) {  // a warp a row
-      for (int u = threadIdx.x >> 5; u < splits * rows; u += blockDim.x >> 5) {
-        const int k = u / rows;
-        const float* from = parts.row(k, u - k * rows);
-        for (int c = threadIdx.x & 31; c < width / 4; c += 32) cp_async16(to + (u * (width / 4) + c) * 16, from + c * 4);
+  const OwnParts here{reinterpret_cast<const float*>(scratch + used),
+                      reinterpret_cast<const float*>(scratch + used) + rows * width, (int64_t)rows * width, width};
+  const uint32_t to = smem_u32(scratch + used);
+  auto near = [](const auto* x) { return *x; };
+  auto far = [](const auto* x) { return __ldcg(x); };
+  const int64_t all = used + (int64_t)rows * splits * width * 4;
+  if constexpr (Parts::kByRow) {
+    // The rows lie apart: their places are found once, a thread a row, then a warp fetches a row (each of its threads
+    // finding it anew made a join of 5 rows of 21 parts take 13 us).
+    if (all + 8 * rows * splits <= room) {  // (a row is a multiple of 16 bytes)
+      const float** const place = reinterpret_cast<const float**>(scratch + all);
+      float* const sum = weight + rows * splits;
+      for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
+        const int k = u / rows, r = u - k * rows;
+        const float* const at = parts.row(k, r);
+        place[u] = at + kPartHead;
+        const float2 ml = far(reinterpret_cast<const float2*>(at));
+        weight[r * splits + k] = ml.x;
+        sum[r * splits + k] = ml.y;
       }
-    } else {
-      const int chunks = rows * width / 4;
-      for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
-        const int k = u / chunks;
-        cp_async16(to + u * 16, parts.part(k) + (u - k * chunks) * 4);
-      }
+      __syncthreads();
+      const int c = threadIdx.x & 31;
+#pragma unroll 4
+      for (int u = threadIdx.x >> 5; u < splits * rows; u += blockDim.x >> 5)
+        if (c < a.pool.D / 4) cp_async16(to + (u * width + kPartHead + c * 4) * 4, place[u] + c * 4);
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+      join_values<T>(a, here, splits, rows, row0, lo, kh, weight, near);
+      return;
+    }
+  } else if (all <= room) {
+    const int chunks = rows * width / 4;
+    for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
+      const int k = u / chunks;
+      cp_async16(to + u * 16, parts.part(k) + (u - k * chunks) * 4);
     }
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
+    join_heads(here, splits, rows, weight, near);
+    join_values<T>(a, here, splits, rows, row0, lo, kh, weight, near);
+    return;
   }
-  if (local)
-    join_fetched<T>(a, OwnParts{here, here + rows * width, (int64_t)rows * width, width}, splits, rows, row0, lo, kh, weight,
-                    [](const auto* x) { return *x; });
-  else
-    join_fetched<T>(a, parts, splits, rows, row0, lo, kh, weight, [](const auto* x) { return __ldcg(x); });
+  join_heads(parts, splits, rows, weight, far);
+  join_values<T>(a, parts, splits, rows, row0, lo, kh, weight, far);
 }
 
 template <typename T>

@@ -171,19 +171,7 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
     }
     cp_async_commit();
   };
-  {
-    int64_t f[R::kStages];
-#pragma unroll
-    for (int t = 0; t < R::kStages; ++t) f[t] = find(t);
-    if (threadIdx.x < R::kKeys)
-#pragma unroll
-      for (int t = 0; t < R::kStages; ++t) s_off[t][threadIdx.x] = f[t];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < R::kStages - 1; ++t) fetch(t);
-
-  // ---- q: bf16 in registers as the products want it, fp32 in shared memory
+  // ---- q: bf16 in registers as the products want it, on its way while the keys are looked up; fp32 in shared memory
   const int first = MW == 1 ? 0 : warp * 16;  // the warp's first row of the item
   uint32_t qa[R::kHalf ? DP / 16 : 1][4];
   auto q_row = [&](int r) {
@@ -204,7 +192,20 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
         qa[k][e] = q && d < D ? *reinterpret_cast<const uint32_t*>(q + d * 2) ^ flip : 0;
       }
     }
-  } else {
+  }
+  {
+    int64_t f[R::kStages];
+#pragma unroll
+    for (int t = 0; t < R::kStages; ++t) f[t] = find(t);
+    if (threadIdx.x < R::kKeys)
+#pragma unroll
+      for (int t = 0; t < R::kStages; ++t) s_off[t][threadIdx.x] = f[t];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < R::kStages - 1; ++t) fetch(t);
+
+  if constexpr (!R::kHalf) {
     uint8_t* qs = smem + R::kBuffers;
     for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += R::kThreads) {
       const int r = u / (DP / 4), d = u % (DP / 4) * 4;

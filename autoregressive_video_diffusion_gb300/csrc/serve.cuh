@@ -115,6 +115,7 @@ struct RowPlan {
 };
 bool attend_by_rows(const AttendParams& p);
 RowPlan plan_rows(const AttendParams& p, int64_t max_kv);
+RowPlan plan_rest(const AttendParams& p, int64_t max_kv);  // behind a shared prefix
 cudaError_t launch_attend_rows(const AttendParams& p, int64_t max_kv, void* ws, cudaStream_t s);
 cudaError_t launch_prefix_rows(const AttendParams& p, const PrefixPlan& pre, cudaStream_t s);
 cudaError_t launch_rest_rows(const AttendParams& p, const RowPlan& r, const PrefixPlan& pre, void* ws, cudaStream_t s);

@@ -47,7 +47,7 @@ SharedPlan plan_shared(const AttendParams& a, int64_t max_kv, int64_t max_prefix
   t.pre.rows = t.tiled ? 256 : rows <= 16 ? 16 : half ? 64 : 128;
   t.pre.tiles = (int)((rows + t.pre.rows - 1) / t.pre.rows);
   t.pre.heads = a.pool.H;
-  t.rest = plan_rows(a, std::max<int64_t>(max_kv - max_prefix, 1));
+  t.rest = plan_rest(a, std::max<int64_t>(max_kv - max_prefix, 1));
   t.rest_bytes = t.rest.bytes;
   if (!t.rest_bytes)  // items in one go leave a part too
     t.rest_bytes = (size_t)t.rest.tiles * a.pool.H * a.b.n_seqs * t.rest.rows * (kPartWidth + a.pool.D) * 4;
