@@ -219,10 +219,17 @@ __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& pa
         sum[r * splits + k] = ml.y;
       }
       __syncthreads();
-      const int c = threadIdx.x & 31;
-#pragma unroll 4
-      for (int u = threadIdx.x >> 5; u < splits * rows; u += blockDim.x >> 5)
-        if (c < a.pool.D / 4) cp_async16(to + (u * width + kPartHead + c * 4) * 4, place[u] + c * 4);
+      const int c = threadIdx.x & 31, warps = blockDim.x >> 5;
+      for (int u0 = threadIdx.x >> 5; u0 < splits * rows; u0 += 8 * warps) {
+        const float* from[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) from[j] = place[min(u0 + j * warps, splits * rows - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int u = u0 + j * warps;
+          if (u < splits * rows && c < a.pool.D / 4) cp_async16(to + (u * width + kPartHead + c * 4) * 4, from[j] + c * 4);
+        }
+      }
       cp_async_commit();
       cp_async_wait<0>();
       __syncthreads();

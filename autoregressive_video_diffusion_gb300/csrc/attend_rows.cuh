@@ -143,15 +143,23 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
   const int n_tiles = (end - begin + R::kKeys - 1) / R::kKeys;
   const int32_t* table = a.b.tables + (int64_t)s * a.b.table_stride;
 
-  auto find = [&](int t) -> int64_t {
+  // A key's table entry is read a tile before its place is needed: nothing waits for the one that was asked for last.
+  struct Key {
+    int blk, row;  // row -1: no key
+  };
+  auto find = [&](int t) -> Key {
     const int x = begin + t * R::kKeys + threadIdx.x;
-    if (threadIdx.x >= R::kKeys || x >= end) return -1;
-    const int pos = keys.pos<FORM>(x), page = pos / bs, blk = table[page];
-    if (blk < 0 || blk >= a.pool.n_blocks) {
+    if (threadIdx.x >= R::kKeys || x >= end) return Key{0, -1};
+    const int pos = keys.pos<FORM>(x), page = pos / bs;
+    return Key{table[page], pos - page * bs};
+  };
+  auto place = [&](const Key& k) -> int64_t {
+    if (k.row < 0) return -1;
+    if (k.blk < 0 || k.blk >= a.pool.n_blocks) {
       set_status(a.b.status, DCP_EDEVICE);
       return -1;
     }
-    return blk * a.pool.s_block + kh * a.pool.s_head + (int64_t)(pos - page * bs) * a.pool.s_row;
+    return k.blk * a.pool.s_block + kh * a.pool.s_head + (int64_t)k.row * a.pool.s_row;
   };
   const uint32_t base = smem_u32(smem);
   const int chunks = D * (int)sizeof(T) / 16;
@@ -159,18 +167,27 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
   auto fetch = [&](int t) {
     if (t < n_tiles) {
       const uint32_t k_at = base + (t % R::kStages) * R::kStage, v_at = k_at + R::kKeys * R::kRow;
+      constexpr int kEach = R::kKeys * kChunks / R::kThreads, kAtOnce = kEach < 4 ? kEach : 4;
 #pragma unroll
-      for (int j = 0; j < R::kKeys * kChunks / R::kThreads; ++j) {
-        const int u = threadIdx.x + j * R::kThreads, row = u / kChunks, ch = u % kChunks;
-        const int64_t off = s_off[t & 3][row];
-        const bool real = off >= 0 && ch < chunks;
-        const int64_t at = real ? off * (int64_t)sizeof(T) + ch * 16 : 0;
-        copy16(k_at + row * R::kRow + ch * 16, a.pool.k + at, real);
-        copy16(v_at + row * R::kRow + ch * 16, a.pool.v + at, real);
+      for (int j0 = 0; j0 < kEach; j0 += kAtOnce) {  // (the copies are not reordered: their places first)
+        int64_t off[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) off[j] = s_off[t & 3][(threadIdx.x + (j0 + j) * R::kThreads) / kChunks];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int u = threadIdx.x + (j0 + j) * R::kThreads, row = u / kChunks, ch = u % kChunks;
+          const bool real = off[j] >= 0 && ch < chunks;
+          const int64_t at = real ? off[j] * (int64_t)sizeof(T) + ch * 16 : 0;
+          copy16(k_at + row * R::kRow + ch * 16, a.pool.k + at, real);
+          copy16(v_at + row * R::kRow + ch * 16, a.pool.v + at, real);
+        }
       }
     }
     cp_async_commit();
   };
+  Key f[R::kStages];
+#pragma unroll
+  for (int t = 0; t < R::kStages; ++t) f[t] = find(t);
   // ---- q: bf16 in registers as the products want it, on its way while the keys are looked up; fp32 in shared memory
   const int first = MW == 1 ? 0 : warp * 16;  // the warp's first row of the item
   uint32_t qa[R::kHalf ? DP / 16 : 1][4];
@@ -182,30 +199,30 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
   if constexpr (R::kHalf) {
     const char* q0 = first + g < rows ? q_row(first + g) : nullptr;
     const char* q1 = first + g + 8 < rows ? q_row(first + g + 8) : nullptr;
-    const uint32_t flip = p.flip | p.flip >> 16;
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const char* q = e & 1 ? q1 : q0;
         const int d = 16 * k + 2 * c + (e >> 1) * 8;
-        qa[k][e] = q && d < D ? *reinterpret_cast<const uint32_t*>(q + d * 2) ^ flip : 0;
+        qa[k][e] = q && d < D ? *reinterpret_cast<const uint32_t*>(q + d * 2) : 0;
       }
     }
   }
-  {
-    int64_t f[R::kStages];
+  if (threadIdx.x < R::kKeys)
 #pragma unroll
-    for (int t = 0; t < R::kStages; ++t) f[t] = find(t);
-    if (threadIdx.x < R::kKeys)
-#pragma unroll
-      for (int t = 0; t < R::kStages; ++t) s_off[t][threadIdx.x] = f[t];
-  }
+    for (int t = 0; t < R::kStages; ++t) s_off[t][threadIdx.x] = place(f[t]);
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < R::kStages - 1; ++t) fetch(t);
 
-  if constexpr (!R::kHalf) {
+  if constexpr (R::kHalf) {
+    const uint32_t flip = p.flip | p.flip >> 16;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qa[k][e] ^= flip;
+  } else {
     uint8_t* qs = smem + R::kBuffers;
     for (int u = threadIdx.x; u < 16 * MW * (DP / 4); u += R::kThreads) {
       const int r = u / (DP / 4), d = u % (DP / 4) * 4;
@@ -230,7 +247,7 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
   const bool idle = first >= rows;
 
   for (int t = 0; t < n_tiles; ++t) {
-    const int64_t ahead = t + R::kStages < n_tiles ? find(t + R::kStages) : -1;
+    const Key ahead = t + R::kStages < n_tiles ? find(t + R::kStages) : Key{0, -1};
     cp_async_wait<R::kStages - 2>();
     __syncthreads();
     fetch(t + R::kStages - 1);
@@ -443,7 +460,7 @@ __device__ __forceinline__ void attend_piece(const RowParams& p, uint8_t* smem,
         }
       }
     }
-    if (threadIdx.x < R::kKeys) s_off[(t + R::kStages) & 3][threadIdx.x] = ahead;
+    if (threadIdx.x < R::kKeys) s_off[(t + R::kStages) & 3][threadIdx.x] = place(ahead);
   }
   cp_async_wait<0>();
 #pragma unroll
