@@ -40,7 +40,7 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   // Items that may differ in length: two CTAs of an SM at a time, each with the same number of key tiles (48 sequences
   // of 200 .. 16000 positions: 324 us, against 354 in pieces of a fixed span; items alike are cut as well by a span,
   // without the sums: one token over 1531 positions 12.3 us, against 14.0).
-  r.even = (int64_t)a.b.max_q * a.G <= 16 && items <= kEvenItems && (a.b.n_seqs > 1 || a.b.kv_per_head) && !few;
+  r.even = (int64_t)a.b.max_q * a.G <= 16 && items <= (a.sink ? kEvenItemsSink : kEvenItems) && (a.b.n_seqs > 1 || a.b.kv_per_head) && !few;
   if (r.even) {
     r.splits = 2 * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
     r.span = 0;

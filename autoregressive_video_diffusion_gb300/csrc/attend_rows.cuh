@@ -26,7 +26,9 @@
 namespace dcp {
 
 constexpr int kMaxSplits = 64;
-constexpr int kEvenItems = 512;  // items whose tiles can be shared evenly
+constexpr int kEvenItems = 512;       // items whose tiles can be shared evenly,
+constexpr int kEvenItemsSink = 1024;  // and under a window whose first positions stay visible (768 items of 4200 keys at most:
+                                      // 251 us, against 256 in pieces of a fixed span)
 
 constexpr int kMaxSms = 160;       // the join's scratch holds a part of two CTAs on each,
 constexpr int kLeastSlots = 32;    // and at least so many of a shared prefix
@@ -571,7 +573,8 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       // single tiles a CTA had up to 13 items, and 32 branches of 20 .. 700 positions behind their prefix took 103 us);
       // a share that would end among these leaves the item to the next CTA.
       constexpr int kBegin = FORM == kRest ? 10 : 0;
-      __shared__ int64_t s_first[kEvenItems + 1];  // tiles before an item
+      constexpr int kItems = FORM == kSink ? kEvenItemsSink : kEvenItems;
+      __shared__ int64_t s_first[kItems + 1];  // tiles before an item
       __shared__ int64_t s_warp[R::kWarps];
       const int items = a.b.n_seqs * a.pool.H, each = (items + R::kThreads - 1) / R::kThreads;
       const int i0 = min(items, (int)threadIdx.x * each), i1 = min(items, i0 + each);
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
       if (blockIdx.x >= ctas) return;
       auto item_at = [&](int64_t x) {  // the last item that begins at or before x
         int item = 0;
-        for (int step = kEvenItems; step; step >>= 1)
+        for (int step = kItems; step; step >>= 1)
           if (item + step < items && s_first[item + step] <= x) item += step;
         return item;
       };

@@ -3,14 +3,22 @@
 //
 //   y = x / sqrt(mean x^2 + eps) * w,  then each pair (a, b) of axis a turns by position[a] * theta: one rounding at the end
 //
-// The mean goes over a head, or over all heads of a token (q and k apart).  A CTA takes a token: its loads are issued
-// first (they depend on nothing), under them it finds the token's place and builds its cos/sin.  A head lies in the
-// registers of a power of two of neighbouring lanes, a 16-byte vector each (two where the pairs are a whole number of
-// vectors apart), so a head's sum is a few shuffles and a token's one barrier; the values are still in registers when
-// the sum is known, which makes it one pass (tokens of more than 128 heads of 128 are read again behind the first ones).
+// The mean goes over a head, or over all heads of a token (q and k apart).  A CTA takes a few tokens at a time: their rows
+// travel to shared memory while it looks up their places and builds their cos/sin, the sums are taken from there, and what
+// is written is computed from there again, so that the data cross HBM once and nothing has to stay in registers in
+// between.  A head is a power of two of neighbouring lanes, two 16-byte vectors each, so its sum is a few shuffles; a warp
+// takes a few heads of one kind at a time.  A token that does not fit shared memory goes through it in pieces, twice where
+// the mean is the token's.
 //
 // Squares leave fp32 for values past 2^60 or below 2^-50 with an eps as small: such a sum is taken again of values scaled
-// by a power of two, which every norm of the row shares, so that any finite values give what the formula says.
+// by a power of two, which every norm of the row shares, so that any values give what the formula says.
+//
+// The bytes would take 57 us for the first case below; what bounds it is the instructions around the arithmetic (66 million
+// warp instructions, issued at two thirds of the schedulers' rate).  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in
+// bf16, means of tokens, three axes, fp32 weights of each head 90 us (4.3 TB/s); 5875 tokens of 20 + 4 + 4 fp32 heads of 96
+// 44 us; 32 tokens 7.8 us.  Steps, us of these two: a token a CTA, its heads in registers 135 / 51; persistent CTAs with the
+// next token's loads in flight 114 / 40; rows through shared memory 116 / 51; two vectors a lane 101 / 52; the head's size a
+// constant 91 / 54; several small tokens at a time 90 / 44.
 #include <algorithm>
 
 #include "append.cuh"
@@ -19,73 +27,27 @@ namespace dcp {
 
 namespace {
 
-constexpr int kNormThreads = 512;     // of a CTA at most
-constexpr int kNormResident = 1024;   // of an SM, by registers
-constexpr int kUnits = 4;             // vectors of q and k a thread has in flight
-constexpr int kBlock = 16;    // tokens whose places a CTA looks up at a time
+constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormCtas = 4;             // of an SM, by registers
+constexpr int kSharedOfSm = 228 << 10;  // and by shared memory, of which a CTA takes some for itself
+constexpr int kSharedOfCta = 3 << 10;
+constexpr int kBlock = 16;              // tokens whose places a CTA looks up at a time
+constexpr int kBlockBytes = 40 << 10;   // it takes as many of them at a time as have about this in rows
+constexpr int kMostBytes = 64 << 10;    // of a CTA's rows: a larger token goes through in pieces
 
-// The factors of a norm: y = (x * up) * r; up is 1 but for values that are taken scaled.
-struct Norm {
-  float up, r;
-};
 constexpr float kMostSum = 0x1p120f, kLeastMean = 0x1p-100f;
 
 // The scale at which a sum that left fp32's comfortable range is taken again, 1 where it did not.
 __device__ __forceinline__ float rescale(float sum, float inv, float eps) {
   return !(sum <= kMostSum) ? 0x1p-80f : fmaf(sum, inv, eps) < kLeastMean ? 0x1p100f : 1.f;
 }
-// The sum was taken of values times c.
-__device__ __forceinline__ Norm norm_of(float sum, float inv, float eps, float c) {
+// The factor of a norm, y = x * factor, from a sum that was taken of values times c.  (It is a number for a root mean square
+// of 2^-126 and more.)
+__device__ __forceinline__ float norm_of(float sum, float inv, float eps, float c) {
   const float m = fmaf(sum, inv, eps * c * c), r = rsqrtf(m);
   const float better = fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r);  // a step of Newton's: 2 ulp to half of one
-  return Norm{fmaxf(c, 1.f), (m > 0.f && m < INFINITY ? better : r) * fminf(c, 1.f)};
-}
-
-// A vector that is read once.
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 x;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(p));
-  return x;
-}
-
-// A vector's elements in pairs, and back.
-template <typename T, int N>
-__device__ __forceinline__ void pairs_of(const uint4& x, uint64_t (&y)[N / 2]) {
-  float f[N];
-  Elems<T>::get(x, f);
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) y[k] = pair(f[2 * k], f[2 * k + 1]);
-}
-template <typename T, int N>
-__device__ __forceinline__ uint4 vector_of(const uint64_t (&y)[N / 2]) {
-  float f[N];
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) unpair(y[k], f[2 * k], f[2 * k + 1]);
-  return Elems<T>::put(f);
-}
-
-// y times consecutive weights of a head, from element `at` on.
-template <int N>
-__device__ __forceinline__ void weigh(const NormParams& n, const char* weight, int at, uint64_t (&y)[N / 2]) {
-  if (!weight) return;
-  if (n.weight_bf16) {
-    uint32_t w[N / 2];
-    if constexpr (N == 8)
-      *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(weight + (int64_t)at * 2));
-    else
-      *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(weight + (int64_t)at * 2));
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) y[k] = mul2(y[k], pair(bf16lo(w[k]), bf16hi(w[k])));
-  } else {
-#pragma unroll
-    for (int k = 0; k < N / 2; k += 2) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(weight + ((int64_t)at + 2 * k) * 4));
-      y[k] = mul2(y[k], pair(w.x, w.y));
-      y[k + 1] = mul2(y[k + 1], pair(w.z, w.w));
-    }
-  }
+  return (m > 0.f && m < INFINITY ? better : r) * c;
 }
 
 // Where element d of a row of LENGTH lies in shared memory: quads of a vector's elements apart, those of neighbouring
@@ -95,74 +57,55 @@ __device__ __forceinline__ int place(int d) {
   return (d % N / 4 * (LENGTH / N) + d / N) * 4 + d % 4;
 }
 
-template <typename T, int PAIRS, bool TOKEN, bool WEIGHTS>
-__global__ void __launch_bounds__(kNormThreads, kNormResident / kNormThreads)
-    norm_kernel(const __grid_constant__ NormParams n) {
+// Shared memory beside the rows, for each token of a block.
+struct Token {
+  Where where;
+  float2 sums[kNormWarps];                // of squares of q and k, by warp
+  float scale[2], factor[2];              // at which they are taken; of the norms where the heads share one
+  // cos and sin of the pairs: (c, s) in the places of the pair's elements, or all cosines, then all sines
+  __align__(16) float cs[2 * DCP_ROPE_MAX_PAIRS];
+};
+
+template <typename T, int PAIRS, bool TOKEN, bool WEIGHTS, bool WIDE>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_kernel(const __grid_constant__ NormParams n) {
   using E = Elems<T>;
-  constexpr int N = E::kN, kWarps = kNormThreads / 32, kEs = sizeof(T);
-  constexpr int kTwo = PAIRS == kHalfVec ? 2 : 1;  // vectors of a unit (a head's part in a lane)
-  constexpr int kHeads = kUnits / kTwo;            // units of as many q and k heads that a thread has in flight
-  constexpr int kValues = kTwo == 2 ? 1 : 2;       // and of v heads
-  __shared__ Where where[kBlock];
-  // cos and sin of a token's pairs: (c, s) in the places of the pair's elements, or all cosines, then all sines
-  __shared__ __align__(16) float cs[kBlock][2 * DCP_ROPE_MAX_PAIRS];
-  __shared__ float2 sums[3][kWarps];
+  constexpr int N = E::kN, kEs = sizeof(T);
+  extern __shared__ __align__(16) uint8_t rows[];          // [token of the block][head of the piece][D]
   __shared__ __align__(16) float ws[WEIGHTS ? 1 : 2][WEIGHTS ? 4 : 128];  // weights that all heads share
-  __shared__ uint4 rows[PAIRS == kHalfAny ? kNormThreads : 1];
   const AppendParams& p = n.a;
-  const int D = p.pool.D, half = p.half, turned = p.Hq + p.pool.H;
-  const int pair_vecs = PAIRS == kHalfVec ? half / N : 0;  // units of two vectors in a head
-  const int per_head = D / N - pair_vecs;
-  const int threads = blockDim.x, e = threadIdx.x & ((1 << n.lanes_log2) - 1), step = threads >> n.lanes_log2;
-  const int h0 = threadIdx.x >> n.lanes_log2;  // the thread's heads: h0, h0 + step, ...
-  const bool there = e < per_head, two = PAIRS == kHalfVec && e < pair_vecs;
-  const int vec = two ? e : e + pair_vecs;  // the unit's (first) vector
+  Token* const tokens = reinterpret_cast<Token*>(rows + n.rows_bytes);
+  constexpr int kVecs = 16;                                // of a head, where WIDE
+  const int D = WIDE ? kVecs * N : p.pool.D, half = p.half, turned = p.Hq + p.pool.H, heads = turned + p.pool.H;
+  // A lane has two vectors of a head, as far apart as the pairs where that is a whole number of vectors, else half a head
+  // apart, so that neighbouring lanes' vectors are neighbours; those left over are one lane's each.
+  const int pair_vecs = WIDE ? kVecs / 2 : PAIRS == kHalfVec ? half / N : D / N / 2, per_head = D / N - pair_vecs, row_bytes = D * kEs;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  const int lanes_log2 = WIDE ? 3 : n.lanes_log2, e = lane & ((1 << lanes_log2) - 1), h0 = lane >> lanes_log2;
+  const int step = 32 >> lanes_log2;                       // heads that a warp has at a time
+  const bool there = WIDE || e < per_head, two = WIDE || e < pair_vecs;
+  const int vec = two ? e : e + pair_vecs;                 // the unit's (first) vector
   const int begin = (int)((int64_t)p.b.total_q * blockIdx.x / gridDim.x);  // the CTA's tokens
   const int end = (int)((int64_t)p.b.total_q * (blockIdx.x + 1) / gridDim.x);
 
-  // The thread's vector of head h0 as a q, a k and a v head, of the token to be loaded, and where they go.  (Heads follow
-  // one another by the same distance, so that a unit's address is a sum.)
-  const int from_k = (h0 - p.Hq) * D * kEs, vec_at = vec * 16;
-  const char* q_src = p.q + (begin * p.q_stride + h0 * D) * kEs + vec_at;
-  const char* k_src = p.k + begin * p.kv_stride * kEs + from_k + vec_at;
-  const char* v_src = p.v + (begin * p.kv_stride + h0 * D) * kEs + vec_at;
-  char* q_dst = p.q_out + (begin * (int64_t)p.Hq + h0) * D * kEs + vec_at;
-  char* const k_dst = p.pool.k + (h0 - p.Hq) * p.pool.s_head * kEs + vec_at;
-  char* const v_dst = p.pool.v + h0 * p.pool.s_head * kEs + vec_at;
-  const int next_head = step * D * kEs;
-  const int64_t next_page_head = step * p.pool.s_head * kEs;
-
-  auto fetch = [&](uint4 (&to)[kTwo], const char* from, bool real) {
-#pragma unroll
-    for (int i = 0; i < kTwo; ++i) to[i] = make_uint4(0, 0, 0, 0);
-    if (!real) return;
-    to[0] = load_once((const uint4*)from);
-    if constexpr (kTwo == 2)
-      if (two) to[1] = load_once((const uint4*)from + pair_vecs);
+  auto unit_at = [&](const uint8_t* row, uint4 (&to)[2]) {
+    to[0] = reinterpret_cast<const uint4*>(row)[vec];
+    to[1] = two ? reinterpret_cast<const uint4*>(row)[vec + pair_vecs] : make_uint4(0, 0, 0, 0);
   };
-  auto put = [&](char* to, const uint4& a, int which) {
-    if (which == 0)
-      *(uint4*)to = a;
-    else
-      ((uint4*)to)[pair_vecs] = a;
-  };
-  auto squares = [&](const uint4 (&a)[kTwo]) {
-    uint64_t s = 0;
+  auto squares = [&](const uint4 (&a)[2]) {
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kTwo; ++i) {
-      uint64_t f[N / 2];
-      pairs_of<T, N>(a[i], f);
+    for (int i = 0; i < 2; ++i) {
+      float f[N];
+      E::get(a[i], f);
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) s = fma2(f[k], f[k], s);
+      for (int k = 0; k < N; ++k) s[k & 1] = fmaf(f[k], f[k], s[k & 1]);
     }
-    float s0, s1;
-    unpair(s, s0, s1);
-    return s0 + s1;
+    return s[0] + s[1];
   };
-  auto scaled_squares = [&](const uint4 (&a)[kTwo], float c) {
+  auto scaled_squares = [&](const uint4 (&a)[2], float c) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTwo; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float f[N];
       E::get(a[i], f);
 #pragma unroll
@@ -170,36 +113,60 @@ __global__ void __launch_bounds__(kNormThreads, kNormResident / kNormThreads)
     }
     return s;
   };
-  // the places and phases of the tokens [first, first + kBlock) of the CTA's
-  auto look_up = [&](int first) {
-    const int last = min(first + kBlock, end);
+  // heads [h, h + count) of tokens [first, last) on their way to shared memory
+  auto load = [&](int first, int last, int h, int count) {
+    const uint32_t to = smem_u32(rows);
+    for (int t = first; t < last; ++t) {
+      auto copy = [&](const char* from, int lo, int hi) {  // heads lo .. hi - 1 of all, head lo at `from`
+        const int a = max(lo, h), b = min(hi, h + count);
+        const char* src = from + (a - lo) * row_bytes + threadIdx.x * 16;
+        uint32_t dst = to + ((t - first) * count + a - h) * row_bytes + threadIdx.x * 16;
+#pragma unroll 1
+        for (int left = (b - a) * row_bytes - (int)threadIdx.x * 16; left > 0; left -= kNormThreads * 16) {
+          cp_async16(dst, src);
+          dst += kNormThreads * 16;
+          src += kNormThreads * 16;
+        }
+      };
+      copy(p.q + t * p.q_stride * kEs, 0, p.Hq);
+      copy(p.k + t * p.kv_stride * kEs, p.Hq, turned);
+      copy(p.v + t * p.kv_stride * kEs, turned, heads);
+    }
+    cp_async_commit();
+  };
+  // the places and phases of tokens [first, last)
+  auto look_up = [&](int first, int last) {
+    if (threadIdx.x < last - first) {
+      tokens[threadIdx.x].where = Where{-1, 0, -1};
+      tokens[threadIdx.x].scale[0] = tokens[threadIdx.x].scale[1] = 1.f;
+    }
     __syncthreads();
-    if (threadIdx.x < kBlock) where[threadIdx.x] = Where{-1, 0, -1};
-    __syncthreads();
-    for (int s = threadIdx.x; s < p.b.n_seqs; s += threads) {
+    for (int s = threadIdx.x; s < p.b.n_seqs; s += kNormThreads) {
       int lo, len;
       int64_t kv;
       const bool sound = seq_rows(p.b, s, lo, len) & seq_kv(p.b, p.pool.bs, p.pool.H, s, 0, kv);
       if (!sound) continue;
-      for (int t = max(lo, first); t < min(lo + len, last); ++t) where[t - first] = Where{kv - len + (t - lo), 0, s};
+      for (int t = max(lo, first); t < min(lo + len, last); ++t)
+        tokens[t - first].where = Where{kv - len + (t - lo), 0, s};
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (last - first) * half; i += threads) {
+    for (int i = threadIdx.x; i < (last - first) * half; i += kNormThreads) {
       const int t = i / half, pair = i - t * half, axis = (pair >= n.first[1]) + (pair >= n.first[2]);
       const int32_t phase =
-          p.positions ? p.positions[axis * (int64_t)p.b.total_q + first + t] : (int32_t)where[t].off;
+          p.positions ? p.positions[axis * (int64_t)p.b.total_q + first + t] : (int32_t)tokens[t].where.off;
       const float2 r =
           turn_at(phase, p.turns[pair], axis == 0 ? n.amplitude[0] : axis == 1 ? n.amplitude[1] : n.amplitude[2]);
+      float* const cs = tokens[t].cs;
       if constexpr (PAIRS == kInterleaved) {
-        *reinterpret_cast<float2*>(&cs[t][place<N, 128>(2 * pair)]) = r;
+        *reinterpret_cast<float2*>(&cs[place<N, 128>(2 * pair)]) = r;
       } else {
-        cs[t][place<N, 64>(pair)] = r.x;
-        cs[t][64 + place<N, 64>(pair)] = r.y;
+        cs[place<N, 64>(pair)] = r.x;
+        cs[64 + place<N, 64>(pair)] = r.y;
       }
     }
     Where w{-1, 0, -1};
     if (threadIdx.x < last - first) {
-      w = where[threadIdx.x];
+      w = tokens[threadIdx.x].where;
       const int64_t c = w.off;
       w.off = -1;
       if (w.seq >= 0 && c >= 0) {
@@ -212,256 +179,307 @@ __global__ void __launch_bounds__(kNormThreads, kNormResident / kNormThreads)
       }
     }
     __syncthreads();
-    if (threadIdx.x < last - first) where[threadIdx.x] = w;
-    __syncthreads();
+    if (threadIdx.x < last - first) tokens[threadIdx.x].where = w;
   };
-  // a unit of a q or k head: norm, weights (of the head whose first element is number `at`), turn by `t`
-  auto turn = [&](const uint4 (&raw)[kTwo], bool real, bool is_q, const Norm& f, int at, const float* t, char* to) {
-    if constexpr (PAIRS == kHalfAny) {  // a head's lanes are in one warp
-      __syncwarp();
-      rows[threadIdx.x] = raw[0];
-      __syncwarp();
+  // Heads [h, h + count) of all: those that are heads lo .. hi - 1, from the first of these on.
+  struct Part {
+    int first, heads, rounds;  // rounds of a warp
+  };
+  auto part = [&](int h, int count, int lo, int hi) {
+    const int first = max(lo, h), some = max(0, min(hi, h + count) - first);
+    return Part{first - lo, some, (some + step - 1) / step};
+  };
+  // each warp's share of the sums of a token's q and k heads [h, h + count), which lie at `row`
+  auto add_squares = [&](Token& tk, const uint8_t* row, int h, int count, bool more, bool scaled) {
+    float s[2];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const Part now = part(h, count, which ? p.Hq : 0, which ? turned : p.Hq);
+      const uint8_t* at = row + (now.first + (which ? p.Hq : 0) - h + warp * step + h0) * row_bytes;
+      s[which] = 0.f;
+      for (int k = warp * step + h0; k < now.heads; k += kNormWarps * step, at += kNormWarps * step * row_bytes) {
+        if (!there) continue;
+        uint4 x[2];
+        unit_at(at, x);
+        s[which] += scaled ? scaled_squares(x, tk.scale[which]) : squares(x);
+      }
     }
-    if (!real) return;
-    const char* weight = is_q ? n.q_weight : n.k_weight;
-    uint64_t a[kTwo][N / 2];
-    const uint64_t r2 = pair(f.r, f.r);
 #pragma unroll
-    for (int j = 0; j < kTwo; ++j) {
-      if (j && !two) continue;
-      pairs_of<T, N>(raw[j], a[j]);
-      if (f.up != 1.f) {
+    for (int o = 16; o; o >>= 1) {
+      s[0] += __shfl_xor_sync(~0u, s[0], o);
+      s[1] += __shfl_xor_sync(~0u, s[1], o);
+    }
+    if (lane == 0) {
+      float2& to = tk.sums[warp];
+      to = more ? make_float2(to.x + s[0], to.y + s[1]) : make_float2(s[0], s[1]);
+    }
+  };
+  // the factors of tokens [place, place + n_tokens) of the block; true where a sum has to be taken again, at another scale
+  auto make_factors = [&](int place, int n_tokens, bool last_time) {
+    __syncthreads();
+    bool again = false;
+    if (threadIdx.x < 2 * n_tokens) {
+      Token& tk = tokens[place + (threadIdx.x >> 1)];
+      const int k = threadIdx.x & 1;
+      float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) a[j][k] = mul2(a[j][k], pair(f.up, f.up));
+      for (int w = 0; w < kNormWarps; ++w) s += k ? tk.sums[w].y : tk.sums[w].x;
+      const float inv = k ? n.inv_k : n.inv_q;
+      tk.factor[k] = norm_of(s, inv, n.eps, tk.scale[k]);
+      if (!last_time && (k || p.Hq)) {
+        tk.scale[k] = rescale(s, inv, n.eps);
+        again = tk.scale[k] != 1.f;
       }
+    }
+    return __syncthreads_or(again);
+  };
+  // weights of a vector's elements, the first of which is element d of a head, and of one element; `own` is where the
+  // head's own weights begin, where each has its own (null: ones)
+  auto weights_at = [&](bool is_q, const char* own, uint32_t d, float (&g)[N]) {
+    if constexpr (!WEIGHTS) {
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) a[j][k] = mul2(a[j][k], r2);
-      const int d = (vec + j * pair_vecs) * N;
-      if constexpr (WEIGHTS) {
-        weigh<N>(n, weight, at + d, a[j]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N / 2; k += 2) {
-          const float4 w = *reinterpret_cast<const float4*>(&ws[!is_q][place<N, 128>(d + 2 * k)]);
-          a[j][k] = mul2(a[j][k], pair(w.x, w.y));
-          a[j][k + 1] = mul2(a[j][k + 1], pair(w.z, w.w));
-        }
+      for (int u = 0; u < N; u += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(&ws[!is_q][place<N, 128>(d + u)]);
+        g[u] = w.x, g[u + 1] = w.y, g[u + 2] = w.z, g[u + 3] = w.w;
       }
+    } else if (!own) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) g[u] = 1.f;
+    } else if (n.weight_bf16) {
+#pragma unroll
+      for (int u = 0; u < N; u += 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(own + 2 * d) + u / 4);
+        g[u] = bf16lo(w.x), g[u + 1] = bf16hi(w.x), g[u + 2] = bf16lo(w.y), g[u + 3] = bf16hi(w.y);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; u += 4) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(own + 4 * d) + u / 4);
+        g[u] = w.x, g[u + 1] = w.y, g[u + 2] = w.z, g[u + 3] = w.w;
+      }
+    }
+  };
+  auto weight_at = [&](bool is_q, const char* own, int d) {
+    if constexpr (!WEIGHTS) return ws[!is_q][place<N, 128>(d)];
+    return !own ? 1.f : n.weight_bf16 ? __bfloat162float(((const __nv_bfloat16*)own)[d]) : ((const float*)own)[d];
+  };
+  // a unit: norm, weights, turn
+  auto put = [&](const bool is_q, const uint4 (&x)[2], float f, const float* cs, const uint8_t* at, const char* own,
+                 uint4* to) {
+    float a[2][N];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      E::get(x[j], a[j]);
+      float g[N];
+      weights_at(is_q, own, (j && !two ? vec : vec + j * pair_vecs) * N, g);
+#pragma unroll
+      for (int u = 0; u < N; ++u) a[j][u] *= f * g[u];
     }
     if constexpr (PAIRS == kHalfVec) {
       if (two) {
 #pragma unroll
-        for (int k = 0; k < N / 2; k += 2) {
-          const float4 c = *reinterpret_cast<const float4*>(&t[place<N, 64>(e * N + 2 * k)]);
-          const float4 s = *reinterpret_cast<const float4*>(&t[64 + place<N, 64>(e * N + 2 * k)]);
-          const uint64_t c2[2] = {pair(c.x, c.y), pair(c.z, c.w)}, s2[2] = {pair(s.x, s.y), pair(s.z, s.w)};
-          const uint64_t minus[2] = {pair(-s.x, -s.y), pair(-s.z, -s.w)};
+        for (int q4 = 0; q4 < N; q4 += 4) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&cs[place<N, 64>(e * N + q4)]);
+          const float4 s4 = *reinterpret_cast<const float4*>(&cs[64 + place<N, 64>(e * N + q4)]);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint64_t x0 = a[0][k + u], x1 = a[1][k + u];
-            a[0][k + u] = fma2(x0, c2[u], mul2(x1, minus[u]));
-            a[1][k + u] = fma2(x1, c2[u], mul2(x0, s2[u]));
-          }
-        }
-        put(to, vector_of<T, N>(a[1]), 1);
-      }
-    } else if constexpr (PAIRS == kInterleaved) {
-      if (vec * N < 2 * half) {
-#pragma unroll
-        for (int k = 0; k < N / 2; k += 2) {
-          const float4 r = *reinterpret_cast<const float4*>(&t[place<N, 128>(vec * N + 2 * k)]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (vec * N + 2 * (k + u) >= 2 * half) continue;
-            const float c = u ? r.z : r.x, s = u ? r.w : r.y;
-            float x0, x1;
-            unpair(a[0][k + u], x0, x1);
-            a[0][k + u] = pair(x0 * c - x1 * s, x0 * s + x1 * c);
+          for (int u = 0; u < 4; ++u) {
+            const float x0 = a[0][q4 + u], x1 = a[1][q4 + u];
+            a[0][q4 + u] = x0 * c[u] - x1 * s[u];
+            a[1][q4 + u] = x0 * s[u] + x1 * c[u];
           }
         }
       }
-    } else if (vec * N < 2 * half) {
-      const uint4* row = rows + threadIdx.x - e;
-      float y[N];
+    } else {
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) unpair(a[0][k], y[2 * k], y[2 * k + 1]);
+      for (int j = 0; j < 2; ++j) {
+        const int d0 = (vec + j * pair_vecs) * N;
+        if (d0 >= 2 * half) continue;
+        const bool whole = 2 * half % N == 0;  // no vector is turned in part
+        if constexpr (PAIRS == kInterleaved) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int d = vec * N + k;
-        if (d >= 2 * half) continue;
-        const int o = d < half ? d + half : d - half;
-        float b = E::one(row, o) * f.up * f.r;
-        if constexpr (!WEIGHTS)
-          b *= ws[!is_q][place<N, 128>(o)];
-        else if (weight)
-          b *= n.weight_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(weight)[at + o])
-                             : reinterpret_cast<const float*>(weight)[at + o];
-        const int at_pair = place<N, 64>(d < half ? d : o);
-        const float c = t[at_pair], s = t[64 + at_pair];
-        y[k] = d < half ? y[k] * c - b * s : y[k] * c + b * s;
+          for (int u = 0; u < N; u += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(&cs[place<N, 128>(d0 + u)]);
+            const float x0 = a[j][u], x1 = a[j][u + 1], x2 = a[j][u + 2], x3 = a[j][u + 3];
+            a[j][u] = x0 * r.x - x1 * r.y, a[j][u + 1] = x0 * r.y + x1 * r.x;
+            a[j][u + 2] = x2 * r.z - x3 * r.w, a[j][u + 3] = x2 * r.w + x3 * r.z;
+            if (whole) continue;
+            if (d0 + u >= 2 * half) a[j][u] = x0, a[j][u + 1] = x1;
+            if (d0 + u + 2 >= 2 * half) a[j][u + 2] = x2, a[j][u + 3] = x3;
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int d = d0 + u;
+            if (d >= 2 * half) continue;
+            const int o = d < half ? d + half : d - half;
+            const float b = E::one(reinterpret_cast<const uint4*>(at), o) * (f * weight_at(is_q, own, o));
+            const int at_pair = place<N, 64>(d < half ? d : o);
+            const float c = cs[at_pair], s = cs[64 + at_pair];
+            a[j][u] = d < half ? a[j][u] * c - b * s : a[j][u] * c + b * s;
+          }
+        }
       }
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k) a[0][k] = pair(y[2 * k], y[2 * k + 1]);
     }
-    put(to, vector_of<T, N>(a[0]), 0);
+    if (two) to[vec + pair_vecs] = E::put(a[1]);
+    to[vec] = E::put(a[0]);
   };
-  // the norm of the head whose units this warp's lanes hold
-  auto norm_of_head = [&](const uint4 (&a)[kTwo]) {
-    auto of_head = [&](float s) {
-      for (int o = 1 << n.lanes_log2 >> 1; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-      return s;
+  // Heads [h, h + count) of n_tokens tokens: norm, weights, turn; values as they are.  A warp takes a few heads at a time,
+  // and its next ones kNormWarps further; who begins goes round, from kind to kind and token to token.
+  const char* const q_weight = WEIGHTS && n.q_weight ? n.q_weight + h0 * D * n.weight_bytes : nullptr;
+  const char* const k_weight = WEIGHTS && n.k_weight ? n.k_weight + h0 * D * n.weight_bytes : nullptr;
+  auto finish = [&](int first, int place, int n_tokens, int h, int count) {
+    const Part qs = part(h, count, 0, p.Hq), ks = part(h, count, p.Hq, turned), vs = part(h, count, turned, heads);
+    const uint8_t* row = rows + h0 * row_bytes;
+    int turn_of = warp;  // rounds before this warp's first of a kind
+    auto next_kind = [&](int rounds) { turn_of = (turn_of - rounds) & (kNormWarps - 1); };
+    auto heads_of = [&](const bool is_q, const Part& now, const Token& tk, const uint8_t* at, char* to, int64_t next,
+                        bool wanted) {
+      const char* own = is_q ? q_weight : k_weight;
+      if constexpr (WEIGHTS)
+        if (own) own += (now.first + turn_of * step) * D * n.weight_bytes;
+      at += turn_of * step * row_bytes;
+      to += (now.first + turn_of * step + h0) * next;
+      float f;
+      if constexpr (TOKEN) f = tk.factor[!is_q];
+      for (int r = turn_of; r < now.rounds; r += kNormWarps) {
+        const bool real = there && r * step + h0 < now.heads;
+        uint4 x[2] = {};
+        if (real) unit_at(at, x);
+        if constexpr (!TOKEN) {
+          auto of_head = [&](float s) {
+            for (int o = 1 << lanes_log2 >> 1; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+            return s;
+          };
+          float s = of_head(squares(x));
+          const float c = rescale(s, n.inv_head, n.eps);
+          if (__any_sync(~0u, c != 1.f)) s = of_head(scaled_squares(x, c));
+          f = norm_of(s, n.inv_head, n.eps, c);
+        }
+        if (real && wanted) put(is_q, x, f, tk.cs, at, own, reinterpret_cast<uint4*>(to));
+        at += kNormWarps * step * row_bytes;
+        to += kNormWarps * step * next;
+        if constexpr (WEIGHTS)
+          if (own) own += kNormWarps * step * D * n.weight_bytes;
+      }
+      next_kind(now.rounds);
     };
-    float s = of_head(squares(a));
-    const float c = rescale(s, n.inv_head, n.eps);
-    if (__any_sync(~0u, c != 1.f)) s = of_head(scaled_squares(a, c));
-    return norm_of(s, n.inv_head, n.eps, c);
+    const int64_t page_head = p.pool.s_head * kEs;
+    for (int t = 0; t < n_tokens; ++t, row += count * row_bytes) {
+      const Token& tk = tokens[place + t];
+      const Where w = tk.where;
+      heads_of(true, qs, tk, row, p.q_out + (first + t) * (int64_t)p.Hq * row_bytes, row_bytes, w.seq >= 0);
+      heads_of(false, ks, tk, row + qs.heads * row_bytes, p.pool.k + w.off * kEs, page_head, w.off >= 0);
+      const uint8_t* at = row + (qs.heads + ks.heads + turn_of * step) * row_bytes;
+      char* to = p.pool.v + w.off * kEs + (vs.first + turn_of * step + h0) * page_head;
+      for (int r = turn_of; r < vs.rounds; r += kNormWarps) {
+        if (there && r * step + h0 < vs.heads && w.off >= 0) {
+          uint4 x[2];
+          unit_at(at, x);
+          reinterpret_cast<uint4*>(to)[vec] = x[0];
+          if (two) reinterpret_cast<uint4*>(to)[vec + pair_vecs] = x[1];
+        }
+        at += kNormWarps * step * row_bytes;
+        to += kNormWarps * step * page_head;
+      }
+      next_kind(vs.rounds);
+    }
   };
 
   allow_dependents();
   wait_for_predecessor();
-  uint4 x[kHeads][kTwo], v[kValues][kTwo];
-  auto load = [&](int j, bool real) {
-    const int h = h0 + j * step;
-    fetch(x[j], (h < p.Hq ? q_src : k_src) + j * next_head, real && there && h < turned);
-  };
-  auto load_value = [&](int j, bool real) {
-    fetch(v[j], v_src + j * next_head, real && there && h0 + j * step < p.pool.H);
-  };
-#pragma unroll
-  for (int j = 0; j < kHeads; ++j) load(j, true);
-#pragma unroll
-  for (int j = 0; j < kValues; ++j) load_value(j, true);
+  load(begin, min(begin + n.tokens, end), 0, n.heads);
   if constexpr (!WEIGHTS) {
-    for (int i = threadIdx.x; i < 2 * D; i += threads) {
+    for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) {
       const int k = i >= D, d = i - k * D;
       const char* w = k ? n.k_weight : n.q_weight;
       ws[k][place<N, 128>(d)] =
           !w ? 1.f : n.weight_bf16 ? __bfloat162float(((const __nv_bfloat16*)w)[d]) : ((const float*)w)[d];
     }
   }
-
-  for (int tok = begin; tok < end; ++tok) {
-    const int i = (tok - begin) % kBlock;
-    if (i == 0) look_up(tok);
-    const Where w = where[i];
-    Norm whole[2];  // of q and k, where the heads share one
-    if constexpr (TOKEN) {
-      float c[2] = {1.f, 1.f};
-#pragma unroll 1
-      for (int again = 0; again < 2; ++again) {
-        float s[2] = {0.f, 0.f};
-        auto add = [&](int h, const uint4 (&a)[kTwo]) {
-          const float t = !again ? squares(a) : scaled_squares(a, h < p.Hq ? c[0] : c[1]);
-          if (h < p.Hq)
-            s[0] += t;
-          else
-            s[1] += t;  // past the last head: zeros
-        };
-#pragma unroll
-        for (int j = 0; j < kHeads; ++j) add(h0 + j * step, x[j]);
-        for (int j = kHeads; h0 + j * step < turned; ++j) {
-          uint4 a[kTwo];
-          fetch(a, (h0 + j * step < p.Hq ? q_src : k_src) + (int64_t)j * next_head, there);
-          add(h0 + j * step, a);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          s[0] += __shfl_xor_sync(~0u, s[0], o);
-          s[1] += __shfl_xor_sync(~0u, s[1], o);
-        }
-        float2* const to = sums[again ? 2 : tok & 1];  // in turns: a barrier a token is enough
-        if ((threadIdx.x & 31) == 0) to[threadIdx.x >> 5] = make_float2(s[0], s[1]);
+  int held = 0;  // first head of the piece that is in shared memory or on its way
+  for (int first = begin; first < end; first += n.tokens) {
+    const int last = min(first + n.tokens, end), place0 = (first - begin) % n.block;  // among the tokens looked up
+    auto have = [&](int h) {  // heads from h on
+      if (held != h) {
         __syncthreads();
-        const int lane = threadIdx.x & 31;
-        const float2 other = lane < threads >> 5 ? to[lane] : make_float2(0.f, 0.f);
-        s[0] = other.x;
-        s[1] = other.y;
-        float scale[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int o = kWarps / 2; o; o >>= 1) s[k] += __shfl_xor_sync(~0u, s[k], o);
-          s[k] = __shfl_sync(~0u, s[k], 0);
-          const float inv = k ? n.inv_k : n.inv_q;
-          scale[k] = k == 0 && p.Hq == 0 ? 1.f : rescale(s[k], inv, n.eps);
-          whole[k] = norm_of(s[k], inv, n.eps, c[k]);
+        load(first, last, h, min(n.heads, heads - h));
+        held = h;
+      }
+      cp_async_wait<0>();
+      __syncthreads();
+    };
+    if (place0 == 0) look_up(first, min(first + n.block, end));
+    if constexpr (TOKEN) {
+      auto add = [&](bool scaled) {
+        for (int h = 0; h < turned; h += n.heads) {
+          const int count = min(n.heads, heads - h);
+          have(h);
+          for (int t = first; t < last; ++t)
+            add_squares(tokens[place0 + t - first], rows + (t - first) * count * row_bytes, h, count, h > 0, scaled);
         }
-        if (again || (scale[0] == 1.f && scale[1] == 1.f)) break;  // the same in every thread
-        c[0] = scale[0];
-        c[1] = scale[1];
+      };
+      add(false);
+      if (make_factors(place0, last - first, false)) {
+        add(true);
+        make_factors(place0, last - first, true);
       }
     }
-    auto unit = [&](int j, const uint4 (&a)[kTwo]) {
-      const int h = h0 + j * step;
-      const bool is_q = h < p.Hq;
-      Norm f;
-      if constexpr (TOKEN)
-        f = is_q ? whole[0] : whole[1];
-      else
-        f = norm_of_head(a);
-      char* const to = is_q ? q_dst + (int64_t)j * next_head : k_dst + w.off * kEs + j * next_page_head;
-      turn(a, there && h < turned && (is_q ? w.seq >= 0 : w.off >= 0), is_q, f, (is_q ? h : h - p.Hq) * D, cs[i], to);
-    };
-    auto value = [&](int j, const uint4 (&a)[kTwo]) {
-      if (!there || h0 + j * step >= p.pool.H || w.off < 0) return;
-      char* const to = v_dst + w.off * kEs + j * next_page_head;
-      put(to, a[0], 0);
-      if constexpr (kTwo == 2)
-        if (two) put(to, a[1], 1);
-    };
-    // heads past the registers first: the next token is loaded where this one's units were
-    for (int j = kHeads; j * step < turned; ++j) {
-      uint4 a[kTwo];
-      fetch(a, (h0 + j * step < p.Hq ? q_src : k_src) + (int64_t)j * next_head, there && h0 + j * step < turned);
-      unit(j, a);
+    for (int h = 0; h < heads; h += n.heads) {
+      const int count = min(n.heads, heads - h);
+      have(h);
+      finish(first, place0, last - first, h, count);
     }
-    for (int j = kValues; h0 + j * step < p.pool.H; ++j) {
-      uint4 a[kTwo];
-      fetch(a, v_src + (int64_t)j * next_head, there);
-      value(j, a);
-    }
-    q_src += p.q_stride * kEs;
-    k_src += p.kv_stride * kEs;
-    v_src += p.kv_stride * kEs;
-#pragma unroll
-    for (int j = 0; j < kValues; ++j) {
-      value(j, v[j]);
-      load_value(j, tok + 1 < end);
-    }
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      unit(j, x[j]);
-      load(j, tok + 1 < end);
-    }
-    q_dst += (int64_t)p.Hq * D * kEs;
+    if (last == end) break;
+    __syncthreads();
+    load(last, min(last + n.tokens, end), 0, n.heads);
+    held = 0;
   }
 }
 
-template <typename T, int PAIRS, bool TOKEN, bool WEIGHTS>
-cudaError_t launch(const NormParams& n, cudaStream_t s) {
-  // No more threads than hold a token's q and k heads in kUnits vectors each: so many tokens are in flight on an SM.
-  const int turned = n.a.Hq + n.a.pool.H, lanes = 1 << n.lanes_log2, each = kUnits / (PAIRS == kHalfVec ? 2 : 1);
-  const int threads = (int)std::max<int64_t>(64, std::min<int64_t>(kNormThreads, ((int64_t)(turned + each - 1) / each * lanes + 31) / 32 * 32));
-  const int64_t room = (int64_t)(kNormResident / threads) * sm_count();
-  return launch_behind(norm_kernel<T, PAIRS, TOKEN, WEIGHTS>, dim3((unsigned)std::min<int64_t>(n.a.b.total_q, room)),
-                       threads, 0, s, n);
+template <typename T, int PAIRS, bool TOKEN, bool WEIGHTS, bool WIDE>
+cudaError_t launch(NormParams& n, cudaStream_t s) {
+  static LaunchCache lc;
+  // A block's tokens, and their places behind the rows.
+  const int heads = n.a.Hq + 2 * n.a.pool.H, row = n.a.pool.D * (int)sizeof(T);
+  n.heads = (int)std::min<int64_t>(heads, kMostBytes / row);
+  n.tokens = std::max(1, std::min(kBlock, kBlockBytes / (n.heads * row)));
+  // no more than leave every CTA that the SMs hold something to do
+  n.tokens = (int)std::min<int64_t>(n.tokens, std::max(1, n.a.b.total_q / (kNormCtas * sm_count())));
+  n.rows_bytes = n.tokens * n.heads * row;
+  n.block = kBlock / n.tokens * n.tokens;
+  const size_t smem = n.rows_bytes + n.block * sizeof(Token);
+  int unused;
+  const cudaError_t e = launch_setup(lc, norm_kernel<T, PAIRS, TOKEN, WEIGHTS, WIDE>, kNormThreads,
+                                     kMostBytes + kBlock * sizeof(Token), &unused);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(kNormCtas, kSharedOfSm / (int64_t)(smem + kSharedOfCta));
+  const int64_t room = ctas * sm_count();
+  return launch_behind(norm_kernel<T, PAIRS, TOKEN, WEIGHTS, WIDE>, dim3((unsigned)std::min<int64_t>(n.a.b.total_q, room)),
+                       kNormThreads, smem, s, n);
 }
 
-template <typename T, int PAIRS>
+template <typename T, int PAIRS, bool WIDE>
 cudaError_t launch_span(NormParams& n, cudaStream_t s) {
-  const int units = n.a.pool.D / Elems<T>::kN - (PAIRS == kHalfVec ? n.a.half / Elems<T>::kN : 0);
-  n.lanes_log2 = 0;
-  while (1 << n.lanes_log2 < units) ++n.lanes_log2;
   const bool weights = n.weight_heads && (n.q_weight || n.k_weight);
-  if (n.token_span) return weights ? launch<T, PAIRS, true, true>(n, s) : launch<T, PAIRS, true, false>(n, s);
-  return weights ? launch<T, PAIRS, false, true>(n, s) : launch<T, PAIRS, false, false>(n, s);
+  if (n.token_span) return weights ? launch<T, PAIRS, true, true, WIDE>(n, s) : launch<T, PAIRS, true, false, WIDE>(n, s);
+  return weights ? launch<T, PAIRS, false, true, WIDE>(n, s) : launch<T, PAIRS, false, false, WIDE>(n, s);
+}
+
+// Heads of 16 vectors, 8 lanes each, have a kernel to which all that depends on the head's size is a constant.
+template <typename T, int PAIRS>
+cudaError_t launch_width(NormParams& n, cudaStream_t s) {
+  const int vecs = n.a.pool.D / Elems<T>::kN, pairs = PAIRS == kHalfVec ? n.a.half / Elems<T>::kN : vecs / 2;
+  n.lanes_log2 = 0;
+  while (1 << n.lanes_log2 < vecs - pairs) ++n.lanes_log2;
+  return vecs == 16 && pairs == 8 ? launch_span<T, PAIRS, true>(n, s) : launch_span<T, PAIRS, false>(n, s);
 }
 
 template <typename T>
 cudaError_t launch_pairs(NormParams& n, cudaStream_t s) {
-  if (!n.a.half_layout) return launch_span<T, kInterleaved>(n, s);
-  if (n.a.half % Elems<T>::kN == 0) return launch_span<T, kHalfVec>(n, s);
-  return launch_span<T, kHalfAny>(n, s);
+  if (!n.a.half_layout) return launch_width<T, kInterleaved>(n, s);
+  if (n.a.half % Elems<T>::kN == 0) return launch_width<T, kHalfVec>(n, s);
+  return launch_width<T, kHalfAny>(n, s);
 }
 
 }  // namespace

@@ -46,9 +46,13 @@ struct NormParams {
   AppendParams a;               // its amplitude is not used
   const char* q_weight;         // nullable: ones
   const char* k_weight;
-  int32_t weight_bf16, weight_heads;  // their type; weights of each head, or one row for all
+  int32_t weight_bf16, weight_bytes;  // their type
+  int32_t weight_heads;         // weights of each head, or one row for all
   int32_t token_span;           // the mean goes over all heads of a token
   int32_t lanes_log2;           // lanes that hold a head
+  int32_t tokens, heads;        // of a CTA at a time: tokens, and heads (all, or those of a piece of one token)
+  int32_t block;                // tokens whose places are looked up at a time, a multiple of `tokens`
+  int32_t rows_bytes;           // of shared memory that they take
   float eps;
   float inv_head, inv_q, inv_k; // 1 / the dims of a head, of all query heads, of all KV heads
   int32_t first[3];             // first pair of each axis, the number of pairs for those that are not there

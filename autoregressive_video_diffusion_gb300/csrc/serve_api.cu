@@ -316,6 +316,7 @@ dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* ba
   n.q_weight = (const char*)norm->q_weight;
   n.k_weight = (const char*)norm->k_weight;
   n.weight_bf16 = norm->weight_dtype == DCP_BF16;
+  n.weight_bytes = elem_size(norm->weight_dtype);
   n.weight_heads = norm->weight_per_head;
   n.token_span = norm->span == DCP_NORM_TOKEN;
   n.eps = norm->eps;

@@ -42,7 +42,7 @@ def check_norm_turned(got, x, w, eps, span, positions, cfgs):
     want, size = norm_turned_64(x, w, eps, span, positions, cfgs)
     # a sum of squares (all positive): at most 16 terms of a head behind one another in a lane and 5 sums of lanes; of a
     # token at most 2 terms a head and 16 more, 5 sums of lanes and 8 of warps.  Half of it in the root; the mean, the root
-    # and four products are a rounding each.
+    # and its correction and three products are a rounding each.
     chain = 24 if span == dcp.DCP_NORM_HEAD else 2 * x.shape[1] + 32
     norm = (0.5 * chain + 7) * 2.0 ** -24
     # the turn as in tests/serving.py: phase off by 2^-30 turns and its rounding, sine and cosine by 2 ulp, three roundings
@@ -94,6 +94,9 @@ def check_attention_sink(cache, q, out, lse, scale, causal, window, sink, kv_of=
 
 
 # ------------------------------------------------------------------------------------------ shared prefixes
+FAR = 1 << 28
+
+
 class Branches(Cache):
     """Pages of sequences in groups: [(prefix, [(new tokens, positions behind the prefix, new tokens among them), ...]),
     ...]; `before` and `after` further sequences that belong to no group.  A branch names its group's full pages and holds
@@ -121,6 +124,11 @@ class Branches(Cache):
             1, *(self.start[b] - self.start[a] for a, b in zip(self.group_at, self.group_at[1:]))))
         kw.update(over)
         return dcp.PrefixGroups(self.start_dev, self.prefix_dev, **kw)
+
+    def far(self, rest=0):
+        """The batch and the groups with bounds so large that prefixes are shared however short they are; `rest` is the bound
+        of what lies behind them."""
+        return dict(batch=self.batch(max_kv=FAR + rest), groups=self.groups(max_prefix=FAR))
 
     def attend(self, q, causal=True, window=-1, sink=0, scale=None, batch=None, groups=None):
         out = torch.full_like(q, math.nan, memory_format=torch.contiguous_format)

@@ -26,9 +26,13 @@ CASES = [
     ("f32", HND, 5, 5, 128, 16, [17], [64], [44, 42, 42], 0, 77),
     ("f32", HND, 1, 1, 4, 1, [3], [3], [2], 0, 5),
     ("bf16", NHD, 2, 2, 24, 3, [4], [9], [0], 1, None),
-    ("bf16", NHD, 200, 3, 128, 16, [2], [9], [128], 1, None),     # more heads than a CTA's registers hold
+    ("bf16", NHD, 200, 3, 128, 16, [2], [9], [128], 1, None),     # many heads
     ("bf16", HND, 150, 150, 64, 16, [2], [9], [64], 0, None),
     ("f32", HND, 90, 1, 128, 16, [2], [9], [120], 1, None),
+    ("bf16", NHD, 300, 3, 128, 16, [2, 3], [9, 3], [128], 1, None),  # and tokens that go through shared memory in pieces
+    ("bf16", HND, 70, 280, 72, 16, [3], [9], [44], 0, 12),
+    ("f32", HND, 100, 40, 128, 16, [2], [9], [128], 1, None),
+    ("f32", NHD, 3, 130, 100, 16, [2], [9], [70], 1, None),
 ]
 
 
@@ -165,6 +169,21 @@ def test_without_norms_turn_as_the_plain_append(gpu):
     assert (one - two).abs().max() <= 2.0 ** -20 * one.abs().max()
     at = new_rows(a, 0)
     assert (a.k[at] - b.k[at]).abs().max() <= 2.0 ** -20 * one.abs().max() and torch.equal(a.v[at], b.v[at])
+
+
+@pytest.mark.parametrize("dtype,hq", [("bf16", 300), ("f32", 6)])
+def test_values_past_the_squares_in_pieces_and_blocks(gpu, dtype, hq):
+    """Tokens whose sums are taken again beside tokens whose sums are not, several in a CTA and one in pieces."""
+    n = 700
+    c = Cache(dtype, NHD, 2, 64 if hq < 10 else 128, 16, [n], [n], seed=hq)
+    scale = 2.0 ** torch.randint(-1, 2, (n, 1, 1), generator=c.g).double().mul(70).cuda()
+    q, k, v = ((c.normal(n, h, c.d).double() * scale).to(c.dt) for h in (hq, 2, 2))
+    cfg, out = dcp.RopeConfig(64, dcp.DCP_ROPE_HALF), torch.empty_like(q)
+    dcp.dcp_norm_rope_append(c.pool(), c.batch(), dcp.dcp_rope_axes([cfg]), dcp.NormConfig(eps=0.0, span=TOKEN), q, k, v,
+                             None, out)
+    assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
+    check_norm_turned(out, q, None, 0.0, TOKEN, np.arange(n)[None], [cfg])
+    check_norm_turned(c.k[c.rows(0, 0, n)], k, None, 0.0, TOKEN, np.arange(n)[None], [cfg])
 
 
 def test_in_a_graph_and_on_another_stream(gpu):

@@ -6,7 +6,7 @@ import torch
 
 import autoregressive_video_diffusion_gb300 as dcp
 from tests.serving import HND, NHD, ints
-from tests.serving_more import Branches, check_attention_sink
+from tests.serving_more import FAR, Branches, check_attention_sink
 
 pytestmark = pytest.mark.gpu
 
@@ -45,13 +45,23 @@ CASES = {
 }
 
 
+# Small prefixes are shared only where the bounds say that they may be long: the tests run with such bounds, and with bounds
+# of what lies behind the prefixes that make an item one CTA's (0), a few CTAs' or an even share's (50000).
+RESTS = [None, 0, 600, 50000]
+
+
+def bounds(c, rest):
+    return {} if rest is None else c.far(rest)
+
+
 @pytest.mark.parametrize("name", CASES)
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "open"])
-def test_shared(gpu, name, causal):
+@pytest.mark.parametrize("rest", RESTS)
+def test_shared(gpu, name, causal, rest):
     dtype, layout, hq, h, d, bs, groups, before, after = CASES[name]
     c = Branches(dtype, layout, h, d, bs, groups, before, after, seed=len(name)).fill()
     q = c.normal(c.start[-1], hq, d)
-    out, lse = c.attend(q, causal)
+    out, lse = c.attend(q, causal, **bounds(c, rest))
     assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
     check_attention_sink(c, q, out, lse, d ** -0.5, causal, -1, 0)
 
@@ -66,8 +76,9 @@ def test_windows(gpu, dtype, nq, window, sink):
     check_attention_sink(c, q, out, lse, 0.125, True, window, sink)
 
 
+@pytest.mark.parametrize("rest", RESTS)
 @pytest.mark.parametrize("dtype,hq", [("bf16", 4), ("bf16", 40), ("f32", 4), ("f32", 40)])
-def test_extremes(gpu, dtype, hq):
+def test_extremes(gpu, rest, dtype, hq):
     """Scores that rise from the prefix to the rest or fall off, by far; an infinity that every row sees; nothing but
     unwritten rows behind the sequences."""
     c = Branches(dtype, NHD, 1, 64, 16, [(500, token([60, 1, 33])), (40, token([300, 2]))], seed=hq)
@@ -77,11 +88,11 @@ def test_extremes(gpu, dtype, hq):
     c.fill()
     q = c.normal(5, hq, 64)
     for scale in (0.125, 30.0, -3.0):
-        out, lse = c.attend(q, scale=scale)
+        out, lse = c.attend(q, scale=scale, **bounds(c, rest))
         check_attention_sink(c, q, out, lse, scale, True, -1, 0)
     c.values[0][7, 0, 3] = c.values[1][7, 0, 3] = c.values[2][7, 0, 3] = math.inf
     c.fill()
-    out, lse = c.attend(q)
+    out, lse = c.attend(q, **bounds(c, rest))
     assert (out[:3, :, 3] == math.inf).all() and torch.isfinite(out[3:]).all()
     out[:3, :, 3] = 0
     for s in range(3):
@@ -89,13 +100,14 @@ def test_extremes(gpu, dtype, hq):
     check_attention_sink(c, q, out, lse, 0.125, True, -1, 0)
 
 
+@pytest.mark.parametrize("rest", RESTS)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_lengths_by_head(gpu, dtype):
+def test_lengths_by_head(gpu, rest, dtype):
     c = Branches(dtype, HND, 4, 64, 16, [(130, token([300, 200, 40]))], (), [(1, 20)], seed=6).fill()
     lens = [[430, 131, 400, 200], [131, 132, 300, 330], [170, 160, 150, 140], [20, 1, 5, 0]]
     c.kv_len = ints(lens)
     q = c.normal(4, 8, 64)
-    out, lse = c.attend(q, False)
+    out, lse = c.attend(q, False, **bounds(c, rest))
     assert dcp.dcp_get_status(c.status) == dcp.DCP_OK
     check_attention_sink(c, q, out, lse, 0.125, False, -1, 0, kv_of=lens)
 
@@ -103,7 +115,8 @@ def test_lengths_by_head(gpu, dtype):
 @pytest.mark.parametrize("dtype,hq,nq", [("bf16", 2, 1), ("bf16", 60, 1), ("bf16", 2, 60), ("f32", 2, 1), ("f32", 2, 100)])
 @pytest.mark.parametrize("what", ["start", "start order", "prefix", "negative prefix", "prefix past the table",
                                   "prefix among the new tokens", "rows", "entry", "length", "q_start"])
-def test_bad_state_is_reported(gpu, dtype, hq, nq, what):
+@pytest.mark.parametrize("rest", [None, 0, 50000])
+def test_bad_state_is_reported(gpu, rest, dtype, hq, nq, what):
     c = Branches(dtype, NHD, 1, 64, 8, [(100, [(nq, nq + 9), (nq, nq)]), (60, [(nq, nq + 3), (nq, nq + 8)])]).fill()
     q = c.normal(4 * nq, hq, 64)
     over = {}
@@ -127,7 +140,9 @@ def test_bad_state_is_reported(gpu, dtype, hq, nq, what):
         c.kv_len[1] = 1 << 28
     else:
         c.q_start[1] = -4
-    out, lse = c.attend(q, groups=c.groups(**over))
+    if rest is not None:
+        over["max_prefix"] = FAR
+    out, lse = c.attend(q, groups=c.groups(**over), batch=c.batch() if rest is None else c.batch(max_kv=FAR + rest))
     assert dcp.dcp_get_status(c.status) == dcp.DCP_EDEVICE
     if what not in ("start", "start order", "rows"):  # the sound group has its result
         r = slice(2 * nq, None)
@@ -135,22 +150,25 @@ def test_bad_state_is_reported(gpu, dtype, hq, nq, what):
         check_attention_sink(c, q[r], out[r], lse[r], 0.125, True, -1, 0)
 
 
-def test_same_as_alone(gpu):
+@pytest.mark.parametrize("rest", RESTS)
+def test_same_as_alone(gpu, rest):
     """Branches read through their group's prefix give what they give one by one, up to the order of sums."""
     c = Branches("bf16", HND, 8, 128, 16, [(2000, token(range(1, 20)))]).fill()
     q = c.normal(19, 40, 128)
-    out, lse = c.attend(q)
+    out, lse = c.attend(q, **bounds(c, rest))
     ws = dcp.new_workspace(dcp.dcp_attention_workspace_size(c.pool(), c.batch(), dcp.AttnConfig(), 40))
     alone, lse_alone = torch.empty_like(out), torch.empty_like(lse)
     dcp.dcp_paged_attention(c.pool(), c.batch(), dcp.AttnConfig(), q, alone, lse_alone, ws)
     assert (lse - lse_alone).abs().max() <= 2.0 ** -16 and (out.float() - alone.float()).abs().max() <= 2.0 ** -8
 
 
-def test_in_a_graph_with_other_lengths(gpu):
+@pytest.mark.parametrize("rest", RESTS)
+def test_in_a_graph_with_other_lengths(gpu, rest):
     """Recorded once, replayed with other prefixes and lengths; the result does not depend on the run."""
     c = Branches("bf16", HND, 2, 64, 16, [(640, token([40, 50, 33])), (320, token([300, 20]))]).fill()
     q = c.normal(5, 20, 64)
-    cfg, pool, batch, groups = dcp.AttnConfig(), c.pool(), c.batch(), c.groups()
+    far = bounds(c, rest)
+    cfg, pool, batch, groups = dcp.AttnConfig(), c.pool(), far.get("batch", c.batch()), far.get("groups", c.groups())
     ws = dcp.new_workspace(dcp.dcp_shared_attention_workspace_size(pool, batch, groups, cfg, 20))
     out, lse = torch.empty_like(q), torch.empty(5, 20, device="cuda")
     dcp.dcp_shared_attention(pool, batch, groups, cfg, q, out, lse, ws)
@@ -181,10 +199,10 @@ def test_two_streams_and_a_workspace_that_others_use(gpu):
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     outs = []
-    for _ in range(3):
+    for rest in (None, 0, 50000):
         with torch.cuda.stream(s):
-            outs.append((a, qa, *a.attend(qa)))
-        outs.append((b, qb, *b.attend(qb)))
+            outs.append((a, qa, *a.attend(qa, **bounds(a, rest))))
+        outs.append((b, qb, *b.attend(qb, **bounds(b, rest))))
     s.synchronize()
     for c, q, out, lse in outs:
         check_attention_sink(c, q, out, lse, c.d ** -0.5, True, -1, 0)
@@ -192,7 +210,7 @@ def test_two_streams_and_a_workspace_that_others_use(gpu):
     cfg, size = dcp.AttnConfig(), 0
     pages = dcp.PagePool(a.k[None], a.v[None], 16, a.status)
     for c, hq in ((a, 40), (b, 4)):
-        size = max(size, dcp.dcp_shared_attention_workspace_size(c.pool(), c.batch(), c.groups(), cfg, hq),
+        size = max(size, dcp.dcp_shared_attention_workspace_size(c.pool(), *c.far().values(), cfg, hq),
                    dcp.dcp_attention_workspace_size(c.pool(), c.batch(), cfg, hq))
     size = max(size, dcp.dcp_pages_workspace_size(pages, 2, a.tables.shape[1]))
     ws = dcp.new_workspace(size)
@@ -200,7 +218,7 @@ def test_two_streams_and_a_workspace_that_others_use(gpu):
     for _ in range(2):
         for c, q in ((a, qa), (b, qb)):
             out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
-            dcp.dcp_shared_attention(c.pool(), c.batch(), c.groups(), cfg, q, out, lse, ws)
+            dcp.dcp_shared_attention(c.pool(), *c.far().values(), cfg, q, out, lse, ws)
             check_attention_sink(c, q, out, lse, c.d ** -0.5, True, -1, 0)
             dcp.dcp_paged_attention(c.pool(), c.batch(), cfg, q, out, lse, ws)
             check_attention_sink(c, q, out, lse, c.d ** -0.5, True, -1, 0)
@@ -209,7 +227,8 @@ def test_two_streams_and_a_workspace_that_others_use(gpu):
     assert dcp.dcp_get_status(a.status) == dcp.DCP_OK == dcp.dcp_get_status(b.status)
 
 
-def test_long_pool(gpu):
+@pytest.mark.parametrize("rest", [None, 0, 50000])
+def test_long_pool(gpu, rest):
     """Element offsets past 2^31 in the pool, strided q, no lse."""
     bs, nb = 64, (1 << 31) // (64 * 128) + 700
     c = Branches("bf16", HND, 1, 128, bs, [(12800, token([100, 70, 20, 9]))], seed=9)
@@ -219,7 +238,8 @@ def test_long_pool(gpu):
     c.table, c.k, c.v = c.tables.cpu().numpy(), k, v
     c.fill()
     q = c.normal(4, 24, 128)[:, 4:22]
-    cfg, pool, batch, groups = dcp.AttnConfig(), c.pool(), c.batch(), c.groups()
+    far = bounds(c, rest)
+    cfg, pool, batch, groups = dcp.AttnConfig(), c.pool(), far.get("batch", c.batch()), far.get("groups", c.groups())
     ws = dcp.new_workspace(dcp.dcp_shared_attention_workspace_size(pool, batch, groups, cfg, 18))
     out = torch.empty(4, 18, 128, dtype=torch.bfloat16, device="cuda")
     dcp.dcp_shared_attention(pool, batch, groups, cfg, q, out, None, ws)
