@@ -196,59 +196,70 @@ __device__ __forceinline__ void join_rows(const AttendParams& a, const Parts& pa
   const int width = kPartHead + a.pool.D;
   // [rows][splits] the parts' maxima, then their weights, [rows][splits] their sums, [rows] the row's factor
   float* const weight = reinterpret_cast<float*>(scratch);
-  const int64_t used = (join_scratch(rows, splits) + 15) & ~(int64_t)15;
-  __syncthreads();
-  const OwnParts here{reinterpret_cast<const float*>(scratch + used),
-                      reinterpret_cast<const float*>(scratch + used) + rows * width, (int64_t)rows * width, width};
-  const uint32_t to = smem_u32(scratch + used);
   auto near = [](const auto* x) { return *x; };
   auto far = [](const auto* x) { return __ldcg(x); };
-  const int64_t all = used + (int64_t)rows * splits * width * 4;
+  auto used_by = [&](int some) { return (join_scratch(some, splits) + 15) & ~(int64_t)15; };
   if constexpr (Parts::kByRow) {
     // The rows lie apart: their places are found once, a thread a row, then a warp fetches a row (each of its threads
-    // finding it anew made a join of 5 rows of 21 parts take 13 us).
-    if (all + 8 * rows * splits <= room) {  // (a row is a multiple of 16 bytes)
-      const float** const place = reinterpret_cast<const float**>(scratch + all);
-      float* const sum = weight + rows * splits;
-      for (int u = threadIdx.x; u < rows * splits; u += blockDim.x) {
-        const int k = u / rows, r = u - k * rows;
-        const float* const at = parts.row(k, r);
+    // finding it anew made a join of 5 rows of 21 parts take 13 us).  As many rows at a time as fit (read from global memory
+    // 5 rows of 39 parts took 30 us).
+    const int some = (int)min((int64_t)rows, (room - 16) / ((int64_t)splits * (width * 4 + 16) + 4));
+    for (int r0 = 0; some && r0 < rows; r0 += some) {
+      const int now = min(some, rows - r0);
+      const int64_t used = used_by(now);
+      const float* const values = reinterpret_cast<const float*>(scratch + used);
+      const float** const place = reinterpret_cast<const float**>(scratch + used + (int64_t)now * splits * width * 4);
+      float* const sum = weight + now * splits;
+      __syncthreads();
+      for (int u = threadIdx.x; u < now * splits; u += blockDim.x) {
+        const int k = u / now, r = u - k * now;
+        const float* const at = parts.row(k, r0 + r);
         place[u] = at + kPartHead;
         const float2 ml = far(reinterpret_cast<const float2*>(at));
         weight[r * splits + k] = ml.x;
         sum[r * splits + k] = ml.y;
       }
       __syncthreads();
+      const uint32_t to = smem_u32(values);
       const int c = threadIdx.x & 31, warps = blockDim.x >> 5;
-      for (int u0 = threadIdx.x >> 5; u0 < splits * rows; u0 += 8 * warps) {
+      for (int u0 = threadIdx.x >> 5; u0 < splits * now; u0 += 8 * warps) {
         const float* from[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) from[j] = place[min(u0 + j * warps, splits * rows - 1)];
+        for (int j = 0; j < 8; ++j) from[j] = place[min(u0 + j * warps, splits * now - 1)];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int u = u0 + j * warps;
-          if (u < splits * rows && c < a.pool.D / 4) cp_async16(to + (u * width + kPartHead + c * 4) * 4, from[j] + c * 4);
+          if (u < splits * now && c < a.pool.D / 4) cp_async16(to + (u * width + kPartHead + c * 4) * 4, from[j] + c * 4);
         }
       }
       cp_async_commit();
       cp_async_wait<0>();
       __syncthreads();
+      join_values<T>(a, OwnParts{values, values + now * width, (int64_t)now * width, width}, splits, now, row0 + r0, lo, kh,
+                     weight, near);
+    }
+    if (some) return;
+  } else {
+    const int64_t used = used_by(rows);
+    __syncthreads();
+    if (used + (int64_t)rows * splits * width * 4 <= room) {
+      const int chunks = rows * width / 4;
+      const uint32_t to = smem_u32(scratch + used);
+      for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
+        const int k = u / chunks;
+        cp_async16(to + u * 16, parts.part(k) + (u - k * chunks) * 4);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+      const float* const values = reinterpret_cast<const float*>(scratch + used);
+      const OwnParts here{values, values + rows * width, (int64_t)rows * width, width};
+      join_heads(here, splits, rows, weight, near);
       join_values<T>(a, here, splits, rows, row0, lo, kh, weight, near);
       return;
     }
-  } else if (all <= room) {
-    const int chunks = rows * width / 4;
-    for (int u = threadIdx.x; u < splits * chunks; u += blockDim.x) {
-      const int k = u / chunks;
-      cp_async16(to + u * 16, parts.part(k) + (u - k * chunks) * 4);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    join_heads(here, splits, rows, weight, near);
-    join_values<T>(a, here, splits, rows, row0, lo, kh, weight, near);
-    return;
   }
+  __syncthreads();
   join_heads(parts, splits, rows, weight, far);
   join_values<T>(a, parts, splits, rows, row0, lo, kh, weight, far);
 }
