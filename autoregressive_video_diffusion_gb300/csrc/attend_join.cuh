@@ -48,33 +48,54 @@ __device__ __forceinline__ float* prefix_part(const PrefixPlan& pre, int D, int 
   return pre.part + ((((int64_t)slot * pre.heads + kh) * pre.tiles + tile) * pre.rows + r) * (kPartHead + D);
 }
 
-// The piece of slot `slot`, by a whole warp: each group with rows and a prefix has a slot, and of those left over as many
-// as its share of all prefixes, rounded down.  (Without rows: len = 0.)  With `note` the groups' slots go to the table.
+// The piece of slot `slot`, by a whole warp.  All pieces are at most L tiles long, L (2 at least) as small as the slots allow among 31
+// lengths from their even share up (a lane tries one each; the last, a piece a group, always fits).  A group without rows or
+// prefix has none.  (Without rows: len = 0.)  With `note` the groups' slots go to the table.
 __device__ __forceinline__ PrefixPiece prefix_piece(const AttendParams& a, const PrefixPlan& pre, int slot, bool note) {
-  const int lane = threadIdx.x & 31;
-  auto units = [&](int g, GroupRows& of) -> int64_t {
-    if (g >= a.groups.n || !group_at(a, g, of) || of.len == 0) return 0;
-    return ((int64_t)of.prefix + pre.unit - 1) / pre.unit;
+  const int lane = threadIdx.x & 31, n = a.groups.n;
+  auto units = [&](int g, GroupRows& of) -> uint32_t {
+    if (g >= n || !group_at(a, g, of) || of.len == 0) return 0;
+    return ((uint32_t)of.prefix + pre.unit - 1) / pre.unit;
   };
   GroupRows of{};
+  const uint32_t mine = units(lane, of);  // of group `lane`: most calls have no more groups than a warp has lanes
   int64_t total = 0;
-  for (int g = lane; g < a.groups.n; g += 32) total += units(g, of);
+  uint32_t most = 0;
+  for (int g = lane; g < n; g += 32) {
+    GroupRows other;
+    const uint32_t w = g == lane ? mine : units(g, other);
+    total += w;
+    most = max(most, w);
+  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  for (int o = 16; o; o >>= 1) {
+    total += __shfl_xor_sync(~0u, total, o);
+    most = max(most, __shfl_xor_sync(~0u, most, o));
+  }
+  const uint32_t even = (uint32_t)((total + pre.slots - 1) / pre.slots);
+  const uint32_t length = lane == 31 ? max(most, 1u) : max(2u, (uint32_t)(even + (uint64_t)even * lane * lane / 64));
+  int64_t pieces = 0;
+  for (int g0 = 0; g0 < n; g0 += 32) {
+    GroupRows other;
+    const uint32_t w = g0 ? units(g0 + lane, other) : mine;
+    for (int k = 0; k < min(32, n - g0); ++k) pieces += (__shfl_sync(~0u, w, k) + length - 1) / length;
+  }
+  const bool fits = lane == 31 || (pieces <= pre.slots && (most + length - 1) / length <= (uint32_t)pre.cap);
+  const uint32_t chosen = __shfl_sync(~0u, length, __ffs(__ballot_sync(~0u, fits)) - 1);
   PrefixPiece found{};
   int first = 0;  // slots of the groups before
-  for (int g0 = 0; g0 < a.groups.n; g0 += 32) {
-    const int64_t w = units(g0 + lane, of);
-    const int n = w ? (int)min((int64_t)pre.cap, min(w, 1 + (pre.slots - a.groups.n) * w / total)) : 0;
-    int end = n;
+  for (int g0 = 0; g0 < n; g0 += 32) {
+    const uint32_t w = g0 ? units(g0 + lane, of) : mine;
+    const int count = (int)((w + chosen - 1) / chosen);
+    int end = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(~0u, end, o);
       if (lane >= o) end += y;
     }
-    const int at = first + end - n;
-    if (note && g0 + lane < a.groups.n) pre.table[g0 + lane] = make_int2(at, n);
-    const uint32_t hit = __ballot_sync(~0u, slot >= at && slot < at + n);
+    const int at = first + end - count;
+    if (note && g0 + lane < n) pre.table[g0 + lane] = make_int2(at, count);
+    const uint32_t hit = __ballot_sync(~0u, slot >= at && slot < at + count);
     if (hit) {
       const int who = __ffs(hit) - 1;
       found.of.g = __shfl_sync(~0u, of.g, who);
@@ -83,7 +104,7 @@ __device__ __forceinline__ PrefixPiece prefix_piece(const AttendParams& a, const
       found.of.len = __shfl_sync(~0u, of.len, who);
       found.of.prefix = __shfl_sync(~0u, of.prefix, who);
       found.split = slot - __shfl_sync(~0u, at, who);
-      found.splits = __shfl_sync(~0u, n, who);
+      found.splits = __shfl_sync(~0u, count, who);
       if (!note) break;
     }
     first += __shfl_sync(~0u, end, 31);

@@ -72,7 +72,7 @@ struct PrefixPlan {
   float* part;                  // [slot][KV head][tile][row][kPartHead + D]
   int2* table;                  // [group] first slot, number of slots
   int32_t slots, tiles, rows, heads;
-  int32_t unit, cap;            // keys of the smallest piece worth a slot; slots of a group at most
+  int32_t unit, cap;            // keys of a tile; slots of a group at most
 };
 
 struct AttendParams {

@@ -59,7 +59,7 @@ SharedPlan plan_shared(const AttendParams& a, int64_t max_kv, int64_t max_prefix
   const int64_t ctas = t.tiled ? sm_count() : 2 * sm_count(), room = ctas / ((int64_t)t.pre.tiles * a.pool.H);
   const int64_t n = a.groups.n;
   t.pre.slots = (int)std::min<int64_t>(65535, std::max(room, n + std::min(n, 2 * room + 1)));
-  t.pre.unit = t.tiled ? 256 : half ? 128 : 64;
+  t.pre.unit = t.tiled ? 128 : half ? 64 : 32;
   t.pre.cap = join_parts_room(a, t.rest) - (t.rest.even ? t.rest.splits : std::max(t.rest.splits, 1));
   t.part_bytes = (size_t)t.pre.slots * t.pre.heads * t.pre.tiles * t.pre.rows * (kPartWidth + a.pool.D) * 4;
   return t;
