@@ -633,28 +633,23 @@ def _rows_of(t: torch.Tensor, pool: KVPool, batch: SeqBatch, heads: int, what: s
     return token if n > 1 else heads * D
 
 
-def _append_args(what: str, pool: KVPool, batch: SeqBatch, q, k, v, positions, n_axes: int, q_out):
-    """(q, its token stride, query heads, k, v, their token stride, positions, q_out) of an append, checked."""
-    kv_stride = _rows_of(k, pool, batch, pool.H, what)
-    if _rows_of(v, pool, batch, pool.H, what) != kv_stride or \
-            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
-                                        not positions.is_cuda or positions.numel() != n_axes * batch.total_q)):
-        raise DcpError(what, DCP_EINVAL)
-    hq, q_stride = 0, 0
-    if q is not None:
-        hq = q.shape[1]
-        q_stride = _rows_of(q, pool, batch, hq, what)
-        if q_out is None or _rows_of(q_out, pool, batch, hq, what) != hq * pool.D:
-            raise DcpError(what, DCP_EINVAL)
-    return _ptr(q), q_stride, hq, _ptr(k), _ptr(v), kv_stride, _ptr(positions), _ptr(q_out)
-
-
 def dcp_rope_append(pool: KVPool, batch: SeqBatch, plan: DcpRopePlanC, q, k: torch.Tensor, v: torch.Tensor,
                     positions, q_out, stream=None) -> None:
     """Turn q and k of the new tokens, put k and v into the pool's pages; q_out gets the turned q.  q, k, v are
     [total_q][heads][D] (views of one fused projection are fine), positions int32 [total_q] or None."""
-    args = _append_args("dcp_rope_append", pool, batch, q, k, v, positions, 1, q_out)
-    _check(lib.dcp_rope_append(pool.ref, batch.ref, plan, *args, _stream(stream)), "dcp_rope_append")
+    kv_stride = _rows_of(k, pool, batch, pool.H, "dcp_rope_append")
+    if _rows_of(v, pool, batch, pool.H, "dcp_rope_append") != kv_stride or \
+            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
+                                        not positions.is_cuda or positions.numel() != batch.total_q)):
+        raise DcpError("dcp_rope_append", DCP_EINVAL)
+    hq, q_stride = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        q_stride = _rows_of(q, pool, batch, hq, "dcp_rope_append")
+        if q_out is None or _rows_of(q_out, pool, batch, hq, "dcp_rope_append") != hq * pool.D:
+            raise DcpError("dcp_rope_append", DCP_EINVAL)
+    _check(lib.dcp_rope_append(pool.ref, batch.ref, plan, _ptr(q), q_stride, hq, _ptr(k), _ptr(v), kv_stride,
+                               _ptr(positions), _ptr(q_out), _stream(stream)), "dcp_rope_append")
 
 
 def dcp_rope_axes(cfgs) -> DcpRopeAxesC:
@@ -691,12 +686,23 @@ def dcp_norm_rope_append(pool: KVPool, batch: SeqBatch, axes: DcpRopeAxesC, norm
                          v: torch.Tensor, positions, q_out, stream=None) -> None:
     """dcp_rope_append with q and k normalised before they turn; positions int32 [n_axes][total_q] (an axis behind the
     other), or None where there is one axis and it is the cache position."""
-    args = _append_args("dcp_norm_rope_append", pool, batch, q, k, v, positions, axes.n_axes, q_out)
-    for w, heads in zip(norm.weights, (args[2], pool.H)):
+    what = "dcp_norm_rope_append"
+    kv_stride = _rows_of(k, pool, batch, pool.H, what)
+    if _rows_of(v, pool, batch, pool.H, what) != kv_stride or \
+            (positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous() or
+                                        not positions.is_cuda or positions.numel() != axes.n_axes * batch.total_q)):
+        raise DcpError(what, DCP_EINVAL)
+    hq, q_stride = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        q_stride = _rows_of(q, pool, batch, hq, what)
+        if q_out is None or _rows_of(q_out, pool, batch, hq, what) != hq * pool.D:
+            raise DcpError(what, DCP_EINVAL)
+    for w, heads in zip(norm.weights, (hq, pool.H)):
         if w is not None and w.shape != ((pool.D,) if w.dim() == 1 else (heads, pool.D)) and (heads or w.dim() == 1):
-            raise DcpError("dcp_norm_rope_append", DCP_EINVAL)
-    _check(lib.dcp_norm_rope_append(pool.ref, batch.ref, axes, norm.ref, *args, _stream(stream)),
-           "dcp_norm_rope_append")
+            raise DcpError(what, DCP_EINVAL)
+    _check(lib.dcp_norm_rope_append(pool.ref, batch.ref, axes, norm.ref, _ptr(q), q_stride, hq, _ptr(k), _ptr(v),
+                                    kv_stride, _ptr(positions), _ptr(q_out), _stream(stream)), what)
 
 
 @dataclass
