@@ -13,8 +13,8 @@
 // summed apart, and a tile's weighted values start from 0 and are added to the running ones by one fma, so that the
 // tensor cores' accumulation (which may truncate) never runs over more than a tile.
 //
-// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 309-325 us,
-// 6.2-6.5 TB/s; one token over 1531 keys 13.2 us (launch and look-ups 3.4, keys 2, two tiles 1.2, parts and join 3);
+// Measured: 48 sequences' tokens, 40 query heads over 8 KV heads of 128, 200 .. 16000 keys (2.02 GB): 307-324 us,
+// 6.2-6.6 TB/s; one token over 1531 keys 12.1 us (launch and look-ups 3, keys 2, two tiles 1.2, parts and join 3);
 // fp32, 3 sequences of 100 .. 513 tokens, 8 heads of 64, 513 .. 3001 keys: 195 us, bound by the tf32 products (40 % of
 // their rate while a CTA runs).
 #pragma once

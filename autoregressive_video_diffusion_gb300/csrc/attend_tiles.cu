@@ -25,7 +25,8 @@
 // NaN before they hand over their weights; rows that do see those get them back in the epilogue, from the cache.
 //
 // Measured: 6240 tokens, 40 query heads over 8 KV heads of 128, 25907 keys: 2155-2180 us, 1520-1540 TFLOP/s.  Causal
-// chunks of 130 .. 2048 tokens behind up to 12000 keys: 700-721 us, 1330-1370 TFLOP/s.  What bounds it is the chain of
+// chunks of 130 .. 2048 tokens behind up to 12000 keys: 680-721 us, 1330-1370 TFLOP/s.  A chunk of 6240 over a window of
+// 18720 and a sink of 6240 positions: 2190-2220 us, 1440-1460 TFLOP/s.  What bounds it is the chain of
 // a row tile (products 1100 clocks, scores ready 300, weights 1150, products awake 300), of which the other row tile's
 // products cover 1100.
 #include <cuda.h>

@@ -469,9 +469,9 @@ typedef struct dcp_norm_config {
 /* dcp_rope_append whose q and k are normalised before they turn, one launch and one pass over the data.  Same arguments,
  * layouts and errors, but
  *   positions_dev: int32 [n_axes][total_q], an axis behind the other; null (the cache position) for one axis only.
- * Everything between reading and the one rounding to the pool's type is held in fp32.  Any finite values are normalised as
- * the formula says (squares that would leave fp32 are taken of scaled values); a row of zeros with eps 0 gives NaN, and an
- * infinity or NaN has its usual effect on what shares its mean. */
+ * Everything between reading and the one rounding to the pool's type is held in fp32.  Values of any size are normalised as
+ * the formula says (squares that would leave fp32 are taken of scaled values), where eps or the mean square's root is 2^-126
+ * or more; a row of zeros with eps 0 gives NaN, and an infinity or NaN has its usual effect on what shares its mean. */
 dcp_status dcp_norm_rope_append(const dcp_kv_pool* pool, const dcp_seq_batch* batch, const dcp_rope_axes* axes,
                                 const dcp_norm_config* norm, const void* q_dev, int64_t q_stride, int32_t Hq,
                                 const void* k_dev, const void* v_dev, int64_t kv_stride, const int32_t* positions_dev,
@@ -513,14 +513,16 @@ dcp_status dcp_paged_attention(const dcp_kv_pool* pool, const dcp_seq_batch* bat
 /* Attention of sequences that share their first positions (branches that dcp_pages_fork made of one session): group g is
  * the sequences start[g] .. start[g+1] - 1, which hold the same keys and values in their first prefix_len[g] positions.
  * Results are those of dcp_paged_attention; a prefix is read once for all of its group, through the table row of any of
- * them (so it is enough that their pages hold the same).  A prefix lies before the new tokens: prefix_len <= kv_len - q_len of each sequence with new tokens.  Sequences
- * before start[0] or from start[n_groups] on share nothing.
+ * its sequences (it is enough that their pages hold the same).  A prefix lies before the new tokens: prefix_len <= kv_len -
+ * q_len of each sequence with new tokens.  Sequences before start[0] or from start[n_groups] on share nothing.
  * Groups are worked on together where that pays: not under a window, nor where a sequence has many rows of its own (more
- * than 64 of a KV head, 128 in fp32). */
+ * than 64 of a KV head, 128 in fp32), nor where little is not read again, (n_seqs - n_groups) * max_prefix positions by the
+ * bounds given (less than 80 MB of keys and values, 30 in fp32). */
 typedef struct dcp_prefix_groups {
   int32_t n_groups;            /* 1 .. n_seqs */
   int32_t max_q;               /* no group has more new tokens, its sequences together */
-  int64_t max_prefix;          /* a bound of the longest prefix, for dividing the work: larger ones still work */
+  int64_t max_prefix;          /* a bound of the longest prefix, for dividing the work (with max_kv - max_prefix as one of
+                                  what lies behind it): longer ones still work */
   const int32_t* start;        /* device [n_groups + 1] */
   const int32_t* prefix_len;   /* device [n_groups] */
 } dcp_prefix_groups;
