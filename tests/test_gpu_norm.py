@@ -186,6 +186,21 @@ def test_values_past_the_squares_in_pieces_and_blocks(gpu, dtype, hq):
     check_norm_turned(c.k[c.rows(0, 0, n)], k, None, 0.0, TOKEN, np.arange(n)[None], [cfg])
 
 
+@pytest.mark.parametrize("span", [HEAD, TOKEN], ids=["head", "token"])
+@pytest.mark.parametrize("shape", [(64,), (2, 64)], ids=["one", "heads"])
+def test_weights_of_one_kind_only(gpu, span, shape):
+    for which in range(2):
+        c = Cache("bf16", HND, 2, 64, 8, [9], [20], seed=which)
+        q, k, v = c.normal(9, 2, 64), c.normal(9, 2, 64), c.normal(9, 2, 64)
+        w, cfg, out = (1 + 0.3 * torch.randn(*shape, generator=c.g)).cuda(), dcp.RopeConfig(44), torch.empty_like(q)
+        weights = (w, None) if which == 0 else (None, w)
+        dcp.dcp_norm_rope_append(c.pool(), c.batch(), dcp.dcp_rope_axes([cfg]), dcp.NormConfig(*weights, span=span), q, k, v,
+                                 None, out)
+        pos = np.arange(11, 20)[None]
+        check_norm_turned(out, q, weights[0], 1e-6, span, pos, [cfg])
+        check_norm_turned(c.k[new_rows(c, 0)], k, weights[1], 1e-6, span, pos, [cfg])
+
+
 def test_in_a_graph_and_on_another_stream(gpu):
     c = Cache("bf16", NHD, 2, 64, 8, [3, 4], [20, 30], seed=4)
     q, k, v = c.normal(7, 4, 64), c.normal(7, 2, 64), c.normal(7, 2, 64)

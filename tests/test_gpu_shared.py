@@ -151,6 +151,18 @@ def test_bad_state_is_reported(gpu, rest, dtype, hq, nq, what):
 
 
 @pytest.mark.parametrize("rest", RESTS)
+def test_rows_behind_the_last_sequence_are_left(gpu, rest):
+    for dtype, hq in (("bf16", 4), ("bf16", 60), ("f32", 4)):
+        c = Branches(dtype, HND, 1, 64, 16, [(100, token([5, 9, 1])), (40, token([300, 2]))], seed=hq).fill()
+        q = c.normal(9, hq, 64)
+        far = dict(total_q=9, **({} if rest is None else dict(max_kv=FAR + rest)))
+        groups = c.groups() if rest is None else c.groups(max_prefix=FAR)
+        out, lse = c.attend(q, batch=c.batch(**far), groups=groups)
+        assert torch.isnan(out[5:]).all() and torch.isnan(lse[5:]).all()
+        check_attention_sink(c, q[:5], out[:5], lse[:5], 0.125, True, -1, 0)
+
+
+@pytest.mark.parametrize("rest", RESTS)
 def test_same_as_alone(gpu, rest):
     """Branches read through their group's prefix give what they give one by one, up to the order of sums."""
     c = Branches("bf16", HND, 8, 128, 16, [(2000, token(range(1, 20)))]).fill()
