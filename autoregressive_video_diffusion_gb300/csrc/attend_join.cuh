@@ -48,9 +48,9 @@ __device__ __forceinline__ float* prefix_part(const PrefixPlan& pre, int D, int 
   return pre.part + ((((int64_t)slot * pre.heads + kh) * pre.tiles + tile) * pre.rows + r) * (kPartHead + D);
 }
 
-// The piece of slot `slot`, by a whole warp.  All pieces are at most L tiles long, L (2 at least) as small as the slots allow among 31
-// lengths from their even share up (a lane tries one each; the last, a piece a group, always fits).  A group without rows or
-// prefix has none.  (Without rows: len = 0.)  With `note` the groups' slots go to the table.
+// The piece of slot `slot`, by a whole warp.  All pieces are at most L tiles long, L (2 at least) as small as the slots
+// allow among 31 lengths from their even share up (a lane tries one each; the last, a piece a group, always fits).  A group
+// without rows or prefix has none.  (A slot without a piece: len = 0.)  With `note` the groups' slots go to the table.
 __device__ __forceinline__ PrefixPiece prefix_piece(const AttendParams& a, const PrefixPlan& pre, int slot, bool note) {
   const int lane = threadIdx.x & 31, n = a.groups.n;
   auto units = [&](int g, GroupRows& of) -> uint32_t {

@@ -40,7 +40,8 @@ RowPlan plan_rows(const AttendParams& a, int64_t max_kv) {
   // Items that may differ in length: two CTAs of an SM at a time, each with the same number of key tiles (48 sequences
   // of 200 .. 16000 positions: 324 us, against 354 in pieces of a fixed span; items alike are cut as well by a span,
   // without the sums: one token over 1531 positions 12.3 us, against 14.0).
-  r.even = (int64_t)a.b.max_q * a.G <= 16 && items <= (a.sink ? kEvenItemsSink : kEvenItems) && (a.b.n_seqs > 1 || a.b.kv_per_head) && !few;
+  r.even = (int64_t)a.b.max_q * a.G <= 16 && items <= (a.sink ? kEvenItemsSink : kEvenItems) &&
+           (a.b.n_seqs > 1 || a.b.kv_per_head) && !few;
   if (r.even) {
     r.splits = 2 * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
     r.span = 0;
@@ -76,7 +77,8 @@ RowPlan plan_rest(const AttendParams& a, int64_t max_kv) {
   if (r.splits <= 1 || max_kv > 16 * keys) return r;
   const int64_t items = (int64_t)r.tiles * a.pool.H * a.b.n_seqs;
   r.even = 0;
-  r.splits = items > kDoneItems ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(2 * sm_count() / items, max_kv / (4 * keys)));
+  const int64_t splits = std::min<int64_t>(2 * sm_count() / items, max_kv / (4 * keys));
+  r.splits = items > kDoneItems || splits < 1 ? 1 : (int)splits;
   r.span = (int)((max_kv + r.splits - 1) / r.splits + keys - 1) / keys * keys;
   r.bytes = (size_t)items * r.splits * r.rows * (kPartHead + a.pool.D) * 4;
   return r;

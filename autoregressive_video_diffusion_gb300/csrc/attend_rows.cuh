@@ -27,8 +27,8 @@ namespace dcp {
 
 constexpr int kMaxSplits = 64;
 constexpr int kEvenItems = 512;       // items whose tiles can be shared evenly,
-constexpr int kEvenItemsSink = 1024;  // and under a window whose first positions stay visible (768 items of 4200 keys at most:
-                                      // 251 us, against 256 in pieces of a fixed span)
+constexpr int kEvenItemsSink = 1024;  // and under a window whose first positions stay visible (768 items of 4200 keys at
+                                      // most: 251 us, against 256 in pieces of a fixed span)
 
 constexpr int kMaxSms = 160;       // the join's scratch holds a part of two CTAs on each,
 constexpr int kLeastSlots = 32;    // and at least so many of a shared prefix
@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(Rows<T, DP, MW>::kThreads, Rows<T, DP, MW>::kC
         if (!opens) piece.begin += (int)(at - f0 - kBegin) * R::kKeys;
         if (!closes) piece.end = seen.begin + (int)(stop - f0 - kBegin) * R::kKeys;
         const int64_t slot = (int64_t)16 * width;  // parts of a CTA: of an item it goes on with, of one it begins
-        float* const part = opens && closes && !(FORM == kRest && p.pre.slots) ? nullptr : p.part + (2 * (int64_t)blockIdx.x + opens) * slot;
+        const bool parted = !opens || !closes || (FORM == kRest && p.pre.slots);
+        float* const part = parted ? p.part + (2 * (int64_t)blockIdx.x + opens) * slot : nullptr;
         attend_piece<T, DP, 1, FORM>(p, smem, s_off, s, kh, lo, len, kv, 0, rows, piece, part);
         if (part) {
           const int64_t c0 = ((f0 + kBegin + 1) * ctas - 1) / total, c1 = (f1 * ctas - 1) / total;
