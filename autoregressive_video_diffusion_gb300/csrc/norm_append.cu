@@ -13,12 +13,14 @@
 // Squares leave fp32 for values past 2^60 or below 2^-50 with an eps as small: such a sum is taken again of values scaled
 // by a power of two, which every norm of the row shares, so that any values give what the formula says.
 //
-// The bytes would take 57 us for the first case below; what bounds it is the instructions around the arithmetic (66 million
-// warp instructions, issued at two thirds of the schedulers' rate).  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in
-// bf16, means of tokens, three axes, fp32 weights of each head 90 us (4.3 TB/s); 5875 tokens of 20 + 4 + 4 fp32 heads of 96
-// 44 us; 32 tokens 7.8 us.  Steps, us of these two: a token a CTA, its heads in registers 135 / 51; persistent CTAs with the
+// The bytes would take 57 us for the first case below; what bounds it is the instructions around the arithmetic (59 million
+// warp instructions, issued at 57 % of the schedulers' rate).  Measured: 6240 tokens of 40 + 40 + 40 heads of 128 in
+// bf16, means of tokens, three axes, fp32 weights of each head 92 us (4.2 TB/s); 5875 tokens of 20 + 4 + 4 fp32 heads of 96
+// 43 us; 32 tokens 7.8 us.  Steps, us of these two: a token a CTA, its heads in registers 135 / 51; persistent CTAs with the
 // next token's loads in flight 114 / 40; rows through shared memory 116 / 51; two vectors a lane 101 / 52; the head's size a
-// constant 91 / 54; several small tokens at a time 90 / 44.
+// constant 91 / 54; several small tokens at a time 90 / 44; three
+// CTAs an SM without spills instead of four 92 / 43 (and 1045 tokens of 20 heads of 80 13 instead of 16 us).  In bulk copies
+// instead of the threads' 16-byte ones 94 / 43 (fewer instructions, but the weights' loads wait longer).
 #include <algorithm>
 
 #include "append.cuh"
@@ -29,7 +31,7 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kNormCtas = 4;             // of an SM, by registers
+constexpr int kNormCtas = 3;             // of an SM, by registers
 constexpr int kSharedOfSm = 228 << 10;  // and by shared memory, of which a CTA takes some for itself
 constexpr int kSharedOfCta = 3 << 10;
 constexpr int kBlock = 16;              // tokens whose places a CTA looks up at a time
